@@ -456,6 +456,90 @@ mxmoe_status fp8bw_grouped_gemm_wgrad_fp8feed(const uint8_t* qdyT, const float* 
                                               const int32_t* offs, int32_t G, int64_t M, int64_t N, int64_t K,
                                               void* dw, mxmoe_dtype dwdt, void* stream);
 
+/* ---------------------------------------------------------------- bf16 grouped GEMM
+ * The three products of an expert layer straight from its row-major bf16 tensors: no quantisation, no
+ * transposed copies, one launch each over every expert's real rows, fp32 sums
+ * (|err| <= 1e-5 * sum |a b| per element, plus half a bf16 ulp for bf16 outputs).
+ *   fwd:   Y[r, n]     = sum_k X[r, k] W[gN + n, k]           y  [M, N]
+ *   dgrad: dX[r, k]    = sum_n dY[r, n] W[gN + n, k]          dx [M, K]
+ *   wgrad: dW[g, n, k] = sum_{r of g} dY[r, n] X[r, k]        dw [G, N, K], 0 for an expert without rows
+ *                                                             (written, also for M == 0)
+ * x [M, K], dy [M, N], w [G*N, K] bf16.  1 <= G <= 1024; N and K are multiples of 8 (not of 128 as in the
+ * block-scaled formats: there are no blocks).  256 rows of an operand must span less than 2 GiB.  M == 0
+ * is a no-op for fwd and dgrad.  A NaN or an infinity reaches exactly the outputs whose sums contain it. */
+mxmoe_status bf16_grouped_gemm_fwd(const void* x, const void* w, const int32_t* offs, int32_t G, int64_t M,
+                                   int64_t N, int64_t K, void* y, mxmoe_dtype ydt, void* stream);
+mxmoe_status bf16_grouped_gemm_dgrad(const void* dy, const void* w, const int32_t* offs, int32_t G, int64_t M,
+                                     int64_t N, int64_t K, void* dx, mxmoe_dtype dxdt, void* stream);
+mxmoe_status bf16_grouped_gemm_wgrad(const void* dy, const void* x, const int32_t* offs, int32_t G, int64_t M,
+                                     int64_t N, int64_t K, void* dw, mxmoe_dtype dwdt, void* stream);
+
+/* ---------------------------------------------------------------- 8-bit integers
+ * int8_quantize_rowwise: x bf16 [R, C] -> q int8 [R, C], s f32 [R]: amax = max_c |x[r, c]|,
+ * s = fl32(amax / 127), q = round-to-nearest-even(127 x / amax) of the exact quotient; an all-zero row has
+ * s = 1 and codes 0; a row with a NaN or an infinity has a scale that is not finite and codes 0 (every
+ * product with it is then NaN or infinite).  C % 8 == 0, R == 0 is a no-op.  For activations (a scale
+ * per token) and for weights [G*N, K] (a scale per output channel).
+ *
+ * int8_quantize_swiglu_rowwise: the same of v[r, c] = g / (1 + e^-g) * u with g = y[r, c], u = y[r, C + c] of
+ * a gate|up tensor y bf16 [R, 2C]: the down projection's input from the gate+up forward's output.  The
+ * codes and scales are those of v in fp64 (fp32 values next to a border are evaluated again).  Values of
+ * v beyond the fp32 range are outside the contract. */
+mxmoe_status int8_quantize_rowwise(const void* x_bf16, int64_t R, int64_t C, int8_t* q, float* s, void* stream);
+mxmoe_status int8_quantize_swiglu_rowwise(const void* y_bf16, int64_t R, int64_t C, int8_t* q, float* s,
+                                          void* stream);
+
+/* int8_grouped_gemm_fwd: Y[r, n] = (sum_k qx[r, k] qw[gN + n, k]) * sx[r] * sw[gN + n]: the sum is exact (int32),
+ * then one fp32 conversion and two fp32 products (|err| <= 2^-22 |Y|, plus half a bf16 ulp for bf16 outputs).
+ * qx [M, K], qw [G*N, K] int8 (any codes, -128 included), sx [M], sw [G*N] f32.  K % 16 == 0, K < 131072 (the
+ * int32 sum), N % 8 == 0, 1 <= G <= 1024; M == 0 is a no-op. */
+mxmoe_status int8_grouped_gemm_fwd(const int8_t* qx, const float* sx, const int8_t* qw, const float* sw,
+                                   const int32_t* offs, int32_t G, int64_t M, int64_t N, int64_t K,
+                                   void* y, mxmoe_dtype ydt, void* stream);
+
+/* ---------------------------------------------------------------- AdamW
+ * adamw_step: one step of AdamW (decoupled weight decay) over `count` tensors in as few launches as the
+ * kernel arguments allow (48 tensors each):
+ *   g' = c g;  m = b1 m + (1 - b1) g';  v = b2 v + (1 - b2) g'^2
+ *   p = (1 - lr wd) p - lr (m / (1 - b1^t)) / (sqrt(v / (1 - b2^t)) + eps);  w = bf16(p)
+ * in fp32, in place.  The gradients (gdt: f32 or bf16) are what the wgrad entry points write, and the bf16
+ * copies w what the quantisers and the bf16 GEMMs read.  state_bits 32: m, v are f32 and ms, vs unused.
+ * state_bits 8: m, v are one byte per element with one f32 scale per 128 consecutive elements (ms, vs
+ * [ceil(n / 128)]); all-zero codes and scales are zero moments:
+ *   m: E4M3 codes, scale max(amax / 448, 2^-126)
+ *   v: code c = 8 E + f > 0 stands for (1 + f / 8) 2^(E - 31), 0 for zero; scale max(vmax / 1.875, 2^-126)
+ * rounded to nearest even, a v > 0 never to zero.  The update itself uses the moments before rounding.  A
+ * gradient that is not finite makes its element, and with 8-bit moments its block's scales, not finite.
+ * The tensor table is read during the call (host memory); tensors must not overlap.  A captured call
+ * replays with the values given here, except those read on the device: *lr_dev (f32) replaces lr and
+ * *step_dev (int64, >= 1) replaces step when not NULL, and *grad_scale (f32) is c (1 when NULL). */
+typedef struct {
+  int64_t n;          /* elements, >= 0 */
+  float* p;           /* weights, f32 [n] */
+  void* w_bf16;       /* bf16 copy [n], or NULL */
+  const void* g;      /* gradient [n], f32 or bf16 */
+  void* m;            /* first moment [n]: f32 or bytes */
+  void* v;            /* second moment [n] */
+  float* ms;          /* 8-bit moments: scales [ceil(n / 128)], else ignored */
+  float* vs;
+} mxmoe_adamw_tensor;
+
+typedef struct {
+  double lr, beta1, beta2, eps, weight_decay;   /* 0 <= beta < 1, eps >= 2^-126 */
+  int64_t step;                                 /* t, counted from 1 */
+  const float* lr_dev;
+  const int64_t* step_dev;
+  const float* grad_scale;
+} mxmoe_adamw_hyper;
+
+mxmoe_status adamw_step(const mxmoe_adamw_tensor* tensors, int32_t count, mxmoe_dtype gdt, int32_t state_bits,
+                        const mxmoe_adamw_hyper* hyper, void* stream);
+
+/* adamw_dequantize: the values of 8-bit moments, q [n] with scales s [ceil(n / 128)] (second_moment 0: the
+ * first moment's codes, 1: the second's), to out [n] (f32, or bf16 rounded to nearest even). */
+mxmoe_status adamw_dequantize(const uint8_t* q, const float* s, int64_t n, int32_t second_moment, void* out,
+                              mxmoe_dtype odt, void* stream);
+
 /* Opt-in offsets validator: copies offs to the host (synchronising `stream`)
  * and checks offs[0] == 0, non-decreasing, offs[G] == M.  Returns
  * MXMOE_ERR_OFFSETS with a message naming the first bad index. */

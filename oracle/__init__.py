@@ -45,6 +45,8 @@ from .blockwise import (bw_quantize_act_1x128, bw_quantize_weight_128x128,
                         bw_group_columns, bw_quantize_colwise_128, pow2_scale)
 from .gemm import (mx_gemm_fwd, mx_gemm_dgrad, mx_gemm_wgrad, bw_gemm_fwd,
                    bw_gemm_dgrad, bw_gemm_wgrad, mxfp4_gemm_fwd, mxfp4_gemm_dgrad, mxfp4_gemm_wgrad, gemm_tolerance, check_gemm)
+from .plain import (dense_gemm_fwd, dense_gemm_dgrad, dense_gemm_wgrad, int8_quantize_rows, int8_gemm_fwd,
+                    adamw, adamw_pack_m, adamw_pack_v, adamw_unpack_m, adamw_unpack_v, adamw_v_values)
 
 __all__ = [
     "E4M3_MAX", "bf16_bits_to_f64", "e4m3_decode", "e4m3_encode",

@@ -27,6 +27,9 @@ __all__ = [
     "fp8bw_colwise_ld_min", "fp8bw_quantize_colwise_128", "fp8bw_grouped_gemm_wgrad",
     "mxfp4_quantize_rowwise", "mxfp4_quantize_colwise", "mxfp4_grouped_gemm_fwd", "mxfp4_grouped_gemm_dgrad",
     "mxfp4_grouped_gemm_wgrad",
+    "bf16_grouped_gemm_fwd", "bf16_grouped_gemm_dgrad", "bf16_grouped_gemm_wgrad",
+    "int8_quantize_rowwise", "int8_quantize_swiglu_rowwise", "int8_grouped_gemm_fwd",
+    "AdamWTable", "adamw_table", "adamw_step", "adamw_dequantize",
     "EXPORTED_SYMBOLS",
 ]
 
@@ -73,6 +76,14 @@ _SIGS = {
     "fp8bw_grouped_gemm_wgrad": (ctypes.c_int, [_p, _p, _p, _p, _i64, _p, _i32, _i64, _i64, _i64, _p, ctypes.c_int,
                                                 _p]),
     "mxmoe_check_offsets": (ctypes.c_int, [_p, _i32, _i64, _p]),
+    "bf16_grouped_gemm_fwd": (ctypes.c_int, [_p, _p, _p, _i32, _i64, _i64, _i64, _p, ctypes.c_int, _p]),
+    "bf16_grouped_gemm_dgrad": (ctypes.c_int, [_p, _p, _p, _i32, _i64, _i64, _i64, _p, ctypes.c_int, _p]),
+    "bf16_grouped_gemm_wgrad": (ctypes.c_int, [_p, _p, _p, _i32, _i64, _i64, _i64, _p, ctypes.c_int, _p]),
+    "int8_quantize_rowwise": (ctypes.c_int, [_p, _i64, _i64, _p, _p, _p]),
+    "int8_quantize_swiglu_rowwise": (ctypes.c_int, [_p, _i64, _i64, _p, _p, _p]),
+    "int8_grouped_gemm_fwd": (ctypes.c_int, [_p, _p, _p, _p, _p, _i32, _i64, _i64, _i64, _p, ctypes.c_int, _p]),
+    "adamw_step": (ctypes.c_int, [_p, _i32, ctypes.c_int, _i32, _p, _p]),
+    "adamw_dequantize": (ctypes.c_int, [_p, _p, _i64, _i32, _p, ctypes.c_int, _p]),
 }
 # the 128-byte tiled layouts: the same arguments as the row-major entry points
 for _n in ("mx_quantize_rowwise", "mx_quantize_colwise", "mx_quantize_dual", "mx_grouped_gemm_fwd",
@@ -599,3 +610,268 @@ def fp8bw_grouped_gemm_wgrad_pow2(qdyT, sdyT, qxT, sxT, offs, M: int, out_dtype:
 def mxmoe_check_offsets(offs, M: int, stream=None) -> None:
     G = offs.numel() - 1
     _check("mxmoe_check_offsets", lib().mxmoe_check_offsets(_ptr(offs), G, M, _stream_handle(stream)))
+
+
+# ---------------------------------------------------------------- plain operands (bf16, int8)
+class _Launch:
+    """The current device and stream of a launch on the tensors' device (they may live on another device
+    than the current one): `with _Launch(stream, x, ...) as handle`."""
+
+    def __init__(self, stream, *tensors):
+        devs = {t.device for t in tensors if t is not None}
+        if len(devs) != 1 or next(iter(devs)).type != "cuda":
+            raise ValueError(f"tensors must be on one GPU, got {sorted(str(d) for d in devs)}")
+        self.stream, self.index, self.guard = stream, next(iter(devs)).index, None
+
+    def __enter__(self):
+        torch = _torch()
+        if torch.cuda.current_device() != self.index:
+            self.guard = torch.cuda.device(self.index)
+            self.guard.__enter__()
+        return _stream_handle(self.stream)
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+        return False
+
+
+def _want(name, t, dtypes, shape):
+    """A tensor argument has one of `dtypes` and the shape (None: any size), or a clear error says so."""
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name}: expected {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
+    if t.dim() != len(shape) or any(w is not None and w != n for w, n in zip(shape, t.shape)):
+        raise ValueError(f"{name}: expected shape {tuple('any' if w is None else w for w in shape)}, got {tuple(t.shape)}")
+
+
+def _bf16_types():
+    torch = _torch()
+    return (torch.bfloat16, torch.int16, torch.uint16)
+
+
+def _groups(offs):
+    _want("offs", offs, (_torch().int32,), (None,))
+    if offs.numel() < 2:
+        raise ValueError("offs: expected G + 1 >= 2 entries")
+    return offs.numel() - 1
+
+
+def _weights(name, w, dtypes, G, N, K):
+    """Expert weights [G*N, K], or the same as [G, N, K]."""
+    _want(name, w, dtypes, (G, N, K) if w.dim() == 3 else (G * N, K))
+
+
+def _bf16_gemm(name, a, b, offs, shape, dims, out_dtype, out, stream):
+    tdt, cdt = _out_dtype(out_dtype)
+    if out is None:
+        out = _empty(shape, tdt, a)
+    else:
+        _want("output", out, (tdt,), shape)
+    G, M, N, K = dims
+    with _Launch(stream, a, b, offs, out) as h:
+        _check(name, getattr(lib(), name)(_ptr(a), _ptr(b), _ptr(offs), G, M, N, K, _ptr(out), cdt, h))
+    return out
+
+
+def bf16_grouped_gemm_fwd(x, w, offs, N: int, out_dtype: str = "f32", y=None, stream=None):
+    """Y [M, N] = per-expert X_g W_g^T of bf16 tensors: x [M, K], w [G*N, K] (or [G, N, K]), offs int32 [G+1].
+    N % 8 == 0, K % 8 == 0."""
+    G = _groups(offs)
+    _want("x", x, _bf16_types(), (None, None))
+    M, K = x.shape
+    _weights("w", w, _bf16_types(), G, N, K)
+    return _bf16_gemm("bf16_grouped_gemm_fwd", x, w, offs, (M, N), (G, M, N, K), out_dtype, y, stream)
+
+
+def bf16_grouped_gemm_dgrad(dy, w, offs, K: int, out_dtype: str = "f32", dx=None, stream=None):
+    """dX [M, K] = per-expert dY_g W_g of bf16 tensors: dy [M, N], w [G*N, K] (or [G, N, K]), the forward's
+    weights as they are."""
+    G = _groups(offs)
+    _want("dy", dy, _bf16_types(), (None, None))
+    M, N = dy.shape
+    _weights("w", w, _bf16_types(), G, N, K)
+    return _bf16_gemm("bf16_grouped_gemm_dgrad", dy, w, offs, (M, K), (G, M, N, K), out_dtype, dx, stream)
+
+
+def bf16_grouped_gemm_wgrad(dy, x, offs, out_dtype: str = "f32", dw=None, stream=None):
+    """dW [G, N, K] = per-expert dY_g^T X_g of bf16 tensors: dy [M, N], x [M, K].  Zero for an expert without
+    rows."""
+    G = _groups(offs)
+    _want("dy", dy, _bf16_types(), (None, None))
+    M, N = dy.shape
+    _want("x", x, _bf16_types(), (M, None))
+    K = x.shape[1]
+    return _bf16_gemm("bf16_grouped_gemm_wgrad", dy, x, offs, (G, N, K), (G, M, N, K), out_dtype, dw, stream)
+
+
+def _int8_rowwise(name, x, C, q, s, stream):
+    torch = _torch()
+    R = x.shape[0]
+    q = _empty((R, C), torch.int8, x) if q is None else q
+    s = _empty((R,), torch.float32, x) if s is None else s
+    _want("q", q, (torch.int8,), (R, C))
+    _want("s", s, (torch.float32,), (R,))
+    with _Launch(stream, x, q, s) as h:
+        _check(name, getattr(lib(), name)(_ptr(x), R, C, _ptr(q), _ptr(s), h))
+    return q, s
+
+
+def int8_quantize_rowwise(x, q=None, s=None, stream=None):
+    """x bf16 [R, C] -> (q int8 [R, C], s f32 [R]): s = amax / 127 of the row, q = nearest of 127 x / amax
+    (tokens of activations, output channels of weights).  C % 8 == 0."""
+    _want("x", x, _bf16_types(), (None, None))
+    return _int8_rowwise("int8_quantize_rowwise", x, x.shape[1], q, s, stream)
+
+
+def int8_quantize_swiglu_rowwise(y, q=None, s=None, stream=None):
+    """y bf16 [R, 2C] (gate columns, then up columns) -> (q int8 [R, C], s f32 [R]) of silu(gate) * up."""
+    _want("y", y, _bf16_types(), (None, None))
+    if y.shape[1] % 2:
+        raise ValueError(f"y: expected gate and up columns, got {y.shape[1]}")
+    return _int8_rowwise("int8_quantize_swiglu_rowwise", y, y.shape[1] // 2, q, s, stream)
+
+
+def int8_grouped_gemm_fwd(qx, sx, qw, sw, offs, N: int, out_dtype: str = "f32", y=None, stream=None):
+    """Y [M, N] = per-expert qx_g qw_g^T (exact) times the token's and the channel's scale: qx int8 [M, K],
+    sx f32 [M], qw int8 [G*N, K] (or [G, N, K]), sw f32 [G*N] (or [G, N]).  N % 8 == 0, K % 16 == 0."""
+    torch = _torch()
+    G = _groups(offs)
+    _want("qx", qx, (torch.int8,), (None, None))
+    M, K = qx.shape
+    _want("sx", sx, (torch.float32,), (M,))
+    _weights("qw", qw, (torch.int8,), G, N, K)
+    _want("sw", sw, (torch.float32,), (G, N) if sw.dim() == 2 else (G * N,))
+    tdt, cdt = _out_dtype(out_dtype)
+    if y is None:
+        y = _empty((M, N), tdt, qx)
+    else:
+        _want("y", y, (tdt,), (M, N))
+    with _Launch(stream, qx, sx, qw, sw, offs, y) as h:
+        _check("int8_grouped_gemm_fwd", lib().int8_grouped_gemm_fwd(
+            _ptr(qx), _ptr(sx), _ptr(qw), _ptr(sw), _ptr(offs), G, M, N, K, _ptr(y), cdt, h))
+    return y
+
+
+# ---------------------------------------------------------------- AdamW
+class _AdamWTensor(ctypes.Structure):
+    _fields_ = [("n", _i64)] + [(k, _p) for k in ("p", "w_bf16", "g", "m", "v", "ms", "vs")]
+
+
+class _AdamWHyper(ctypes.Structure):
+    _fields_ = [(k, ctypes.c_double) for k in ("lr", "beta1", "beta2", "eps", "weight_decay")] + \
+               [("step", _i64)] + [(k, _p) for k in ("lr_dev", "step_dev", "grad_scale")]
+
+
+class AdamWTable:
+    """The tensors of an optimizer step (adamw_table makes it): their addresses, checked once.  It keeps the
+    tensors alive; make a new one when a tensor is replaced by another."""
+
+    def __init__(self, entries, array, bits, grad_dtype, like):
+        self.entries, self.array, self.bits, self.grad_dtype, self.like = entries, array, bits, grad_dtype, like
+
+
+def adamw_table(params, grads, exp_avg, exp_avg_sq, weights=None, exp_avg_scales=None, exp_avg_sq_scales=None):
+    """Tensors of adamw_step, as lists of one length (all contiguous, on one GPU, none overlapping another that
+    the step writes).
+
+    params f32; grads all f32 or all bf16; weights (optional) the bf16 copies, entries may be None; exp_avg and
+    exp_avg_sq the moments: all f32, or all uint8 with exp_avg_scales and exp_avg_sq_scales f32 [ceil(n / 128)]
+    (zeros in codes and scales are zero moments)."""
+    torch = _torch()
+    count = len(params)
+    if count == 0:
+        raise ValueError("params: expected at least one tensor")
+    eight = exp_avg[0].dtype == torch.uint8 if len(exp_avg) else False
+    if eight != (exp_avg_scales is not None) or eight != (exp_avg_sq_scales is not None):
+        raise ValueError("exp_avg_scales and exp_avg_sq_scales go with uint8 moments, and only with them")
+    none = [None] * count
+    lists = {"params": params, "weights": none if weights is None else weights, "grads": grads, "exp_avg": exp_avg,
+             "exp_avg_sq": exp_avg_sq, "exp_avg_scales": exp_avg_scales if eight else none,
+             "exp_avg_sq_scales": exp_avg_sq_scales if eight else none}
+    for k, v in lists.items():
+        if len(v) != count:
+            raise ValueError(f"{k}: expected {count} tensors, got {len(v)}")
+    gdt = grads[0].dtype
+    if gdt not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"grads: expected float32 or bfloat16, got {gdt}")
+    state = torch.uint8 if eight else torch.float32
+    types = {"params": torch.float32, "weights": torch.bfloat16, "grads": gdt, "exp_avg": state, "exp_avg_sq": state,
+             "exp_avg_scales": torch.float32, "exp_avg_sq_scales": torch.float32}
+    array, entries, spans = (_AdamWTensor * count)(), [], []
+    for i in range(count):
+        row = [lists[k][i] for k in lists]
+        n = params[i].numel()
+        for k, t in zip(lists, row):
+            if t is None:
+                if k != "weights" and not (k.endswith("scales") and not eight):
+                    raise ValueError(f"{k}[{i}] is None")
+                continue
+            want = (n + 127) // 128 if k.endswith("scales") else n
+            if t.dtype != types[k]:
+                raise TypeError(f"{k}[{i}]: expected {types[k]}, got {t.dtype}")
+            if t.numel() != want:
+                raise ValueError(f"{k}[{i}]: expected {want} elements, got {t.numel()}")
+            if t.device != params[0].device:
+                raise ValueError(f"{k}[{i}] is on {t.device}, params[0] on {params[0].device}")
+            if want:
+                spans.append((_ptr(t), _ptr(t) + want * t.element_size(), k != "grads", f"{k}[{i}]"))
+        array[i] = _AdamWTensor(n, *[_ptr(t) for t in row])
+        entries.append(row)
+    last = None                       # of the spans so far, the one that ends last, and the last-ending written one
+    wrote = None
+    for s in sorted(spans):
+        hit = last if s[2] else wrote
+        if hit is not None and s[0] < hit[1]:
+            raise ValueError(f"{s[3]} and {hit[3]} overlap")
+        last = s if last is None or s[1] > last[1] else last
+        if s[2]:
+            wrote = s if wrote is None or s[1] > wrote[1] else wrote
+    return AdamWTable(entries, array, 8 if eight else 32, MXMOE_BF16 if gdt == torch.bfloat16 else MXMOE_F32, params[0])
+
+
+def adamw_step(table, step, lr, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8,
+               weight_decay: float = 0.01, grad_scale=None, stream=None) -> None:
+    """One AdamW step over the table's tensors, in place, in one launch (per 48 tensors).
+
+    step (counted from 1) and lr are numbers, or GPU scalars (int64 / float32 tensors) that the kernel reads,
+    for a step captured into a graph.  grad_scale: a float32 GPU scalar that multiplies every gradient
+    (clipping), or None."""
+    torch = _torch()
+    hyper = _AdamWHyper(0.0, float(beta1), float(beta2), float(eps), float(weight_decay), 1, None, None, None)
+    scalars = []
+    if isinstance(lr, torch.Tensor):
+        scalars.append(("lr", lr, torch.float32, "lr_dev"))
+    else:
+        hyper.lr = float(lr)
+    if isinstance(step, torch.Tensor):
+        scalars.append(("step", step, torch.int64, "step_dev"))
+    else:
+        hyper.step = int(step)
+    if grad_scale is not None:
+        scalars.append(("grad_scale", grad_scale, torch.float32, "grad_scale"))
+    for name, t, dt, field in scalars:
+        if t.dtype != dt or t.numel() != 1:
+            raise TypeError(f"{name}: expected one {dt} on the GPU, got {t.dtype} of {t.numel()}")
+        setattr(hyper, field, _ptr(t))
+    with _Launch(stream, table.like, *[t for _, t, _, _ in scalars]) as h:
+        _check("adamw_step", lib().adamw_step(ctypes.addressof(table.array), len(table.array), table.grad_dtype,
+                                              table.bits, ctypes.addressof(hyper), h))
+
+
+def adamw_dequantize(q, s, moment: str, out_dtype: str = "f32", out=None, stream=None):
+    """Values of 8-bit moments: q uint8 (any shape), s f32 [ceil(n / 128)], moment "exp_avg" or "exp_avg_sq"
+    (their codes differ); out has q's shape."""
+    torch = _torch()
+    if moment not in ("exp_avg", "exp_avg_sq"):
+        raise ValueError(f"moment: expected 'exp_avg' or 'exp_avg_sq', got {moment!r}")
+    _want("q", q, (torch.uint8,), q.shape)
+    _want("s", s, (torch.float32,), ((q.numel() + 127) // 128,))
+    tdt, cdt = _out_dtype(out_dtype)
+    if out is None:
+        out = _empty(q.shape, tdt, q)
+    else:
+        _want("out", out, (tdt,), q.shape)
+    with _Launch(stream, q, s, out) as h:
+        _check("adamw_dequantize", lib().adamw_dequantize(_ptr(q), _ptr(s), q.numel(), int(moment == "exp_avg_sq"),
+                                                          _ptr(out), cdt, h))
+    return out

@@ -1,5 +1,6 @@
 // C ABI of the MXFP8 expert-GEMM library: host-side argument validation (before any HIP call),
 // device check, dispatch to the kernels.  See include/mxmoe.h for the contract of each entry point.
+#include <math.h>
 #include <stdarg.h>
 #include <stdio.h>
 #include <string.h>
@@ -765,6 +766,168 @@ mxmoe_status fp8bw_grouped_gemm_dgrad_fp8feed(const uint8_t* qdy, const float* s
                                               int64_t K, void* dx, mxmoe_dtype dxdt, void* stream) {
   return bw_gemm_common(kDgrad, "fp8bw_grouped_gemm_dgrad_fp8feed", kFeedFast, qdy, sdy, qwT, sw, offs, G, M, N, K,
                         dx, (int)dxdt, stream);
+}
+
+// ---- plain operands: bf16 and int8 grouped GEMMs -------------------------------------------------
+static mxmoe_status dense_common(int mode, bool int8, const char* fn, const void* a, const float* sa, const void* b,
+                                 const float* sb, const int32_t* offs, int32_t G, int64_t M, int64_t N, int64_t K,
+                                 void* out, int dt, void* stream) {
+  if (G < 1 || G > kMaxG) return fail(MXMOE_ERR_SHAPE, "%s: G = %d outside [1, %d]", fn, (int)G, (int)kMaxG);
+  const int kmul = int8 ? 16 : 8;
+  if (M < 0 || N <= 0 || K <= 0 || M > INT32_MAX || N > INT32_MAX || K > INT32_MAX || N % 8 || K % kmul)
+    return fail(MXMOE_ERR_SHAPE, "%s: need 0 <= M, N > 0 a multiple of 8, K > 0 a multiple of %d, each below 2^31 "
+                "(M=%lld N=%lld K=%lld)", fn, kmul, (long long)M, (long long)N, (long long)K);
+  if (int8 && K >= 131072) return fail(MXMOE_ERR_SHAPE, "%s: K = %lld must be below 131072", fn, (long long)K);
+  if (dt != MXMOE_F32 && dt != MXMOE_BF16) return fail(MXMOE_ERR_DTYPE, "%s: unknown output dtype %d", fn, dt);
+  GemmArgs p;
+  memset(&p, 0, sizeof p);
+  p.a = (const uint8_t*)a; p.sa = sa; p.b = (const uint8_t*)b; p.sb = sb; p.offs = offs; p.out = out;
+  p.M = M; p.N = N; p.K = K; p.G = G;
+  p.out_bf16 = dt == MXMOE_BF16;
+  const int64_t es = int8 ? 1 : 2;
+  p.lda = es * (mode == kFwd ? K : N);
+  p.ldb = es * K;
+  TRY(check_strides(fn, p, 256));
+  TRY(check_ptr(fn, "offs", offs, 4));
+  if (mode != kWgrad && M == 0) return ok();
+  TRY(check_ptr(fn, "output", out, 16));
+  if (M > 0) TRY(check_ptr(fn, "A operand", a, 16));
+  if (M > 0 || mode != kWgrad) TRY(check_ptr(fn, "B operand", b, 16));
+  if (int8) {
+    TRY(check_ptr(fn, "A scales", sa, 4));
+    TRY(check_ptr(fn, "B scales", sb, 4));
+  }
+  TRY(check_device());
+  return launched(launch_dense_gemm(mode, int8, p, (hipStream_t)stream), fn);
+}
+
+mxmoe_status bf16_grouped_gemm_fwd(const void* x, const void* w, const int32_t* offs, int32_t G, int64_t M, int64_t N,
+                                   int64_t K, void* y, mxmoe_dtype ydt, void* stream) {
+  return dense_common(kFwd, false, "bf16_grouped_gemm_fwd", x, nullptr, w, nullptr, offs, G, M, N, K, y, (int)ydt,
+                      stream);
+}
+
+mxmoe_status bf16_grouped_gemm_dgrad(const void* dy, const void* w, const int32_t* offs, int32_t G, int64_t M,
+                                     int64_t N, int64_t K, void* dx, mxmoe_dtype dxdt, void* stream) {
+  return dense_common(kDgrad, false, "bf16_grouped_gemm_dgrad", dy, nullptr, w, nullptr, offs, G, M, N, K, dx,
+                      (int)dxdt, stream);
+}
+
+mxmoe_status bf16_grouped_gemm_wgrad(const void* dy, const void* x, const int32_t* offs, int32_t G, int64_t M,
+                                     int64_t N, int64_t K, void* dw, mxmoe_dtype dwdt, void* stream) {
+  return dense_common(kWgrad, false, "bf16_grouped_gemm_wgrad", dy, nullptr, x, nullptr, offs, G, M, N, K, dw,
+                      (int)dwdt, stream);
+}
+
+mxmoe_status int8_grouped_gemm_fwd(const int8_t* qx, const float* sx, const int8_t* qw, const float* sw,
+                                   const int32_t* offs, int32_t G, int64_t M, int64_t N, int64_t K, void* y,
+                                   mxmoe_dtype ydt, void* stream) {
+  return dense_common(kFwd, true, "int8_grouped_gemm_fwd", qx, sx, qw, sw, offs, G, M, N, K, y, (int)ydt, stream);
+}
+
+static mxmoe_status int8_rowwise_impl(const char* fn, const void* x, int64_t R, int64_t C, bool gated, int8_t* q,
+                                      float* s, void* stream) {
+  if (R < 0 || C <= 0 || C % 8 || C > INT32_MAX)
+    return fail(MXMOE_ERR_SHAPE, "%s: need R >= 0, 0 < C < 2^31, C %% 8 == 0 (R=%lld C=%lld)", fn, (long long)R,
+                (long long)C);
+  if (R == 0) return ok();
+  TRY(check_ptr(fn, "x", x, 16));
+  TRY(check_ptr(fn, "q", q, 16));
+  TRY(check_ptr(fn, "s", s, 4));
+  TRY(check_device());
+  return launched(launch_int8_rowwise((const uint16_t*)x, R, C, gated, q, s, (hipStream_t)stream), fn);
+}
+
+mxmoe_status int8_quantize_rowwise(const void* x, int64_t R, int64_t C, int8_t* q, float* s, void* stream) {
+  return int8_rowwise_impl("int8_quantize_rowwise", x, R, C, false, q, s, stream);
+}
+
+mxmoe_status int8_quantize_swiglu_rowwise(const void* y, int64_t R, int64_t C, int8_t* q, float* s, void* stream) {
+  return int8_rowwise_impl("int8_quantize_swiglu_rowwise", y, R, C, true, q, s, stream);
+}
+
+// ---- AdamW -----------------------------------------------------------------------------------
+mxmoe_status adamw_step(const mxmoe_adamw_tensor* tensors, int32_t count, mxmoe_dtype gdt, int32_t state_bits,
+                        const mxmoe_adamw_hyper* hyper, void* stream) {
+  const char* fn = "adamw_step";
+  if (count < 0) return fail(MXMOE_ERR_SHAPE, "%s: count = %d", fn, (int)count);
+  if (state_bits != 8 && state_bits != 32)
+    return fail(MXMOE_ERR_DTYPE, "%s: moments of 32 or 8 bits, not %d", fn, (int)state_bits);
+  if (gdt != MXMOE_F32 && gdt != MXMOE_BF16) return fail(MXMOE_ERR_DTYPE, "%s: unknown gradient dtype %d", fn, (int)gdt);
+  if (!hyper || (count && !tensors)) return fail(MXMOE_ERR_NULL, "%s: tensors or hyper is NULL", fn);
+  const mxmoe_adamw_hyper& h = *hyper;
+  if (!(h.beta1 >= 0 && h.beta1 < 1 && h.beta2 >= 0 && h.beta2 < 1) || !(h.eps >= 0x1p-126 && h.eps <= 1e30) ||
+      !(h.lr - h.lr == 0) || !(h.weight_decay - h.weight_decay == 0) || (!h.step_dev && h.step < 1))
+    return fail(MXMOE_ERR_SHAPE, "%s: need finite lr and weight_decay, 0 <= beta1, beta2 < 1, eps >= 2^-126, step >= 1", fn);
+  if (h.lr_dev && !aligned(h.lr_dev, 4)) return fail(MXMOE_ERR_ALIGN, "%s: lr_dev not 4-byte aligned", fn);
+  if (h.step_dev && !aligned(h.step_dev, 8)) return fail(MXMOE_ERR_ALIGN, "%s: step_dev not 8-byte aligned", fn);
+  if (h.grad_scale && !aligned(h.grad_scale, 4)) return fail(MXMOE_ERR_ALIGN, "%s: grad_scale not 4-byte aligned", fn);
+  int64_t total = 0;
+  for (int32_t k = 0; k < count; ++k) {
+    const mxmoe_adamw_tensor& t = tensors[k];
+    if (t.n < 0 || t.n > ((int64_t)1 << 40))
+      return fail(MXMOE_ERR_SHAPE, "%s: tensor %d has n = %lld", fn, (int)k, (long long)t.n);
+    if (t.n == 0) continue;
+    const void* need[4] = {t.p, t.g, t.m, t.v};
+    for (const void* q : need) {
+      if (!q) return fail(MXMOE_ERR_NULL, "%s: tensor %d: p, g, m or v is NULL", fn, (int)k);
+      if (!aligned(q, 16)) return fail(MXMOE_ERR_ALIGN, "%s: tensor %d: p, g, m or v not 16-byte aligned", fn, (int)k);
+    }
+    if (t.w_bf16 && !aligned(t.w_bf16, 16))
+      return fail(MXMOE_ERR_ALIGN, "%s: tensor %d: w_bf16 not 16-byte aligned", fn, (int)k);
+    if (state_bits == 8) {
+      if (!t.ms || !t.vs) return fail(MXMOE_ERR_NULL, "%s: tensor %d: ms or vs is NULL", fn, (int)k);
+      if (!aligned(t.ms, 4) || !aligned(t.vs, 4))
+        return fail(MXMOE_ERR_ALIGN, "%s: tensor %d: ms or vs not 4-byte aligned", fn, (int)k);
+    }
+    total += (t.n + 1023) / 1024;
+  }
+  if (total == 0) return ok();
+  TRY(check_device());
+  AdamwArgs p;
+  memset(&p, 0, sizeof p);
+  p.b1 = (float)h.beta1; p.c1 = (float)(1.0 - h.beta1);
+  p.b2 = (float)h.beta2; p.c2 = (float)(1.0 - h.beta2);
+  p.eps = (float)h.eps;
+  p.lr = h.lr; p.beta1 = h.beta1; p.beta2 = h.beta2; p.wd = h.weight_decay;
+  p.t = h.step < 1 ? 1 : h.step;
+  p.decay = (float)(1.0 - h.lr * h.weight_decay);
+  p.step_size = (float)(h.lr / (1.0 - pow(h.beta1, (double)p.t)));
+  p.inv_bc2 = (float)(1.0 / (1.0 - pow(h.beta2, (double)p.t)));
+  p.lr_dev = h.lr_dev; p.step_dev = h.step_dev; p.grad_scale = h.grad_scale;
+  p.per = adamw_elements_per_block(total);
+  int32_t k = 0;
+  while (k < count) {
+    int64_t blocks = 0;
+    p.count = 0;
+    for (; k < count && p.count < kAdamwTensors; ++k) {
+      if (tensors[k].n == 0) continue;
+      const int64_t nb = (tensors[k].n + p.per - 1) / p.per;
+      if (blocks + nb > INT32_MAX) break;
+      p.t_[p.count] = tensors[k];
+      p.first[p.count++] = (int32_t)blocks;
+      blocks += nb;
+    }
+    if (p.count == 0) break;
+    const hipError_t e = launch_adamw(p, (int)blocks, state_bits == 8, gdt == MXMOE_BF16, (hipStream_t)stream);
+    if (e != hipSuccess) return launched(e, fn);
+  }
+  return ok();
+}
+
+mxmoe_status adamw_dequantize(const uint8_t* q, const float* s, int64_t n, int32_t second_moment, void* out,
+                              mxmoe_dtype odt, void* stream) {
+  const char* fn = "adamw_dequantize";
+  if (n < 0 || n > ((int64_t)1 << 40)) return fail(MXMOE_ERR_SHAPE, "%s: n = %lld", fn, (long long)n);
+  if (second_moment != 0 && second_moment != 1)
+    return fail(MXMOE_ERR_DTYPE, "%s: second_moment = %d, expected 0 or 1", fn, (int)second_moment);
+  if (odt != MXMOE_F32 && odt != MXMOE_BF16) return fail(MXMOE_ERR_DTYPE, "%s: unknown output dtype %d", fn, (int)odt);
+  if (n == 0) return ok();
+  TRY(check_ptr(fn, "q", q, 16));
+  TRY(check_ptr(fn, "s", s, 4));
+  TRY(check_ptr(fn, "out", out, 16));
+  TRY(check_device());
+  return launched(launch_adamw_values(q, s, n, second_moment == 1, odt == MXMOE_BF16, out, (hipStream_t)stream), fn);
 }
 
 mxmoe_status mxmoe_check_offsets(const int32_t* offs, int32_t G, int64_t M, void* stream) {
