@@ -8,7 +8,11 @@
 // scale max(amax / 448, 2^-126); v has five bits of exponent and three of mantissa and no sign (code
 // 8 E + f, 1 .. 255, is (1 + f / 8) 2^(E - 31), code 0 is zero) with the scale max(vmax / 1.875, 2^-126).
 // Both round to nearest even; a v that is not zero never becomes zero, so its quotient cannot blow up.
-// The update uses the moments before they are rounded.  Everything is computed in fp32.
+// The update uses the moments before they are rounded.  Everything is computed in fp32.  The moments'
+// operations are rounded one by one in the order written (no contraction into fused multiply-adds, scales
+// formed with the rounded reciprocals of 448 and 1.875, quotients by the scale correctly rounded), so that
+// the codes are those of the same formula in any fp32 implementation: a value next to a border between two
+// codes does not depend on how a compiler fuses.
 //
 // Bound: HBM.  Bytes per element: weight 8, copy 2, gradient 4 or 2, moments 16 (fp32) or 4.06 (8 bits).
 // A lane owns four consecutive elements (16-byte accesses of the fp32 arrays), so 32 lanes hold a block of
@@ -51,18 +55,23 @@ __device__ __forceinline__ void decode_v(uint32_t w, float s, float (&v)[4]) {
 #pragma unroll
   for (int e = 0; e < 4; ++e) v[e] = decode_v1((w >> (8 * e)) & 255u, s);
 }
-__device__ __forceinline__ uint32_t encode_m(const float (&m)[4], float inv) {
+// a / s with r the rounded reciprocal of s: one correction of the product rounds correctly (Markstein).
+__device__ __forceinline__ float quotient(float a, float s, float r) {
+  const float q = a * r;
+  return fmaf(fmaf(-q, s, a), r, q);
+}
+__device__ __forceinline__ uint32_t encode_m(const float (&m)[4], float s, float inv) {
   float y[4];
 #pragma unroll
-  for (int e = 0; e < 4; ++e) y[e] = fminf(fmaxf(m[e] * inv, -448.0f), 448.0f);
+  for (int e = 0; e < 4; ++e) y[e] = fminf(fmaxf(quotient(m[e], s, inv), -448.0f), 448.0f);
   int o = __builtin_amdgcn_cvt_pk_fp8_f32(y[0], y[1], 0, false);
   return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(y[2], y[3], o, true);
 }
-__device__ __forceinline__ uint32_t encode_v(const float (&v)[4], float inv) {
+__device__ __forceinline__ uint32_t encode_v(const float (&v)[4], float s, float inv) {
   uint32_t w = 0;
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
-    const uint32_t bits = __float_as_uint(v[e] * inv);
+    const uint32_t bits = __float_as_uint(quotient(v[e], s, inv));
     int c = (int)((bits + 0x7FFFFu + ((bits >> 20) & 1u)) >> 20) - 96 * 8;
     c = v[e] > 0.0f ? min(max(c, 1), 255) : 0;
     w |= (uint32_t)c << (8 * e);
@@ -73,6 +82,13 @@ __device__ __forceinline__ uint32_t encode_v(const float (&v)[4], float inv) {
 struct Consts {
   float scale, b1, c1, b2, c2, decay, step, inv_bc2, eps;
 };
+
+__device__ __forceinline__ void moments(float& m, float& v, float g, const Consts& c) {
+#pragma clang fp contract(off)
+  const float ge = g * c.scale;
+  m = c.b1 * m + c.c1 * ge;
+  v = c.b2 * v + c.c2 * ge * ge;
+}
 
 // b^t for t >= 1 by repeated squaring (every lane the same)
 __device__ double power(double b, int64_t t) {
@@ -164,9 +180,7 @@ __global__ __launch_bounds__(NT) void adamw_kernel(AdamwArgs p) {
     }
 #pragma unroll
     for (int e = 0; e < kVec; ++e) {
-      const float ge = g[e] * c.scale;
-      m[e] = fmaf(c.b1, m[e], c.c1 * ge);
-      v[e] = fmaf(c.b2, v[e], c.c2 * ge * ge);
+      moments(m[e], v[e], g[e], c);
       // hardware square root and reciprocal (one unit in the last place each, of an update that is far
       // smaller than the weight)
       const float root = __builtin_amdgcn_sqrtf(v[e] * c.inv_bc2) + c.eps;
@@ -183,13 +197,13 @@ __global__ __launch_bounds__(NT) void adamw_kernel(AdamwArgs p) {
       am = max32(am);
       av = max32(av);
       auto scale_of = [](uint32_t bits, float top) {
-        const float s = __uint_as_float(bits) / top;
+        const float s = __uint_as_float(bits) * (1.0f / top);
         return s < kTinyScale ? kTinyScale : s;
       };
       ms = scale_of(am, 448.0f);
       vs = scale_of(av, kTop);
-      mq = encode_m(m, 1.0f / ms);
-      vq = encode_v(v, 1.0f / vs);
+      mq = encode_m(m, ms, 1.0f / ms);
+      vq = encode_v(v, vs, 1.0f / vs);
       if (left > 0 && (threadIdx.x & 31) == 0) {
         t.ms[i / 128] = ms;
         t.vs[i / 128] = vs;
