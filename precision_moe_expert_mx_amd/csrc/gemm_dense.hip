@@ -8,12 +8,18 @@
 //   wgrad:   out[i, j] = sum_t dY[r0 + t, i] X[r0 + t, j]     L = m_g   (both have t as their rows)
 //   int8:    out[i, j] = sx[row_i] sw[gN + j] sum_t qx[row_i, t] qw[gN + j, t]   (int32 sum, exact)
 //
-// Tiling: 256 x 256 outputs per workgroup of 8 waves (2 along A x 4 along B, 128 x 64 each).  The
-// contraction advances 128 bytes per stage (64 bf16, 128 int8) through two LDS stages filled by
-// direct-to-LDS loads.  An operand contiguous along t is staged as 256 rows of 128 bytes; one with t as
-// its rows as 64 rows of 256 columns (512 bytes), which the matrix instruction's fragments are read from
-// with the transposing LDS read (ds_read_b64_tr_b16: 16 lanes read 4 rows x 16 columns and each gets one
-// column's 4 values), so no operand is ever transposed in memory.
+// Tiling: 256 x 256 outputs per workgroup of 4 waves, one per SIMD, 128 x 128 outputs each (256 of a lane's
+// 512 registers hold sums).  The widest wave tile is the point: a k-step of a wave reads 4 + 4 fragments
+// from LDS for 16 matrix instructions, 64 B per clock and CU at the full matrix rate, and the stage loads
+// write another 32, of the 128 that LDS moves; eight waves of 128 x 64 would need all of it (measured:
+// 1000-1060 TFLOP/s).  The contraction advances 64 bytes per stage (32 bf16, 64 int8: two k-steps) through a
+// ring of five 32 KiB LDS stages filled by direct-to-LDS loads, four stages ahead and without draining them:
+// a wave waits only until its share of the next stage has landed (a counted vmcnt), and reads the fragments
+// of a k-step while it multiplies the one before, across stages too.
+// An operand contiguous along t is staged as 256 rows of 64 bytes; one with t as its rows as 32 rows of 256
+// columns (512 bytes), which fragments are read from with the transposing LDS read (ds_read_b64_tr_b16: 16
+// lanes read 4 rows x 16 columns and each gets one column's 4 values), so no operand is ever transposed in
+// memory.  A tile with at most 128 (64) valid A rows runs as 128 (64) x 256.
 #include <type_traits>
 
 #include "grouped_tile.h"
@@ -24,16 +30,19 @@ namespace {
 using Tile = GroupTile;
 
 constexpr int BM = 256, BN = 256;                // A / B rows (output rows / columns) per tile
-constexpr int BKB = 128;                         // contraction bytes per stage
-constexpr int kWavesM = 2, kWavesN = 4;
+constexpr int BKB = 64;                          // contraction bytes per stage
+constexpr int kWavesM = 2, kWavesN = 2;
 constexpr int kWaves = kWavesM * kWavesN;
 constexpr int NT = 64 * kWaves;
-constexpr int WM = BM / kWavesM, WN = BN / kWavesN;
-constexpr int kOp = BM * BKB;                    // bytes of one operand's stage (both layouts): 32 KiB
+constexpr int WN = BN / kWavesN;                 // output columns per wave
+constexpr int NJ = WN / 32;
+constexpr int kOp = BM * BKB;                    // bytes of one operand's stage (both layouts): 16 KiB
 constexpr int kStage = 2 * kOp;
-constexpr int kEpi = kWaves * 64 * (128 * (WN / 32) + 16);   // the epilogue's staged rows
-constexpr int kLds = 2 * kStage > kEpi ? 2 * kStage : kEpi;
-static_assert(BM == BN, "one stage size for both operands");
+constexpr int kRing = 5;                         // stages in LDS
+constexpr int kLoads = kOp / 1024 / kWaves;      // 1 KiB loads per wave, stage and (whole) operand
+constexpr int kLds = kRing * kStage;
+static_assert(BM == BN && kLoads == 4, "one stage size for both operands");
+static_assert(kWaves * 64 * (128 * NJ + 16) <= kLds, "staged epilogue must fit in LDS");
 
 typedef float v16f __attribute__((ext_vector_type(16)));
 typedef int v16i __attribute__((ext_vector_type(16)));
@@ -42,48 +51,79 @@ typedef short v8s __attribute__((ext_vector_type(8)));
 
 enum DenseType { kBf16 = 0, kInt8 = 1 };
 
-// Staged rows of 128 bytes: 16-byte chunk c of row r at position c ^ ((r >> 1) & 7), so that the lanes of
-// one 16-byte LDS read (consecutive rows, same logical chunk) hit distinct banks.
-__device__ __forceinline__ int row_swz(int r) { return (r >> 1) & 7; }
+// Staged rows of 64 bytes, four to the 256 bytes that 16 lanes read at once: 16-byte chunk c of row r at
+// position c ^ ((r >> 2) & 3), so that 16 consecutive rows' chunks hit distinct banks.
+__device__ __forceinline__ int row_swz(int r) { return (r >> 2) & 3; }
 // Staged contraction rows of 512 bytes: 64-byte piece c of row t at piece c ^ col_swz(t).  One transposing
 // read takes 64 bytes of rows t .. t + 3 and t + 8 .. t + 11: eight different pieces of the 512 bytes.
 __device__ __forceinline__ int col_swz(int t) { return (t & 3) | ((t >> 1) & 4); }
 
+// One operand of a wave: its share of a stage's loads (kLoads of 1 KiB, fewer of A in a tile of fewer
+// rows) as 32-bit lane offsets from a wave-uniform base that moves by `step` bytes per stage, and its
+// fragments' LDS offsets in a stage.
 template <bool COLS_>
 struct Operand {
   static constexpr bool COLS = COLS_;
-  // This wave's share of a stage: four loads of 1 KiB.  Offsets are relative to a wave-uniform base that
-  // moves by `step` bytes per stage; `at` is the position along the contraction (bytes of a row, or rows)
-  // that decides whether a piece lies inside it.
-  uint32_t off[4];
-  int at[4];
-  const uint8_t* base;
+  uint32_t off[kLoads];
+  uint32_t frag[COLS ? 4 : 2];
+  const uint8_t* base;                           // of the next stage to load
   int64_t step;
-};
 
-// MFMA fragment of 32 rows (outputs r0 .. r0 + 31) x 32 contraction bytes (k-step kk of the stage):
-// lane l holds row r0 + l % 32, bytes 16 (l / 32) .. + 15 of the k-step.
-template <bool COLS>
-__device__ __forceinline__ v4i read_frag(const char* st, int r0, int kk, int lane) {
-  if constexpr (!COLS) {
-    const int r = r0 + (lane & 31), c = 2 * kk + (lane >> 5);
-    return *(const v4i*)(st + r * BKB + ((c ^ row_swz(r)) << 4));
-  } else {
-    // bf16 elements: rows t = 16 kk + 8 (l / 32) + 0..7 of the column r0 + l % 32, four rows per read.
-    // Lane i of a 16-lane group points at row i / 4, columns 4 (i % 4) .. + 3 of the group's 4 x 16 block.
-    const int i = lane & 15;
-    const int t = 16 * kk + 8 * (lane >> 5) + (i >> 2);
-    const int cb = 2 * (r0 + (lane & 16) + 4 * (i & 3));       // byte of the row
-    v4s v[2];
+  // Load j of wave w fills the 1 KiB piece loads * w + j of the operand's stage.  Rows (columns) past the
+  // `lim` valid ones repeat the last valid one.
+  __device__ __forceinline__ void place(int lane, int w, int loads, const uint8_t* src, int64_t ld, int lim, int tps) {
+    base = src;
+    step = COLS ? tps * ld : BKB;
 #pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      const int tq = t + 4 * q;
-      const char* p = st + tq * 512 + (cb ^ (col_swz(tq) << 6));
-      v[q] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) v4s*)p);
+    for (int j = 0; j < kLoads; ++j) {
+      if (j >= loads) continue;
+      if constexpr (!COLS) {
+        const int r = 16 * (loads * w + j) + (lane >> 2);
+        off[j] = (uint32_t)(min(r, lim - 1) * ld) + 16 * ((lane & 3) ^ row_swz(r));
+      } else {
+        const int r = 2 * (loads * w + j) + (lane >> 5);
+        const int c = (lane & 31) ^ (col_swz(r) << 2);     // 16-byte chunk: eight columns
+        off[j] = (uint32_t)(r * ld) + 2 * min(8 * c, lim - 8);
+      }
     }
-    return __builtin_bit_cast(v4i, __builtin_shufflevector(v[0], v[1], 0, 1, 2, 3, 4, 5, 6, 7));
   }
-}
+  // Position of this lane's piece of load j along the contraction (bytes of a row, or rows).
+  __device__ __forceinline__ int at(int lane, int w, int loads, int j) const {
+    const int p = loads * w + j;
+    return COLS ? 2 * p + (lane >> 5) : 16 * ((lane & 3) ^ row_swz(16 * p + (lane >> 2)));
+  }
+
+  // Fragments start at row (column) r0 of the tile, a multiple of 32.
+  __device__ __forceinline__ void place_frags(int lane, int r0) {
+    if constexpr (!COLS) {
+      const int r = r0 + (lane & 31);
+#pragma unroll
+      for (int kk = 0; kk < 2; ++kk) frag[kk] = r * BKB + (((2 * kk + (lane >> 5)) ^ row_swz(r)) << 4);
+    } else {
+      // lane i of a 16-lane group points at row i / 4, columns 4 (i % 4) .. + 3 of the group's 4 x 16 block
+      const int i16 = lane & 15;
+      const int t = 8 * (lane >> 5) + (i16 >> 2);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        frag[i] = t * 512 + ((2 * (r0 + 32 * i + (lane & 16) + 4 * (i16 & 3))) ^ (col_swz(t) << 6));
+    }
+  }
+  // Matrix instruction's fragment i (32 rows or columns) of k-step kk of the stage at st: lane l holds row
+  // 32 i + l % 32, bytes 16 (l / 32) .. + 15 of the k-step's 32.
+  __device__ __forceinline__ v4i read(const char* st, int kk, int i) const {
+    if constexpr (!COLS) {
+      return *(const v4i*)(st + frag[kk] + 32 * BKB * i);
+    } else {
+      // bf16: contraction rows 16 kk + 8 (l / 32) + 0..7, four per read
+      v4s v[2];
+#pragma unroll
+      for (int q = 0; q < 2; ++q)
+        v[q] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+            (__attribute__((address_space(3))) v4s*)(st + frag[i] + (16 * kk + 4 * q) * 512));
+      return __builtin_bit_cast(v4i, __builtin_shufflevector(v[0], v[1], 0, 1, 2, 3, 4, 5, 6, 7));
+    }
+  }
+};
 
 template <int TYPE>
 struct Acc;
@@ -102,76 +142,44 @@ struct Acc<kInt8> {
   }
 };
 
-template <int MODE, int TYPE>
+// Wait until at most N of this wave's loads are in flight (and its LDS accesses are done), then the barrier.
+template <int N>
+__device__ __forceinline__ void landed_barrier() {
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
+}
+
+// NI: 32-row fragments of A per wave (the tile has 64 NI rows)
+template <int MODE, int TYPE, int NI>
 __device__ __forceinline__ void run_tile(const GemmArgs& p, const Tile& t, char* lds) {
   constexpr bool A_COLS = MODE == kWgrad, B_COLS = MODE != kFwd;
   constexpr int ES = TYPE == kInt8 ? 1 : 2;               // bytes per element
   constexpr int TPS = BKB / ES;                           // contraction elements per stage
-  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
+  constexpr int WM = 32 * NI;
+  static_assert(!A_COLS || NI == 4, "the weight gradient's tiles are whole");
+  constexpr int LA = A_COLS ? kLoads : NI;                // loads of A per wave and stage
+  constexpr int LS = LA + kLoads;                         // loads per wave and stage
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = w / kWavesN, wn = w % kWavesN;
   const int64_t e_row0 = t.row0 - (int64_t)t.mt * BM;     // first routed row of the expert
   const int64_t L = MODE == kFwd ? p.K : (MODE == kDgrad ? p.N : (int64_t)t.e_rows);
-  const int nsteps = (int)((L + TPS - 1) / TPS);
+  const int nfull = (int)(L / TPS);                       // whole stages
+  const int tail = (int)(L % TPS);                        // contraction elements of a last, partial one
+  const int nsteps = nfull + (tail ? 1 : 0);
   const int64_t nout = MODE == kFwd ? p.N : p.K;          // output columns
   const int a_lim = MODE == kWgrad ? (int)min((int64_t)BM, p.N - (int64_t)t.mt * BM) : t.rows;
   const int b_lim = (int)min((int64_t)BN, nout - (int64_t)t.nt * BN);
 
-  // ---- operand geometry: rows (columns) past the tile's valid ones repeat the last valid one ----
   Operand<A_COLS> a;
   Operand<B_COLS> b;
-  auto setup = [&](auto& o, const uint8_t* src, int64_t ld, int lim) {
-    constexpr bool COLS = std::remove_reference_t<decltype(o)>::COLS;
-    o.base = src;
-    o.step = COLS ? TPS * ld : BKB;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if constexpr (!COLS) {
-        const int r = 32 * w + 8 * j + (lane >> 3);
-        const int c = (lane & 7) ^ row_swz(r);
-        o.off[j] = (uint32_t)(min(r, lim - 1) * ld) + 16 * c;
-        o.at[j] = 16 * c;
-      } else {
-        const int r = 8 * w + 2 * j + (lane >> 5);
-        const int c = (lane & 31) ^ (col_swz(r) << 2);     // 16-byte chunk: eight columns
-        o.off[j] = (uint32_t)(r * ld) + 2 * min(8 * c, lim - 8);
-        o.at[j] = r;
-      }
-    }
-  };
-  if constexpr (MODE == kFwd) {
-    setup(a, p.a + t.row0 * p.lda, p.lda, a_lim);
-    setup(b, p.b + ((int64_t)t.g * p.N + (int64_t)t.nt * BN) * p.ldb, p.ldb, b_lim);
-  } else if constexpr (MODE == kDgrad) {
-    setup(a, p.a + t.row0 * p.lda, p.lda, a_lim);
-    setup(b, p.b + (int64_t)t.g * p.N * p.ldb + 2 * (int64_t)t.nt * BN, p.ldb, b_lim);
-  } else {
-    setup(a, p.a + e_row0 * p.lda + 2 * (int64_t)t.mt * BM, p.lda, a_lim);
-    setup(b, p.b + e_row0 * p.ldb + 2 * (int64_t)t.nt * BN, p.ldb, b_lim);
-  }
+  a.place(lane, w, LA, A_COLS ? p.a + e_row0 * p.lda + 2 * (int64_t)t.mt * BM : p.a + t.row0 * p.lda, p.lda, a_lim, TPS);
+  b.place(lane, w, kLoads,
+          MODE == kFwd     ? p.b + ((int64_t)t.g * p.N + (int64_t)t.nt * BN) * p.ldb
+          : MODE == kDgrad ? p.b + (int64_t)t.g * p.N * p.ldb + 2 * (int64_t)t.nt * BN
+                           : p.b + e_row0 * p.ldb + 2 * (int64_t)t.nt * BN,
+          p.ldb, b_lim, TPS);
+  a.place_frags(lane, WM * wm);
+  b.place_frags(lane, WN * wn);
 
-  // Loads of stage ks into buffer ks % 2 (which no wave reads any more).  Pieces past the contraction's
-  // end are not loaded but zeroed where they would have landed (both operands: the memory there may hold
-  // anything, NaN included).
-  auto issue_op = [&](const auto& o, int ks, int left, char* st) {
-    constexpr bool COLS = std::remove_reference_t<decltype(o)>::COLS;
-    const int lim = COLS ? left : left * ES;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      char* dst = st + (4 * w + j) * 1024;
-      if (o.at[j] < lim) dma16s(o.off[j], o.base + (int64_t)ks * o.step, dst);
-      else *(uint4*)(dst + 16 * lane) = make_uint4(0, 0, 0, 0);
-    }
-  };
-  auto issue = [&](int ks) {
-    char* st = lds + (ks & 1) * kStage;
-    const int left = (int)min(L - (int64_t)ks * TPS, (int64_t)TPS);
-    issue_op(a, ks, left, st);
-    issue_op(b, ks, left, st + kOp);
-  };
-
-  const int wm = w / kWavesN, wn = w % kWavesN;
-  // a wave whose A rows all lie past the valid ones only moves its share of the loads
-  const bool active = __builtin_amdgcn_readfirstlane((int)(WM * wm < a_lim && WN * wn < b_lim)) != 0;
-  constexpr int NI = WM / 32, NJ = WN / 32;
   typedef typename Acc<TYPE>::type vacc;
   vacc acc[NI][NJ];
 #pragma unroll
@@ -181,30 +189,103 @@ __device__ __forceinline__ void run_tile(const GemmArgs& p, const Tile& t, char*
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[i][j][r] = 0;
 
-  if (nsteps > 0) issue(0);
-  for (int ks = 0; ks < nsteps; ++ks) {
-    stage_barrier();                               // stage ks landed; stage ks - 1 fully read
-    if (ks + 1 < nsteps) issue(ks + 1);
-    if (!active) continue;
-    const char* A = lds + (ks & 1) * kStage;
-    const char* B = A + kOp;
+  auto slot_at = [&](int slot) { return lds + slot * kStage; };
+  auto load_a = [&](int j, char* st) {
+    dma16s(a.off[j], (const uint8_t*)uniform64((int64_t)a.base), st + (LA * w + j) * 1024);
+  };
+  auto load_b = [&](int j, char* st) {
+    dma16s(b.off[j], (const uint8_t*)uniform64((int64_t)b.base), st + kOp + (kLoads * w + j) * 1024);
+  };
+  auto loaded = [&]() {
+    a.base += a.step;
+    b.base += b.step;
+  };
+  // A whole stage at once, the partial one too: its pieces past the contraction's end are not loaded but
+  // zeroed where they would have landed (both operands: the memory there may hold anything, NaN included).
+  auto load_stage = [&](int ks, char* st) {
+    if (ks < nfull) {
 #pragma unroll
-    for (int kk = 0; kk < 4; ++kk) {
-      v4i af[NI], bf[NJ];
+      for (int j = 0; j < LA; ++j) load_a(j, st);
 #pragma unroll
-      for (int j = 0; j < NJ; ++j) bf[j] = read_frag<B_COLS>(B, WN * wn + 32 * j, kk, lane);
+      for (int j = 0; j < kLoads; ++j) load_b(j, st);
+      loaded();
+    } else if (ks < nsteps) {
 #pragma unroll
-      for (int i = 0; i < NI; ++i) af[i] = read_frag<A_COLS>(A, WM * wm + 32 * i, kk, lane);
+      for (int j = 0; j < LA; ++j) {
+        if (a.at(lane, w, LA, j) < (A_COLS ? tail : tail * ES)) load_a(j, st);
+        else *(uint4*)(st + (LA * w + j) * 1024 + 16 * lane) = make_uint4(0, 0, 0, 0);
+      }
 #pragma unroll
-      for (int i = 0; i < NI; ++i)
-#pragma unroll
-        for (int j = 0; j < NJ; ++j) acc[i][j] = Acc<TYPE>::mfma(bf[j], af[i], acc[i][j]);
+      for (int j = 0; j < kLoads; ++j) {
+        if (b.at(lane, w, kLoads, j) < (B_COLS ? tail : tail * ES)) load_b(j, st);
+        else *(uint4*)(st + kOp + (kLoads * w + j) * 1024 + 16 * lane) = make_uint4(0, 0, 0, 0);
+      }
     }
+  };
+
+  v4i af[2][NI], bf[2][NJ];                        // fragments of the current and the next k-step
+  // The two k-steps of the stage at st: each multiplies its fragments while it reads the next k-step's (the
+  // second one's from the stage after, sn).  MORE: the loads of a whole stage into sl go out in between.
+  auto compute = [&](auto more, const char* st, const char* sn, char* sl) {
+    constexpr bool MORE = decltype(more)::value;
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk) {
+#pragma unroll
+      for (int i = 0; i < NI; ++i) {
+#pragma unroll
+        for (int j = NJ * i / NI; j < NJ * (i + 1) / NI; ++j) bf[1 - kk][j] = b.read((kk == 0 ? st : sn) + kOp, 1 - kk, j);
+        af[1 - kk][i] = a.read(kk == 0 ? st : sn, 1 - kk, i);
+        if constexpr (MORE) {
+          if (kk == 0) {
+#pragma unroll
+            for (int j = LA * i / NI; j < LA * (i + 1) / NI; ++j) load_a(j, sl);
+          } else {
+#pragma unroll
+            for (int j = kLoads * i / NI; j < kLoads * (i + 1) / NI; ++j) load_b(j, sl);
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) acc[i][j] = Acc<TYPE>::mfma(bf[kk][j], af[kk][i], acc[i][j]);
+        __builtin_amdgcn_sched_barrier(0);         // keep the reads and loads spread as written
+      }
+    }
+    if constexpr (MORE) loaded();
+  };
+
+  // prologue: stages 0 .. kRing - 2 on their way, stage 0 landed, its first fragments read
+  for (int s = 0; s < kRing - 1; ++s) load_stage(s, slot_at(s));
+  if (nfull >= kRing - 1) landed_barrier<(kRing - 2) * LS>();
+  else landed_barrier<0>();
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) bf[0][j] = b.read(lds + kOp, 0, j);
+#pragma unroll
+  for (int i = 0; i < NI; ++i) af[0][i] = a.read(lds, 0, i);
+
+  // Stage ks: once stage ks + 1 has landed everywhere (its loads are older than those of the kRing - 3
+  // stages after it), stage ks - 1 is fully read too, and its slot takes stage ks + kRing - 1.
+  int ks = 0, slot = 0;
+  auto next_slot = [&](int s) { return s + 1 == kRing ? 0 : s + 1; };
+  for (; ks + kRing - 1 < nfull; ++ks) {
+    landed_barrier<(kRing - 3) * LS>();
+    const int n = next_slot(slot);
+    compute(std::true_type{}, slot_at(slot), slot_at(n), slot_at(slot == 0 ? kRing - 1 : slot - 1));
+    slot = n;
+  }
+  for (; ks < nsteps; ++ks) {
+    // the last stages: fewer loads in flight, and a partial stage has fewer than the count assumes
+    const int after = nfull - 1 - (ks + 1);
+    if (!tail && after >= 2) landed_barrier<2 * LS>();
+    else if (!tail && after == 1) landed_barrier<LS>();
+    else landed_barrier<0>();
+    const int n = next_slot(slot);
+    load_stage(ks + kRing - 1, slot_at(slot == 0 ? kRing - 1 : slot - 1));
+    compute(std::false_type{}, slot_at(slot), slot_at(n), nullptr);
+    slot = n;
   }
 
   // ---- epilogue: whole row pieces through LDS (store_tile_rows) ----
   const int64_t out_row0 = MODE == kWgrad ? (int64_t)t.g * p.N + (int64_t)t.mt * BM : t.row0;
-  stage_barrier();
+  landed_barrier<0>();
   char* reg = lds + w * 64 * (128 * NJ + 16);
   if constexpr (TYPE == kInt8) {
     // lane l holds row 32 i + l % 32 and columns 32 j + 8 q + 4 (l / 32) .. + 3 of its wave's tile
@@ -226,10 +307,10 @@ __device__ __forceinline__ void run_tile(const GemmArgs& p, const Tile& t, char*
 #pragma unroll
           for (int k = 0; k < 4; ++k) out[i][j][4 * q + k] = (float)acc[i][j][4 * q + k] * (rs[i] * cs[k]);
       }
-    store_tile_rows<NI, NJ, 2>(out, reg, p.out_bf16, p.out, out_row0, nout, (int64_t)t.nt * BN, WM * wm, WN * wn,
+    store_tile_rows<NI, NJ, NI < 2 ? 1 : 2>(out, reg, p.out_bf16, p.out, out_row0, nout, (int64_t)t.nt * BN, WM * wm, WN * wn,
                                a_lim, b_lim);
   } else {
-    store_tile_rows<NI, NJ, 2>(acc, reg, p.out_bf16, p.out, out_row0, nout, (int64_t)t.nt * BN, WM * wm, WN * wn,
+    store_tile_rows<NI, NJ, NI < 2 ? 1 : 2>(acc, reg, p.out_bf16, p.out, out_row0, nout, (int64_t)t.nt * BN, WM * wm, WN * wn,
                                a_lim, b_lim);
   }
 }
@@ -246,10 +327,12 @@ __global__ __launch_bounds__(NT, 1) void dense_grouped_gemm_kernel(GemmArgs p) {
   t.e_rows = __builtin_amdgcn_readfirstlane(t.e_rows);
   t.row0 = uniform64(t.row0);
   __syncthreads();                               // scheduler scratch is reused for operands
-  run_tile<MODE, TYPE>(p, t, lds);
+  if (MODE == kWgrad || t.rows > 128) run_tile<MODE, TYPE, 4>(p, t, lds);
+  else if (t.rows > 64) run_tile<MODE, TYPE, MODE == kWgrad ? 4 : 2>(p, t, lds);
+  else run_tile<MODE, TYPE, MODE == kWgrad ? 4 : 1>(p, t, lds);
 }
 
-static_assert(5 * (kMaxG + 1) * 4 <= kStage, "scheduler scratch must fit in the first stage");
+static_assert(5 * (kMaxG + 1) * 4 <= kLds, "scheduler scratch must fit in LDS");
 
 }  // namespace
 
