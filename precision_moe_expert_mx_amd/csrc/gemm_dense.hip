@@ -12,11 +12,13 @@
 // 512 registers hold sums).  The widest wave tile is the point: a k-step of a wave reads 4 + 4 fragments
 // from LDS for 16 matrix instructions, 64 B per clock and CU at the full matrix rate, and the stage loads
 // write another 32, of the 128 that LDS moves; eight waves of 128 x 64 would need all of it (measured:
-// 1000-1060 TFLOP/s).  The contraction advances 64 bytes per stage (32 bf16, 64 int8: two k-steps) through a
-// ring of five 32 KiB LDS stages filled by direct-to-LDS loads, four stages ahead and without draining them:
-// a wave waits only until its share of the next stage has landed (a counted vmcnt), and reads the fragments
-// of a k-step while it multiplies the one before, across stages too.
-// An operand contiguous along t is staged as 256 rows of 64 bytes; one with t as its rows as 32 rows of 256
+// 1000-1060 TFLOP/s).  The contraction advances 128 bytes per stage (64 bf16, 128 int8: four k-steps), whole
+// cache lines of an operand that is contiguous along it (with 64-byte stages the forward made twice the L2
+// requests and ran 10% slower at the same power).  LDS holds five operand stages of 32 KiB: A and B of two
+// stages and the next A, filled by direct-to-LDS loads that are never drained: a wave waits only until its
+// share of the next stage has landed (a counted vmcnt), and reads the fragments of a k-step while it
+// multiplies the one before, across stages too.
+// An operand contiguous along t is staged as 256 rows of 128 bytes; one with t as its rows as 64 rows of 256
 // columns (512 bytes), which fragments are read from with the transposing LDS read (ds_read_b64_tr_b16: 16
 // lanes read 4 rows x 16 columns and each gets one column's 4 values), so no operand is ever transposed in
 // memory.  A tile with at most 128 (64) valid A rows runs as 128 (64) x 256.
@@ -30,18 +32,18 @@ namespace {
 using Tile = GroupTile;
 
 constexpr int BM = 256, BN = 256;                // A / B rows (output rows / columns) per tile
-constexpr int BKB = 64;                          // contraction bytes per stage
+constexpr int BKB = 128;                         // contraction bytes per stage
+constexpr int KS = BKB / 32;                     // k-steps (matrix instructions deep) per stage
 constexpr int kWavesM = 2, kWavesN = 2;
 constexpr int kWaves = kWavesM * kWavesN;
 constexpr int NT = 64 * kWaves;
 constexpr int WN = BN / kWavesN;                 // output columns per wave
 constexpr int NJ = WN / 32;
-constexpr int kOp = BM * BKB;                    // bytes of one operand's stage (both layouts): 16 KiB
-constexpr int kStage = 2 * kOp;
-constexpr int kRing = 5;                         // stages in LDS
+constexpr int kOp = BM * BKB;                    // bytes of one operand's stage (both layouts): 32 KiB
+constexpr int kSlots = 5;                        // operand stages in LDS: A p at slot 2p % 5, B p at (2p + 1) % 5
 constexpr int kLoads = kOp / 1024 / kWaves;      // 1 KiB loads per wave, stage and (whole) operand
-constexpr int kLds = kRing * kStage;
-static_assert(BM == BN && kLoads == 4, "one stage size for both operands");
+constexpr int kLds = kSlots * kOp;
+static_assert(BM == BN && kLoads == 8, "one stage size for both operands");
 static_assert(kWaves * 64 * (128 * NJ + 16) <= kLds, "staged epilogue must fit in LDS");
 
 typedef float v16f __attribute__((ext_vector_type(16)));
@@ -51,9 +53,9 @@ typedef short v8s __attribute__((ext_vector_type(8)));
 
 enum DenseType { kBf16 = 0, kInt8 = 1 };
 
-// Staged rows of 64 bytes, four to the 256 bytes that 16 lanes read at once: 16-byte chunk c of row r at
-// position c ^ ((r >> 2) & 3), so that 16 consecutive rows' chunks hit distinct banks.
-__device__ __forceinline__ int row_swz(int r) { return (r >> 2) & 3; }
+// Staged rows of 128 bytes, two to the 256 bytes that 16 lanes read at once: 16-byte chunk c of row r at
+// position c ^ ((r >> 1) & 7), so that 16 consecutive rows' chunks hit distinct banks.
+__device__ __forceinline__ int row_swz(int r) { return (r >> 1) & 7; }
 // Staged contraction rows of 512 bytes: 64-byte piece c of row t at piece c ^ col_swz(t).  One transposing
 // read takes 64 bytes of rows t .. t + 3 and t + 8 .. t + 11: eight different pieces of the 512 bytes.
 __device__ __forceinline__ int col_swz(int t) { return (t & 3) | ((t >> 1) & 4); }
@@ -65,7 +67,7 @@ template <bool COLS_>
 struct Operand {
   static constexpr bool COLS = COLS_;
   uint32_t off[kLoads];
-  uint32_t frag[COLS ? 4 : 2];
+  uint32_t frag[4];                              // by fragment (COLS) or by k-step
   const uint8_t* base;                           // of the next stage to load
   int64_t step;
 
@@ -78,8 +80,8 @@ struct Operand {
     for (int j = 0; j < kLoads; ++j) {
       if (j >= loads) continue;
       if constexpr (!COLS) {
-        const int r = 16 * (loads * w + j) + (lane >> 2);
-        off[j] = (uint32_t)(min(r, lim - 1) * ld) + 16 * ((lane & 3) ^ row_swz(r));
+        const int r = 8 * (loads * w + j) + (lane >> 3);
+        off[j] = (uint32_t)(min(r, lim - 1) * ld) + 16 * ((lane & 7) ^ row_swz(r));
       } else {
         const int r = 2 * (loads * w + j) + (lane >> 5);
         const int c = (lane & 31) ^ (col_swz(r) << 2);     // 16-byte chunk: eight columns
@@ -90,7 +92,7 @@ struct Operand {
   // Position of this lane's piece of load j along the contraction (bytes of a row, or rows).
   __device__ __forceinline__ int at(int lane, int w, int loads, int j) const {
     const int p = loads * w + j;
-    return COLS ? 2 * p + (lane >> 5) : 16 * ((lane & 3) ^ row_swz(16 * p + (lane >> 2)));
+    return COLS ? 2 * p + (lane >> 5) : 16 * ((lane & 7) ^ row_swz(8 * p + (lane >> 3)));
   }
 
   // Fragments start at row (column) r0 of the tile, a multiple of 32.
@@ -98,7 +100,7 @@ struct Operand {
     if constexpr (!COLS) {
       const int r = r0 + (lane & 31);
 #pragma unroll
-      for (int kk = 0; kk < 2; ++kk) frag[kk] = r * BKB + (((2 * kk + (lane >> 5)) ^ row_swz(r)) << 4);
+      for (int kk = 0; kk < KS; ++kk) frag[kk] = r * BKB + (((2 * kk + (lane >> 5)) ^ row_swz(r)) << 4);
     } else {
       // lane i of a 16-lane group points at row i / 4, columns 4 (i % 4) .. + 3 of the group's 4 x 16 block
       const int i16 = lane & 15;
@@ -156,7 +158,7 @@ __device__ __forceinline__ void run_tile(const GemmArgs& p, const Tile& t, char*
   constexpr int TPS = BKB / ES;                           // contraction elements per stage
   constexpr int WM = 32 * NI;
   static_assert(!A_COLS || NI == 4, "the weight gradient's tiles are whole");
-  constexpr int LA = A_COLS ? kLoads : NI;                // loads of A per wave and stage
+  constexpr int LA = A_COLS ? kLoads : 2 * NI;            // loads of A per wave and stage
   constexpr int LS = LA + kLoads;                         // loads per wave and stage
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = w / kWavesN, wn = w % kWavesN;
@@ -189,98 +191,103 @@ __device__ __forceinline__ void run_tile(const GemmArgs& p, const Tile& t, char*
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[i][j][r] = 0;
 
-  auto slot_at = [&](int slot) { return lds + slot * kStage; };
   auto load_a = [&](int j, char* st) {
     dma16s(a.off[j], (const uint8_t*)uniform64((int64_t)a.base), st + (LA * w + j) * 1024);
   };
   auto load_b = [&](int j, char* st) {
-    dma16s(b.off[j], (const uint8_t*)uniform64((int64_t)b.base), st + kOp + (kLoads * w + j) * 1024);
+    dma16s(b.off[j], (const uint8_t*)uniform64((int64_t)b.base), st + (kLoads * w + j) * 1024);
   };
-  auto loaded = [&]() {
-    a.base += a.step;
-    b.base += b.step;
-  };
-  // A whole stage at once, the partial one too: its pieces past the contraction's end are not loaded but
-  // zeroed where they would have landed (both operands: the memory there may hold anything, NaN included).
-  auto load_stage = [&](int ks, char* st) {
+  // All of an operand's stage ks at once, the last, partial one too: its pieces past the contraction's end are
+  // not loaded but zeroed where they would have landed (both operands: the memory there may hold anything,
+  // NaN included).
+  auto load_all = [&](auto& o, auto load, int loads, int ks, char* st) {
     if (ks < nfull) {
 #pragma unroll
-      for (int j = 0; j < LA; ++j) load_a(j, st);
-#pragma unroll
-      for (int j = 0; j < kLoads; ++j) load_b(j, st);
-      loaded();
+      for (int j = 0; j < kLoads; ++j)
+        if (j < loads) load(j, st);
+      o.base += o.step;
     } else if (ks < nsteps) {
-#pragma unroll
-      for (int j = 0; j < LA; ++j) {
-        if (a.at(lane, w, LA, j) < (A_COLS ? tail : tail * ES)) load_a(j, st);
-        else *(uint4*)(st + (LA * w + j) * 1024 + 16 * lane) = make_uint4(0, 0, 0, 0);
-      }
+      const int lim = std::remove_reference_t<decltype(o)>::COLS ? tail : tail * ES;
 #pragma unroll
       for (int j = 0; j < kLoads; ++j) {
-        if (b.at(lane, w, kLoads, j) < (B_COLS ? tail : tail * ES)) load_b(j, st);
-        else *(uint4*)(st + kOp + (kLoads * w + j) * 1024 + 16 * lane) = make_uint4(0, 0, 0, 0);
+        if (j >= loads) continue;
+        if (o.at(lane, w, loads, j) < lim) load(j, st);
+        else *(uint4*)(st + (loads * w + j) * 1024 + 16 * lane) = make_uint4(0, 0, 0, 0);
       }
     }
   };
+  auto all_a = [&](int ks, char* st) { load_all(a, load_a, LA, ks, st); };
+  auto all_b = [&](int ks, char* st) { load_all(b, load_b, kLoads, ks, st); };
 
   v4i af[2][NI], bf[2][NJ];                        // fragments of the current and the next k-step
-  // The two k-steps of the stage at st: each multiplies its fragments while it reads the next k-step's (the
-  // second one's from the stage after, sn).  MORE: the loads of a whole stage into sl go out in between.
-  auto compute = [&](auto more, const char* st, const char* sn, char* sl) {
-    constexpr bool MORE = decltype(more)::value;
+  // K-step kk: multiply its fragments while the next k-step's are read (at `sa`, `sb`, k-step nk there).
+  // LOAD 1: loads kk, kk + 1 of each pair of A's next stage go out in between; 2: all of B's.
+  auto kstep = [&](auto load, int kk, const char* sa, const char* sb, int nk, char* dst) {
+    constexpr int LOAD = decltype(load)::value;
+    const int cur = kk & 1, nxt = 1 - cur;
 #pragma unroll
-    for (int kk = 0; kk < 2; ++kk) {
+    for (int i = 0; i < NI; ++i) {
 #pragma unroll
-      for (int i = 0; i < NI; ++i) {
+      for (int j = NJ * i / NI; j < NJ * (i + 1) / NI; ++j) bf[nxt][j] = b.read(sb, nk, j);
+      af[nxt][i] = a.read(sa, nk, i);
+      if constexpr (LOAD == 1) {
 #pragma unroll
-        for (int j = NJ * i / NI; j < NJ * (i + 1) / NI; ++j) bf[1 - kk][j] = b.read((kk == 0 ? st : sn) + kOp, 1 - kk, j);
-        af[1 - kk][i] = a.read(kk == 0 ? st : sn, 1 - kk, i);
-        if constexpr (MORE) {
-          if (kk == 0) {
+        for (int j = LA / 2 * i / NI; j < LA / 2 * (i + 1) / NI; ++j) load_a(LA / 2 * kk + j, dst);
+      } else if constexpr (LOAD == 2) {
 #pragma unroll
-            for (int j = LA * i / NI; j < LA * (i + 1) / NI; ++j) load_a(j, sl);
-          } else {
-#pragma unroll
-            for (int j = kLoads * i / NI; j < kLoads * (i + 1) / NI; ++j) load_b(j, sl);
-          }
-        }
-#pragma unroll
-        for (int j = 0; j < NJ; ++j) acc[i][j] = Acc<TYPE>::mfma(bf[kk][j], af[kk][i], acc[i][j]);
-        __builtin_amdgcn_sched_barrier(0);         // keep the reads and loads spread as written
+        for (int j = kLoads * i / NI; j < kLoads * (i + 1) / NI; ++j) load_b(j, dst);
       }
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) acc[i][j] = Acc<TYPE>::mfma(bf[cur][j], af[cur][i], acc[i][j]);
+      __builtin_amdgcn_sched_barrier(0);           // keep the reads and loads spread as written
     }
-    if constexpr (MORE) loaded();
   };
+  typedef std::integral_constant<int, 0> None;
+  typedef std::integral_constant<int, 1> LoadA;
+  typedef std::integral_constant<int, 2> LoadB;
 
-  // prologue: stages 0 .. kRing - 2 on their way, stage 0 landed, its first fragments read
-  for (int s = 0; s < kRing - 1; ++s) load_stage(s, slot_at(s));
-  if (nfull >= kRing - 1) landed_barrier<(kRing - 2) * LS>();
+  // prologue: stages 0 and 1 on their way, stage 0 landed, its first fragments read
+  all_a(0, lds);
+  all_b(0, lds + kOp);
+  all_a(1, lds + 2 * kOp);
+  all_b(1, lds + 3 * kOp);
+  if (nfull >= 2) landed_barrier<LS>();
   else landed_barrier<0>();
 #pragma unroll
   for (int j = 0; j < NJ; ++j) bf[0][j] = b.read(lds + kOp, 0, j);
 #pragma unroll
   for (int i = 0; i < NI; ++i) af[0][i] = a.read(lds, 0, i);
 
-  // Stage ks: once stage ks + 1 has landed everywhere (its loads are older than those of the kRing - 3
-  // stages after it), stage ks - 1 is fully read too, and its slot takes stage ks + kRing - 1.
-  int ks = 0, slot = 0;
-  auto next_slot = [&](int s) { return s + 1 == kRing ? 0 : s + 1; };
-  for (; ks + kRing - 1 < nfull; ++ks) {
-    landed_barrier<(kRing - 3) * LS>();
-    const int n = next_slot(slot);
-    compute(std::true_type{}, slot_at(slot), slot_at(n), slot_at(slot == 0 ? kRing - 1 : slot - 1));
-    slot = n;
+  // Stage ks, its first fragments in registers.  A of stage ks + 2 goes out during its first two k-steps, into
+  // the slot that B of stage ks - 1 left.  Before its last k-step, stage ks + 1 has to have landed everywhere
+  // (all but the loads of A just issued); then this stage is fully read too, and B of stage ks + 2 goes into
+  // A's slot.  (A's own lead is two stages, B's one: 1000-2000 clocks.)
+  int ks = 0, slot = 0;                            // slot of A of stage ks
+  auto at_slot = [&](int k) {
+    const int q = slot + k;
+    return lds + (q >= kSlots ? q - kSlots : q) * kOp;
+  };
+  for (; ks + 2 < nfull; ++ks) {
+    char *sa = at_slot(0), *sb = at_slot(1), *na = at_slot(2), *nb = at_slot(3), *nna = at_slot(4);
+    kstep(LoadA{}, 0, sa, sb, 1, nna);
+    kstep(LoadA{}, 1, sa, sb, 2, nna);
+    a.base += a.step;
+    kstep(None{}, 2, sa, sb, 3, nullptr);
+    landed_barrier<LA>();
+    kstep(LoadB{}, 3, na, nb, 0, sa);
+    b.base += b.step;
+    slot = slot + 2 >= kSlots ? slot + 2 - kSlots : slot + 2;
   }
-  for (; ks < nsteps; ++ks) {
-    // the last stages: fewer loads in flight, and a partial stage has fewer than the count assumes
-    const int after = nfull - 1 - (ks + 1);
-    if (!tail && after >= 2) landed_barrier<2 * LS>();
-    else if (!tail && after == 1) landed_barrier<LS>();
-    else landed_barrier<0>();
-    const int n = next_slot(slot);
-    load_stage(ks + kRing - 1, slot_at(slot == 0 ? kRing - 1 : slot - 1));
-    compute(std::false_type{}, slot_at(slot), slot_at(n), nullptr);
-    slot = n;
+  for (; ks < nsteps; ++ks) {                      // the last two or three stages
+    char *sa = at_slot(0), *sb = at_slot(1), *na = at_slot(2), *nb = at_slot(3), *nna = at_slot(4);
+    all_a(ks + 2, nna);
+    kstep(None{}, 0, sa, sb, 1, nullptr);
+    kstep(None{}, 1, sa, sb, 2, nullptr);
+    kstep(None{}, 2, sa, sb, 3, nullptr);
+    landed_barrier<0>();
+    all_b(ks + 2, sa);
+    kstep(None{}, 3, na, nb, 0, nullptr);
+    slot = slot + 2 >= kSlots ? slot + 2 - kSlots : slot + 2;
   }
 
   // ---- epilogue: whole row pieces through LDS (store_tile_rows) ----
