@@ -61,8 +61,8 @@ __device__ __forceinline__ int row_swz(int r) { return (r >> 1) & 7; }
 __device__ __forceinline__ int col_swz(int t) { return (t & 3) | ((t >> 1) & 4); }
 
 // One operand of a wave: its share of a stage's loads (kLoads of 1 KiB, fewer of A in a tile of fewer
-// rows) as 32-bit lane offsets from a wave-uniform base that moves by `step` bytes per stage, and its
-// fragments' LDS offsets in a stage.
+// rows; load j of wave w fills the stage's 1 KiB piece kWaves j + w) as 32-bit lane offsets from a
+// wave-uniform base that moves by `step` bytes per stage, and its fragments' LDS offsets in a stage.
 template <bool COLS_>
 struct Operand {
   static constexpr bool COLS = COLS_;
@@ -71,28 +71,50 @@ struct Operand {
   const uint8_t* base;                           // of the next stage to load
   int64_t step;
 
-  // Load j of wave w fills the 1 KiB piece loads * w + j of the operand's stage.  Rows (columns) past the
-  // `lim` valid ones repeat the last valid one.
-  __device__ __forceinline__ void place(int lane, int w, int loads, const uint8_t* src, int64_t ld, int lim, int tps) {
+  // Rows (columns) past the `lim` valid ones repeat the last valid one.
+  __device__ __forceinline__ void place(int lane, int w, const uint8_t* src, int64_t ld, int lim, int tps) {
     base = src;
     step = COLS ? tps * ld : BKB;
 #pragma unroll
     for (int j = 0; j < kLoads; ++j) {
-      if (j >= loads) continue;
       if constexpr (!COLS) {
-        const int r = 8 * (loads * w + j) + (lane >> 3);
+        const int r = 8 * (kWaves * j + w) + (lane >> 3);
         off[j] = (uint32_t)(min(r, lim - 1) * ld) + 16 * ((lane & 7) ^ row_swz(r));
       } else {
-        const int r = 2 * (loads * w + j) + (lane >> 5);
+        const int r = 2 * (kWaves * j + w) + (lane >> 5);
         const int c = (lane & 31) ^ (col_swz(r) << 2);     // 16-byte chunk: eight columns
         off[j] = (uint32_t)(r * ld) + 2 * min(8 * c, lim - 8);
       }
     }
   }
-  // Position of this lane's piece of load j along the contraction (bytes of a row, or rows).
-  __device__ __forceinline__ int at(int lane, int w, int loads, int j) const {
-    const int p = loads * w + j;
+  // Load j of a stage into its slot.
+  __device__ __forceinline__ void load(int w, int j, char* st) const {
+    dma16s(off[j], (const uint8_t*)uniform64((int64_t)base), st + (kWaves * j + w) * 1024);
+  }
+  __device__ __forceinline__ void load_all(int w, int loads, char* st) const {
+#pragma unroll
+    for (int j = 0; j < kLoads; ++j)
+      if (j < loads) load(w, j, st);
+  }
+  // Position along the contraction of this lane's piece of load j (bytes of a row, or rows).
+  static __device__ __forceinline__ int at(int lane, int w, int j) {
+    const int p = kWaves * j + w;
     return COLS ? 2 * p + (lane >> 5) : 16 * ((lane & 7) ^ row_swz(8 * p + (lane >> 3)));
+  }
+  // The stage to load is the contraction's last, with `lim` bytes (COLS: rows): lanes whose piece lies past
+  // its end load the row's first piece (the column's first row) instead, and zero() clears it in LDS once the
+  // stage has landed (in both operands: what is next in memory may be anything, NaN included).
+  __device__ __forceinline__ void clamp(int lane, int w, int lim, uint32_t ld) {
+#pragma unroll
+    for (int j = 0; j < kLoads; ++j) {
+      const int k = at(lane, w, j);
+      if (k >= lim) off[j] -= COLS ? k * ld : k;
+    }
+  }
+  static __device__ __forceinline__ void zero(int lane, int w, int loads, int lim, char* st) {
+#pragma unroll
+    for (int j = 0; j < kLoads; ++j)
+      if (j < loads && at(lane, w, j) >= lim) *(uint4*)(st + (kWaves * j + w) * 1024 + 16 * lane) = make_uint4(0, 0, 0, 0);
   }
 
   // Fragments start at row (column) r0 of the tile, a multiple of 32.
@@ -150,193 +172,392 @@ __device__ __forceinline__ void landed_barrier() {
   asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
 }
 
-// NI: 32-row fragments of A per wave (the tile has 64 NI rows)
-template <int MODE, int TYPE, int NI>
-__device__ __forceinline__ void run_tile(const GemmArgs& p, const Tile& t, char* lds) {
-  constexpr bool A_COLS = MODE == kWgrad, B_COLS = MODE != kFwd;
-  constexpr int ES = TYPE == kInt8 ? 1 : 2;               // bytes per element
-  constexpr int TPS = BKB / ES;                           // contraction elements per stage
-  constexpr int WM = 32 * NI;
-  static_assert(!A_COLS || NI == 4, "the weight gradient's tiles are whole");
-  constexpr int LA = A_COLS ? kLoads : 2 * NI;            // loads of A per wave and stage
-  constexpr int LS = LA + kLoads;                         // loads per wave and stage
-  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int wm = w / kWavesN, wn = w % kWavesN;
-  const int64_t e_row0 = t.row0 - (int64_t)t.mt * BM;     // first routed row of the expert
-  const int64_t L = MODE == kFwd ? p.K : (MODE == kDgrad ? p.N : (int64_t)t.e_rows);
-  const int nfull = (int)(L / TPS);                       // whole stages
-  const int tail = (int)(L % TPS);                        // contraction elements of a last, partial one
-  const int nsteps = nfull + (tail ? 1 : 0);
-  const int64_t nout = MODE == kFwd ? p.N : p.K;          // output columns
-  const int a_lim = MODE == kWgrad ? (int)min((int64_t)BM, p.N - (int64_t)t.mt * BM) : t.rows;
-  const int b_lim = (int)min((int64_t)BN, nout - (int64_t)t.nt * BN);
+// This wave's LDS accesses are done, then the barrier.
+__device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 
-  Operand<A_COLS> a;
-  Operand<B_COLS> b;
-  a.place(lane, w, LA, A_COLS ? p.a + e_row0 * p.lda + 2 * (int64_t)t.mt * BM : p.a + t.row0 * p.lda, p.lda, a_lim, TPS);
-  b.place(lane, w, kLoads,
-          MODE == kFwd     ? p.b + ((int64_t)t.g * p.N + (int64_t)t.nt * BN) * p.ldb
-          : MODE == kDgrad ? p.b + (int64_t)t.g * p.N * p.ldb + 2 * (int64_t)t.nt * BN
-                           : p.b + e_row0 * p.ldb + 2 * (int64_t)t.nt * BN,
-          p.ldb, b_lim, TPS);
-  a.place_frags(lane, WM * wm);
-  b.place_frags(lane, WN * wn);
+// The lane number as a value of its own at each call: what is computed from it is computed there, instead
+// of being hoisted out of the tile loop into registers that the accumulators need.
+__device__ __forceinline__ int fresh_lane() {
+  int lane = threadIdx.x & 63;
+  asm volatile("" : "+v"(lane));
+  return lane;
+}
 
-  typedef typename Acc<TYPE>::type vacc;
-  vacc acc[NI][NJ];
+// Store 32 rows of a wave's tile (value(j, q, e): fragment j, accumulator register 4 q + e) as whole row
+// pieces through RB * 32 bytes of LDS of its own: rows of RB bytes (256 or 128) whose 16-byte chunk c is at
+// c ^ (r mod chunks); a bf16 chunk's two 8-byte halves (from lanes 0..31 and 32..63) change places in rows
+// 16..31, so that the lanes of a write spread over the banks.  Rows at or past row_lim and columns at or past
+// col_lim are not written.
+template <bool BF16, int RB, typename Value>
+__device__ __forceinline__ void store_rows(Value value, char* reg, void* out, int64_t out_row0, int64_t nout,
+                                           int64_t col0, int r0, int c0, int row_lim, int col_lim) {
+  constexpr int kCols = BF16 ? RB / 2 : RB / 4;           // columns per pass
+  constexpr int kJ = kCols / 32;                          // fragments per pass
+  constexpr int kCh = RB / 16;                            // chunks per staged row
+  constexpr int kPieces = 32 * kCh / 64;
+  const int lane = fresh_lane(), h = lane >> 5, r = lane & 31;
 #pragma unroll
-  for (int i = 0; i < NI; ++i)
+  for (int pass = 0; pass < NJ / kJ; ++pass) {
 #pragma unroll
-    for (int j = 0; j < NJ; ++j)
-#pragma unroll
-      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0;
-
-  auto load_a = [&](int j, char* st) {
-    dma16s(a.off[j], (const uint8_t*)uniform64((int64_t)a.base), st + (LA * w + j) * 1024);
-  };
-  auto load_b = [&](int j, char* st) {
-    dma16s(b.off[j], (const uint8_t*)uniform64((int64_t)b.base), st + (kLoads * w + j) * 1024);
-  };
-  // All of an operand's stage ks at once, the last, partial one too: its pieces past the contraction's end are
-  // not loaded but zeroed where they would have landed (both operands: the memory there may hold anything,
-  // NaN included).
-  auto load_all = [&](auto& o, auto load, int loads, int ks, char* st) {
-    if (ks < nfull) {
-#pragma unroll
-      for (int j = 0; j < kLoads; ++j)
-        if (j < loads) load(j, st);
-      o.base += o.step;
-    } else if (ks < nsteps) {
-      const int lim = std::remove_reference_t<decltype(o)>::COLS ? tail : tail * ES;
-#pragma unroll
-      for (int j = 0; j < kLoads; ++j) {
-        if (j >= loads) continue;
-        if (o.at(lane, w, loads, j) < lim) load(j, st);
-        else *(uint4*)(st + (loads * w + j) * 1024 + 16 * lane) = make_uint4(0, 0, 0, 0);
-      }
-    }
-  };
-  auto all_a = [&](int ks, char* st) { load_all(a, load_a, LA, ks, st); };
-  auto all_b = [&](int ks, char* st) { load_all(b, load_b, kLoads, ks, st); };
-
-  v4i af[2][NI], bf[2][NJ];                        // fragments of the current and the next k-step
-  // K-step kk: multiply its fragments while the next k-step's are read (at `sa`, `sb`, k-step nk there).
-  // LOAD 1: loads kk, kk + 1 of each pair of A's next stage go out in between; 2: all of B's.
-  auto kstep = [&](auto load, int kk, const char* sa, const char* sb, int nk, char* dst) {
-    constexpr int LOAD = decltype(load)::value;
-    const int cur = kk & 1, nxt = 1 - cur;
-#pragma unroll
-    for (int i = 0; i < NI; ++i) {
-#pragma unroll
-      for (int j = NJ * i / NI; j < NJ * (i + 1) / NI; ++j) bf[nxt][j] = b.read(sb, nk, j);
-      af[nxt][i] = a.read(sa, nk, i);
-      if constexpr (LOAD == 1) {
-#pragma unroll
-        for (int j = LA / 2 * i / NI; j < LA / 2 * (i + 1) / NI; ++j) load_a(LA / 2 * kk + j, dst);
-      } else if constexpr (LOAD == 2) {
-#pragma unroll
-        for (int j = kLoads * i / NI; j < kLoads * (i + 1) / NI; ++j) load_b(j, dst);
-      }
-#pragma unroll
-      for (int j = 0; j < NJ; ++j) acc[i][j] = Acc<TYPE>::mfma(bf[cur][j], af[cur][i], acc[i][j]);
-      __builtin_amdgcn_sched_barrier(0);           // keep the reads and loads spread as written
-    }
-  };
-  typedef std::integral_constant<int, 0> None;
-  typedef std::integral_constant<int, 1> LoadA;
-  typedef std::integral_constant<int, 2> LoadB;
-
-  // prologue: stages 0 and 1 on their way, stage 0 landed, its first fragments read
-  all_a(0, lds);
-  all_b(0, lds + kOp);
-  all_a(1, lds + 2 * kOp);
-  all_b(1, lds + 3 * kOp);
-  if (nfull >= 2) landed_barrier<LS>();
-  else landed_barrier<0>();
-#pragma unroll
-  for (int j = 0; j < NJ; ++j) bf[0][j] = b.read(lds + kOp, 0, j);
-#pragma unroll
-  for (int i = 0; i < NI; ++i) af[0][i] = a.read(lds, 0, i);
-
-  // Stage ks, its first fragments in registers.  A of stage ks + 2 goes out during its first two k-steps, into
-  // the slot that B of stage ks - 1 left.  Before its last k-step, stage ks + 1 has to have landed everywhere
-  // (all but the loads of A just issued); then this stage is fully read too, and B of stage ks + 2 goes into
-  // A's slot.  (A's own lead is two stages, B's one: 1000-2000 clocks.)
-  int ks = 0, slot = 0;                            // slot of A of stage ks
-  auto at_slot = [&](int k) {
-    const int q = slot + k;
-    return lds + (q >= kSlots ? q - kSlots : q) * kOp;
-  };
-  for (; ks + 2 < nfull; ++ks) {
-    char *sa = at_slot(0), *sb = at_slot(1), *na = at_slot(2), *nb = at_slot(3), *nna = at_slot(4);
-    kstep(LoadA{}, 0, sa, sb, 1, nna);
-    kstep(LoadA{}, 1, sa, sb, 2, nna);
-    a.base += a.step;
-    kstep(None{}, 2, sa, sb, 3, nullptr);
-    landed_barrier<LA>();
-    kstep(LoadB{}, 3, na, nb, 0, sa);
-    b.base += b.step;
-    slot = slot + 2 >= kSlots ? slot + 2 - kSlots : slot + 2;
-  }
-  for (; ks < nsteps; ++ks) {                      // the last two or three stages
-    char *sa = at_slot(0), *sb = at_slot(1), *na = at_slot(2), *nb = at_slot(3), *nna = at_slot(4);
-    all_a(ks + 2, nna);
-    kstep(None{}, 0, sa, sb, 1, nullptr);
-    kstep(None{}, 1, sa, sb, 2, nullptr);
-    kstep(None{}, 2, sa, sb, 3, nullptr);
-    landed_barrier<0>();
-    all_b(ks + 2, sa);
-    kstep(None{}, 3, na, nb, 0, nullptr);
-    slot = slot + 2 >= kSlots ? slot + 2 - kSlots : slot + 2;
-  }
-
-  // ---- epilogue: whole row pieces through LDS (store_tile_rows) ----
-  const int64_t out_row0 = MODE == kWgrad ? (int64_t)t.g * p.N + (int64_t)t.mt * BM : t.row0;
-  landed_barrier<0>();
-  char* reg = lds + w * 64 * (128 * NJ + 16);
-  if constexpr (TYPE == kInt8) {
-    // lane l holds row 32 i + l % 32 and columns 32 j + 8 q + 4 (l / 32) .. + 3 of its wave's tile
-    const float* sx = (const float*)p.sa;
-    const float* sw = (const float*)p.sb + (int64_t)t.g * p.N + (int64_t)t.nt * BN;
-    v16f out[NI][NJ];
-    float rs[NI];
-#pragma unroll
-    for (int i = 0; i < NI; ++i) rs[i] = sx[t.row0 + min(WM * wm + 32 * i + (lane & 31), a_lim - 1)];
-#pragma unroll
-    for (int j = 0; j < NJ; ++j)
+    for (int jj = 0; jj < kJ; ++jj)
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        const int c = min(WN * wn + 32 * j + 8 * q + 4 * (lane >> 5), b_lim - 4);
-        const float4 s = make_float4(sw[c], sw[c + 1], sw[c + 2], sw[c + 3]);
-        const float cs[4] = {s.x, s.y, s.z, s.w};
+        float v[4];
 #pragma unroll
-        for (int i = 0; i < NI; ++i)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) out[i][j][4 * q + k] = (float)acc[i][j][4 * q + k] * (rs[i] * cs[k]);
+        for (int e = 0; e < 4; ++e) v[e] = value(kJ * pass + jj, q, e);
+        if constexpr (BF16)
+          *(uint2*)(reg + r * RB + (((4 * jj + q) ^ (r & (kCh - 1))) << 4) + ((h ^ (r >> 4)) << 3)) =
+              make_uint2(f32_to_bf16_bits(v[0]) | (f32_to_bf16_bits(v[1]) << 16),
+                         f32_to_bf16_bits(v[2]) | (f32_to_bf16_bits(v[3]) << 16));
+        else
+          *(float4*)(reg + r * RB + (((8 * jj + 2 * q + h) ^ (r & (kCh - 1))) << 4)) =
+              make_float4(v[0], v[1], v[2], v[3]);
       }
-    store_tile_rows<NI, NJ, NI < 2 ? 1 : 2>(out, reg, p.out_bf16, p.out, out_row0, nout, (int64_t)t.nt * BN, WM * wm, WN * wn,
-                               a_lim, b_lim);
-  } else {
-    store_tile_rows<NI, NJ, NI < 2 ? 1 : 2>(acc, reg, p.out_bf16, p.out, out_row0, nout, (int64_t)t.nt * BN, WM * wm, WN * wn,
-                               a_lim, b_lim);
+    uint4 v[kPieces];
+#pragma unroll
+    for (int it = 0; it < kPieces; ++it) {
+      const int pr = 64 / kCh * it + lane / kCh;
+      v[it] = *(const uint4*)(reg + pr * RB + (((lane ^ pr) & (kCh - 1)) << 4));
+      if (BF16 && it >= kPieces / 2) v[it] = make_uint4(v[it].z, v[it].w, v[it].x, v[it].y);
+    }
+    // (keep the reads together ahead of the stores, so that a pass waits for LDS once)
+#pragma unroll
+    for (int it = 0; it < kPieces; ++it)
+      asm volatile("" : "+v"(v[it].x), "+v"(v[it].y), "+v"(v[it].z), "+v"(v[it].w));
+    const int tc = c0 + kCols * pass + (BF16 ? 8 : 4) * (lane & (kCh - 1));        // tile column
+#pragma unroll
+    for (int it = 0; it < kPieces; ++it) {
+      const int tr = r0 + 64 / kCh * it + lane / kCh;
+      if (tr >= row_lim || tc >= col_lim) continue;
+      const int64_t idx = (out_row0 + tr) * nout + col0 + tc;
+      if constexpr (BF16) *(uint4*)((uint16_t*)out + idx) = v[it];
+      else *(uint4*)((float*)out + idx) = v[it];
+    }
   }
 }
 
+// The tiles of a workgroup as one stream of stages.  Loads run two stages ahead of the multiplication, across
+// tiles too, so the pipeline is not emptied for an epilogue.
+template <int MODE, int TYPE>
+struct Runner {
+  static constexpr bool A_COLS = MODE == kWgrad, B_COLS = MODE != kFwd;
+  static constexpr int ES = TYPE == kInt8 ? 1 : 2;        // bytes per element
+  static constexpr int TPS = BKB / ES;                    // contraction elements per stage
+  typedef typename Acc<TYPE>::type vacc;
+
+  struct Geometry {                                       // of a tile (wave-uniform)
+    int g, mt, nt;
+    int a_lim, b_lim;                                     // valid output rows / columns
+    int64_t row0, e_row0;                                 // first routed row of the tile / of the expert
+    int nfull, tail, nsteps;                              // whole stages, elements of a partial one, stages
+  };
+
+  const GemmArgs& p;
+  char* lds;
+  const Tile& mine;                                       // lane k: tile k of this workgroup
+  const int w, wm, wn;
+  Operand<A_COLS> a;                                      // of the stage to load
+  Operand<B_COLS> b;
+  int lk = 0, lend = 0, lks = 0, lfull = 0, ltail = 0, lsteps = 0;   // its tile, stage and the tile's stages
+  bool loading = false;
+
+  __device__ __forceinline__ Runner(const GemmArgs& p_, char* lds_, const Tile& mine_)
+      : p(p_), lds(lds_), mine(mine_), w(__builtin_amdgcn_readfirstlane(threadIdx.x >> 6)), wm(w / kWavesN),
+        wn(w % kWavesN) {}
+
+  __device__ __forceinline__ Geometry geometry(int k) const {
+    auto get = [&](int v) { return __builtin_amdgcn_readlane(v, k); };
+    Geometry t;
+    t.g = get(mine.g);
+    t.mt = get(mine.mt);
+    t.nt = get(mine.nt);
+    const int e_rows = get(mine.e_rows);
+    t.row0 = get((int)mine.row0);                         // (routed rows fit 31 bits)
+    t.e_row0 = t.row0 - (int64_t)t.mt * BM;
+    t.a_lim = MODE == kWgrad ? (int)min((int64_t)BM, p.N - (int64_t)t.mt * BM) : get(mine.rows);
+    t.b_lim = (int)min((int64_t)BN, (MODE == kFwd ? p.N : p.K) - (int64_t)t.nt * BN);
+    const int64_t L = MODE == kFwd ? p.K : (MODE == kDgrad ? p.N : (int64_t)e_rows);
+    t.nfull = (int)(L / TPS);
+    t.tail = (int)(L % TPS);
+    t.nsteps = t.nfull + (t.tail ? 1 : 0);
+    return t;
+  }
+
+  // Loads start at tile k's stage 0.
+  __device__ __forceinline__ void place(int k) {
+    const Geometry t = geometry(k);
+    const int lane = fresh_lane();
+    a.place(lane, w, A_COLS ? p.a + t.e_row0 * p.lda + 2 * (int64_t)t.mt * BM : p.a + t.row0 * p.lda, p.lda, t.a_lim, TPS);
+    b.place(lane, w,
+            MODE == kFwd     ? p.b + ((int64_t)t.g * p.N + (int64_t)t.nt * BN) * p.ldb
+            : MODE == kDgrad ? p.b + (int64_t)t.g * p.N * p.ldb + 2 * (int64_t)t.nt * BN
+                             : p.b + t.e_row0 * p.ldb + 2 * (int64_t)t.nt * BN,
+            p.ldb, t.b_lim, TPS);
+    lks = 0;
+    lfull = t.nfull;
+    ltail = t.tail;
+    lsteps = t.nsteps;
+  }
+  // Point the loads at the next stage of the stream (`loading` false at its end).  Returns the contraction
+  // elements of a partial stage, 0 of a whole one.
+  __device__ __forceinline__ int next_stage() {
+    while (loading && lks == lsteps) {                    // (a tile of an expert without rows has no stages)
+      if (++lk == lend) loading = false;
+      else place(lk);
+    }
+    if (!loading || lks < lfull) return 0;
+    const int lane = fresh_lane();
+    a.clamp(lane, w, A_COLS ? ltail : ltail * ES, (uint32_t)p.lda);
+    b.clamp(lane, w, B_COLS ? ltail : ltail * ES, (uint32_t)p.ldb);
+    return ltail;
+  }
+  __device__ __forceinline__ void loaded() {
+    ++lks;
+    a.base += a.step;
+    b.base += b.step;
+  }
+  // A partial stage has landed everywhere: clear what lies past its end, before anyone reads it.
+  __device__ __forceinline__ void clear(int la, int lim, char* sa, char* sb) {
+    const int lane = fresh_lane();
+    a.zero(lane, w, la, A_COLS ? lim : lim * ES, sa);
+    b.zero(lane, w, kLoads, B_COLS ? lim : lim * ES, sb);
+    lds_barrier();
+  }
+
+  // Tiles k0 .. k1 - 1, all with NI 32-row fragments of A per wave (64 NI rows).
+  template <int NI>
+  __device__ __forceinline__ void run(int k0, int k1) {
+    constexpr int WM = 32 * NI;
+    constexpr int LA = 2 * NI;                            // loads of A per wave and stage
+    constexpr int LS = LA + kLoads;
+    const int lane = fresh_lane();
+    a.place_frags(lane, WM * wm);
+    b.place_frags(lane, WN * wn);
+    v4i af[2][NI], bf[2][NJ];                      // fragments of the current and the next k-step
+    vacc acc[NI][NJ];
+
+    // Group i of a k-step: row fragment i times the NJ column fragments.  The next k-step's reads are spread
+    // over the groups, the fragments that its first group needs first.
+    auto multiply = [&](int cur, int i) {
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) acc[i][j] = Acc<TYPE>::mfma(bf[cur][j], af[cur][i], acc[i][j]);
+    };
+    auto read = [&](int nxt, const char* sa, const char* sb, int nk, int from, int to) {
+#pragma unroll
+      for (int r = 0; r < NJ + NI; ++r)
+        if (r >= from && r < to) {
+          if (r < NJ) bf[nxt][r] = b.read(sb, nk, r);
+          else af[nxt][r - NJ] = a.read(sa, nk, r - NJ);
+        }
+    };
+    // K-steps 0 .. 2 of a stage: multiply while k-step kk + 1 is read.  LOAD: half of A's loads go out too.
+    auto kstep = [&](auto load, int kk, const char* sa, const char* sb, char* dst) {
+#pragma unroll
+      for (int i = 0; i < NI; ++i) {
+        read(1 - (kk & 1), sa, sb, kk + 1, i * (NJ + NI) / NI, (i + 1) * (NJ + NI) / NI);
+        if constexpr (decltype(load)::value) {
+#pragma unroll
+          for (int j = LA / 2 * i / NI; j < LA / 2 * (i + 1) / NI; ++j) a.load(w, LA / 2 * kk + j, dst);
+        }
+        multiply(kk & 1, i);
+        __builtin_amdgcn_sched_barrier(0);         // keep the reads and loads spread as written
+      }
+    };
+    // K-step 3: while its first group multiplies, `landed` waits for the next stage and meets the other waves;
+    // then the next stage's first fragments are read.  LOAD: all of B's loads go out.
+    auto last_kstep = [&](auto load, auto landed, const char* na, const char* nb, char* dst) {
+      constexpr int G = NI > 1 ? NI - 1 : 1;       // groups that read
+#pragma unroll
+      for (int i = 0; i < NI; ++i) {
+        const int g = NI > 1 ? i - 1 : 0;
+        if (NI == 1) landed();
+        if (g >= 0) {
+          read(0, na, nb, 0, g * (NJ + NI) / G, (g + 1) * (NJ + NI) / G);
+          if constexpr (decltype(load)::value) {
+#pragma unroll
+            for (int j = kLoads * g / G; j < kLoads * (g + 1) / G; ++j) b.load(w, j, dst);
+          }
+        }
+        multiply(1, i);
+        __builtin_amdgcn_sched_barrier(0);
+        if (NI > 1 && i == 0) landed();
+      }
+    };
+
+    // prologue: stages 0 and 1 of the stream on their way, stage 0 landed, its first fragments read
+    // slots of this stage's A and B, the next one's, and the one after's A
+    char *s0 = lds, *s1 = lds + kOp, *s2 = lds + 2 * kOp, *s3 = lds + 3 * kOp, *s4 = lds + 4 * kOp;
+    auto rotate = [&]() {
+      char *x0 = s0, *x1 = s1;
+      s0 = s2;
+      s1 = s3;
+      s2 = s4;
+      s3 = x0;
+      s4 = x1;
+    };
+    lk = k0;
+    lend = k1;
+    loading = true;
+    place(k0);
+    const int lim0 = next_stage();
+    if (loading) {
+      a.load_all(w, LA, s0);
+      b.load_all(w, kLoads, s1);
+      loaded();
+    }
+    int lim1 = next_stage();                       // of the stage after the one to multiply
+    if (loading) {
+      a.load_all(w, LA, s2);
+      b.load_all(w, kLoads, s3);
+      loaded();
+      landed_barrier<LS>();
+    } else {
+      landed_barrier<0>();
+    }
+    if (lim0) clear(LA, lim0, s0, s1);
+    int lim2 = next_stage();                       // of the stage to load
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) bf[0][j] = b.read(s1, 0, j);
+#pragma unroll
+    for (int i = 0; i < NI; ++i) af[0][i] = a.read(s0, 0, i);
+
+    for (int k = k0; k < k1; ++k) {
+#pragma unroll
+      for (int i = 0; i < NI; ++i)
+#pragma unroll
+        for (int j = 0; j < NJ; ++j)
+#pragma unroll
+          for (int r = 0; r < 16; ++r) acc[i][j][r] = 0;
+      auto keep = [&]() {                          // (accumulators stay in accumulation registers)
+#pragma unroll
+        for (int i = 0; i < NI; ++i)
+#pragma unroll
+          for (int j = 0; j < NJ; ++j) asm volatile("" : "+a"(acc[i][j]));
+      };
+      keep();
+      // A stage.  A of the stage two on goes out during its first two k-steps, into the slot that B of the
+      // stage before left.  In its last k-step, once its own last fragments are in registers, the next stage has
+      // to have landed everywhere (all but the loads of A just issued); this stage's slots are free then, and B
+      // of the stage two on goes into A's.  (A's own lead is two stages, B's one: 1000-2000 clocks.)
+      int left = loading ? geometry(k).nsteps : 0, rest = loading ? 0 : geometry(k).nsteps;
+      for (; left > 0; --left) {
+        kstep(std::true_type{}, 0, s0, s1, s4);
+        kstep(std::true_type{}, 1, s0, s1, s4);
+        kstep(std::false_type{}, 2, s0, s1, nullptr);
+        last_kstep(std::true_type{}, [&]() {
+          landed_barrier<LA>();
+          if (__builtin_expect(lim1 != 0, 0)) clear(LA, lim1, s2, s3);
+        }, s2, s3, s0);
+        loaded();
+        lim1 = lim2;
+        lim2 = 0;
+        if (__builtin_expect(lks >= lfull, 0)) {
+          lim2 = next_stage();
+          if (!loading) {                          // the stream's last two stages follow
+            rest = left - 1;
+            left = 1;
+          }
+        }
+        rotate();
+      }
+      keep();
+      for (; rest > 0; --rest) {
+        kstep(std::false_type{}, 0, s0, s1, nullptr);
+        kstep(std::false_type{}, 1, s0, s1, nullptr);
+        kstep(std::false_type{}, 2, s0, s1, nullptr);
+        last_kstep(std::false_type{}, [&]() {
+          landed_barrier<0>();
+          if (lim1) clear(LA, lim1, s2, s3);
+        }, s2, s3, nullptr);
+        lim1 = 0;
+        rotate();
+      }
+
+      keep();
+      // ---- epilogue, through the slot that the last stage's B left ----
+      const Geometry t = geometry(k);
+      constexpr int RB = TYPE == kInt8 ? 128 : 256;
+      char* reg = s4 + 8192 * w;
+      const int64_t nout = MODE == kFwd ? p.N : p.K;
+      const int64_t out_row0 = (MODE == kWgrad ? (int64_t)t.g * p.N : t.e_row0) + (int64_t)t.mt * BM;
+      const int64_t col0 = (int64_t)t.nt * BN;
+      float row_scale[NI];
+      const float4* col_scale = (const float4*)(reg + 4096 + 512);
+      if constexpr (TYPE == kInt8) {
+        // scales of the wave's rows and columns, behind its staged rows (older loads are those of A and B of
+        // the stages ahead: waiting for these few waits for them too, which have to land soon anyway)
+        const int l = fresh_lane();
+        const float* sx = (const float*)p.sa + t.row0;
+        const float* sw = (const float*)p.sb + (int64_t)t.g * p.N + col0;
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          dma4((const uint8_t*)(sx + min(WM * wm + 64 * q + l, t.a_lim - 1)), reg + 4096 + 256 * q);
+          dma4((const uint8_t*)(sw + min(WN * wn + 64 * q + l, t.b_lim - 1)), reg + 4608 + 256 * q);
+        }
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+#pragma unroll
+        for (int i = 0; i < NI; ++i) row_scale[i] = *(const float*)(reg + 4096 + 4 * (32 * i + (l & 31)));
+      }
+#pragma unroll
+      for (int i = 0; i < NI; ++i) {
+        auto value = [&](int j, int q, int e) -> float {
+          if constexpr (TYPE == kInt8) {
+            const float4 c = col_scale[8 * j + 2 * q + (lane >> 5)];
+            const float c4[4] = {c.x, c.y, c.z, c.w};
+            return (float)acc[i][j][4 * q + e] * (row_scale[i] * c4[e]);
+          } else {
+            return acc[i][j][4 * q + e];
+          }
+        };
+        if (p.out_bf16)
+          store_rows<true, RB>(value, reg, p.out, out_row0, nout, col0, WM * wm + 32 * i, WN * wn, t.a_lim, t.b_lim);
+        else
+          store_rows<false, RB>(value, reg, p.out, out_row0, nout, col0, WM * wm + 32 * i, WN * wn, t.a_lim, t.b_lim);
+      }
+      lds_barrier();                               // that slot is loaded into next
+    }
+  }
+
+  // Tiles 0 .. count - 1, in runs of the same height.
+  __device__ __forceinline__ void run_all(int count) {
+    if constexpr (MODE == kWgrad) {
+      run<4>(0, count);
+    } else {
+      const int ni = mine.rows > 128 ? 4 : (mine.rows > 64 ? 2 : 1);
+      for (int k = 0; k < count;) {
+        const int n = __builtin_amdgcn_readlane(ni, k);
+        const uint64_t other = __ballot(ni != n) >> k;
+        const int end = min(count, other ? k + __builtin_ctzll(other) : count);
+        if (n == 4) run<4>(k, end);
+        else if (n == 2) run<2>(k, end);
+        else run<1>(k, end);
+        k = end;
+      }
+    }
+  }
+};
+
+// One workgroup per CU (all of its LDS), tiles b, b + grid, ... of the launch.  The list of tiles is built
+// once per 64 tiles of a workgroup; lane k keeps tile k.
 template <int MODE, int TYPE>
 __global__ __launch_bounds__(NT, 1) void dense_grouped_gemm_kernel(GemmArgs p) {
   __shared__ __attribute__((aligned(16))) char lds[kLds];
-  Tile t;
-  if (!decode_grouped_tile<MODE, false, BM, BN, NT, 32, MODE != kWgrad>(p, lds, t)) return;
-  t.g = __builtin_amdgcn_readfirstlane(t.g);
-  t.mt = __builtin_amdgcn_readfirstlane(t.mt);
-  t.nt = __builtin_amdgcn_readfirstlane(t.nt);
-  t.rows = __builtin_amdgcn_readfirstlane(t.rows);
-  t.e_rows = __builtin_amdgcn_readfirstlane(t.e_rows);
-  t.row0 = uniform64(t.row0);
-  __syncthreads();                               // scheduler scratch is reused for operands
-  if (MODE == kWgrad || t.rows > 128) run_tile<MODE, TYPE, 4>(p, t, lds);
-  else if (t.rows > 64) run_tile<MODE, TYPE, MODE == kWgrad ? 4 : 2>(p, t, lds);
-  else run_tile<MODE, TYPE, MODE == kWgrad ? 4 : 1>(p, t, lds);
+  constexpr bool kPartialLast = MODE != kWgrad;
+  for (int64_t round = 0;; ++round) {
+    build_tile_list<MODE, false, BM, BN, NT, 32, kPartialLast>(p, lds);
+    // a short list is spread over the XCDs in equal runs
+    const int chunk = min(chunk_tiles(MODE), max(1, listed_tiles<MODE, kPartialLast>(p, lds) / kXcd));
+    const int64_t b = blockIdx.x + gridDim.x * (64 * round + (threadIdx.x & 63));
+    Tile mine;
+    const bool have = b <= 0x3FFFFFFF &&
+                      locate_tile<MODE, false, BM, BN, 32, kPartialLast>(p, lds, list_position((int)b, chunk), mine);
+    const int count = __popcll(__ballot(have));    // positions grow with b: the first `count` lanes have a tile
+    __syncthreads();                               // the list's LDS is reused for operands
+    if (count == 0) return;
+    Runner<MODE, TYPE> r(p, lds, mine);
+    r.run_all(count);
+    if (count < 64) return;
+  }
 }
 
 static_assert(5 * (kMaxG + 1) * 4 <= kLds, "scheduler scratch must fit in LDS");
@@ -352,9 +573,12 @@ hipError_t launch_dense_gemm(int mode, bool int8, const GemmArgs& p, hipStream_t
     tiles = ((p.M + BM - 1) / BM + p.G) * ntc;
   }
   if (tiles == 0) return hipSuccess;
-  const int64_t per = (int64_t)kXcd * chunk_tiles(mode);
-  const int64_t grid = (tiles + per - 1) / per * per;
-  if (grid > 0x7FFFFFFF) return hipErrorInvalidValue;
+  if (tiles > 0x3FFFFFFF) return hipErrorInvalidValue;
+  int dev = 0, cus = 0;
+  hipError_t e = hipGetDevice(&dev);
+  if (e == hipSuccess) e = hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev);
+  if (e != hipSuccess) return e;
+  const int64_t grid = max(cus, 1);
   const dim3 g((unsigned)grid);
   if (int8) hipLaunchKernelGGL((dense_grouped_gemm_kernel<kFwd, kInt8>), g, dim3(NT), 0, st, p);
   else if (mode == kFwd) hipLaunchKernelGGL((dense_grouped_gemm_kernel<kFwd, kBf16>), g, dim3(NT), 0, st, p);
