@@ -465,7 +465,7 @@ mxmoe_status fp8bw_grouped_gemm_wgrad_fp8feed(const uint8_t* qdyT, const float* 
  *   wgrad: dW[g, n, k] = sum_{r of g} dY[r, n] X[r, k]        dw [G, N, K], 0 for an expert without rows
  *                                                             (written, also for M == 0)
  * x [M, K], dy [M, N], w [G*N, K] bf16.  1 <= G <= 1024; N and K are multiples of 8 (not of 128 as in the
- * block-scaled formats: there are no blocks).  256 rows of an operand must span less than 2 GiB.  M == 0
+ * block-scaled formats: there are no blocks).  256 rows of an operand or of an fp32 output must span less than 2 GiB.  M == 0
  * is a no-op for fwd and dgrad.  A NaN or an infinity reaches exactly the outputs whose sums contain it. */
 mxmoe_status bf16_grouped_gemm_fwd(const void* x, const void* w, const int32_t* offs, int32_t G, int64_t M,
                                    int64_t N, int64_t K, void* y, mxmoe_dtype ydt, void* stream);

@@ -788,6 +788,8 @@ static mxmoe_status dense_common(int mode, bool int8, const char* fn, const void
   p.lda = es * (mode == kFwd ? K : N);
   p.ldb = es * K;
   TRY(check_strides(fn, p, 256));
+  if ((mode == kFwd ? N : K) > ((int64_t)1 << 21) - 64)      // 256 fp32 output rows span less than 2 GiB too
+    return fail(MXMOE_ERR_SHAPE, "%s: output rows too long (N=%lld K=%lld)", fn, (long long)N, (long long)K);
   TRY(check_ptr(fn, "offs", offs, 4));
   if (mode != kWgrad && M == 0) return ok();
   TRY(check_ptr(fn, "output", out, 16));

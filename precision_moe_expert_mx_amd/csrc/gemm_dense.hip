@@ -91,10 +91,10 @@ struct Operand {
   __device__ __forceinline__ void load(int w, int j, char* st) const {
     dma16s(off[j], (const uint8_t*)uniform64((int64_t)base), st + (kWaves * j + w) * 1024);
   }
-  __device__ __forceinline__ void load_all(int w, int loads, char* st) const {
+  __device__ __forceinline__ void load(int w, int from, int to, char* st) const {
 #pragma unroll
     for (int j = 0; j < kLoads; ++j)
-      if (j < loads) load(w, j, st);
+      if (j >= from && j < to) load(w, j, st);
   }
   // Position along the contraction of this lane's piece of load j (bytes of a row, or rows).
   static __device__ __forceinline__ int at(int lane, int w, int j) {
@@ -186,11 +186,11 @@ __device__ __forceinline__ int fresh_lane() {
 // Store 32 rows of a wave's tile (value(j, q, e): fragment j, accumulator register 4 q + e) as whole row
 // pieces through RB * 32 bytes of LDS of its own: rows of RB bytes (256 or 128) whose 16-byte chunk c is at
 // c ^ (r mod chunks); a bf16 chunk's two 8-byte halves (from lanes 0..31 and 32..63) change places in rows
-// 16..31, so that the lanes of a write spread over the banks.  Rows at or past row_lim and columns at or past
-// col_lim are not written.
+// 16..31, so that the lanes of a write spread over the banks.  `out` is the buffer of the tile's valid rows
+// from its first column on (row_bytes apart); columns at or past col_lim are not written.
 template <bool BF16, int RB, typename Value>
-__device__ __forceinline__ void store_rows(Value value, char* reg, void* out, int64_t out_row0, int64_t nout,
-                                           int64_t col0, int r0, int c0, int row_lim, int col_lim) {
+__device__ __forceinline__ void store_rows(Value value, char* reg, __amdgpu_buffer_rsrc_t out, uint32_t row_bytes,
+                                           int r0, int c0, int col_lim) {
   constexpr int kCols = BF16 ? RB / 2 : RB / 4;           // columns per pass
   constexpr int kJ = kCols / 32;                          // fragments per pass
   constexpr int kCh = RB / 16;                            // chunks per staged row
@@ -207,8 +207,8 @@ __device__ __forceinline__ void store_rows(Value value, char* reg, void* out, in
         for (int e = 0; e < 4; ++e) v[e] = value(kJ * pass + jj, q, e);
         if constexpr (BF16)
           *(uint2*)(reg + r * RB + (((4 * jj + q) ^ (r & (kCh - 1))) << 4) + ((h ^ (r >> 4)) << 3)) =
-              make_uint2(f32_to_bf16_bits(v[0]) | (f32_to_bf16_bits(v[1]) << 16),
-                         f32_to_bf16_bits(v[2]) | (f32_to_bf16_bits(v[3]) << 16));
+              make_uint2(__builtin_bit_cast(uint32_t, v2bf{(__bf16)v[0], (__bf16)v[1]}),
+                         __builtin_bit_cast(uint32_t, v2bf{(__bf16)v[2], (__bf16)v[3]}));
         else
           *(float4*)(reg + r * RB + (((8 * jj + 2 * q + h) ^ (r & (kCh - 1))) << 4)) =
               make_float4(v[0], v[1], v[2], v[3]);
@@ -224,15 +224,13 @@ __device__ __forceinline__ void store_rows(Value value, char* reg, void* out, in
 #pragma unroll
     for (int it = 0; it < kPieces; ++it)
       asm volatile("" : "+v"(v[it].x), "+v"(v[it].y), "+v"(v[it].z), "+v"(v[it].w));
+    // lanes past the last column, and by the resource's length rows past the last one, store nothing
     const int tc = c0 + kCols * pass + (BF16 ? 8 : 4) * (lane & (kCh - 1));        // tile column
+    const uint32_t at = (uint32_t)((r0 + lane / kCh) * row_bytes) + (BF16 ? 2 : 4) * tc;
 #pragma unroll
-    for (int it = 0; it < kPieces; ++it) {
-      const int tr = r0 + 64 / kCh * it + lane / kCh;
-      if (tr >= row_lim || tc >= col_lim) continue;
-      const int64_t idx = (out_row0 + tr) * nout + col0 + tc;
-      if constexpr (BF16) *(uint4*)((uint16_t*)out + idx) = v[it];
-      else *(uint4*)((float*)out + idx) = v[it];
-    }
+    for (int it = 0; it < kPieces; ++it)
+      __builtin_amdgcn_raw_buffer_store_b128(v4u_{v[it].x, v[it].y, v[it].z, v[it].w}, out,
+                                             tc < col_lim ? at + it * (64 / kCh) * row_bytes : 0xFFFFFFF0u, 0, 0);
   }
 }
 
@@ -259,7 +257,6 @@ struct Runner {
   Operand<A_COLS> a;                                      // of the stage to load
   Operand<B_COLS> b;
   int lk = 0, lend = 0, lks = 0, lfull = 0, ltail = 0, lsteps = 0;   // its tile, stage and the tile's stages
-  bool loading = false;
 
   __device__ __forceinline__ Runner(const GemmArgs& p_, char* lds_, const Tile& mine_)
       : p(p_), lds(lds_), mine(mine_), w(__builtin_amdgcn_readfirstlane(threadIdx.x >> 6)), wm(w / kWavesN),
@@ -298,23 +295,33 @@ struct Runner {
     ltail = t.tail;
     lsteps = t.nsteps;
   }
-  // Point the loads at the next stage of the stream (`loading` false at its end).  Returns the contraction
-  // elements of a partial stage, 0 of a whole one.
-  __device__ __forceinline__ int next_stage() {
-    while (loading && lks == lsteps) {                    // (a tile of an expert without rows has no stages)
-      if (++lk == lend) loading = false;
-      else place(lk);
+  // The stage to load is one past the tile's whole ones: point the loads at its partial one (returns its
+  // contraction elements; 0 for a whole stage) or at the first stage of the next tile that has any.  Past the
+  // stream's end they stay where they are: the last stages load again what they need not, into free slots.
+  __device__ __forceinline__ int settle() {
+    if (lks == lsteps) {
+      int k = lk + 1;
+      while (k < lend && MODE == kWgrad && __builtin_amdgcn_readlane(mine.e_rows, k) == 0) ++k;
+      if (k >= lend) {
+        --lks;
+        a.base -= a.step;
+        b.base -= b.step;
+        return 0;
+      }
+      lk = k;
+      place(k);
     }
-    if (!loading || lks < lfull) return 0;
+    if (lks < lfull) return 0;
     const int lane = fresh_lane();
     a.clamp(lane, w, A_COLS ? ltail : ltail * ES, (uint32_t)p.lda);
     b.clamp(lane, w, B_COLS ? ltail : ltail * ES, (uint32_t)p.ldb);
     return ltail;
   }
-  __device__ __forceinline__ void loaded() {
+  __device__ __forceinline__ int advance() {
     ++lks;
     a.base += a.step;
     b.base += b.step;
+    return __builtin_expect(lks >= lfull, 0) ? settle() : 0;
   }
   // A partial stage has landed everywhere: clear what lies past its end, before anyone reads it.
   __device__ __forceinline__ void clear(int la, int lim, char* sa, char* sb) {
@@ -329,7 +336,6 @@ struct Runner {
   __device__ __forceinline__ void run(int k0, int k1) {
     constexpr int WM = 32 * NI;
     constexpr int LA = 2 * NI;                            // loads of A per wave and stage
-    constexpr int LS = LA + kLoads;
     const int lane = fresh_lane();
     a.place_frags(lane, WM * wm);
     b.place_frags(lane, WN * wn);
@@ -350,22 +356,19 @@ struct Runner {
           else af[nxt][r - NJ] = a.read(sa, nk, r - NJ);
         }
     };
-    // K-steps 0 .. 2 of a stage: multiply while k-step kk + 1 is read.  LOAD: half of A's loads go out too.
-    auto kstep = [&](auto load, int kk, const char* sa, const char* sb, char* dst) {
+    // K-steps 0 .. 2 of a stage: multiply while k-step kk + 1 is read; load(i) issues a load or two in group i.
+    auto kstep = [&](auto load, int kk, const char* sa, const char* sb) {
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
         read(1 - (kk & 1), sa, sb, kk + 1, i * (NJ + NI) / NI, (i + 1) * (NJ + NI) / NI);
-        if constexpr (decltype(load)::value) {
-#pragma unroll
-          for (int j = LA / 2 * i / NI; j < LA / 2 * (i + 1) / NI; ++j) a.load(w, LA / 2 * kk + j, dst);
-        }
+        load(i);
         multiply(kk & 1, i);
         __builtin_amdgcn_sched_barrier(0);         // keep the reads and loads spread as written
       }
     };
     // K-step 3: while its first group multiplies, `landed` waits for the next stage and meets the other waves;
-    // then the next stage's first fragments are read.  LOAD: all of B's loads go out.
-    auto last_kstep = [&](auto load, auto landed, const char* na, const char* nb, char* dst) {
+    // then the next stage's first fragments are read.
+    auto last_kstep = [&](auto load, auto landed, const char* na, const char* nb) {
       constexpr int G = NI > 1 ? NI - 1 : 1;       // groups that read
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
@@ -373,10 +376,7 @@ struct Runner {
         if (NI == 1) landed();
         if (g >= 0) {
           read(0, na, nb, 0, g * (NJ + NI) / G, (g + 1) * (NJ + NI) / G);
-          if constexpr (decltype(load)::value) {
-#pragma unroll
-            for (int j = kLoads * g / G; j < kLoads * (g + 1) / G; ++j) b.load(w, j, dst);
-          }
+          load(g, G);
         }
         multiply(1, i);
         __builtin_amdgcn_sched_barrier(0);
@@ -384,42 +384,30 @@ struct Runner {
       }
     };
 
-    // prologue: stages 0 and 1 of the stream on their way, stage 0 landed, its first fragments read
     // slots of this stage's A and B, the next one's, and the one after's A
     char *s0 = lds, *s1 = lds + kOp, *s2 = lds + 2 * kOp, *s3 = lds + 3 * kOp, *s4 = lds + 4 * kOp;
-    auto rotate = [&]() {
-      char *x0 = s0, *x1 = s1;
-      s0 = s2;
-      s1 = s3;
-      s2 = s4;
-      s3 = x0;
-      s4 = x1;
-    };
-    lk = k0;
+    // prologue: stage 0 of the stream and all but half of B of stage 1 on their way, stage 0 landed, its first
+    // fragments read
+    constexpr int LB = MODE == kWgrad ? kLoads : kLoads / 2;   // of B's loads
+    int lim1 = 0, lim2 = 0;                        // of a partial stage: the next to multiply, the one to load
     lend = k1;
-    loading = true;
-    place(k0);
-    const int lim0 = next_stage();
-    if (loading) {
-      a.load_all(w, LA, s0);
-      b.load_all(w, kLoads, s1);
-      loaded();
-    }
-    int lim1 = next_stage();                       // of the stage after the one to multiply
-    if (loading) {
-      a.load_all(w, LA, s2);
-      b.load_all(w, kLoads, s3);
-      loaded();
-      landed_barrier<LS>();
+    lk = k0;
+    while (MODE == kWgrad && lk < k1 && __builtin_amdgcn_readlane(mine.e_rows, lk) == 0) ++lk;
+    const bool any = lk < k1;                      // (wgrad: perhaps none of the experts has rows)
+    if (any) {
+      place(lk);
+      const int lim0 = settle();
+      a.load(w, 0, LA, s0);
+      b.load(w, 0, kLoads, s1);
+      lim2 = advance();
+      a.load(w, 0, LA, s2);
+      b.load(w, 0, LB, s3);
+      landed_barrier<LA + LB>();
+      if (lim0) clear(LA, lim0, s0, s1);
+      read(0, s0, s1, 0, 0, NJ + NI);
     } else {
       landed_barrier<0>();
     }
-    if (lim0) clear(LA, lim0, s0, s1);
-    int lim2 = next_stage();                       // of the stage to load
-#pragma unroll
-    for (int j = 0; j < NJ; ++j) bf[0][j] = b.read(s1, 0, j);
-#pragma unroll
-    for (int i = 0; i < NI; ++i) af[0][i] = a.read(s0, 0, i);
 
     for (int k = k0; k < k1; ++k) {
 #pragma unroll
@@ -435,42 +423,28 @@ struct Runner {
           for (int j = 0; j < NJ; ++j) asm volatile("" : "+a"(acc[i][j]));
       };
       keep();
-      // A stage.  A of the stage two on goes out during its first two k-steps, into the slot that B of the
-      // stage before left.  In its last k-step, once its own last fragments are in registers, the next stage has
-      // to have landed everywhere (all but the loads of A just issued); this stage's slots are free then, and B
-      // of the stage two on goes into A's.  (A's own lead is two stages, B's one: 1000-2000 clocks.)
-      int left = loading ? geometry(k).nsteps : 0, rest = loading ? 0 : geometry(k).nsteps;
-      for (; left > 0; --left) {
-        kstep(std::true_type{}, 0, s0, s1, s4);
-        kstep(std::true_type{}, 1, s0, s1, s4);
-        kstep(std::false_type{}, 2, s0, s1, nullptr);
-        last_kstep(std::true_type{}, [&]() {
-          landed_barrier<LA>();
-          if (__builtin_expect(lim1 != 0, 0)) clear(LA, lim1, s2, s3);
-        }, s2, s3, s0);
-        loaded();
+      // A stage.  Its loads go out evenly (about one per group: more at once and the address unit holds up the
+      // wave): the rest of B of the next stage, A of the stage two on into the slot that B of the stage before
+      // left, and, once this stage's last fragments are in registers everywhere and the next stage has landed
+      // (all but the loads of A just issued), the first half of B of the stage two on into this A's slot.
+      for (int left = geometry(k).nsteps; left > 0; --left) {
+        kstep([&](int i) { b.load(w, LB + (kLoads - LB) * i / NI, LB + (kLoads - LB) * (i + 1) / NI, s3); }, 0, s0, s1);
         lim1 = lim2;
-        lim2 = 0;
-        if (__builtin_expect(lks >= lfull, 0)) {
-          lim2 = next_stage();
-          if (!loading) {                          // the stream's last two stages follow
-            rest = left - 1;
-            left = 1;
-          }
-        }
-        rotate();
-      }
-      keep();
-      for (; rest > 0; --rest) {
-        kstep(std::false_type{}, 0, s0, s1, nullptr);
-        kstep(std::false_type{}, 1, s0, s1, nullptr);
-        kstep(std::false_type{}, 2, s0, s1, nullptr);
-        last_kstep(std::false_type{}, [&]() {
-          landed_barrier<0>();
-          if (lim1) clear(LA, lim1, s2, s3);
-        }, s2, s3, nullptr);
-        lim1 = 0;
-        rotate();
+        lim2 = advance();
+        kstep([&](int i) { a.load(w, i, i + 1, s4); }, 1, s0, s1);
+        kstep([&](int i) { a.load(w, NI + i, NI + i + 1, s4); }, 2, s0, s1);
+        last_kstep([&](int g, int G) { b.load(w, LB * g / G, LB * (g + 1) / G, s0); },
+                   [&]() {
+                     landed_barrier<LA>();
+                     if (__builtin_expect(lim1 != 0, 0)) clear(LA, lim1, s2, s3);
+                   },
+                   s2, s3);
+        char *x0 = s0, *x1 = s1;                   // the next stage's slots
+        s0 = s2;
+        s1 = s3;
+        s2 = s4;
+        s3 = x0;
+        s4 = x1;
       }
 
       keep();
@@ -481,6 +455,11 @@ struct Runner {
       const int64_t nout = MODE == kFwd ? p.N : p.K;
       const int64_t out_row0 = (MODE == kWgrad ? (int64_t)t.g * p.N : t.e_row0) + (int64_t)t.mt * BM;
       const int64_t col0 = (int64_t)t.nt * BN;
+      const uint32_t row_bytes = (uint32_t)nout * (p.out_bf16 ? 2 : 4);
+      // (a tile's valid rows, less the columns before it)
+      const __amdgpu_buffer_rsrc_t out = __builtin_amdgcn_make_buffer_rsrc(
+          (char*)p.out + out_row0 * row_bytes + col0 * (p.out_bf16 ? 2 : 4), 0,
+          (int)(t.a_lim * row_bytes - (uint32_t)col0 * (p.out_bf16 ? 2 : 4)), 0x00020000);
       float row_scale[NI];
       const float4* col_scale = (const float4*)(reg + 4096 + 512);
       if constexpr (TYPE == kInt8) {
@@ -510,12 +489,13 @@ struct Runner {
           }
         };
         if (p.out_bf16)
-          store_rows<true, RB>(value, reg, p.out, out_row0, nout, col0, WM * wm + 32 * i, WN * wn, t.a_lim, t.b_lim);
+          store_rows<true, RB>(value, reg, out, row_bytes, WM * wm + 32 * i, WN * wn, t.b_lim);
         else
-          store_rows<false, RB>(value, reg, p.out, out_row0, nout, col0, WM * wm + 32 * i, WN * wn, t.a_lim, t.b_lim);
+          store_rows<false, RB>(value, reg, out, row_bytes, WM * wm + 32 * i, WN * wn, t.b_lim);
       }
       lds_barrier();                               // that slot is loaded into next
     }
+    landed_barrier<0>();                           // (the loads past the end: LDS is another run's next)
   }
 
   // Tiles 0 .. count - 1, in runs of the same height.
