@@ -21,7 +21,8 @@
 // An operand contiguous along t is staged as 256 rows of 128 bytes; one with t as its rows as 64 rows of 256
 // columns (512 bytes), which fragments are read from with the transposing LDS read (ds_read_b64_tr_b16: 16
 // lanes read 4 rows x 16 columns and each gets one column's 4 values), so no operand is ever transposed in
-// memory.  A tile with at most 128 (64) valid A rows runs as 128 (64) x 256.
+// memory.  The row fragments of a tile alternate between the two row halves of the waves, and fragments
+// without valid rows are skipped, so that a tile of few rows costs what its rows do, 64 at a time.
 #include <type_traits>
 
 #include "grouped_tile.h"
@@ -29,7 +30,11 @@
 namespace mxmoe {
 namespace {
 
-using Tile = GroupTile;
+struct Tile {
+  int g, mt, nt;   // expert, row tile, column tile
+  int row0;        // first routed row of the expert
+  int e_rows;      // rows of the expert
+};
 
 constexpr int BM = 256, BN = 256;                // A / B rows (output rows / columns) per tile
 constexpr int BKB = 128;                         // contraction bytes per stage
@@ -38,7 +43,8 @@ constexpr int kWavesM = 2, kWavesN = 2;
 constexpr int kWaves = kWavesM * kWavesN;
 constexpr int NT = 64 * kWaves;
 constexpr int WN = BN / kWavesN;                 // output columns per wave
-constexpr int NJ = WN / 32;
+constexpr int NI = BM / kWavesM / 32;            // row fragments per wave: fragment i is rows 32 (kWavesM i + wm) .. + 31
+constexpr int NJ = WN / 32;                      // column fragments per wave, consecutive
 constexpr int kOp = BM * BKB;                    // bytes of one operand's stage (both layouts): 32 KiB
 constexpr int kSlots = 5;                        // operand stages in LDS: A p at slot 2p % 5, B p at (2p + 1) % 5
 constexpr int kLoads = kOp / 1024 / kWaves;      // 1 KiB loads per wave, stage and (whole) operand
@@ -63,7 +69,7 @@ __device__ __forceinline__ int col_swz(int t) { return (t & 3) | ((t >> 1) & 4);
 // One operand of a wave: its share of a stage's loads (kLoads of 1 KiB, fewer of A in a tile of fewer
 // rows; load j of wave w fills the stage's 1 KiB piece kWaves j + w) as 32-bit lane offsets from a
 // wave-uniform base that moves by `step` bytes per stage, and its fragments' LDS offsets in a stage.
-template <bool COLS_>
+template <bool COLS_, int STRIDE>               // STRIDE: rows (columns) from one fragment to the next
 struct Operand {
   static constexpr bool COLS = COLS_;
   uint32_t off[kLoads];
@@ -129,14 +135,14 @@ struct Operand {
       const int t = 8 * (lane >> 5) + (i16 >> 2);
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        frag[i] = t * 512 + ((2 * (r0 + 32 * i + (lane & 16) + 4 * (i16 & 3))) ^ (col_swz(t) << 6));
+        frag[i] = t * 512 + ((2 * (r0 + STRIDE * i + (lane & 16) + 4 * (i16 & 3))) ^ (col_swz(t) << 6));
     }
   }
   // Matrix instruction's fragment i (32 rows or columns) of k-step kk of the stage at st: lane l holds row
-  // 32 i + l % 32, bytes 16 (l / 32) .. + 15 of the k-step's 32.
+  // r0 + STRIDE i + l % 32, bytes 16 (l / 32) .. + 15 of the k-step's 32.
   __device__ __forceinline__ v4i read(const char* st, int kk, int i) const {
     if constexpr (!COLS) {
-      return *(const v4i*)(st + frag[kk] + 32 * BKB * i);
+      return *(const v4i*)(st + frag[kk] + STRIDE * BKB * i);
     } else {
       // bf16: contraction rows 16 kk + 8 (l / 32) + 0..7, four per read
       v4s v[2];
@@ -234,6 +240,127 @@ __device__ __forceinline__ void store_rows(Value value, char* reg, __amdgpu_buff
   }
 }
 
+// ---- the launch's list of tiles, built in LDS by every workgroup from the device-resident offsets ----
+// It is made of entries: (expert, its whole row tiles) or (expert, its partial last row tile), each for all
+// column tiles.  Forward, dgrad: experts are taken in segments whose weights stay in the 256 MiB memory-side
+// cache; a segment's whole row tiles come first, expert by expert, then its partial ones, largest first.  (A
+// partial tile reads the same weights as the whole ones for less work: with all of them at the end of the
+// launch, the 64-expert layers read their weights from HBM twice, 75 us of 330; in expert order, a workgroup's
+// few tiles would differ too much in cost.)  Weight gradient: an entry per expert, most rows first, since
+// its cost is its contraction's.
+constexpr int64_t kSegmentBytes = 96 << 20;
+
+struct TileList {
+  int32_t* offs;      // [G + 1] clamped offsets
+  int32_t* entry;     // [2 G] expert, or kMaxG + expert for its partial tile
+  int32_t* first;     // [2 G + 1] tiles before the entry
+  __device__ __forceinline__ explicit TileList(char* lds)
+      : offs((int32_t*)lds), entry(offs + kMaxG + 1), first(entry + 2 * kMaxG) {}
+};
+constexpr int kListBytes = (kMaxG + 1 + 2 * kMaxG + 2 * kMaxG + 1) * 4;
+
+template <int MODE>
+__device__ __forceinline__ int list_entries(const GemmArgs& p) { return MODE == kWgrad ? p.G : 2 * p.G; }
+
+template <int MODE, int ES>
+__device__ __forceinline__ void build_list(const GemmArgs& p, const TileList& l) {
+  const int tid = threadIdx.x, G = p.G;
+  for (int g = tid; g <= G; g += NT) l.offs[g] = (int32_t)clamp_off(p.offs[g], p.M);
+  __syncthreads();
+  const int64_t weights = p.N * p.K * ES;
+  const int seg = MODE == kWgrad ? G : (int)min((int64_t)G, max((int64_t)1, kSegmentBytes / weights));
+  auto rows = [&](int g) { return max(l.offs[g + 1] - l.offs[g], 0); };
+  auto key = [&](int g) { return MODE == kWgrad ? rows(g) : rows(g) % BM; };
+  // rank of expert g among its segment's by key, ties by index: eight lanes count an eighth each (an index
+  // order past kLptMaxG experts, whose count would take too long)
+  for (int idx = tid; idx < 8 * ((G + 7) / 8 * 8); idx += NT) {
+    const int g = idx >> 3, part = idx & 7;
+    const bool in = g < G;
+    const int s0 = in ? g / seg * seg : 0, s1 = in ? min(G, s0 + seg) : 0;
+    int rank = 0;
+    if (G <= kLptMaxG) {
+      const int mg = in ? key(g) : 0;
+      for (int h = s0 + part; h < s1; h += 8) {
+        const int mh = key(h);
+        rank += (mh > mg) || (mh == mg && h < g);
+      }
+      rank += __shfl_xor(rank, 1, 64);
+      rank += __shfl_xor(rank, 2, 64);
+      rank += __shfl_xor(rank, 4, 64);
+    } else {
+      rank = g - s0;
+    }
+    if (in && part == 0) {
+      if (MODE == kWgrad) {
+        l.entry[rank] = g;
+      } else {
+        l.entry[s0 + g] = g;                       // (2 s0 + (g - s0))
+        l.entry[s0 + s1 + rank] = kMaxG + g;       // (2 s0 + (s1 - s0) + rank)
+      }
+    }
+  }
+  __syncthreads();
+  if (tid < 64) {
+    const int ntc = cdiv(MODE == kFwd ? p.N : p.K, BN), n = list_entries<MODE>(p);
+    int carry = 0;
+    for (int base = 0; base < n; base += 64) {
+      const int q = base + tid;
+      int c = 0;
+      if (q < n) {
+        const int e = l.entry[q];
+        if (MODE == kWgrad) c = cdiv(p.N, BM) * ntc;
+        else c = (e < kMaxG ? rows(e) / BM : (rows(e - kMaxG) % BM ? 1 : 0)) * ntc;
+      }
+      int incl = c;
+#pragma unroll
+      for (int d = 1; d < 64; d <<= 1) {
+        const int v = __shfl_up(incl, d, 64);
+        if (tid >= d) incl += v;
+      }
+      if (q < n) l.first[q] = carry + incl - c;
+      carry += __shfl(incl, 63, 64);
+    }
+    if (tid == 0) l.first[n] = carry;
+  }
+  __syncthreads();
+}
+
+// Tile lt of the list (lanes ask for different ones); false past its end.  Inside an entry, columns of up to
+// four row tiles.
+template <int MODE>
+__device__ __forceinline__ bool locate(const GemmArgs& p, const TileList& l, int lt, Tile& t) {
+  const int n = list_entries<MODE>(p);
+  if (lt >= l.first[n]) return false;
+  int lo = 0, hi = n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (l.first[mid] <= lt) lo = mid; else hi = mid - 1;
+  }
+  const int e = l.entry[lo], r = lt - l.first[lo];
+  const bool partial = e >= kMaxG;
+  t.g = partial ? e - kMaxG : e;
+  t.row0 = l.offs[t.g];
+  t.e_rows = max(l.offs[t.g + 1] - t.row0, 0);
+  const int ntc = cdiv(MODE == kFwd ? p.N : p.K, BN);
+  const int mtc = MODE == kWgrad ? cdiv(p.N, BM) : t.e_rows / BM;
+  if (partial) {
+    t.mt = mtc;
+    t.nt = r;
+  } else {
+    const int span = kGroupM * ntc, fm = r / span * kGroupM, gsz = min(mtc - fm, kGroupM), q = r % span;
+    t.mt = fm + q % gsz;
+    t.nt = q / gsz;
+  }
+  return true;
+}
+
+// List position of workgroup position b: runs of `chunk` consecutive tiles go to one XCD (workgroups are
+// dispatched round-robin over the XCDs), so that tiles sharing operands share an L2.
+__device__ __forceinline__ int list_position(int b, int chunk) {
+  const int x = b % kXcd, q = b / kXcd;
+  return ((q / chunk) * kXcd + x) * chunk + (q % chunk);
+}
+
 // The tiles of a workgroup as one stream of stages.  Loads run two stages ahead of the multiplication, across
 // tiles too, so the pipeline is not emptied for an epilogue.
 template <int MODE, int TYPE>
@@ -254,8 +381,8 @@ struct Runner {
   char* lds;
   const Tile& mine;                                       // lane k: tile k of this workgroup
   const int w, wm, wn;
-  Operand<A_COLS> a;                                      // of the stage to load
-  Operand<B_COLS> b;
+  Operand<A_COLS, 32 * kWavesM> a;                                      // of the stage to load
+  Operand<B_COLS, 32> b;
   int lk = 0, lend = 0, lks = 0, lfull = 0, ltail = 0, lsteps = 0;   // its tile, stage and the tile's stages
 
   __device__ __forceinline__ Runner(const GemmArgs& p_, char* lds_, const Tile& mine_)
@@ -269,9 +396,9 @@ struct Runner {
     t.mt = get(mine.mt);
     t.nt = get(mine.nt);
     const int e_rows = get(mine.e_rows);
-    t.row0 = get((int)mine.row0);                         // (routed rows fit 31 bits)
-    t.e_row0 = t.row0 - (int64_t)t.mt * BM;
-    t.a_lim = MODE == kWgrad ? (int)min((int64_t)BM, p.N - (int64_t)t.mt * BM) : get(mine.rows);
+    t.e_row0 = get(mine.row0);
+    t.row0 = t.e_row0 + (int64_t)t.mt * BM;
+    t.a_lim = (int)min((int64_t)BM, (MODE == kWgrad ? p.N : e_rows) - (int64_t)t.mt * BM);
     t.b_lim = (int)min((int64_t)BN, (MODE == kFwd ? p.N : p.K) - (int64_t)t.nt * BN);
     const int64_t L = MODE == kFwd ? p.K : (MODE == kDgrad ? p.N : (int64_t)e_rows);
     t.nfull = (int)(L / TPS);
@@ -331,22 +458,22 @@ struct Runner {
     lds_barrier();
   }
 
-  // Tiles k0 .. k1 - 1, all with NI 32-row fragments of A per wave (64 NI rows).
-  template <int NI>
-  __device__ __forceinline__ void run(int k0, int k1) {
-    constexpr int WM = 32 * NI;
-    constexpr int LA = 2 * NI;                            // loads of A per wave and stage
+  // Tiles 0 .. count - 1 of the workgroup.
+  __device__ __forceinline__ void run(int count) {
     const int lane = fresh_lane();
-    a.place_frags(lane, WM * wm);
+    a.place_frags(lane, 32 * wm);
     b.place_frags(lane, WN * wn);
     v4i af[2][NI], bf[2][NJ];                      // fragments of the current and the next k-step
     vacc acc[NI][NJ];
+    int ni = NI;                                   // fragments of the wave with valid rows (and columns)
 
     // Group i of a k-step: row fragment i times the NJ column fragments.  The next k-step's reads are spread
     // over the groups, the fragments that its first group needs first.
-    auto multiply = [&](int cur, int i) {
+    auto multiply = [&](auto all, int cur, int i) {
+      if (decltype(all)::value || i < ni) {
 #pragma unroll
-      for (int j = 0; j < NJ; ++j) acc[i][j] = Acc<TYPE>::mfma(bf[cur][j], af[cur][i], acc[i][j]);
+        for (int j = 0; j < NJ; ++j) acc[i][j] = Acc<TYPE>::mfma(bf[cur][j], af[cur][i], acc[i][j]);
+      }
     };
     auto read = [&](int nxt, const char* sa, const char* sb, int nk, int from, int to) {
 #pragma unroll
@@ -357,30 +484,28 @@ struct Runner {
         }
     };
     // K-steps 0 .. 2 of a stage: multiply while k-step kk + 1 is read; load(i) issues a load or two in group i.
-    auto kstep = [&](auto load, int kk, const char* sa, const char* sb) {
+    auto kstep = [&](auto all, auto load, int kk, const char* sa, const char* sb) {
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
         read(1 - (kk & 1), sa, sb, kk + 1, i * (NJ + NI) / NI, (i + 1) * (NJ + NI) / NI);
         load(i);
-        multiply(kk & 1, i);
+        multiply(all, kk & 1, i);
         __builtin_amdgcn_sched_barrier(0);         // keep the reads and loads spread as written
       }
     };
     // K-step 3: while its first group multiplies, `landed` waits for the next stage and meets the other waves;
     // then the next stage's first fragments are read.
-    auto last_kstep = [&](auto load, auto landed, const char* na, const char* nb) {
-      constexpr int G = NI > 1 ? NI - 1 : 1;       // groups that read
+    auto last_kstep = [&](auto all, auto load, auto landed, const char* na, const char* nb) {
+      constexpr int G = NI - 1;                    // groups that read
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
-        const int g = NI > 1 ? i - 1 : 0;
-        if (NI == 1) landed();
-        if (g >= 0) {
-          read(0, na, nb, 0, g * (NJ + NI) / G, (g + 1) * (NJ + NI) / G);
-          load(g, G);
+        if (i > 0) {
+          read(0, na, nb, 0, (i - 1) * (NJ + NI) / G, i * (NJ + NI) / G);
+          load(i - 1, G);
         }
-        multiply(1, i);
+        multiply(all, 1, i);
         __builtin_amdgcn_sched_barrier(0);
-        if (NI > 1 && i == 0) landed();
+        if (i == 0) landed();
       }
     };
 
@@ -388,12 +513,13 @@ struct Runner {
     char *s0 = lds, *s1 = lds + kOp, *s2 = lds + 2 * kOp, *s3 = lds + 3 * kOp, *s4 = lds + 4 * kOp;
     // prologue: stage 0 of the stream and all but half of B of stage 1 on their way, stage 0 landed, its first
     // fragments read
-    constexpr int LB = MODE == kWgrad ? kLoads : kLoads / 2;   // of B's loads
+    // of B, in the last k-step (measured: with B in columns all of them, dgrad +3%, wgrad +5%; in rows half, +1%)
+    constexpr int LB = B_COLS ? kLoads : kLoads / 2;
+    constexpr int LA = kLoads;
     int lim1 = 0, lim2 = 0;                        // of a partial stage: the next to multiply, the one to load
-    lend = k1;
-    lk = k0;
-    while (MODE == kWgrad && lk < k1 && __builtin_amdgcn_readlane(mine.e_rows, lk) == 0) ++lk;
-    const bool any = lk < k1;                      // (wgrad: perhaps none of the experts has rows)
+    lend = count;
+    while (MODE == kWgrad && lk < count && __builtin_amdgcn_readlane(mine.e_rows, lk) == 0) ++lk;
+    const bool any = lk < count;                      // (wgrad: perhaps none of the experts has rows)
     if (any) {
       place(lk);
       const int lim0 = settle();
@@ -409,44 +535,52 @@ struct Runner {
       landed_barrier<0>();
     }
 
-    for (int k = k0; k < k1; ++k) {
+    // A stage.  Its loads go out evenly (about one per group: more at once and the address unit holds up the
+    // wave): the rest of B of the next stage, A of the stage two on into the slot that B of the stage before
+    // left, and, once this stage's last fragments are in registers everywhere and the next stage has landed
+    // (all but the loads of A just issued), the first part of B of the stage two on into this A's slot.
+    // ALL: every fragment of the wave has valid rows (the tests of `ni` cost a fifth of a stage).
+    auto stage = [&](auto all) {
+      kstep(all, [&](int i) { b.load(w, LB + (kLoads - LB) * i / NI, LB + (kLoads - LB) * (i + 1) / NI, s3); }, 0, s0, s1);
+      lim1 = lim2;
+      lim2 = advance();
+      kstep(all, [&](int i) { a.load(w, i, i + 1, s4); }, 1, s0, s1);
+      kstep(all, [&](int i) { a.load(w, NI + i, NI + i + 1, s4); }, 2, s0, s1);
+      last_kstep(all, [&](int g, int G) { b.load(w, LB * g / G, LB * (g + 1) / G, s0); },
+                 [&]() {
+                   landed_barrier<LA>();
+                   if (__builtin_expect(lim1 != 0, 0)) clear(LA, lim1, s2, s3);
+                 },
+                 s2, s3);
+      char *x0 = s0, *x1 = s1;                     // the next stage's slots
+      s0 = s2;
+      s1 = s3;
+      s2 = s4;
+      s3 = x0;
+      s4 = x1;
+    };
+    auto keep = [&]() {                            // (accumulators stay in accumulation registers)
+#pragma unroll
+      for (int i = 0; i < NI; ++i)
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) asm volatile("" : "+a"(acc[i][j]));
+    };
+
+    for (int k = 0; k < count; ++k) {
 #pragma unroll
       for (int i = 0; i < NI; ++i)
 #pragma unroll
         for (int j = 0; j < NJ; ++j)
 #pragma unroll
           for (int r = 0; r < 16; ++r) acc[i][j][r] = 0;
-      auto keep = [&]() {                          // (accumulators stay in accumulation registers)
-#pragma unroll
-        for (int i = 0; i < NI; ++i)
-#pragma unroll
-          for (int j = 0; j < NJ; ++j) asm volatile("" : "+a"(acc[i][j]));
-      };
       keep();
-      // A stage.  Its loads go out evenly (about one per group: more at once and the address unit holds up the
-      // wave): the rest of B of the next stage, A of the stage two on into the slot that B of the stage before
-      // left, and, once this stage's last fragments are in registers everywhere and the next stage has landed
-      // (all but the loads of A just issued), the first half of B of the stage two on into this A's slot.
-      for (int left = geometry(k).nsteps; left > 0; --left) {
-        kstep([&](int i) { b.load(w, LB + (kLoads - LB) * i / NI, LB + (kLoads - LB) * (i + 1) / NI, s3); }, 0, s0, s1);
-        lim1 = lim2;
-        lim2 = advance();
-        kstep([&](int i) { a.load(w, i, i + 1, s4); }, 1, s0, s1);
-        kstep([&](int i) { a.load(w, NI + i, NI + i + 1, s4); }, 2, s0, s1);
-        last_kstep([&](int g, int G) { b.load(w, LB * g / G, LB * (g + 1) / G, s0); },
-                   [&]() {
-                     landed_barrier<LA>();
-                     if (__builtin_expect(lim1 != 0, 0)) clear(LA, lim1, s2, s3);
-                   },
-                   s2, s3);
-        char *x0 = s0, *x1 = s1;                   // the next stage's slots
-        s0 = s2;
-        s1 = s3;
-        s2 = s4;
-        s3 = x0;
-        s4 = x1;
-      }
-
+      const Geometry now = geometry(k);
+      ni = WN * wn < now.b_lim ? min(NI, (now.a_lim - 32 * wm + 63) / 64) : 0;
+      int left = now.nsteps;
+      if (ni == NI)
+        for (; left > 0; --left) stage(std::true_type{});
+      keep();
+      for (; left > 0; --left) stage(std::false_type{});
       keep();
       // ---- epilogue, through the slot that the last stage's B left ----
       const Geometry t = geometry(k);
@@ -470,7 +604,8 @@ struct Runner {
         const float* sw = (const float*)p.sb + (int64_t)t.g * p.N + col0;
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
-          dma4((const uint8_t*)(sx + min(WM * wm + 64 * q + l, t.a_lim - 1)), reg + 4096 + 256 * q);
+          // (row 32 i + r of the wave is the tile's 32 (2 i + wm) + r)
+          dma4((const uint8_t*)(sx + min(64 * (2 * q + (l >> 5)) + 32 * wm + (l & 31), t.a_lim - 1)), reg + 4096 + 256 * q);
           dma4((const uint8_t*)(sw + min(WN * wn + 64 * q + l, t.b_lim - 1)), reg + 4608 + 256 * q);
         }
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
@@ -489,31 +624,13 @@ struct Runner {
           }
         };
         if (p.out_bf16)
-          store_rows<true, RB>(value, reg, out, row_bytes, WM * wm + 32 * i, WN * wn, t.b_lim);
+          store_rows<true, RB>(value, reg, out, row_bytes, 32 * (2 * i + wm), WN * wn, t.b_lim);
         else
-          store_rows<false, RB>(value, reg, out, row_bytes, WM * wm + 32 * i, WN * wn, t.b_lim);
+          store_rows<false, RB>(value, reg, out, row_bytes, 32 * (2 * i + wm), WN * wn, t.b_lim);
       }
       lds_barrier();                               // that slot is loaded into next
     }
     landed_barrier<0>();                           // (the loads past the end: LDS is another run's next)
-  }
-
-  // Tiles 0 .. count - 1, in runs of the same height.
-  __device__ __forceinline__ void run_all(int count) {
-    if constexpr (MODE == kWgrad) {
-      run<4>(0, count);
-    } else {
-      const int ni = mine.rows > 128 ? 4 : (mine.rows > 64 ? 2 : 1);
-      for (int k = 0; k < count;) {
-        const int n = __builtin_amdgcn_readlane(ni, k);
-        const uint64_t other = __ballot(ni != n) >> k;
-        const int end = min(count, other ? k + __builtin_ctzll(other) : count);
-        if (n == 4) run<4>(k, end);
-        else if (n == 2) run<2>(k, end);
-        else run<1>(k, end);
-        k = end;
-      }
-    }
   }
 };
 
@@ -522,25 +639,24 @@ struct Runner {
 template <int MODE, int TYPE>
 __global__ __launch_bounds__(NT, 1) void dense_grouped_gemm_kernel(GemmArgs p) {
   __shared__ __attribute__((aligned(16))) char lds[kLds];
-  constexpr bool kPartialLast = MODE != kWgrad;
   for (int64_t round = 0;; ++round) {
-    build_tile_list<MODE, false, BM, BN, NT, 32, kPartialLast>(p, lds);
+    const TileList list(lds);
+    build_list<MODE, TYPE == kInt8 ? 1 : 2>(p, list);
     // a short list is spread over the XCDs in equal runs
-    const int chunk = min(chunk_tiles(MODE), max(1, listed_tiles<MODE, kPartialLast>(p, lds) / kXcd));
+    const int chunk = min(chunk_tiles(MODE), max(1, list.first[list_entries<MODE>(p)] / kXcd));
     const int64_t b = blockIdx.x + gridDim.x * (64 * round + (threadIdx.x & 63));
     Tile mine;
-    const bool have = b <= 0x3FFFFFFF &&
-                      locate_tile<MODE, false, BM, BN, 32, kPartialLast>(p, lds, list_position((int)b, chunk), mine);
+    const bool have = b <= 0x3FFFFFFF && locate<MODE>(p, list, list_position((int)b, chunk), mine);
     const int count = __popcll(__ballot(have));    // positions grow with b: the first `count` lanes have a tile
     __syncthreads();                               // the list's LDS is reused for operands
     if (count == 0) return;
-    Runner<MODE, TYPE> r(p, lds, mine);
-    r.run_all(count);
+    Runner<MODE, TYPE>(p, lds, mine).run(count);
     if (count < 64) return;
+    __syncthreads();
   }
 }
 
-static_assert(5 * (kMaxG + 1) * 4 <= kLds, "scheduler scratch must fit in LDS");
+static_assert(kListBytes <= kLds, "the list must fit in LDS");
 
 }  // namespace
 

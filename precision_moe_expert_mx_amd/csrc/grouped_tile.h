@@ -24,7 +24,6 @@ struct GroupTile {
   int64_t col0;   // wgrad, gated forward: first column of the expert in the column-wise layout
   int nblk;       // wgrad: blocks (of the column-wise layout) in the expert's contraction
   int64_t col_end;  // gated forward: columns of the column-wise layout holding blocks (all experts)
-  int e_rows;       // rows of the expert
 };
 
 __device__ __forceinline__ int cdiv(int64_t a, int b) { return (int)((a + b - 1) / b); }
@@ -43,8 +42,8 @@ __device__ __forceinline__ int64_t uniform64(int64_t v) {
 // partial last row tiles after them, the ones with the most rows first (for G <= kLptMaxG), so that
 // the launch's last round holds the tiles with the fewest rows (cheaper where idle waves skip their
 // MFMAs).
-template <int MODE, bool CB, int TBM, int TBN, int TNT, int CBLK, bool PARTIAL_LAST>
-__device__ __forceinline__ void build_tile_list(const GemmArgs& p, char* lds) {
+template <int MODE, bool CB, int TBM, int TBN, int TNT, int CBLK, bool PARTIAL_LAST = false>
+__device__ bool decode_grouped_tile(const GemmArgs& p, char* lds, GroupTile& t) {
   int32_t* s_rs = (int32_t*)lds;             // clamped offsets [G+1]
   int32_t* s_pre = s_rs + (kMaxG + 1);       // tile prefix over the processing order [G+1]
   int32_t* s_cb = s_pre + (kMaxG + 1);       // wgrad: first 32-block of each expert [G+1]
@@ -123,28 +122,12 @@ __device__ __forceinline__ void build_tile_list(const GemmArgs& p, char* lds) {
     if (lane == 0) (wv == 0 ? s_pre : (cb_wave ? s_cb : s_pre2))[G] = carry;
   }
   __syncthreads();
-}
 
-// Tiles of the list that build_tile_list left in LDS.
-template <int MODE, bool PARTIAL_LAST>
-__device__ __forceinline__ int listed_tiles(const GemmArgs& p, const char* lds) {
-  const int32_t* s_pre = (const int32_t*)lds + (kMaxG + 1);
-  const int32_t* s_pre2 = (const int32_t*)lds + 3 * (kMaxG + 1) + kMaxG;
-  return s_pre[p.G] + (PARTIAL_LAST && MODE != kWgrad ? s_pre2[p.G] : 0);
-}
-
-// Tile lt_all of the list (false past its end).  Lanes may ask for different ones.
-template <int MODE, bool CB, int TBM, int TBN, int CBLK, bool PARTIAL_LAST>
-__device__ __forceinline__ bool locate_tile(const GemmArgs& p, const char* lds, int lt_all, GroupTile& t) {
-  const int32_t* s_rs = (const int32_t*)lds;
-  const int32_t* s_pre = s_rs + (kMaxG + 1);
-  const int32_t* s_cb = s_pre + (kMaxG + 1);
-  const int32_t* s_ord = s_cb + (kMaxG + 1);
-  const int32_t* s_pre2 = s_ord + kMaxG;
-  constexpr bool kSplit = PARTIAL_LAST && MODE != kWgrad;
-  const int G = p.G;
-  const int ntc = cdiv(MODE == kFwd ? p.N : p.K, TBN);
-  const int mtc_w = cdiv(p.N, TBM);
+  // workgroup -> logical tile: chunks of kChunk consecutive tiles per XCD visit
+  constexpr int kChunk = chunk_tiles(MODE);
+  const int b = blockIdx.x;
+  const int x = b % kXcd, q = b / kXcd;
+  const int lt_all = ((q / kChunk) * kXcd + x) * kChunk + (q % kChunk);
   const int n_full = s_pre[G];
   if (lt_all >= n_full + (kSplit ? s_pre2[G] : 0)) return false;
   int g, mt, nt, mtc;
@@ -186,7 +169,6 @@ __device__ __forceinline__ bool locate_tile(const GemmArgs& p, const char* lds, 
   t.rows = (int)min((int64_t)TBM, (int64_t)s_rs[g + 1] - t.row0);
   t.col0 = CB ? CBLK * (int64_t)s_cb[g] : 0;
   t.col_end = CB ? CBLK * (int64_t)s_cb[G] : 0;
-  t.e_rows = m_g;
   t.nblk = cdiv(m_g, CBLK);
   if (MODE == kWgrad) {
     // offsets that are not monotone could place an expert past the leading dimension: clip
@@ -195,20 +177,6 @@ __device__ __forceinline__ bool locate_tile(const GemmArgs& p, const char* lds, 
     if (t.nblk > room) t.nblk = (int)room;
   }
   return true;
-}
-
-// List position of tile b of the launch: runs of `chunk` consecutive tiles go to one XCD (workgroups are
-// dispatched round-robin over the XCDs).
-__device__ __forceinline__ int list_position(int b, int chunk) {
-  const int x = b % kXcd, q = b / kXcd;
-  return ((q / chunk) * kXcd + x) * chunk + (q % chunk);
-}
-
-// This workgroup's tile, one tile per workgroup.
-template <int MODE, bool CB, int TBM, int TBN, int TNT, int CBLK, bool PARTIAL_LAST = false>
-__device__ bool decode_grouped_tile(const GemmArgs& p, char* lds, GroupTile& t) {
-  build_tile_list<MODE, CB, TBM, TBN, TNT, CBLK, PARTIAL_LAST>(p, lds);
-  return locate_tile<MODE, CB, TBM, TBN, CBLK, PARTIAL_LAST>(p, lds, list_position(blockIdx.x, chunk_tiles(MODE)), t);
 }
 
 // Store a wave's accumulator tile as whole row pieces.  The tile is NI x NJ fragments of 32 x 32 in
