@@ -613,35 +613,37 @@ def mxmoe_check_offsets(offs, M: int, stream=None) -> None:
 
 
 # ---------------------------------------------------------------- plain operands (bf16, int8)
-class _Launch:
-    """The current device and stream of a launch on the tensors' device (they may live on another device
-    than the current one): `with _Launch(stream, x, ...) as handle`."""
-
-    def __init__(self, stream, *tensors):
-        devs = {t.device for t in tensors if t is not None}
-        if len(devs) != 1 or next(iter(devs)).type != "cuda":
-            raise ValueError(f"tensors must be on one GPU, got {sorted(str(d) for d in devs)}")
-        self.stream, self.index, self.guard = stream, next(iter(devs)).index, None
-
-    def __enter__(self):
-        torch = _torch()
-        if torch.cuda.current_device() != self.index:
-            self.guard = torch.cuda.device(self.index)
-            self.guard.__enter__()
-        return _stream_handle(self.stream)
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
-        return False
+def _run(name, tensors, stream, *args):
+    """Launch entry point `name` on the tensors' device (they may live on another one than the current) and on
+    that device's current stream unless one is given; the stream is the last argument."""
+    torch = _torch()
+    dev = tensors[0].device
+    if dev.type != "cuda":
+        raise ValueError("tensors must be on the GPU")
+    for t in tensors:
+        if t.device != dev:
+            raise ValueError(f"tensors must be on one GPU, got {dev} and {t.device}")
+    if torch.cuda.current_device() != dev.index:
+        with torch.cuda.device(dev):
+            return _run(name, tensors, stream, *args)
+    if stream is None:
+        stream = torch._C._cuda_getCurrentRawStream(dev.index)
+    elif not isinstance(stream, int):
+        stream = stream.cuda_stream
+    status = getattr(lib(), name)(*args, stream)
+    if status:
+        _check(name, status)
 
 
 def _want(name, t, dtypes, shape):
-    """A tensor argument has one of `dtypes` and the shape (None: any size), or a clear error says so."""
+    """A tensor argument is contiguous, of one of `dtypes` and of the shape (None: any size), or a clear error
+    says what it is not."""
     if t.dtype not in dtypes:
         raise TypeError(f"{name}: expected {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
-    if t.dim() != len(shape) or any(w is not None and w != n for w, n in zip(shape, t.shape)):
+    if t.shape != shape and (t.dim() != len(shape) or any(w is not None and w != n for w, n in zip(shape, t.shape))):
         raise ValueError(f"{name}: expected shape {tuple('any' if w is None else w for w in shape)}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: tensors must be contiguous")
 
 
 def _bf16_types():
@@ -656,6 +658,12 @@ def _groups(offs):
     return offs.numel() - 1
 
 
+def _rows(name, x, dtypes):
+    """The shape of a matrix argument."""
+    _want(name, x, dtypes, (None, None))
+    return x.shape
+
+
 def _weights(name, w, dtypes, G, N, K):
     """Expert weights [G*N, K], or the same as [G, N, K]."""
     _want(name, w, dtypes, (G, N, K) if w.dim() == 3 else (G * N, K))
@@ -667,88 +675,83 @@ def _bf16_gemm(name, a, b, offs, shape, dims, out_dtype, out, stream):
         out = _empty(shape, tdt, a)
     else:
         _want("output", out, (tdt,), shape)
-    G, M, N, K = dims
-    with _Launch(stream, a, b, offs, out) as h:
-        _check(name, getattr(lib(), name)(_ptr(a), _ptr(b), _ptr(offs), G, M, N, K, _ptr(out), cdt, h))
+    _run(name, (a, b, offs, out), stream, a.data_ptr(), b.data_ptr(), offs.data_ptr(), *dims, out.data_ptr(), cdt)
     return out
 
 
 def bf16_grouped_gemm_fwd(x, w, offs, N: int, out_dtype: str = "f32", y=None, stream=None):
     """Y [M, N] = per-expert X_g W_g^T of bf16 tensors: x [M, K], w [G*N, K] (or [G, N, K]), offs int32 [G+1].
     N % 8 == 0, K % 8 == 0."""
+    bf16 = _bf16_types()
     G = _groups(offs)
-    _want("x", x, _bf16_types(), (None, None))
-    M, K = x.shape
-    _weights("w", w, _bf16_types(), G, N, K)
+    M, K = _rows("x", x, bf16)
+    _weights("w", w, bf16, G, N, K)
     return _bf16_gemm("bf16_grouped_gemm_fwd", x, w, offs, (M, N), (G, M, N, K), out_dtype, y, stream)
 
 
 def bf16_grouped_gemm_dgrad(dy, w, offs, K: int, out_dtype: str = "f32", dx=None, stream=None):
     """dX [M, K] = per-expert dY_g W_g of bf16 tensors: dy [M, N], w [G*N, K] (or [G, N, K]), the forward's
     weights as they are."""
+    bf16 = _bf16_types()
     G = _groups(offs)
-    _want("dy", dy, _bf16_types(), (None, None))
-    M, N = dy.shape
-    _weights("w", w, _bf16_types(), G, N, K)
+    M, N = _rows("dy", dy, bf16)
+    _weights("w", w, bf16, G, N, K)
     return _bf16_gemm("bf16_grouped_gemm_dgrad", dy, w, offs, (M, K), (G, M, N, K), out_dtype, dx, stream)
 
 
 def bf16_grouped_gemm_wgrad(dy, x, offs, out_dtype: str = "f32", dw=None, stream=None):
     """dW [G, N, K] = per-expert dY_g^T X_g of bf16 tensors: dy [M, N], x [M, K].  Zero for an expert without
     rows."""
+    bf16 = _bf16_types()
     G = _groups(offs)
-    _want("dy", dy, _bf16_types(), (None, None))
-    M, N = dy.shape
-    _want("x", x, _bf16_types(), (M, None))
+    M, N = _rows("dy", dy, bf16)
+    _want("x", x, bf16, (M, None))
     K = x.shape[1]
     return _bf16_gemm("bf16_grouped_gemm_wgrad", dy, x, offs, (G, N, K), (G, M, N, K), out_dtype, dw, stream)
 
 
-def _int8_rowwise(name, x, C, q, s, stream):
+def _int8_rowwise(name, x, R, C, q, s, stream):
     torch = _torch()
-    R = x.shape[0]
     q = _empty((R, C), torch.int8, x) if q is None else q
     s = _empty((R,), torch.float32, x) if s is None else s
     _want("q", q, (torch.int8,), (R, C))
     _want("s", s, (torch.float32,), (R,))
-    with _Launch(stream, x, q, s) as h:
-        _check(name, getattr(lib(), name)(_ptr(x), R, C, _ptr(q), _ptr(s), h))
+    _run(name, (x, q, s), stream, x.data_ptr(), R, C, q.data_ptr(), s.data_ptr())
     return q, s
 
 
 def int8_quantize_rowwise(x, q=None, s=None, stream=None):
     """x bf16 [R, C] -> (q int8 [R, C], s f32 [R]): s = amax / 127 of the row, q = nearest of 127 x / amax
     (tokens of activations, output channels of weights).  C % 8 == 0."""
-    _want("x", x, _bf16_types(), (None, None))
-    return _int8_rowwise("int8_quantize_rowwise", x, x.shape[1], q, s, stream)
+    R, C = _rows("x", x, _bf16_types())
+    return _int8_rowwise("int8_quantize_rowwise", x, R, C, q, s, stream)
 
 
 def int8_quantize_swiglu_rowwise(y, q=None, s=None, stream=None):
     """y bf16 [R, 2C] (gate columns, then up columns) -> (q int8 [R, C], s f32 [R]) of silu(gate) * up."""
-    _want("y", y, _bf16_types(), (None, None))
-    if y.shape[1] % 2:
-        raise ValueError(f"y: expected gate and up columns, got {y.shape[1]}")
-    return _int8_rowwise("int8_quantize_swiglu_rowwise", y, y.shape[1] // 2, q, s, stream)
+    R, C2 = _rows("y", y, _bf16_types())
+    if C2 % 2:
+        raise ValueError(f"y: expected gate and up columns, got {C2}")
+    return _int8_rowwise("int8_quantize_swiglu_rowwise", y, R, C2 // 2, q, s, stream)
 
 
 def int8_grouped_gemm_fwd(qx, sx, qw, sw, offs, N: int, out_dtype: str = "f32", y=None, stream=None):
     """Y [M, N] = per-expert qx_g qw_g^T (exact) times the token's and the channel's scale: qx int8 [M, K],
     sx f32 [M], qw int8 [G*N, K] (or [G, N, K]), sw f32 [G*N] (or [G, N]).  N % 8 == 0, K % 16 == 0."""
     torch = _torch()
+    i8, f32 = (torch.int8,), (torch.float32,)
     G = _groups(offs)
-    _want("qx", qx, (torch.int8,), (None, None))
-    M, K = qx.shape
-    _want("sx", sx, (torch.float32,), (M,))
-    _weights("qw", qw, (torch.int8,), G, N, K)
-    _want("sw", sw, (torch.float32,), (G, N) if sw.dim() == 2 else (G * N,))
+    M, K = _rows("qx", qx, i8)
+    _want("sx", sx, f32, (M,))
+    _weights("qw", qw, i8, G, N, K)
+    _want("sw", sw, f32, (G, N) if sw.dim() == 2 else (G * N,))
     tdt, cdt = _out_dtype(out_dtype)
     if y is None:
         y = _empty((M, N), tdt, qx)
     else:
         _want("y", y, (tdt,), (M, N))
-    with _Launch(stream, qx, sx, qw, sw, offs, y) as h:
-        _check("int8_grouped_gemm_fwd", lib().int8_grouped_gemm_fwd(
-            _ptr(qx), _ptr(sx), _ptr(qw), _ptr(sw), _ptr(offs), G, M, N, K, _ptr(y), cdt, h))
+    _run("int8_grouped_gemm_fwd", (qx, sx, qw, sw, offs, y), stream, qx.data_ptr(), sx.data_ptr(), qw.data_ptr(),
+         sw.data_ptr(), offs.data_ptr(), G, M, N, K, y.data_ptr(), cdt)
     return y
 
 
@@ -853,9 +856,8 @@ def adamw_step(table, step, lr, beta1: float = 0.9, beta2: float = 0.999, eps: f
         if t.dtype != dt or t.numel() != 1:
             raise TypeError(f"{name}: expected one {dt} on the GPU, got {t.dtype} of {t.numel()}")
         setattr(hyper, field, _ptr(t))
-    with _Launch(stream, table.like, *[t for _, t, _, _ in scalars]) as h:
-        _check("adamw_step", lib().adamw_step(ctypes.addressof(table.array), len(table.array), table.grad_dtype,
-                                              table.bits, ctypes.addressof(hyper), h))
+    _run("adamw_step", (table.like, *[t for _, t, _, _ in scalars]), stream, ctypes.addressof(table.array),
+         len(table.array), table.grad_dtype, table.bits, ctypes.addressof(hyper))
 
 
 def adamw_dequantize(q, s, moment: str, out_dtype: str = "f32", out=None, stream=None):
@@ -871,7 +873,6 @@ def adamw_dequantize(q, s, moment: str, out_dtype: str = "f32", out=None, stream
         out = _empty(q.shape, tdt, q)
     else:
         _want("out", out, (tdt,), q.shape)
-    with _Launch(stream, q, s, out) as h:
-        _check("adamw_dequantize", lib().adamw_dequantize(_ptr(q), _ptr(s), q.numel(), int(moment == "exp_avg_sq"),
-                                                          _ptr(out), cdt, h))
+    _run("adamw_dequantize", (q, s, out), stream, q.data_ptr(), s.data_ptr(), q.numel(), int(moment == "exp_avg_sq"),
+         out.data_ptr(), cdt)
     return out

@@ -800,6 +800,7 @@ static mxmoe_status dense_common(int mode, bool int8, const char* fn, const void
     TRY(check_ptr(fn, "B scales", sb, 4));
   }
   TRY(check_device());
+  if (mode == kFwd && few_rows(p)) return launched(launch_few_rows_gemm(int8, p, (hipStream_t)stream), fn);
   return launched(launch_dense_gemm(mode, int8, p, (hipStream_t)stream), fn);
 }
 

@@ -257,6 +257,9 @@ hipError_t launch_mx_gemm(int mode, const GemmArgs& a, hipStream_t st);
 hipError_t launch_bw_gemm(int mode, const GemmArgs& a, hipStream_t st);
 // plain operands: bf16 (all modes; leading dimensions in bytes), or int8 forward (sa, sb: fp32 row scales)
 hipError_t launch_dense_gemm(int mode, bool int8, const GemmArgs& a, hipStream_t st);
+// the same forward for few rows per expert, and whether a call is of that kind
+bool few_rows(const GemmArgs& a);
+hipError_t launch_few_rows_gemm(bool int8, const GemmArgs& a, hipStream_t st);
 
 // x [R, C] (gated: gate|up [R, 2C]) -> codes [R, C] and row scales [R]
 hipError_t launch_int8_rowwise(const uint16_t* x, int64_t R, int64_t C, bool gated, int8_t* q, float* s,

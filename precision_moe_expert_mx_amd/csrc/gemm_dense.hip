@@ -674,7 +674,8 @@ hipError_t launch_dense_gemm(int mode, bool int8, const GemmArgs& p, hipStream_t
   hipError_t e = hipGetDevice(&dev);
   if (e == hipSuccess) e = hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev);
   if (e != hipSuccess) return e;
-  const int64_t grid = max(cus, 1);
+  // (positions of a list of T tiles lie below 2 T + 8, see list_position and its chunk)
+  const int64_t grid = min((int64_t)max(cus, 1), 2 * tiles + 8);
   const dim3 g((unsigned)grid);
   if (int8) hipLaunchKernelGGL((dense_grouped_gemm_kernel<kFwd, kInt8>), g, dim3(NT), 0, st, p);
   else if (mode == kFwd) hipLaunchKernelGGL((dense_grouped_gemm_kernel<kFwd, kBf16>), g, dim3(NT), 0, st, p);
