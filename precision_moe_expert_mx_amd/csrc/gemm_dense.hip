@@ -17,7 +17,14 @@
 // requests and ran 10% slower at the same power).  LDS holds five operand stages of 32 KiB: A and B of two
 // stages and the next A, filled by direct-to-LDS loads that are never drained: a wave waits only until its
 // share of the next stage has landed (a counted vmcnt), and reads the fragments of a k-step while it
-// multiplies the one before, across stages too.
+// multiplies the one before, across stages and tiles too: a workgroup per CU runs its tiles as one stream of
+// stages.  Few tiles are made 128 x 128 (five stages in LDS), so that more CUs have one.
+//
+// Bound: the matrix cores, and on random operands the chip's power, which sets their clock: of a stage's 2048
+// matrix clocks the loop takes 2300-2400 and a tile 13000 more (measured with GRBM_GUI_ACTIVE at K 1280 .. 10240),
+// at 1.7-1.9 GHz.  One product of 16384 x 16384 x 5120: forward 1400-1470 TFLOP/s, dgrad 1360-1400, wgrad
+// 1270-1390, int8 2500-2600 (the range is that of different cards).
+//
 // An operand contiguous along t is staged as 256 rows of 128 bytes; one with t as its rows as 64 rows of 256
 // columns (512 bytes), which fragments are read from with the transposing LDS read (ds_read_b64_tr_b16: 16
 // lanes read 4 rows x 16 columns and each gets one column's 4 values), so no operand is ever transposed in
@@ -36,21 +43,25 @@ struct Tile {
   int e_rows;      // rows of the expert
 };
 
-constexpr int BM = 256, BN = 256;                // A / B rows (output rows / columns) per tile
 constexpr int BKB = 128;                         // contraction bytes per stage
 constexpr int KS = BKB / 32;                     // k-steps (matrix instructions deep) per stage
 constexpr int kWavesM = 2, kWavesN = 2;
 constexpr int kWaves = kWavesM * kWavesN;
 constexpr int NT = 64 * kWaves;
-constexpr int WN = BN / kWavesN;                 // output columns per wave
-constexpr int NI = BM / kWavesM / 32;            // row fragments per wave: fragment i is rows 32 (kWavesM i + wm) .. + 31
-constexpr int NJ = WN / 32;                      // column fragments per wave, consecutive
-constexpr int kOp = BM * BKB;                    // bytes of one operand's stage (both layouts): 32 KiB
-constexpr int kSlots = 5;                        // operand stages in LDS: A p at slot 2p % 5, B p at (2p + 1) % 5
-constexpr int kLoads = kOp / 1024 / kWaves;      // 1 KiB loads per wave, stage and (whole) operand
-constexpr int kLds = kSlots * kOp;
-static_assert(BM == BN && kLoads == 8, "one stage size for both operands");
-static_assert(kWaves * 64 * (128 * NJ + 16) <= kLds, "staged epilogue must fit in LDS");
+
+// Tile sizes: TD row and TD column fragments of 32 per wave, 256 x 256 (TD 4) or 128 x 128 (TD 2) outputs.
+template <int TD>
+struct Shape {
+  static constexpr int BM = 32 * kWavesM * TD, BN = 32 * kWavesN * TD;   // output rows / columns per tile
+  static constexpr int WN = 32 * TD;             // output columns per wave, consecutive
+  static constexpr int kOp = BM * BKB;           // bytes of one operand's stage (both layouts)
+  static constexpr int kLoads = kOp / 1024 / kWaves;   // 1 KiB loads per wave, stage and operand
+  // operand stages in LDS: A p at slot 2p % kSlots, B p after it.  256: two stages and the next A (160 KiB);
+  // 128: five stages
+  static constexpr int kSlots = TD == 4 ? 5 : 10;
+  static constexpr int kLds = kSlots * kOp;
+  static_assert(BM == BN, "one stage size for both operands");
+};
 
 typedef float v16f __attribute__((ext_vector_type(16)));
 typedef int v16i __attribute__((ext_vector_type(16)));
@@ -62,16 +73,19 @@ enum DenseType { kBf16 = 0, kInt8 = 1 };
 // Staged rows of 128 bytes, two to the 256 bytes that 16 lanes read at once: 16-byte chunk c of row r at
 // position c ^ ((r >> 1) & 7), so that 16 consecutive rows' chunks hit distinct banks.
 __device__ __forceinline__ int row_swz(int r) { return (r >> 1) & 7; }
-// Staged contraction rows of 512 bytes: 64-byte piece c of row t at piece c ^ col_swz(t).  One transposing
-// read takes 64 bytes of rows t .. t + 3 and t + 8 .. t + 11: eight different pieces of the 512 bytes.
-__device__ __forceinline__ int col_swz(int t) { return (t & 3) | ((t >> 1) & 4); }
+// Staged contraction rows of 128 TD bytes: 64-byte piece c of row t at piece c ^ col_swz(t).  One transposing
+// read takes 64 bytes of rows t .. t + 3 and t + 8 .. t + 11: different pieces of the 512 bytes (256: of each half).
+template <int TD>
+__device__ __forceinline__ int col_swz(int t) { return ((t & 3) | ((t >> 1) & 4)) & (2 * TD - 1); }
 
 // One operand of a wave: its share of a stage's loads (kLoads of 1 KiB, fewer of A in a tile of fewer
 // rows; load j of wave w fills the stage's 1 KiB piece kWaves j + w) as 32-bit lane offsets from a
 // wave-uniform base that moves by `step` bytes per stage, and its fragments' LDS offsets in a stage.
-template <bool COLS_, int STRIDE>               // STRIDE: rows (columns) from one fragment to the next
+template <bool COLS_, int STRIDE, int TD>       // STRIDE: rows (columns) from one fragment to the next
 struct Operand {
   static constexpr bool COLS = COLS_;
+  static constexpr int kLoads = Shape<TD>::kLoads;
+  static constexpr int kRow = 128 * TD;          // COLS: bytes of a staged contraction row
   uint32_t off[kLoads];
   uint32_t frag[4];                              // by fragment (COLS) or by k-step
   const uint8_t* base;                           // of the next stage to load
@@ -87,8 +101,8 @@ struct Operand {
         const int r = 8 * (kWaves * j + w) + (lane >> 3);
         off[j] = (uint32_t)(min(r, lim - 1) * ld) + 16 * ((lane & 7) ^ row_swz(r));
       } else {
-        const int r = 2 * (kWaves * j + w) + (lane >> 5);
-        const int c = (lane & 31) ^ (col_swz(r) << 2);     // 16-byte chunk: eight columns
+        const int r = 1024 / kRow * (kWaves * j + w) + lane / (kRow / 16);
+        const int c = lane % (kRow / 16) ^ (col_swz<TD>(r) << 2);     // 16-byte chunk: eight columns
         off[j] = (uint32_t)(r * ld) + 2 * min(8 * c, lim - 8);
       }
     }
@@ -105,7 +119,7 @@ struct Operand {
   // Position along the contraction of this lane's piece of load j (bytes of a row, or rows).
   static __device__ __forceinline__ int at(int lane, int w, int j) {
     const int p = kWaves * j + w;
-    return COLS ? 2 * p + (lane >> 5) : 16 * ((lane & 7) ^ row_swz(8 * p + (lane >> 3)));
+    return COLS ? 1024 / kRow * p + lane / (kRow / 16) : 16 * ((lane & 7) ^ row_swz(8 * p + (lane >> 3)));
   }
   // The stage to load is the contraction's last, with `lim` bytes (COLS: rows): lanes whose piece lies past
   // its end load the row's first piece (the column's first row) instead, and zero() clears it in LDS once the
@@ -134,8 +148,8 @@ struct Operand {
       const int i16 = lane & 15;
       const int t = 8 * (lane >> 5) + (i16 >> 2);
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        frag[i] = t * 512 + ((2 * (r0 + STRIDE * i + (lane & 16) + 4 * (i16 & 3))) ^ (col_swz(t) << 6));
+      for (int i = 0; i < TD; ++i)
+        frag[i] = t * kRow + ((2 * (r0 + STRIDE * i + (lane & 16) + 4 * (i16 & 3))) ^ (col_swz<TD>(t) << 6));
     }
   }
   // Matrix instruction's fragment i (32 rows or columns) of k-step kk of the stage at st: lane l holds row
@@ -149,7 +163,7 @@ struct Operand {
 #pragma unroll
       for (int q = 0; q < 2; ++q)
         v[q] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-            (__attribute__((address_space(3))) v4s*)(st + frag[i] + (16 * kk + 4 * q) * 512));
+            (__attribute__((address_space(3))) v4s*)(st + frag[i] + (16 * kk + 4 * q) * kRow));
       return __builtin_bit_cast(v4i, __builtin_shufflevector(v[0], v[1], 0, 1, 2, 3, 4, 5, 6, 7));
     }
   }
@@ -194,7 +208,7 @@ __device__ __forceinline__ int fresh_lane() {
 // c ^ (r mod chunks); a bf16 chunk's two 8-byte halves (from lanes 0..31 and 32..63) change places in rows
 // 16..31, so that the lanes of a write spread over the banks.  `out` is the buffer of the tile's valid rows
 // from its first column on (row_bytes apart); columns at or past col_lim are not written.
-template <bool BF16, int RB, typename Value>
+template <bool BF16, int RB, int NJ, typename Value>
 __device__ __forceinline__ void store_rows(Value value, char* reg, __amdgpu_buffer_rsrc_t out, uint32_t row_bytes,
                                            int r0, int c0, int col_lim) {
   constexpr int kCols = BF16 ? RB / 2 : RB / 4;           // columns per pass
@@ -262,8 +276,9 @@ constexpr int kListBytes = (kMaxG + 1 + 2 * kMaxG + 2 * kMaxG + 1) * 4;
 template <int MODE>
 __device__ __forceinline__ int list_entries(const GemmArgs& p) { return MODE == kWgrad ? p.G : 2 * p.G; }
 
-template <int MODE, int ES>
+template <int MODE, int ES, int TD>
 __device__ __forceinline__ void build_list(const GemmArgs& p, const TileList& l) {
+  constexpr int BM = Shape<TD>::BM, BN = Shape<TD>::BN;
   const int tid = threadIdx.x, G = p.G;
   for (int g = tid; g <= G; g += NT) l.offs[g] = (int32_t)clamp_off(p.offs[g], p.M);
   __syncthreads();
@@ -327,8 +342,9 @@ __device__ __forceinline__ void build_list(const GemmArgs& p, const TileList& l)
 
 // Tile lt of the list (lanes ask for different ones); false past its end.  Inside an entry, columns of up to
 // four row tiles.
-template <int MODE>
+template <int MODE, int TD>
 __device__ __forceinline__ bool locate(const GemmArgs& p, const TileList& l, int lt, Tile& t) {
+  constexpr int BM = Shape<TD>::BM, BN = Shape<TD>::BN;
   const int n = list_entries<MODE>(p);
   if (lt >= l.first[n]) return false;
   int lo = 0, hi = n - 1;
@@ -363,8 +379,11 @@ __device__ __forceinline__ int list_position(int b, int chunk) {
 
 // The tiles of a workgroup as one stream of stages.  Loads run two stages ahead of the multiplication, across
 // tiles too, so the pipeline is not emptied for an epilogue.
-template <int MODE, int TYPE>
+template <int MODE, int TYPE, int TD>
 struct Runner {
+  typedef Shape<TD> S;
+  static constexpr int BM = S::BM, BN = S::BN, WN = S::WN, kOp = S::kOp, kLoads = S::kLoads, kSlots = S::kSlots;
+  static constexpr int NI = TD, NJ = TD;                  // row / column fragments per wave
   static constexpr bool A_COLS = MODE == kWgrad, B_COLS = MODE != kFwd;
   static constexpr int ES = TYPE == kInt8 ? 1 : 2;        // bytes per element
   static constexpr int TPS = BKB / ES;                    // contraction elements per stage
@@ -381,8 +400,8 @@ struct Runner {
   char* lds;
   const Tile& mine;                                       // lane k: tile k of this workgroup
   const int w, wm, wn;
-  Operand<A_COLS, 32 * kWavesM> a;                                      // of the stage to load
-  Operand<B_COLS, 32> b;
+  Operand<A_COLS, 32 * kWavesM, TD> a;                                      // of the stage to load
+  Operand<B_COLS, 32, TD> b;
   int lk = 0, lend = 0, lks = 0, lfull = 0, ltail = 0, lsteps = 0;   // its tile, stage and the tile's stages
 
   __device__ __forceinline__ Runner(const GemmArgs& p_, char* lds_, const Tile& mine_)
@@ -451,9 +470,9 @@ struct Runner {
     return __builtin_expect(lks >= lfull, 0) ? settle() : 0;
   }
   // A partial stage has landed everywhere: clear what lies past its end, before anyone reads it.
-  __device__ __forceinline__ void clear(int la, int lim, char* sa, char* sb) {
+  __device__ __forceinline__ void clear(int lim, char* sa, char* sb) {
     const int lane = fresh_lane();
-    a.zero(lane, w, la, A_COLS ? lim : lim * ES, sa);
+    a.zero(lane, w, kLoads, A_COLS ? lim : lim * ES, sa);
     b.zero(lane, w, kLoads, B_COLS ? lim : lim * ES, sb);
     lds_barrier();
   }
@@ -509,55 +528,93 @@ struct Runner {
       }
     };
 
-    // slots of this stage's A and B, the next one's, and the one after's A
-    char *s0 = lds, *s1 = lds + kOp, *s2 = lds + 2 * kOp, *s3 = lds + 3 * kOp, *s4 = lds + 4 * kOp;
-    // prologue: stage 0 of the stream and all but half of B of stage 1 on their way, stage 0 landed, its first
-    // fragments read
-    // of B, in the last k-step (measured: with B in columns all of them, dgrad +3%, wgrad +5%; in rows half, +1%)
-    constexpr int LB = B_COLS ? kLoads : kLoads / 2;
+    // slots of this stage's A and B, the next one's, and of the loads (256: A of the stage two on; 128: of the
+    // stage four on)
+    char *s0 = lds, *s1 = lds + kOp, *s2 = lds + 2 * kOp, *s3 = lds + 3 * kOp, *s4 = lds + (kSlots - (TD == 4 ? 1 : 2)) * kOp;
+    // prologue: the first stages of the stream on their way (256: 0 and, but for a part of B, 1; 128: 0 .. 3),
+    // stage 0 landed, its first fragments read
+    // Part of B that goes out in the last k-step (256; measured: with B in columns all of it, dgrad +3%,
+    // wgrad +5%; in rows half, +1%)
     constexpr int LA = kLoads;
-    int lim1 = 0, lim2 = 0;                        // of a partial stage: the next to multiply, the one to load
+    constexpr int LB = B_COLS ? kLoads : kLoads / 2;
+    int lim1 = 0, lim2 = 0, lim3 = 0, lim4 = 0;    // of a partial stage: the next to multiply, and those after it
     lend = count;
     while (MODE == kWgrad && lk < count && __builtin_amdgcn_readlane(mine.e_rows, lk) == 0) ++lk;
-    const bool any = lk < count;                      // (wgrad: perhaps none of the experts has rows)
+    const bool any = lk < count;                   // (wgrad: perhaps none of the experts has rows)
     if (any) {
       place(lk);
       const int lim0 = settle();
       a.load(w, 0, LA, s0);
       b.load(w, 0, kLoads, s1);
-      lim2 = advance();
-      a.load(w, 0, LA, s2);
-      b.load(w, 0, LB, s3);
-      landed_barrier<LA + LB>();
-      if (lim0) clear(LA, lim0, s0, s1);
+      if constexpr (TD == 4) {
+        lim2 = advance();
+        a.load(w, 0, LA, s2);
+        b.load(w, 0, LB, s3);
+        landed_barrier<LA + LB>();
+      } else {
+        lim2 = advance();
+        a.load(w, 0, LA, s2);
+        b.load(w, 0, kLoads, s3);
+        lim3 = advance();
+        a.load(w, 0, LA, lds + 4 * kOp);
+        b.load(w, 0, kLoads, lds + 5 * kOp);
+        lim4 = advance();
+        a.load(w, 0, LA, lds + 6 * kOp);
+        b.load(w, 0, kLoads, lds + 7 * kOp);
+        landed_barrier<3 * 2 * kLoads>();
+      }
+      if (lim0) clear(lim0, s0, s1);
       read(0, s0, s1, 0, 0, NJ + NI);
     } else {
       landed_barrier<0>();
     }
 
     // A stage.  Its loads go out evenly (about one per group: more at once and the address unit holds up the
-    // wave): the rest of B of the next stage, A of the stage two on into the slot that B of the stage before
+    // wave).  256: the rest of B of the next stage, A of the stage two on into the slot that B of the stage before
     // left, and, once this stage's last fragments are in registers everywhere and the next stage has landed
-    // (all but the loads of A just issued), the first part of B of the stage two on into this A's slot.
+    // (all but the loads of A just issued), the first part of B of the stage two on into this A's slot.  128: A
+    // and B of the stage four on into the slots of the stage before; a stage is too short to lead by one.
     // ALL: every fragment of the wave has valid rows (the tests of `ni` cost a fifth of a stage).
     auto stage = [&](auto all) {
-      kstep(all, [&](int i) { b.load(w, LB + (kLoads - LB) * i / NI, LB + (kLoads - LB) * (i + 1) / NI, s3); }, 0, s0, s1);
-      lim1 = lim2;
-      lim2 = advance();
-      kstep(all, [&](int i) { a.load(w, i, i + 1, s4); }, 1, s0, s1);
-      kstep(all, [&](int i) { a.load(w, NI + i, NI + i + 1, s4); }, 2, s0, s1);
-      last_kstep(all, [&](int g, int G) { b.load(w, LB * g / G, LB * (g + 1) / G, s0); },
-                 [&]() {
-                   landed_barrier<LA>();
-                   if (__builtin_expect(lim1 != 0, 0)) clear(LA, lim1, s2, s3);
-                 },
-                 s2, s3);
-      char *x0 = s0, *x1 = s1;                     // the next stage's slots
-      s0 = s2;
-      s1 = s3;
-      s2 = s4;
-      s3 = x0;
-      s4 = x1;
+      if constexpr (TD == 4) {
+        kstep(all, [&](int i) { b.load(w, LB + (kLoads - LB) * i / NI, LB + (kLoads - LB) * (i + 1) / NI, s3); }, 0, s0, s1);
+        lim1 = lim2;
+        lim2 = advance();
+        kstep(all, [&](int i) { a.load(w, i, i + 1, s4); }, 1, s0, s1);
+        kstep(all, [&](int i) { a.load(w, NI + i, NI + i + 1, s4); }, 2, s0, s1);
+        last_kstep(all, [&](int g, int G) { b.load(w, LB * g / G, LB * (g + 1) / G, s0); },
+                   [&]() {
+                     landed_barrier<LA>();
+                     if (__builtin_expect(lim1 != 0, 0)) clear(lim1, s2, s3);
+                   },
+                   s2, s3);
+        char *x0 = s0, *x1 = s1;                   // the next stage's slots
+        s0 = s2;
+        s1 = s3;
+        s2 = s4;
+        s3 = x0;
+        s4 = x1;
+      } else {
+        lim1 = lim2;
+        lim2 = lim3;
+        lim3 = lim4;
+        lim4 = advance();
+        kstep(all, [&](int i) { a.load(w, i, i + 1, s4); }, 0, s0, s1);
+        kstep(all, [&](int i) { a.load(w, 2 + i, 3 + i, s4); }, 1, s0, s1);
+        kstep(all, [&](int i) { b.load(w, i, i + 1, s4 + kOp); }, 2, s0, s1);
+        last_kstep(all, [&](int, int) { b.load(w, 2, 4, s4 + kOp); },
+                   [&]() {
+                     landed_barrier<2 * 2 * kLoads + 6>();
+                     if (__builtin_expect(lim1 != 0, 0)) clear(lim1, s2, s3);
+                   },
+                   s2, s3);
+        auto next = [&](char* s) { return s == lds + (kSlots - 2) * kOp ? lds : s + 2 * kOp; };
+        s4 = s0;
+        s0 = s2;
+        s1 = s3;
+        s2 = next(s2);
+        s3 = s2 + kOp;
+      }
     };
     auto keep = [&]() {                            // (accumulators stay in accumulation registers)
 #pragma unroll
@@ -584,7 +641,7 @@ struct Runner {
       keep();
       // ---- epilogue, through the slot that the last stage's B left ----
       const Geometry t = geometry(k);
-      constexpr int RB = TYPE == kInt8 ? 128 : 256;
+      constexpr int RB = TYPE == kInt8 || TD == 2 ? 128 : 256;
       char* reg = s4 + 8192 * w;
       const int64_t nout = MODE == kFwd ? p.N : p.K;
       const int64_t out_row0 = (MODE == kWgrad ? (int64_t)t.g * p.N : t.e_row0) + (int64_t)t.mt * BM;
@@ -603,7 +660,7 @@ struct Runner {
         const float* sx = (const float*)p.sa + t.row0;
         const float* sw = (const float*)p.sb + (int64_t)t.g * p.N + col0;
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
+        for (int q = 0; q < TD / 2; ++q) {
           // (row 32 i + r of the wave is the tile's 32 (2 i + wm) + r)
           dma4((const uint8_t*)(sx + min(64 * (2 * q + (l >> 5)) + 32 * wm + (l & 31), t.a_lim - 1)), reg + 4096 + 256 * q);
           dma4((const uint8_t*)(sw + min(WN * wn + 64 * q + l, t.b_lim - 1)), reg + 4608 + 256 * q);
@@ -624,9 +681,9 @@ struct Runner {
           }
         };
         if (p.out_bf16)
-          store_rows<true, RB>(value, reg, out, row_bytes, 32 * (2 * i + wm), WN * wn, t.b_lim);
+          store_rows<true, RB, NJ>(value, reg, out, row_bytes, 32 * (2 * i + wm), WN * wn, t.b_lim);
         else
-          store_rows<false, RB>(value, reg, out, row_bytes, 32 * (2 * i + wm), WN * wn, t.b_lim);
+          store_rows<false, RB, NJ>(value, reg, out, row_bytes, 32 * (2 * i + wm), WN * wn, t.b_lim);
       }
       lds_barrier();                               // that slot is loaded into next
     }
@@ -636,52 +693,66 @@ struct Runner {
 
 // One workgroup per CU (all of its LDS), tiles b, b + grid, ... of the launch.  The list of tiles is built
 // once per 64 tiles of a workgroup; lane k keeps tile k.
-template <int MODE, int TYPE>
+template <int MODE, int TYPE, int TD>
 __global__ __launch_bounds__(NT, 1) void dense_grouped_gemm_kernel(GemmArgs p) {
-  __shared__ __attribute__((aligned(16))) char lds[kLds];
+  __shared__ __attribute__((aligned(16))) char lds[Shape<TD>::kLds];
   for (int64_t round = 0;; ++round) {
     const TileList list(lds);
-    build_list<MODE, TYPE == kInt8 ? 1 : 2>(p, list);
+    build_list<MODE, TYPE == kInt8 ? 1 : 2, TD>(p, list);
     // a short list is spread over the XCDs in equal runs
     const int chunk = min(chunk_tiles(MODE), max(1, list.first[list_entries<MODE>(p)] / kXcd));
     const int64_t b = blockIdx.x + gridDim.x * (64 * round + (threadIdx.x & 63));
     Tile mine;
-    const bool have = b <= 0x3FFFFFFF && locate<MODE>(p, list, list_position((int)b, chunk), mine);
+    const bool have = b <= 0x3FFFFFFF && locate<MODE, TD>(p, list, list_position((int)b, chunk), mine);
     const int count = __popcll(__ballot(have));    // positions grow with b: the first `count` lanes have a tile
     __syncthreads();                               // the list's LDS is reused for operands
     if (count == 0) return;
-    Runner<MODE, TYPE>(p, lds, mine).run(count);
+    Runner<MODE, TYPE, TD>(p, lds, mine).run(count);
     if (count < 64) return;
     __syncthreads();
   }
 }
 
-static_assert(kListBytes <= kLds, "the list must fit in LDS");
+static_assert(kListBytes <= Shape<2>::kLds && kListBytes <= Shape<4>::kLds, "the list must fit in LDS");
 
-}  // namespace
-
-hipError_t launch_dense_gemm(int mode, bool int8, const GemmArgs& p, hipStream_t st) {
-  int64_t tiles;
-  if (mode == kWgrad) {
-    tiles = (int64_t)p.G * ((p.N + BM - 1) / BM) * ((p.K + BN - 1) / BN);
-  } else {
-    const int64_t ntc = ((mode == kFwd ? p.N : p.K) + BN - 1) / BN;
-    tiles = ((p.M + BM - 1) / BM + p.G) * ntc;
-  }
-  if (tiles == 0) return hipSuccess;
+template <int MODE, int TYPE, int TD>
+hipError_t launch_tiles(const GemmArgs& p, int64_t tiles, int cus, hipStream_t st) {
   if (tiles > 0x3FFFFFFF) return hipErrorInvalidValue;
+  // (positions of a list of T tiles lie below 2 T + 8, see list_position and its chunk)
+  const dim3 grid((unsigned)min((int64_t)cus, 2 * tiles + 8));
+  hipLaunchKernelGGL((dense_grouped_gemm_kernel<MODE, TYPE, TD>), grid, dim3(NT), 0, st, p);
+  return hipGetLastError();
+}
+
+template <int MODE, int TYPE>
+hipError_t launch_mode(const GemmArgs& p, hipStream_t st) {
   int dev = 0, cus = 0;
   hipError_t e = hipGetDevice(&dev);
   if (e == hipSuccess) e = hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev);
   if (e != hipSuccess) return e;
-  // (positions of a list of T tiles lie below 2 T + 8, see list_position and its chunk)
-  const int64_t grid = min((int64_t)max(cus, 1), 2 * tiles + 8);
-  const dim3 g((unsigned)grid);
-  if (int8) hipLaunchKernelGGL((dense_grouped_gemm_kernel<kFwd, kInt8>), g, dim3(NT), 0, st, p);
-  else if (mode == kFwd) hipLaunchKernelGGL((dense_grouped_gemm_kernel<kFwd, kBf16>), g, dim3(NT), 0, st, p);
-  else if (mode == kDgrad) hipLaunchKernelGGL((dense_grouped_gemm_kernel<kDgrad, kBf16>), g, dim3(NT), 0, st, p);
-  else hipLaunchKernelGGL((dense_grouped_gemm_kernel<kWgrad, kBf16>), g, dim3(NT), 0, st, p);
-  return hipGetLastError();
+  auto count = [&](int64_t bm, bool most) -> int64_t {   // tiles of bm x bm outputs: at most, or about
+    const int64_t ntc = ((MODE == kFwd ? p.N : p.K) + bm - 1) / bm;
+    if (MODE == kWgrad) return p.G * ((p.N + bm - 1) / bm) * ntc;
+    return ((p.M + bm - 1) / bm + (most ? p.G : min((int64_t)p.G, p.M) / 2)) * ntc;
+  };
+  // 128 x 128 tiles where 256 x 256 ones would leave CUs idle.  A round of small tiles takes 0.33 to 0.42 of a
+  // round of large ones; measured, 256 against 128, us: 7 experts of 5003 rows, N 1000, K 1120: forward (92
+  // tiles or 344) 32 / 27, wgrad (140 or 504) 41 / 27; one expert of 4096 rows, N = K = 2048: wgrad (64 or 256)
+  // 79 / 43; 8 experts of 4096 rows, N = K = 2048: forward (160 or 576) 50 / 52, wgrad (512 or 2048) 50 / 59;
+  // 4 experts of 8192 rows, N = K = 4096: wgrad (1024 or 4096) 255 / 368.
+  auto rounds = [&](int64_t tiles) { return (double)((tiles + cus - 1) / cus); };
+  const bool use_small = 0.38 * rounds(count(128, false)) < rounds(count(256, false));
+  return use_small ? launch_tiles<MODE, TYPE, 2>(p, count(128, true), cus, st)
+                   : launch_tiles<MODE, TYPE, 4>(p, count(256, true), cus, st);
+}
+
+}  // namespace
+
+hipError_t launch_dense_gemm(int mode, bool int8, const GemmArgs& p, hipStream_t st) {
+  if (int8) return launch_mode<kFwd, kInt8>(p, st);
+  if (mode == kFwd) return launch_mode<kFwd, kBf16>(p, st);
+  if (mode == kDgrad) return launch_mode<kDgrad, kBf16>(p, st);
+  return launch_mode<kWgrad, kBf16>(p, st);
 }
 
 }  // namespace mxmoe
