@@ -12,14 +12,18 @@
 //
 // Bound: HBM, 2 + 1 bytes per element (SwiGLU: 4 + 1).  A row is held in registers between the maximum
 // and the conversion, by 1, 2 or 4 waves according to its length (at most 4 x 16 bytes per lane and
-// operand); rows of more than 8192 elements are read again.
+// operand); rows of more than 8192 elements are read again.  With SwiGLU the chain of a row (loads, maximum,
+// one fp64 evaluation, conversion) has to hide behind the other rows of a CU: 128 registers, so that 16 waves
+// fit, and no memory access in the usual chain (a candidate's values are kept, not read again: 4.4 -> 6 TB/s).
+// Measured: 65536 x 7168 plain 6.3 TB/s; SwiGLU 65536 x 2048 5.6-6.0, 32768 x 8192 5.9, 49152 x 1408 4.7,
+// 49152 x 1024 3.4 (the work per row, not per element, counts there).
 #include "common.h"
 
 namespace mxmoe {
 namespace {
 
 constexpr int NT = 256;
-constexpr int NCH = 4;                            // 16-byte chunks (8 elements) per lane and operand
+constexpr int kMaxChunks = 4;                     // 16-byte chunks (8 elements) per lane and operand
 
 __device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
@@ -27,15 +31,16 @@ __device__ __forceinline__ void unpack8(uint4 v, float (&f)[8]) {
   f[0] = bf_lo(v.x); f[1] = bf_hi(v.x); f[2] = bf_lo(v.y); f[3] = bf_hi(v.y);
   f[4] = bf_lo(v.z); f[5] = bf_hi(v.z); f[6] = bf_lo(v.w); f[7] = bf_hi(v.w);
 }
-// fp32 SwiGLU with the hardware exponential and reciprocal: relative error below 1e-6 + 2e-7 |g| (the
-// rounding of g log2(e) enters e^-g multiplied by |g|).
+// fp32 SwiGLU with the hardware exponential and reciprocal.  In units of 2^-24: e^-g is off by 2 (the
+// exponential, one unit in the last place) and 1.4 |g| (the rounding of g log2(e) and of log2(e)), 1 + e^-g by 1
+// more, the reciprocal by 2, the two products by 1 each: 7 + 1.4 |g|.
 __device__ __forceinline__ float swiglu32(float g, float u) {
   return g * __builtin_amdgcn_rcpf(1.0f + __expf(-g)) * u;
 }
 // The same in fp64, of element c of a gate|up row (read again: few elements come here).
+__device__ __forceinline__ double swiglu64(double g, double u) { return g / (1.0 + exp(-g)) * u; }
 __device__ __forceinline__ double swiglu64(const uint16_t* row, int64_t C, int64_t c) {
-  const double g = __uint_as_float((uint32_t)row[c] << 16), u = __uint_as_float((uint32_t)row[C + c] << 16);
-  return g / (1.0 + exp(-g)) * u;
+  return swiglu64((double)__uint_as_float((uint32_t)row[c] << 16), (double)__uint_as_float((uint32_t)row[C + c] << 16));
 }
 
 template <int WPR>
@@ -53,10 +58,16 @@ __device__ __forceinline__ uint32_t row_max(uint32_t m, uint32_t* red) {
   }
   return m;
 }
+// The same of a value that few lanes have (0 elsewhere): lane by lane.
 template <int WPR>
-__device__ __forceinline__ double row_max64(double m, double* red) {
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) m = fmax(m, __shfl_xor(m, d, 64));
+__device__ __forceinline__ double row_max64(double v, double* red) {
+  double m = 0;
+  for (uint64_t have = __ballot(v > 0); have; have &= have - 1) {
+    const int from = __builtin_ctzll(have);
+    const uint64_t bits = __double_as_longlong(v);
+    const uint32_t lo = __builtin_amdgcn_readlane((uint32_t)bits, from), hi = __builtin_amdgcn_readlane((uint32_t)(bits >> 32), from);
+    m = fmax(m, __longlong_as_double((int64_t)((uint64_t)hi << 32 | lo)));
+  }
   if constexpr (WPR > 1) {
     const int w = threadIdx.x >> 6;
     __syncthreads();
@@ -68,12 +79,12 @@ __device__ __forceinline__ double row_max64(double m, double* red) {
   return m;
 }
 
-// WPR waves per row.  A block's rows past R repeat row R - 1 without storing (every wave meets the
+// WPR waves per row, NCH chunks per lane.  A block's rows past R repeat row R - 1 without storing (every wave meets the
 // block's barriers).
-template <bool GATED, int WPR>
-__global__ __launch_bounds__(NT) void int8_rowwise_kernel(const uint16_t* x, int64_t R, int64_t C, int8_t* q,
+template <bool GATED, int WPR, int NCH>
+__global__ __launch_bounds__(NT, GATED && WPR == 2 ? 3 : 4) void int8_rowwise_kernel(const uint16_t* x, int64_t R, int64_t C, int8_t* q,
                                                           float* s) {
-  static_assert(8 * NCH == 32, "a bit per element held");
+  static_assert(8 * NCH <= 32, "a bit per element held");
   __shared__ uint32_t red[NT / 64];
   __shared__ double red64[NT / 64];
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
@@ -137,6 +148,7 @@ __global__ __launch_bounds__(NT) void int8_rowwise_kernel(const uint16_t* x, int
       for (int64_t seg = 0; seg < nseg; ++seg) {
         if (nseg > 1) load(seg);
         uint32_t some = 0;                         // this lane's candidates, a bit each
+        float gc = 0, uc = 0;                      // the last one's values (almost always the only one)
 #pragma unroll
         for (int k = 0; k < NCH; ++k) {
           float g[8], u[8];
@@ -144,9 +156,14 @@ __global__ __launch_bounds__(NT) void int8_rowwise_kernel(const uint16_t* x, int
           unpack8(b[k], u);
 #pragma unroll
           for (int e = 0; e < 8; ++e)
-            if (fabsf(h[k][e]) >= cand && g[e] != 0 && u[e] != 0) some |= 1u << (8 * k + e);
+            if (fabsf(h[k][e]) >= cand && g[e] != 0 && u[e] != 0) {
+              some |= 1u << (8 * k + e);
+              gc = g[e];
+              uc = u[e];
+            }
         }
-        for (; some; some &= some - 1) {
+        if (some) amax64 = fmax(amax64, fabs(swiglu64((double)gc, (double)uc)));
+        for (some &= ~(0x80000000u >> __builtin_clz(some | 1)); some; some &= some - 1) {
           const int bit = __builtin_ctz(some);
           amax64 = fmax(amax64, fabs(swiglu64(src, C, seg * kSeg + 8 * (l + 64 * WPR * (bit >> 3)) + (bit & 7))));
         }
@@ -160,40 +177,52 @@ __global__ __launch_bounds__(NT) void int8_rowwise_kernel(const uint16_t* x, int
   if (zero) scale = 1.0f;
   if (live && l == 0) s[row] = scale;
 
-  // 127 v / amax; v and amax are first moved by a power of two so that the reciprocal stays normal
-  const float mv = amax < 0x1p-60f ? 0x1p64f : (amax > 0x1p60f ? 0x1p-64f : 1.0f);
-  const float den = amax * mv, num = 127.0f * mv, rc = __builtin_amdgcn_rcpf(den);
   const bool dead = zero || !finite;               // codes 0 (a row with a NaN or an infinity: the scale says so)
+  // 127 v / amax.  Plain rows: v and amax are first moved by a power of two so that the reciprocal stays
+  // normal; a product and one correction.  SwiGLU: one product, rounded by adding 1.5 * 2^23 in the same
+  // instruction (the code is then the low byte); the elements nearer to a border than fp32 can tell are
+  // evaluated again in fp64 below, those of a row so small that fp32 lost them all.  A factor of 0 gives
+  // codes 0 (NaN converts to 0; in the sum it leaves a low byte that is not used).
+  const float mv = amax < 0x1p-60f ? 0x1p64f : (amax > 0x1p60f ? 0x1p-64f : 1.0f);
+  const float den = amax * mv, num = dead ? 0.0f : 127.0f * mv, rc = __builtin_amdgcn_rcpf(den);
+  constexpr float kMagic = 12582912.0f;
+  const float factor = tiny || dead ? 0.0f : 127.0f / amax;
   for (int64_t seg = 0; seg < nseg; ++seg) {
     if (nseg > 1) load(seg);
-    uint32_t some = 0;                             // elements that fp32 cannot decide, a bit each
+    uint32_t some = 0;                             // positions where some lane's element is near a border
 #pragma unroll
     for (int k = 0; k < NCH; ++k) {
-      float v[8], g[8];
+      float g[8];
       unpack8(a[k], g);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = GATED ? h[k][e] : g[e];
-      int code[8];
+      uint32_t code[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const float n = v[e] * num;
-        const float t0 = n * rc;
-        const float t = fmaf(fmaf(-t0, den, n), rc, t0);
-        const float r = rintf(t);
-        if constexpr (GATED)
-          if (fabsf(t - r) > 0.5f - fabsf(t) * (1.5e-6f + 2e-7f * fabsf(g[e]))) some |= 1u << (8 * k + e);
-        code[e] = dead ? 0 : (int)r;
+        if constexpr (GATED) {
+          const float v = h[k][e];
+          const float m = fmaf(v, factor, kMagic), r = m - kMagic;
+          // error of v * factor, at most |r| + 1: v's, and 3 * 2^-24 of the maximum, the quotient and this test
+          const float near = fmaf(-1.0f - fabsf(r), fmaf(1e-7f, fabsf(g[e]), 7e-7f), 0.5f);
+          if (__ballot(fabsf(fmaf(v, factor, -r)) > near)) some |= 1u << (8 * k + e);
+          code[e] = __float_as_uint(m);
+        } else {
+          const float n = g[e] * num;
+          const float t0 = n * rc;
+          code[e] = (uint32_t)(int)rintf(fmaf(fmaf(-t0, den, n), rc, t0));
+        }
       }
       const int64_t c = seg * kSeg + 8 * (l + 64 * WPR * k);
-      auto pack = [&](int e) {
-        return (uint32_t)(code[e] & 255) | (uint32_t)(code[e + 1] & 255) << 8 | (uint32_t)(code[e + 2] & 255) << 16 |
-               (uint32_t)code[e + 3] << 24;
+      auto pack = [&](int e) {                     // the low bytes of four
+        const uint32_t lo = __builtin_amdgcn_perm(code[e + 1], code[e], 0x0C0C0400u);
+        const uint32_t hi = __builtin_amdgcn_perm(code[e + 3], code[e + 2], 0x0C0C0400u);
+        return lo | hi << 16;
       };
-      if (live && c < C) store8_nt((uint2*)(q + row * C + c), make_uint2(pack(0), pack(4)));
+      uint2 out = make_uint2(pack(0), pack(4));
+      if (GATED && dead) out = make_uint2(0, 0);
+      if (live && c < C) store8_nt((uint2*)(q + row * C + c), out);
     }
     if constexpr (GATED) {
       if (dead || !live) some = 0;
-      else if (tiny) some = 0xFFFFFFFFu;
+      else if (tiny) some = (uint32_t)((1ull << (8 * NCH)) - 1);
       for (; some; some &= some - 1) {
         const int bit = __builtin_ctz(some);
         const int64_t c = seg * kSeg + 8 * (l + 64 * WPR * (bit >> 3)) + (bit & 7);
@@ -207,20 +236,27 @@ __global__ __launch_bounds__(NT) void int8_rowwise_kernel(const uint16_t* x, int
 
 hipError_t launch_int8_rowwise(const uint16_t* x, int64_t R, int64_t C, bool gated, int8_t* q, float* s,
                                hipStream_t st) {
-  // waves per row: as few as hold it
-  const int wpr = C <= 512 * NCH ? 1 : (C <= 1024 * NCH ? 2 : 4);
+  // as few waves per row as hold it, and as few chunks per lane (a row of 1024: 2.5 -> 5 TB/s with 2 instead of 4)
+  const int wpr = C <= 512 * kMaxChunks ? 1 : (C <= 1024 * kMaxChunks ? 2 : 4);
+  const int nch = wpr == 1 ? (int)((C + 511) / 512) : kMaxChunks;
   const int64_t per = NT / 64 / wpr;
   const int64_t grid = (R + per - 1) / per;
   if (grid > 0x7FFFFFFF) return hipErrorInvalidValue;
-  const dim3 g((unsigned)grid), b(NT);
+  auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(NT), 0, st, x, R, C, q, s); };
   if (gated) {
-    if (wpr == 1) hipLaunchKernelGGL((int8_rowwise_kernel<true, 1>), g, b, 0, st, x, R, C, q, s);
-    else if (wpr == 2) hipLaunchKernelGGL((int8_rowwise_kernel<true, 2>), g, b, 0, st, x, R, C, q, s);
-    else hipLaunchKernelGGL((int8_rowwise_kernel<true, 4>), g, b, 0, st, x, R, C, q, s);
+    if (wpr == 4) go(int8_rowwise_kernel<true, 4, 4>);
+    else if (wpr == 2) go(int8_rowwise_kernel<true, 2, 4>);
+    else if (nch == 4) go(int8_rowwise_kernel<true, 1, 4>);
+    else if (nch == 3) go(int8_rowwise_kernel<true, 1, 3>);
+    else if (nch == 2) go(int8_rowwise_kernel<true, 1, 2>);
+    else go(int8_rowwise_kernel<true, 1, 1>);
   } else {
-    if (wpr == 1) hipLaunchKernelGGL((int8_rowwise_kernel<false, 1>), g, b, 0, st, x, R, C, q, s);
-    else if (wpr == 2) hipLaunchKernelGGL((int8_rowwise_kernel<false, 2>), g, b, 0, st, x, R, C, q, s);
-    else hipLaunchKernelGGL((int8_rowwise_kernel<false, 4>), g, b, 0, st, x, R, C, q, s);
+    if (wpr == 4) go(int8_rowwise_kernel<false, 4, 4>);
+    else if (wpr == 2) go(int8_rowwise_kernel<false, 2, 4>);
+    else if (nch == 4) go(int8_rowwise_kernel<false, 1, 4>);
+    else if (nch == 3) go(int8_rowwise_kernel<false, 1, 3>);
+    else if (nch == 2) go(int8_rowwise_kernel<false, 1, 2>);
+    else go(int8_rowwise_kernel<false, 1, 1>);
   }
   return hipGetLastError();
 }
