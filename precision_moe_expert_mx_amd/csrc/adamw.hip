@@ -16,7 +16,9 @@
 //
 // Bound: HBM.  Bytes per element: weight 8, copy 2, gradient 4 or 2, moments 16 (fp32) or 4.06 (8 bits).
 // A lane owns four consecutive elements (16-byte accesses of the fp32 arrays), so 32 lanes hold a block of
-// 128 and meet for its two maxima by lane permutes; every byte is touched once, non-temporally.
+// 128 and meet for its two maxima by lane permutes; every byte is touched once, non-temporally.  Measured
+// on 235M elements with fp32 / bf16 gradients: fp32 moments 5.56 / 5.59 TB/s (1268 / 1177 us), 8-bit moments
+// 5.48 / 5.45 (777 / 695 us).
 #include "common.h"
 
 namespace mxmoe {
@@ -237,27 +239,56 @@ __global__ __launch_bounds__(NT) void adamw_kernel(AdamwArgs p) {
   }
 }
 
-// Values of 8-bit moments, four per lane.
+// Values of 8-bit moments: a lane's two groups of eight consecutive elements (8-byte reads, 16- or 32-byte
+// writes), 2048 elements apart.  Bound: HBM, 3 or 5 bytes per element.
+constexpr int kGroup = 8, kGroups = 2;
 template <bool SECOND, bool BF16>
 __global__ __launch_bounds__(NT) void adamw_values_kernel(const uint8_t* __restrict__ q, const float* __restrict__ s,
                                                           int64_t n, void* __restrict__ out) {
-  const int64_t i = ((int64_t)blockIdx.x * NT + threadIdx.x) * kVec;
-  if (i >= n) return;
-  const int left = (int)min((int64_t)kVec, n - i);
-  uint32_t w = 0;
-  if (left == kVec) w = __builtin_nontemporal_load((const uint32_t*)(q + i));
-  else
-    for (int e = 0; e < left; ++e) w |= (uint32_t)q[i + e] << (8 * e);
-  float v[4];
-  if constexpr (SECOND) decode_v(w, s[i / 128], v);
-  else decode_m(w, s[i / 128], v);
-  if (left == kVec) {
-    if constexpr (BF16) store8_nt((uint2*)((uint16_t*)out + i), make_uint2(bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])));
-    else store4f_nt((float*)out + i, v);
-  } else {
-    for (int e = 0; e < left; ++e) {
-      if constexpr (BF16) ((uint16_t*)out)[i + e] = (uint16_t)bf16_pair(v[e], 0.0f);
-      else ((float*)out)[i + e] = v[e];
+  uint2 w[kGroups];
+  float sc[kGroups];
+  const int64_t first = (int64_t)blockIdx.x * (NT * kGroup * kGroups) + kGroup * threadIdx.x;
+#pragma unroll
+  for (int k = 0; k < kGroups; ++k) {
+    const int64_t i = first + (int64_t)k * NT * kGroup;
+    w[k] = make_uint2(0, 0);
+    sc[k] = 0;
+    if (i >= n) continue;
+    sc[k] = s[i / 128];
+    if (i + kGroup <= n) {
+      const v2u_ v = __builtin_nontemporal_load((const v2u_*)(q + i));
+      w[k] = make_uint2(v[0], v[1]);
+    } else {
+      for (int e = 0; e < (int)(n - i); ++e) (e < 4 ? w[k].x : w[k].y) |= (uint32_t)q[i + e] << (8 * (e & 3));
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < kGroups; ++k) {
+    const int64_t i = first + (int64_t)k * NT * kGroup;
+    if (i >= n) continue;
+    float v[2][4];
+    if constexpr (SECOND) {
+      decode_v(w[k].x, sc[k], v[0]);
+      decode_v(w[k].y, sc[k], v[1]);
+    } else {
+      decode_m(w[k].x, sc[k], v[0]);
+      decode_m(w[k].y, sc[k], v[1]);
+    }
+    if (i + kGroup <= n) {
+      if constexpr (BF16) {
+        __builtin_nontemporal_store(v4u_{bf16_pair(v[0][0], v[0][1]), bf16_pair(v[0][2], v[0][3]),
+                                         bf16_pair(v[1][0], v[1][1]), bf16_pair(v[1][2], v[1][3])},
+                                    (v4u_*)((uint16_t*)out + i));
+      } else {
+        store4f_nt((float*)out + i, v[0]);
+        store4f_nt((float*)out + i + 4, v[1]);
+      }
+    } else {
+      for (int e = 0; e < (int)(n - i); ++e) {
+        const float x = e < 4 ? v[0][e & 3] : v[1][e & 3];
+        if constexpr (BF16) ((uint16_t*)out)[i + e] = (uint16_t)bf16_pair(x, 0.0f);
+        else ((float*)out)[i + e] = x;
+      }
     }
   }
 }
@@ -278,7 +309,7 @@ hipError_t launch_adamw(const AdamwArgs& p, int blocks, bool eight, bool gbf16, 
 
 hipError_t launch_adamw_values(const uint8_t* q, const float* s, int64_t n, bool second, bool bf16, void* out,
                                hipStream_t st) {
-  const int64_t grid = (n + kIter - 1) / kIter;
+  const int64_t per = NT * kGroup * kGroups, grid = (n + per - 1) / per;
   if (grid > 0x7FFFFFFF) return hipErrorInvalidValue;
   const dim3 g((unsigned)grid), b(NT);
   if (second && bf16) hipLaunchKernelGGL((adamw_values_kernel<true, true>), g, b, 0, st, q, s, n, out);

@@ -285,3 +285,37 @@ def test_table_refuses():
     with pytest.raises(mm.MxMoeError, match="aligned"):
         m.adamw_step(m.adamw_table([z(260)[1:257]], [g], [a], [b]), 1, 1e-3)
     assert not p.any()
+
+
+def test_8_bit_moments_equal_any_fp32_implementation():
+    """The moments' operations are rounded one by one, so a plain fp32 implementation of the formula has the
+    same codes and scales bit for bit, over several steps."""
+    m = require_gpu()
+    rng = np.random.default_rng(45)
+    n = 300_001
+    d, _ = _make(rng, n, 8, "bf16")
+    table = _table(m, [d], 8)
+    f = np.float32
+    scale = f(0.3)
+    c = torch.full((1,), float(scale), device="cuda")
+    mq, ms, vq, vs = (host(d[k]) for k in ("m", "ms", "v", "vs"))
+    values_m = np.array([oracle.e4m3_decode(np.array([k], np.uint8))[0] for k in range(256)])
+    pad = lambda a, fill=0: np.concatenate([a, np.full(-a.size % 128, fill, a.dtype)])  # noqa: E731
+    spread = lambda s: np.repeat(s, 128)[:n]  # noqa: E731
+    for step in (1, 2, 3):
+        g = host(d["g"].float()) * scale
+        m1 = f(0.9) * (values_m.astype(f)[mq] * spread(ms)) + f(1 - 0.9) * g
+        v1 = f(0.95) * (oracle.adamw_v_values().astype(f)[vq] * spread(vs)) + f(1 - 0.95) * g * g
+        assert m1.dtype == f and v1.dtype == f
+        ms = np.maximum(np.abs(pad(m1)).reshape(-1, 128).max(1) * (f(1) / f(448)), f(2.0 ** -126))
+        vs = np.maximum(pad(v1).reshape(-1, 128).max(1) * (f(1) / f(1.875)), f(2.0 ** -126))
+        mq = oracle.e4m3_encode(np.clip(m1 / spread(ms), -448, 448).astype(np.float64))
+        bits = (v1 / spread(vs)).view(np.uint32)
+        code = ((bits + 0x7FFFF + ((bits >> 20) & 1)) >> 20).astype(np.int64) - 96 * 8
+        vq = np.where(v1 > 0, np.clip(code, 1, 255), 0).astype(np.uint8)
+        m.adamw_step(table, step, 1e-3, grad_scale=c, **HYPER)
+        for k, want in (("ms", ms), ("vs", vs), ("m", mq), ("v", vq)):
+            got = host(d[k])
+            if k == "m":                              # -0 and 0 are the same value
+                got, want = np.where(got == 128, 0, got), np.where(want == 128, 0, want)
+            assert np.array_equal(got, want), (step, k, int((got != want).sum()))
