@@ -626,6 +626,49 @@ def other_configs_leg(m, torch, steps=5, warmup=2):
     return res
 
 
+def plain_leg(m, torch, steps=5, warmup=2):
+    """The DeepSeek-V3-16B down layer (64 experts, 49152 rows) on plain operands, beside the MXFP8 headline: its
+    training step in bf16 (forward, dgrad, wgrad), the AdamW step of its weights with fp32 and with 8-bit
+    moments, and its forward in 8-bit integers after the SwiGLU quantiser, for all rows and for 48."""
+    from workloads import make_workload
+    lay = make_workload("dsv3_16b", ["down"]).layers[0]
+    G, M, N, K = lay.G, lay.M, lay.N, lay.K
+    x, dy, offs = (to_device(torch, a) for a in (lay.x, lay.dy, lay.offs))
+    w = to_device(torch, lay.w.reshape(G * N, K))
+    n = G * N * K
+    ops = []
+
+    def add(name, kind, fn, work):
+        ops.append(Op(name, kind, fn, work, name))
+
+    y, dx = (torch.empty(s, dtype=torch.bfloat16, device="cuda") for s in ((M, N), (M, K)))
+    dw = torch.empty((G, N, K), device="cuda")
+    flops = 2.0 * M * N * K
+    add("bf16_fwd", "gemm", lambda: m.bf16_grouped_gemm_fwd(x, w, offs, N, "bf16", y=y), flops)
+    add("bf16_dgrad", "gemm", lambda: m.bf16_grouped_gemm_dgrad(dy, w, offs, K, "bf16", dx=dx), flops)
+    add("bf16_wgrad", "gemm", lambda: m.bf16_grouped_gemm_wgrad(dy, x, offs, dw=dw), flops)
+    p, copy = w.float().view(-1), w.clone().view(-1)
+    zeros = lambda size, dt: torch.zeros(size, dtype=dt, device="cuda")  # noqa: E731
+    f32 = m.adamw_table([p], [dw], [zeros(n, torch.float32)], [zeros(n, torch.float32)], weights=[copy])
+    u8 = m.adamw_table([p], [dw], [zeros(n, torch.uint8)], [zeros(n, torch.uint8)], weights=[copy],
+                       exp_avg_scales=[zeros(n // 128, torch.float32)],
+                       exp_avg_sq_scales=[zeros(n // 128, torch.float32)])
+    add("adamw_fp32_moments", "quant", lambda: m.adamw_step(f32, 1, 1e-6), 30.0 * n)
+    add("adamw_8bit_moments", "quant", lambda: m.adamw_step(u8, 1, 1e-6), 18.125 * n)
+    qw, sw = m.int8_quantize_rowwise(w)
+    gate_up = torch.randn((M, 2 * K), device="cuda", dtype=torch.bfloat16)
+    qh, sh = m.int8_quantize_swiglu_rowwise(gate_up)
+    few = torch.arange(G + 1, device="cuda", dtype=torch.int32).clamp_(max=48)
+    add("int8_swiglu_quantise", "quant", lambda: m.int8_quantize_swiglu_rowwise(gate_up, qh, sh), 5.0 * M * K)
+    add("int8_fwd", "gemm", lambda: m.int8_grouped_gemm_fwd(qh, sh, qw, sw, offs, N, "bf16", y=y), flops)
+    add("int8_fwd_48_rows", "quant", lambda: m.int8_grouped_gemm_fwd(qh[:48], sh[:48], qw, sw, few, N, "bf16"),
+        48.0 * N * K)
+    time_ops(torch, ops, steps, warmup)
+    res = {"layer": {"G": G, "M": M, "N": N, "K": K}, "ops": {op.name: op_summary(op) for op in ops}}
+    log("plain operands: " + ", ".join(f"{op.name} {float(np.mean(op.ms)):.3f} ms" for op in ops))
+    return res
+
+
 def blockwise_leg(m, torch, steps=5, sample_rows=256):
     """DeepSeek-style blockwise FP8 (1x128 activation tiles, 128x128 weight blocks, 128-token blocks
     for the weight gradient, fp32 scales, promotion every 128), also in its power-of-two scale mode
@@ -883,6 +926,7 @@ def main():
         torch.cuda.empty_cache()
         extra["blockwise_vs_mx"] = blockwise_leg(m, torch)
         extra["other_configs"] = other_configs_leg(m, torch)
+        extra["plain_operands"] = plain_leg(m, torch)
 
     cpu = None
     if not args.no_cpu_baseline:

@@ -19,7 +19,7 @@
 // 128 and meet for its two maxima by lane permutes; every byte is touched once, non-temporally.  Measured
 // on 235M elements with fp32 / bf16 gradients: fp32 moments 5.56 / 5.59 TB/s (1268 / 1177 us), 8-bit moments
 // 5.48 / 5.45 (777 / 695 us).
-#include "common.h"
+#include "plain.h"
 
 namespace mxmoe {
 namespace {

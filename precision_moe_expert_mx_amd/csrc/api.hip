@@ -8,7 +8,7 @@
 #include <mutex>
 #include <vector>
 
-#include "common.h"
+#include "plain.h"
 
 using namespace mxmoe;
 

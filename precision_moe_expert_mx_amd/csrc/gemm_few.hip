@@ -9,7 +9,7 @@
 // of X come the same way (they stay in L2).  An expert's rows are taken 32 at a time.
 #include <type_traits>
 
-#include "common.h"
+#include "plain.h"
 
 namespace mxmoe {
 namespace {

@@ -17,7 +17,7 @@
 // fit, and no memory access in the usual chain (a candidate's values are kept, not read again: 4.4 -> 6 TB/s).
 // Measured: 65536 x 7168 plain 6.3 TB/s; SwiGLU 65536 x 2048 5.6-6.0, 32768 x 8192 5.9, 49152 x 1408 4.7,
 // 49152 x 1024 3.4 (the work per row, not per element, counts there).
-#include "common.h"
+#include "plain.h"
 
 namespace mxmoe {
 namespace {
