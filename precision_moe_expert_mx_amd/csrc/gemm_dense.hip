@@ -319,7 +319,9 @@ __device__ __forceinline__ void build_list(const GemmArgs& p, const TileList& l)
   __syncthreads();
   if (tid < 64) {
     const int ntc = cdiv(MODE == kFwd ? p.N : p.K, BN), n = list_entries<MODE>(p);
-    int carry = 0;
+    // (64 bits, and at most 2^30: offsets that are not monotone could list more tiles than the host counted)
+    const int64_t most = 1 << 30;
+    int64_t carry = 0;
     for (int base = 0; base < n; base += 64) {
       const int q = base + tid;
       int c = 0;
@@ -328,16 +330,16 @@ __device__ __forceinline__ void build_list(const GemmArgs& p, const TileList& l)
         if (MODE == kWgrad) c = cdiv(p.N, BM) * ntc;
         else c = (e < kMaxG ? rows(e) / BM : (rows(e - kMaxG) % BM ? 1 : 0)) * ntc;
       }
-      int incl = c;
+      int64_t incl = c;
 #pragma unroll
       for (int d = 1; d < 64; d <<= 1) {
-        const int v = __shfl_up(incl, d, 64);
+        const int64_t v = __shfl_up((long long)incl, d, 64);
         if (tid >= d) incl += v;
       }
-      if (q < n) l.first[q] = carry + incl - c;
-      carry += __shfl(incl, 63, 64);
+      if (q < n) l.first[q] = (int32_t)min(carry + incl - c, most);
+      carry += __shfl((long long)incl, 63, 64);
     }
-    if (tid == 0) l.first[n] = carry;
+    if (tid == 0) l.first[n] = (int32_t)min(carry, most);
   }
   __syncthreads();
 }

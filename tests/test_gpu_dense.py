@@ -257,3 +257,69 @@ def test_gradients_against_differences():
         bw = (oracle.dense_gemm_wgrad(dy, x, offs)[1] * np.abs(f(uw).reshape(dw.shape))).sum()
         assert abs((dx * f(ux)).sum() - slope_x) <= 1e-5 * bx
         assert abs((dw * f(uw).reshape(dw.shape)).sum() - slope_w) <= 1e-5 * bw
+
+
+@pytest.mark.parametrize("sizes", [[255, 0, 257, 1000, 64, 1, 900], [129, 640, 63, 320, 1, 1700]])
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_many_tiles_odd_sizes(sizes, dt):
+    """Enough columns for 256 x 256 tiles: partial row tiles of every height, columns and contractions that end
+    inside a tile, a stage and a 16-byte piece."""
+    m = require_gpu()
+    rng = np.random.default_rng(len(sizes))
+    _run(m, *_layer(rng, sizes, 4104, 200), 4104, 200, dt, "f")
+    _run(m, *_layer(rng, sizes, 72, 4232), 72, 4232, dt, "d")
+    _run(m, *_layer(rng, [130, 0, 77], 2568, 2440), 2568, 2440, dt, "w")
+
+
+def test_many_tiles_other_rows_do_not_leak():
+    m = require_gpu()
+    rng = np.random.default_rng(14)
+    offs, x, w, dy = _layer(rng, [300, 5, 700, 256, 1000, 600], 4104, 72)
+    nan = np.uint16(0x7FC0)
+    row = 304                                        # last row of expert 1
+    keep = np.arange(len(x)) != row
+    xn = x.copy()
+    xn[row] = nan
+    y = _values(m.bf16_grouped_gemm_fwd(_bf16(xn), _bf16(w), dev(offs), 4104))
+    ref = oracle.dense_gemm_fwd(x, w, offs, 4104)
+    assert np.isnan(y[row]).all() and oracle.check_gemm(y[keep], ref[0][keep], ref[1][keep], "f32")[0]
+    offs, x, w, dy = _layer(rng, [130, 77], 2568, 2440)
+    xn = x.copy()
+    xn[130] = nan                                    # first row of expert 1, next to the end of expert 0's contraction
+    dw = _values(m.bf16_grouped_gemm_wgrad(_bf16(dy), _bf16(xn), dev(offs)))
+    ref = oracle.dense_gemm_wgrad(dy, x, offs)
+    assert np.isnan(dw[1]).all() and oracle.check_gemm(dw[0], ref[0][0], ref[1][0], "f32")[0]
+
+
+def test_more_tiles_than_a_workgroup_lists_at_once():
+    """1024 experts' weight gradients: 80 tiles per CU, two lists of 64; experts of 0 to 3 rows."""
+    m = require_gpu()
+    rng = np.random.default_rng(15)
+    sizes = np.arange(1024) % 4
+    offs = routing_offsets(sizes)
+    M, N, K = int(offs[-1]), 1280, 1024
+    x, dy = random_bf16(rng, (M, K)), random_bf16(rng, (M, N))
+    dw = torch.full((1024, N, K), float("nan"), dtype=torch.bfloat16, device="cuda")
+    m.bf16_grouped_gemm_wgrad(_bf16(dy), _bf16(x), dev(offs), "bf16", dw=dw)
+    assert torch.isfinite(dw).all() and not dw[::4].any()
+    for g in (1, 2, 3, 511, 777, 1022, 1023):
+        r = slice(int(offs[g]), int(offs[g + 1]))
+        ref = oracle.dense_gemm_wgrad(dy[r], x[r], np.array([0, sizes[g]], np.int32))
+        ok, worst, _ = oracle.check_gemm(_values(dw[g:g + 1]), *ref, "bf16")
+        assert ok, (g, worst)
+
+
+@pytest.mark.parametrize("bad", [[0, 50, 20, 300, 10], [-5, 10, 10, 90, 40], [100, 0, 100, 0, 100]])
+def test_invalid_offsets_stay_inside_the_buffers(bad):
+    """Offsets out of order or past M: the results are unspecified, but nothing outside the outputs is written."""
+    m = require_gpu()
+    rng = np.random.default_rng(16)
+    M, N, K = 100, 264, 136
+    o, x, w, dy = dev(np.array(bad, np.int32)), _bf16(random_bf16(rng, (M, K))), _bf16(random_bf16(rng, (4 * N, K))), \
+        _bf16(random_bf16(rng, (M, N)))
+    y, dx, dw = (torch.full((s + 4096,), 3.0, device="cuda") for s in (M * N, M * K, 4 * N * K))
+    m.bf16_grouped_gemm_fwd(x, w, o, N, y=y[:M * N].view(M, N))
+    m.bf16_grouped_gemm_dgrad(dy, w, o, K, dx=dx[:M * K].view(M, K))
+    m.bf16_grouped_gemm_wgrad(dy, x, o, dw=dw[:4 * N * K].view(4, N, K))
+    for t in (y, dx, dw):
+        assert (t[-4096:] == 3.0).all()

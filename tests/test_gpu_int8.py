@@ -203,3 +203,14 @@ def test_expert_mlp_in_8_bits():
         torch.cuda.synchronize()
         for a, b in zip(captured, eager):
             assert torch.equal(a, b), k
+
+
+def test_gemm_many_tiles_odd_sizes():
+    """Enough columns for 256 x 256 tiles, with partial rows, columns and contractions; and few rows spread over
+    many columns."""
+    m = require_gpu()
+    rng = np.random.default_rng(7)
+    for sizes in ([255, 0, 257, 1000, 64, 1, 900], [129, 640, 63, 320, 1, 1700]):
+        for dt in ("f32", "bf16"):
+            _gemm(m, rng, sizes, 4104, 208, dt, lo=-128)
+    _gemm(m, rng, [1, 0, 33, 2, 0, 20], 4104, 1040, "f32", lo=-128)
