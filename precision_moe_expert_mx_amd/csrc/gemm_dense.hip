@@ -18,7 +18,8 @@
 // stages and the next A, filled by direct-to-LDS loads that are never drained: a wave waits only until its
 // share of the next stage has landed (a counted vmcnt), and reads the fragments of a k-step while it
 // multiplies the one before, across stages and tiles too: a workgroup per CU runs its tiles as one stream of
-// stages.  Few tiles are made 128 x 128 (five stages in LDS), so that more CUs have one.
+// stages.  Few tiles are made 128 x 128, by the same kernel with slots of 16 KiB, two workgroups to a CU: more CUs
+// have work, and one workgroup multiplies while the other waits for its loads or stores its outputs.
 //
 // Bound: the matrix cores, and on random operands the chip's power, which sets their clock: of a stage's 2048
 // matrix clocks the loop takes 2300-2400 and a tile 13000 more (measured with GRBM_GUI_ACTIVE at K 1280 .. 10240),
@@ -57,9 +58,9 @@ struct Shape {
   static constexpr int WN = 32 * TD;             // output columns per wave, consecutive
   static constexpr int kOp = BM * BKB;           // bytes of one operand's stage (both layouts)
   static constexpr int kLoads = kOp / 1024 / kWaves;   // 1 KiB loads per wave, stage and operand
-  // operand stages in LDS: A p at slot 2p % kSlots, B p after it.  256: two stages and the next A (160 KiB);
-  // 128: five stages
-  static constexpr int kSlots = TD == 4 ? 5 : 10;
+  // operand stages in LDS: A p at slot 2p % kSlots, B p after it: two stages and the next A
+  static constexpr int kSlots = 5;
+  static constexpr int kPerCu = TD == 4 ? 1 : 2;  // workgroups per CU (160 KiB of LDS either way)
   static constexpr int kLds = kSlots * kOp;
   static_assert(BM == BN, "one stage size for both operands");
 };
@@ -532,16 +533,15 @@ struct Runner {
       }
     };
 
-    // slots of this stage's A and B, the next one's, and of the loads (256: A of the stage two on; 128: of the
-    // stage four on)
-    char *s0 = lds, *s1 = lds + kOp, *s2 = lds + 2 * kOp, *s3 = lds + 3 * kOp, *s4 = lds + (kSlots - (TD == 4 ? 1 : 2)) * kOp;
-    // prologue: the first stages of the stream on their way (256: 0 and, but for a part of B, 1; 128: 0 .. 3),
-    // stage 0 landed, its first fragments read
-    // Part of B that goes out in the last k-step (256; measured: with B in columns all of it, dgrad +3%,
-    // wgrad +5%; in rows half, +1%)
+    // slots of this stage's A and B, the next one's, and of A of the stage two on
+    char *s0 = lds, *s1 = lds + kOp, *s2 = lds + 2 * kOp, *s3 = lds + 3 * kOp, *s4 = lds + 4 * kOp;
+    // prologue: the first stages of the stream on their way (0 and, but for a part of B, 1), stage 0 landed, its
+    // first fragments read
+    // Part of B that goes out in the last k-step (measured: with B in columns all of it, dgrad +3%, wgrad +5%; in
+    // rows half, +1%)
     constexpr int LA = kLoads;
     constexpr int LB = B_COLS ? kLoads : kLoads / 2;
-    int lim1 = 0, lim2 = 0, lim3 = 0, lim4 = 0;    // of a partial stage: the next to multiply, and those after it
+    int lim1 = 0, lim2 = 0;                        // of a partial stage: the next to multiply, the one after it
     lend = count;
     while (MODE == kWgrad && lk < count && __builtin_amdgcn_readlane(mine.e_rows, lk) == 0) ++lk;
     const bool any = lk < count;                   // (wgrad: perhaps none of the experts has rows)
@@ -550,23 +550,10 @@ struct Runner {
       const int lim0 = settle();
       a.load(w, 0, LA, s0);
       b.load(w, 0, kLoads, s1);
-      if constexpr (TD == 4) {
-        lim2 = advance();
-        a.load(w, 0, LA, s2);
-        b.load(w, 0, LB, s3);
-        landed_barrier<LA + LB>();
-      } else {
-        lim2 = advance();
-        a.load(w, 0, LA, s2);
-        b.load(w, 0, kLoads, s3);
-        lim3 = advance();
-        a.load(w, 0, LA, lds + 4 * kOp);
-        b.load(w, 0, kLoads, lds + 5 * kOp);
-        lim4 = advance();
-        a.load(w, 0, LA, lds + 6 * kOp);
-        b.load(w, 0, kLoads, lds + 7 * kOp);
-        landed_barrier<3 * 2 * kLoads>();
-      }
+      lim2 = advance();
+      a.load(w, 0, LA, s2);
+      b.load(w, 0, LB, s3);
+      landed_barrier<LA + LB>();
       if (lim0) clear(lim0, s0, s1);
       read(0, s0, s1, 0, 0, NJ + NI);
     } else {
@@ -574,51 +561,28 @@ struct Runner {
     }
 
     // A stage.  Its loads go out evenly (about one per group: more at once and the address unit holds up the
-    // wave).  256: the rest of B of the next stage, A of the stage two on into the slot that B of the stage before
-    // left, and, once this stage's last fragments are in registers everywhere and the next stage has landed
-    // (all but the loads of A just issued), the first part of B of the stage two on into this A's slot.  128: A
-    // and B of the stage four on into the slots of the stage before; a stage is too short to lead by one.
+    // wave): the rest of B of the next stage, A of the stage two on into the slot that B of the stage before left,
+    // and, once this stage's last fragments are in registers everywhere and the next stage has landed (all but the
+    // loads of A just issued), the first part of B of the stage two on into this A's slot.
     // ALL: every fragment of the wave has valid rows (the tests of `ni` cost a fifth of a stage).
     auto stage = [&](auto all) {
-      if constexpr (TD == 4) {
-        kstep(all, [&](int i) { b.load(w, LB + (kLoads - LB) * i / NI, LB + (kLoads - LB) * (i + 1) / NI, s3); }, 0, s0, s1);
-        lim1 = lim2;
-        lim2 = advance();
-        kstep(all, [&](int i) { a.load(w, i, i + 1, s4); }, 1, s0, s1);
-        kstep(all, [&](int i) { a.load(w, NI + i, NI + i + 1, s4); }, 2, s0, s1);
-        last_kstep(all, [&](int g, int G) { b.load(w, LB * g / G, LB * (g + 1) / G, s0); },
-                   [&]() {
-                     landed_barrier<LA>();
-                     if (__builtin_expect(lim1 != 0, 0)) clear(lim1, s2, s3);
-                   },
-                   s2, s3);
-        char *x0 = s0, *x1 = s1;                   // the next stage's slots
-        s0 = s2;
-        s1 = s3;
-        s2 = s4;
-        s3 = x0;
-        s4 = x1;
-      } else {
-        lim1 = lim2;
-        lim2 = lim3;
-        lim3 = lim4;
-        lim4 = advance();
-        kstep(all, [&](int i) { a.load(w, i, i + 1, s4); }, 0, s0, s1);
-        kstep(all, [&](int i) { a.load(w, 2 + i, 3 + i, s4); }, 1, s0, s1);
-        kstep(all, [&](int i) { b.load(w, i, i + 1, s4 + kOp); }, 2, s0, s1);
-        last_kstep(all, [&](int, int) { b.load(w, 2, 4, s4 + kOp); },
-                   [&]() {
-                     landed_barrier<2 * 2 * kLoads + 6>();
-                     if (__builtin_expect(lim1 != 0, 0)) clear(lim1, s2, s3);
-                   },
-                   s2, s3);
-        auto next = [&](char* s) { return s == lds + (kSlots - 2) * kOp ? lds : s + 2 * kOp; };
-        s4 = s0;
-        s0 = s2;
-        s1 = s3;
-        s2 = next(s2);
-        s3 = s2 + kOp;
-      }
+      kstep(all, [&](int i) { b.load(w, LB + (kLoads - LB) * i / NI, LB + (kLoads - LB) * (i + 1) / NI, s3); }, 0, s0, s1);
+      lim1 = lim2;
+      lim2 = advance();
+      kstep(all, [&](int i) { a.load(w, i, i + 1, s4); }, 1, s0, s1);
+      kstep(all, [&](int i) { a.load(w, NI + i, NI + i + 1, s4); }, 2, s0, s1);
+      last_kstep(all, [&](int g, int G) { b.load(w, LB * g / G, LB * (g + 1) / G, s0); },
+                 [&]() {
+                   landed_barrier<LA>();
+                   if (__builtin_expect(lim1 != 0, 0)) clear(lim1, s2, s3);
+                 },
+                 s2, s3);
+      char *x0 = s0, *x1 = s1;                     // the next stage's slots
+      s0 = s2;
+      s1 = s3;
+      s2 = s4;
+      s3 = x0;
+      s4 = x1;
     };
     auto keep = [&]() {                            // (accumulators stay in accumulation registers)
 #pragma unroll
@@ -648,7 +612,7 @@ struct Runner {
       // ---- epilogue, through the slot that the last stage's B left ----
       const Geometry t = geometry(k);
       constexpr int RB = TYPE == kInt8 || TD == 2 ? 128 : 256;
-      char* reg = s4 + 8192 * w;
+      char* reg = s4 + kOp / kWaves * w;
       const int64_t nout = MODE == kFwd ? p.N : p.K;
       const int64_t out_row0 = (MODE == kWgrad ? (int64_t)t.g * p.N : t.e_row0) + (int64_t)t.mt * BM;
       const int64_t col0 = (int64_t)t.nt * BN;
@@ -657,31 +621,49 @@ struct Runner {
       const __amdgpu_buffer_rsrc_t out = __builtin_amdgcn_make_buffer_rsrc(
           (char*)p.out + out_row0 * row_bytes + col0 * (p.out_bf16 ? 2 : 4), 0,
           (int)(t.a_lim * row_bytes - (uint32_t)col0 * (p.out_bf16 ? 2 : 4)), 0x00020000);
-      float row_scale[NI];
+      // scales of the wave's rows (32 i + r of the wave is the tile's 32 (2 i + wm) + r) and columns; past the last
+      // one that one's.  256: the columns' would spill registers and are staged behind the wave's rows in LDS.
+      // (Older loads are those of A and B of the stages ahead: waiting for these few waits for them too, which have
+      // to land soon anyway.)
+      float row_scale[NI], col_regs[NJ][4][4];
       const float4* col_scale = (const float4*)(reg + 4096 + 512);
       if constexpr (TYPE == kInt8) {
-        // scales of the wave's rows and columns, behind its staged rows (older loads are those of A and B of
-        // the stages ahead: waiting for these few waits for them too, which have to land soon anyway)
         const int l = fresh_lane();
         const float* sx = (const float*)p.sa + t.row0;
         const float* sw = (const float*)p.sb + (int64_t)t.g * p.N + col0;
+        if constexpr (TD == 4) {
 #pragma unroll
-        for (int q = 0; q < TD / 2; ++q) {
-          // (row 32 i + r of the wave is the tile's 32 (2 i + wm) + r)
-          dma4((const uint8_t*)(sx + min(64 * (2 * q + (l >> 5)) + 32 * wm + (l & 31), t.a_lim - 1)), reg + 4096 + 256 * q);
-          dma4((const uint8_t*)(sw + min(WN * wn + 64 * q + l, t.b_lim - 1)), reg + 4608 + 256 * q);
+          for (int q = 0; q < 2; ++q) {
+            dma4((const uint8_t*)(sx + min(64 * (2 * q + (l >> 5)) + 32 * wm + (l & 31), t.a_lim - 1)), reg + 4096 + 256 * q);
+            dma4((const uint8_t*)(sw + min(WN * wn + 64 * q + l, t.b_lim - 1)), reg + 4608 + 256 * q);
+          }
+          asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+#pragma unroll
+          for (int i = 0; i < NI; ++i) row_scale[i] = *(const float*)(reg + 4096 + 4 * (32 * i + (l & 31)));
+        } else {
+#pragma unroll
+          for (int i = 0; i < NI; ++i) row_scale[i] = sx[min(32 * (2 * i + wm) + (l & 31), t.a_lim - 1)];
+#pragma unroll
+          for (int j = 0; j < NJ; ++j)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              // (N % 8 == 0: four columns are all valid or none)
+              const float* c = sw + min(WN * wn + 32 * j + 8 * q + 4 * (l >> 5), t.b_lim - 4);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) col_regs[j][q][e] = c[e];
+            }
         }
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-#pragma unroll
-        for (int i = 0; i < NI; ++i) row_scale[i] = *(const float*)(reg + 4096 + 4 * (32 * i + (l & 31)));
       }
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
         auto value = [&](int j, int q, int e) -> float {
           if constexpr (TYPE == kInt8) {
-            const float4 c = col_scale[8 * j + 2 * q + (lane >> 5)];
-            const float c4[4] = {c.x, c.y, c.z, c.w};
-            return (float)acc[i][j][4 * q + e] * (row_scale[i] * c4[e]);
+            float c = col_regs[j][q][e];
+            if constexpr (TD == 4) {
+              const float4 c4 = col_scale[8 * j + 2 * q + (lane >> 5)];
+              c = e == 0 ? c4.x : e == 1 ? c4.y : e == 2 ? c4.z : c4.w;
+            }
+            return (float)acc[i][j][4 * q + e] * (row_scale[i] * c);
           } else {
             return acc[i][j][4 * q + e];
           }
@@ -698,10 +680,10 @@ struct Runner {
   }
 };
 
-// One workgroup per CU (all of its LDS), tiles b, b + grid, ... of the launch.  The list of tiles is built
+// A workgroup per CU, or two of small tiles (all of its LDS), tiles b, b + grid, ... of the launch.  The list of tiles is built
 // once per 64 tiles of a workgroup; lane k keeps tile k.
 template <int MODE, int TYPE, int TD>
-__global__ __launch_bounds__(NT, 1) void dense_grouped_gemm_kernel(GemmArgs p) {
+__global__ __launch_bounds__(NT, Shape<TD>::kPerCu) void dense_grouped_gemm_kernel(GemmArgs p) {
   __shared__ __attribute__((aligned(16))) char lds[Shape<TD>::kLds];
   for (int64_t round = 0;; ++round) {
     const TileList list(lds);
@@ -726,7 +708,7 @@ template <int MODE, int TYPE, int TD>
 hipError_t launch_tiles(const GemmArgs& p, int64_t tiles, int cus, hipStream_t st) {
   if (tiles > 0x3FFFFFFF) return hipErrorInvalidValue;
   // (positions of a list of T tiles lie below 2 T + 8, see list_position and its chunk)
-  const dim3 grid((unsigned)min((int64_t)cus, 2 * tiles + 8));
+  const dim3 grid((unsigned)min((int64_t)cus * Shape<TD>::kPerCu, 2 * tiles + 8));
   hipLaunchKernelGGL((dense_grouped_gemm_kernel<MODE, TYPE, TD>), grid, dim3(NT), 0, st, p);
   return hipGetLastError();
 }
@@ -742,13 +724,14 @@ hipError_t launch_mode(const GemmArgs& p, hipStream_t st) {
     if (MODE == kWgrad) return p.G * ((p.N + bm - 1) / bm) * ntc;
     return ((p.M + bm - 1) / bm + (most ? p.G : min((int64_t)p.G, p.M) / 2)) * ntc;
   };
-  // 128 x 128 tiles where 256 x 256 ones would leave CUs idle.  A round of small tiles takes 0.33 to 0.42 of a
-  // round of large ones; measured, 256 against 128, us: 7 experts of 5003 rows, N 1000, K 1120: forward (92
-  // tiles or 344) 32 / 27, wgrad (140 or 504) 41 / 27; one expert of 4096 rows, N = K = 2048: wgrad (64 or 256)
-  // 79 / 43; 8 experts of 4096 rows, N = K = 2048: forward (160 or 576) 50 / 52, wgrad (512 or 2048) 50 / 59;
-  // 4 experts of 8192 rows, N = K = 4096: wgrad (1024 or 4096) 255 / 368.
-  auto rounds = [&](int64_t tiles) { return (double)((tiles + cus - 1) / cus); };
-  const bool use_small = 0.38 * rounds(count(128, false)) < rounds(count(256, false));
+  // 128 x 128 tiles where 256 x 256 ones would leave CUs idle.  In units of a round of large tiles, c small ones per
+  // CU take about 0.2 + 0.33 c; measured, 256 against 128, us (tiles): 7 experts of 5003 rows, N 1000, K 1120:
+  // forward 31.5 / 25.1 (92, 344), wgrad 39.9 / 23.7 (140, 504); 8 experts of 8192 rows, N = K = 2048: dgrad 88.9 /
+  // 75.9 (288, 1088), of 4096 rows 48.8 / 48.8 (160, 576); 32 experts of 8192 rows, N 1408, K 2048: forward 75 / 63
+  // (288, 880), wgrad 93 / 98 (1536, 5632); 4 experts of 8192 rows, N = K = 4096: wgrad 233 / 262 (1024, 4096).
+  // Large layers lose up to a half with them.
+  auto per_cu = [&](int64_t tiles) { return (double)((tiles + cus - 1) / cus); };
+  const bool use_small = 0.2 + 0.33 * per_cu(count(128, false)) < per_cu(count(256, false));
   return use_small ? launch_tiles<MODE, TYPE, 2>(p, count(128, true), cus, st)
                    : launch_tiles<MODE, TYPE, 4>(p, count(256, true), cus, st);
 }

@@ -130,15 +130,20 @@ __global__ __launch_bounds__(NT) void few_rows_kernel(GemmArgs p, int blocks) {
 
 }  // namespace
 
-// Few rows: up to 8 per expert on average, 1 where the tiled kernel has 1024 tiles or more of weights to stream
-// (it then reads them at 5.5 TB/s itself), 64 where it has at most 64 (a fourth of the CUs).  Measured, this
-// kernel against the tiled one, us, bf16: 64 experts, N 2816, K 2048: 48 rows 78 / 110, 384 rows 149 / 177, 768
-// rows 169 / 175; 8 experts, N 4096, K 7168: 1 row 23 / 86, 64 rows 107 / 138, 128 rows 135 / 138; 16 experts,
-// N 16384, K 5120: 1 row 40 / 100, 16 rows 364 / 345, 128 rows 670 / 486; 4 experts, N 512, K 256: 7 / 12.
+// Few rows, for which this kernel's many small workgroups beat the tiled one.  With up to 128 tiles of 256 columns
+// of the experts that rows can reach: up to 3 2^16 outputs.  With more, the tiled kernel streams weights at 4 to 5.9
+// TB/s itself, and this one is faster on up to 8 rows per expert where a weight row has 4 KiB or more (each wave has a
+// quarter of it) and the layer has fewer than 1024 tiles.  Measured, this kernel against the tiled one, us, bf16 and
+// int8: one expert, N 4096, K 7168: 1 row 16 / 58 and 10 / 32, 48 rows 44 / 59 and 24 / 33; 2 experts, N 8192, K 4096:
+// 16 rows 31 / 56 and 19 / 22, 64 rows 71 / 56 and 36 / 22; 8 experts, N 4096, K 7168: 8 rows 59 / 96 and 34 / 52,
+// 64 rows 107 / 104 and 55 / 56; 64 experts, N 2816, K 2048: 48 rows 79 / 100 and 48 / 48, 384 rows 148 / 168 and
+// 80 / 73; N 2048, K 1408: 126 rows 67 / 61 and 40 / 37; 16 experts, N 16384, K 5120: 1 row 40 / 70 and 24 / 27,
+// 8 rows 219 / 184 and 113 / 100.
 // (Rows that all reach one expert cost it more: 512 on one of 64 experts pass its weights, from L2, 16 times.)
 bool few_rows(const GemmArgs& p) {
-  const int64_t tiles = p.G * ((p.N + 255) / 256);
-  return p.M <= p.G * (int64_t)(tiles >= 1024 ? 1 : tiles > 64 ? 8 : 64);
+  const int64_t columns = (p.N + 255) / 256;
+  if (min((int64_t)p.G, p.M) * columns <= 128) return p.M * p.N <= 3 << 16;
+  return p.M <= 8 * (int64_t)p.G && p.ldb >= 4096 && p.G * columns < 1024;
 }
 
 hipError_t launch_few_rows_gemm(bool int8, const GemmArgs& p, hipStream_t st) {

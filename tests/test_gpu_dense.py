@@ -323,3 +323,23 @@ def test_invalid_offsets_stay_inside_the_buffers(bad):
     m.bf16_grouped_gemm_wgrad(dy, x, o, dw=dw[:4 * N * K].view(4, N, K))
     for t in (y, dx, dw):
         assert (t[-4096:] == 3.0).all()
+
+
+@pytest.mark.parametrize("rows", [1, 3, 65, 300, 500])
+def test_few_rows_over_many_experts(rows):
+    """Serving a layer of 64 experts: any number of rows per expert, most of them none or a few."""
+    m = require_gpu()
+    G, N, K = 64, 2056, 2056
+    gen = torch.Generator(device="cuda").manual_seed(rows)
+    to = torch.randint(0, G, (rows,), device="cuda", generator=gen)
+    to[rows // 2:] = torch.where(to[rows // 2:] % 4 == 0, 5, to[rows // 2:])          # (expert 5 gets more)
+    offs = torch.zeros(G + 1, device="cuda", dtype=torch.int32)
+    offs[1:] = torch.bincount(to, minlength=G).cumsum(0)
+    x = torch.randn(rows, K, device="cuda", generator=gen).bfloat16()
+    w = torch.randn(G * N, K, device="cuda", generator=gen).bfloat16()
+    y = m.bf16_grouped_gemm_fwd(x, w, offs, N).double()
+    o = offs.tolist()
+    for g in range(G):
+        if o[g + 1] > o[g]:
+            a, b = x[o[g]:o[g + 1]].double(), w[g * N:(g + 1) * N].double().t().contiguous()
+            assert bool(((y[o[g]:o[g + 1]] - a @ b).abs() <= 1e-5 * (a.abs() @ b.abs())).all()), g

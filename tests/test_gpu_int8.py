@@ -214,3 +214,27 @@ def test_gemm_many_tiles_odd_sizes():
         for dt in ("f32", "bf16"):
             _gemm(m, rng, sizes, 4104, 208, dt, lo=-128)
     _gemm(m, rng, [1, 0, 33, 2, 0, 20], 4104, 1040, "f32", lo=-128)
+
+
+@pytest.mark.parametrize("rows", [1, 7, 70, 300, 500])
+def test_gemm_few_rows_over_many_experts(rows):
+    """64 experts and a long contraction, most experts with none or a few rows.  Sums below 2^53 are exact in
+    float64, and an output is off by at most the roundings of the sum, of the scales' product and of the result:
+    2^-24 each, and less than 2^-22 together."""
+    m = require_gpu()
+    G, N, K = 64, 2056, 4112
+    gen = torch.Generator(device="cuda").manual_seed(rows)
+    to = torch.randint(0, G, (rows,), device="cuda", generator=gen)
+    offs = torch.zeros(G + 1, device="cuda", dtype=torch.int32)
+    offs[1:] = torch.bincount(to, minlength=G).cumsum(0)
+    qx = torch.randint(-128, 128, (rows, K), device="cuda", generator=gen, dtype=torch.int8)
+    qw = torch.randint(-128, 128, (G * N, K), device="cuda", generator=gen, dtype=torch.int8)
+    sx = torch.rand(rows, device="cuda", generator=gen) + 0.5
+    sw = torch.rand(G * N, device="cuda", generator=gen) + 0.5
+    y = m.int8_grouped_gemm_fwd(qx, sx, qw, sw, offs, N).double()
+    o = offs.tolist()
+    for g in range(G):
+        if o[g + 1] > o[g]:
+            r, c = slice(o[g], o[g + 1]), slice(g * N, (g + 1) * N)
+            ref = (qx[r].double() @ qw[c].double().t().contiguous()) * sx[r].double()[:, None] * sw[c].double()
+            assert bool(((y[r] - ref).abs() <= 2.0 ** -22 * ref.abs()).all()), g
