@@ -11,6 +11,7 @@ without it raises, and there is no fallback path.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional, Tuple
 
@@ -158,6 +159,7 @@ def mx_colwise_ld(M: int, G: Optional[int] = None) -> int:
 
 
 # ---------------------------------------------------------------- torch plumbing
+@functools.lru_cache(None)
 def _torch():
     import torch
     return torch
@@ -193,6 +195,7 @@ def _empty(shape, dtype, like):
     return _torch().empty(shape, dtype=dtype, device=like.device)
 
 
+@functools.lru_cache(None)
 def _out_dtype(dt: str):
     torch = _torch()
     if dt == "f32":
@@ -616,18 +619,18 @@ def mxmoe_check_offsets(offs, M: int, stream=None) -> None:
 def _run(name, tensors, stream, *args):
     """Launch entry point `name` on the tensors' device (they may live on another one than the current) and on
     that device's current stream unless one is given; the stream is the last argument."""
-    torch = _torch()
-    dev = tensors[0].device
-    if dev.type != "cuda":
+    index = tensors[0].get_device()
+    if index < 0:
         raise ValueError("tensors must be on the GPU")
     for t in tensors:
-        if t.device != dev:
-            raise ValueError(f"tensors must be on one GPU, got {dev} and {t.device}")
-    if torch.cuda.current_device() != dev.index:
-        with torch.cuda.device(dev):
+        if t.get_device() != index:
+            raise ValueError(f"tensors must be on one GPU, got {tensors[0].device} and {t.device}")
+    _C = _torch()._C
+    if _C._cuda_getDevice() != index:
+        with _torch().cuda.device(index):
             return _run(name, tensors, stream, *args)
     if stream is None:
-        stream = torch._C._cuda_getCurrentRawStream(dev.index)
+        stream = _C._cuda_getCurrentRawStream(index)
     elif not isinstance(stream, int):
         stream = stream.cuda_stream
     status = getattr(lib(), name)(*args, stream)
@@ -638,30 +641,35 @@ def _run(name, tensors, stream, *args):
 def _want(name, t, dtypes, shape):
     """A tensor argument is contiguous, of one of `dtypes` and of the shape (None: any size), or a clear error
     says what it is not."""
+    if t.shape == shape and t.dtype in dtypes and t.is_contiguous():
+        return
     if t.dtype not in dtypes:
         raise TypeError(f"{name}: expected {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
-    if t.shape != shape and (t.dim() != len(shape) or any(w is not None and w != n for w, n in zip(shape, t.shape))):
+    if t.dim() != len(shape) or any(w is not None and w != n for w, n in zip(shape, t.shape)):
         raise ValueError(f"{name}: expected shape {tuple('any' if w is None else w for w in shape)}, got {tuple(t.shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name}: tensors must be contiguous")
 
 
+@functools.lru_cache(None)
 def _bf16_types():
     torch = _torch()
     return (torch.bfloat16, torch.int16, torch.uint16)
 
 
 def _groups(offs):
-    _want("offs", offs, (_torch().int32,), (None,))
-    if offs.numel() < 2:
+    n = offs.numel()
+    _want("offs", offs, (_torch().int32,), (n,))
+    if n < 2:
         raise ValueError("offs: expected G + 1 >= 2 entries")
-    return offs.numel() - 1
+    return n - 1
 
 
 def _rows(name, x, dtypes):
     """The shape of a matrix argument."""
-    _want(name, x, dtypes, (None, None))
-    return x.shape
+    shape = x.shape
+    _want(name, x, dtypes, shape if len(shape) == 2 else (None, None))
+    return shape
 
 
 def _weights(name, w, dtypes, G, N, K):
