@@ -376,14 +376,22 @@ __device__ __forceinline__ bool locate(const GemmArgs& p, const TileList& l, int
 }
 
 // List position of workgroup position b: runs of `chunk` consecutive tiles go to one XCD (workgroups are
-// dispatched round-robin over the XCDs), so that tiles sharing operands share an L2.  Runs of 32, the tiles that an
-// XCD's CUs have at a time, are 1-3% faster than 16 for dgrad and 1-4% for wgrad (64 experts' 2048 x 1408: 2% slower);
-// forward: the same on average, but up to 6% slower (4 experts, N = K = 4096), for a launch's end is less even.
-template <int MODE>
-constexpr int kRun = MODE == kFwd ? 16 : 32;
+// dispatched round-robin over the XCDs), so that tiles sharing operands share an L2.
 __device__ __forceinline__ int list_position(int b, int chunk) {
   const int x = b % kXcd, q = b / kXcd;
   return ((q / chunk) * kXcd + x) * chunk + (q % chunk);
+}
+
+// Runs of 32, the tiles that an XCD's CUs have at a time, share most, shorter ones spread work more evenly.  Measured,
+// 32 against the shorter run taken below: dgrad 1-3% faster on lists of 1088 tiles and more, 7% slower on 387; wgrad
+// 1-4% faster from 160 tiles per expert on, 2-8% slower at 48 to 64 (experts differ in cost); forward equal, or up to
+// 6% slower.
+template <int MODE, int TD>
+__device__ __forceinline__ int run_tiles(const GemmArgs& p, int tiles) {
+  int run = 16;
+  if (MODE == kDgrad && tiles >= 1024) run = 32;
+  if (MODE == kWgrad) run = (int64_t)cdiv(p.N, Shape<TD>::BM) * cdiv(p.K, Shape<TD>::BN) >= 128 ? 32 : 8;
+  return min(run, max(1, tiles / kXcd));           // (a short list: equal runs)
 }
 
 // The tiles of a workgroup as one stream of stages.  Loads run two stages ahead of the multiplication, across
@@ -692,8 +700,7 @@ __global__ __launch_bounds__(NT, Shape<TD>::kPerCu) void dense_grouped_gemm_kern
   for (int64_t round = 0;; ++round) {
     const TileList list(lds);
     build_list<MODE, TYPE == kInt8 ? 1 : 2, TD>(p, list);
-    // a short list is spread over the XCDs in equal runs
-    const int chunk = min(kRun<MODE>, max(1, list.first[list_entries<MODE>(p)] / kXcd));
+    const int chunk = run_tiles<MODE, TD>(p, list.first[list_entries<MODE>(p)]);
     const int64_t b = blockIdx.x + gridDim.x * (64 * round + (threadIdx.x & 63));
     Tile mine;
     const bool have = b <= 0x3FFFFFFF && locate<MODE, TD>(p, list, list_position((int)b, chunk), mine);
