@@ -319,3 +319,22 @@ def test_8_bit_moments_equal_any_fp32_implementation():
             if k == "m":                              # -0 and 0 are the same value
                 got, want = np.where(got == 128, 0, got), np.where(want == 128, 0, want)
             assert np.array_equal(got, want), (step, k, int((got != want).sum()))
+
+
+def test_tensor_beyond_32_bits():
+    """The last elements of a tensor of more than 2^32 elements step as they would alone."""
+    m = require_gpu()
+    n = (1 << 32) + 1000
+    k = 128 * 9 + n % 128                         # whole blocks of 128 and the last, short one
+    p = torch.full((n,), 0.5, device="cuda")
+    g = torch.empty(n, device="cuda", dtype=torch.bfloat16).fill_(0.25)
+    g[-k:] = torch.randn(k, device="cuda").bfloat16()
+    mq, vq = (torch.zeros(n, device="cuda", dtype=torch.uint8) for _ in range(2))
+    ms, vs = (torch.zeros((n + 127) // 128, device="cuda") for _ in range(2))
+    tail = [t[-k:].clone() for t in (p, g, mq, vq)] + [t[-((k + 127) // 128):].clone() for t in (ms, vs)]
+    for a in ((p, g, mq, vq, ms, vs), tail):
+        table = m.adamw_table([a[0]], [a[1]], [a[2]], [a[3]], exp_avg_scales=[a[4]], exp_avg_sq_scales=[a[5]])
+        m.adamw_step(table, 1, 1e-2)
+    assert torch.equal(p[-k:], tail[0]) and torch.equal(mq[-k:], tail[2]) and torch.equal(vq[-k:], tail[3])
+    out = m.adamw_dequantize(mq, ms, "exp_avg", "bf16")
+    assert torch.equal(out[-k:], m.adamw_dequantize(tail[2], tail[4], "exp_avg", "bf16"))

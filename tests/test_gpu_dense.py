@@ -343,3 +343,36 @@ def test_few_rows_over_many_experts(rows):
         if o[g + 1] > o[g]:
             a, b = x[o[g]:o[g + 1]].double(), w[g * N:(g + 1) * N].double().t().contiguous()
             assert bool(((y[o[g]:o[g + 1]] - a @ b).abs() <= 1e-5 * (a.abs() @ b.abs())).all()), g
+
+
+def test_operands_and_outputs_beyond_32_bits():
+    """Weights, weight gradients and activations of more than 4 GiB: the last expert's rows are right."""
+    m = require_gpu()
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    G, N, K = 40, 8192, 8200
+    w = torch.empty((G * N, K), device="cuda", dtype=torch.bfloat16).normal_(generator=gen)
+    for rows in (20, 700):                       # (few rows, whole tiles)
+        offs = torch.zeros(G + 1, device="cuda", dtype=torch.int32)
+        offs[-1] = rows
+        x = torch.randn(rows, K, device="cuda", generator=gen).bfloat16()
+        dy = torch.randn(rows, N, device="cuda", generator=gen).bfloat16()
+        last = w[-N:].float()
+        for got, a, b in ((m.bf16_grouped_gemm_fwd(x, w, offs, N), x, last.t().contiguous()),
+                          (m.bf16_grouped_gemm_dgrad(dy, w, offs, K), dy, last)):
+            a, b = a[-3:].double(), b.double()
+            assert bool(((got[-3:].double() - a @ b).abs() <= 1e-5 * (a.abs() @ b.abs())).all())
+        dw = m.bf16_grouped_gemm_wgrad(dy, x, offs, "bf16")
+        a, b = dy[:, -5:].double().t().contiguous(), x.double()
+        tol = 1e-5 * (a.abs() @ b.abs())
+        assert bool(((dw[-1, -5:].double() - a @ b).abs() <= tol + 2.0 ** -8 * ((a @ b).abs() + tol)).all())
+        assert not bool(dw[-2].any())
+        del dw
+    del w
+    # rows of activations past 4 GiB
+    rows, N, K = 300000, 64, 8192
+    x = torch.empty((rows, K), device="cuda", dtype=torch.bfloat16).normal_(generator=gen)
+    w = torch.randn(2 * N, K, device="cuda", generator=gen).bfloat16()
+    offs = torch.tensor([0, 1, rows], device="cuda", dtype=torch.int32)
+    y = m.bf16_grouped_gemm_fwd(x, w, offs, N)
+    a, b = x[-300:].double(), w[N:].double().t().contiguous()
+    assert bool(((y[-300:].double() - a @ b).abs() <= 1e-5 * (a.abs() @ b.abs())).all())

@@ -238,3 +238,16 @@ def test_gemm_few_rows_over_many_experts(rows):
             r, c = slice(o[g], o[g + 1]), slice(g * N, (g + 1) * N)
             ref = (qx[r].double() @ qw[c].double().t().contiguous()) * sx[r].double()[:, None] * sw[c].double()
             assert bool(((y[r] - ref).abs() <= 2.0 ** -22 * ref.abs()).all()), g
+
+
+def test_rowwise_beyond_32_bits():
+    """The last rows of a tensor of more than 2^32 elements have the codes that they have alone."""
+    m = require_gpu()
+    R, C = 530000, 8208
+    x = torch.empty((R, C), device="cuda", dtype=torch.bfloat16).normal_()
+    q, s = m.int8_quantize_rowwise(x)
+    q1, s1 = m.int8_quantize_rowwise(x[-7:].clone())
+    assert torch.equal(q[-7:], q1) and torch.equal(s[-7:], s1)
+    q, s = m.int8_quantize_swiglu_rowwise(x)
+    q1, s1 = m.int8_quantize_swiglu_rowwise(x[-7:].clone())
+    assert torch.equal(q[-7:], q1) and torch.equal(s[-7:], s1)
