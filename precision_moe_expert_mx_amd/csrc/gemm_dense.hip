@@ -709,7 +709,8 @@ __global__ __launch_bounds__(NT, Shape<TD>::kPerCu) void dense_grouped_gemm_kern
     const int64_t b = blockIdx.x + gridDim.x * (64 * round + (threadIdx.x & 63));
     Tile mine;
     const bool have = b <= 0x3FFFFFFF && locate<MODE, TD>(p, list, list_position((int)b, chunk), mine);
-    const int count = __popcll(__ballot(have));    // positions grow with b: the first `count` lanes have a tile
+    // (b grows by a multiple of the XCDs, so list positions grow too: the first `count` lanes have a tile)
+    const int count = __popcll(__ballot(have));
     __syncthreads();                               // the list's LDS is reused for operands
     if (count == 0) return;
     Runner<MODE, TYPE, TD>(p, lds, mine).run(count);
@@ -723,8 +724,11 @@ static_assert(kListBytes <= Shape<2>::kLds && kListBytes <= Shape<4>::kLds, "the
 template <int MODE, int TYPE, int TD>
 hipError_t launch_tiles(const GemmArgs& p, int64_t tiles, int cus, hipStream_t st) {
   if (tiles > 0x3FFFFFFF) return hipErrorInvalidValue;
-  // (positions of a list of T tiles lie below 2 T + 8, see list_position and its chunk)
-  const dim3 grid((unsigned)min((int64_t)cus * Shape<TD>::kPerCu, 2 * tiles + 8));
+  // Positions of a list of T tiles lie below 2 T + 8 (list_position and its chunk).  Whole rounds over the XCDs: a
+  // workgroup then stays on one, so that its list positions grow, whatever the offsets hold (out of order they can
+  // list more tiles than `tiles`).
+  const int64_t most = max(kXcd, cus * Shape<TD>::kPerCu / kXcd * kXcd);
+  const dim3 grid((unsigned)min(most, (2 * tiles + 8 + kXcd - 1) / kXcd * kXcd));
   hipLaunchKernelGGL((dense_grouped_gemm_kernel<MODE, TYPE, TD>), grid, dim3(NT), 0, st, p);
   return hipGetLastError();
 }
