@@ -22,6 +22,8 @@
 namespace mxmoe {
 namespace {
 
+typedef unsigned short v2us __attribute__((ext_vector_type(2)));
+
 constexpr int NT = 256;
 constexpr int kMaxChunks = 4;                     // 16-byte chunks (8 elements) per lane and operand
 
@@ -33,7 +35,8 @@ __device__ __forceinline__ void unpack8(uint4 v, float (&f)[8]) {
 }
 // fp32 SwiGLU with the hardware exponential and reciprocal.  In units of 2^-24: e^-g is off by 2 (the
 // exponential, one unit in the last place) and 1.4 |g| (the rounding of g log2(e) and of log2(e)), 1 + e^-g by 1
-// more, the reciprocal by 2, the two products by 1 each: 7 + 1.4 |g|.
+// more, the reciprocal by 2, the two products by 1 each: 7 + 1.4 |g|.  That holds for g >= -87; below, e^-g
+// overflows or its reciprocal is subnormal, and so is g / 2 of a |g| below 2^-124: then |v| <= 1.5e-36 |u|.
 __device__ __forceinline__ float swiglu32(float g, float u) {
   return g * __builtin_amdgcn_rcpf(1.0f + __expf(-g)) * u;
 }
@@ -120,6 +123,7 @@ __global__ __launch_bounds__(NT, GATED && WPR == 2 ? 3 : 4) void int8_rowwise_ke
 
   // the magnitude bits of a float order like its value, and a NaN's above every finite value's
   uint32_t m = 0;
+  v2us um = {0, 0};                                // SwiGLU: this lane's largest |u| as bf16 bits, in two halves
   for (int64_t seg = 0; seg < nseg; ++seg) {
     load(seg);
 #pragma unroll
@@ -127,6 +131,9 @@ __global__ __launch_bounds__(NT, GATED && WPR == 2 ? 3 : 4) void int8_rowwise_ke
       if constexpr (GATED) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) m = max(m, __float_as_uint(h[k][e]) & 0x7FFFFFFFu);
+        const uint32_t uv[4] = {b[k].x, b[k].y, b[k].z, b[k].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) um = __builtin_elementwise_max(um, __builtin_bit_cast(v2us, uv[e] & 0x7FFF7FFFu));
       } else {
         const uint32_t wv[4] = {a[k].x, a[k].y, a[k].z, a[k].w};
 #pragma unroll
@@ -138,13 +145,18 @@ __global__ __launch_bounds__(NT, GATED && WPR == 2 ? 3 : 4) void int8_rowwise_ke
   float amax = __uint_as_float(m);
 
   // SwiGLU: the row's maximum in fp64, among the elements that can be it (fp32 value within 4e-5 of the
-  // fp32 maximum; all of them when that maximum is so small that an element may have vanished in fp32)
+  // fp32 maximum; all of them when that maximum is so small that an element may have vanished in fp32, and all of
+  // a lane's when one of its |u| is so large that a value which fp32 does not hold to the bound above could count:
+  // without such a one they are below 1.5e-3 of the maximum, and their codes 0 either way; the test takes 1-4%)
   double amax64 = 0;
   const bool finite = m < 0x7F800000u;
   const bool tiny = GATED && amax < 1e-30f;
+  bool lost = false;                               // (in some lane of the wave)
   if constexpr (GATED) {
     if (finite) {
-      const float cand = tiny ? 0.0f : amax * (1.0f - 4e-5f);
+      const bool mine = __uint_as_float((uint32_t)max(um[0], um[1]) << 16) > 1e33f * amax;
+      lost = __ballot(mine) != 0;
+      const float cand = tiny || mine ? 0.0f : amax * (1.0f - 4e-5f);
       for (int64_t seg = 0; seg < nseg; ++seg) {
         if (nseg > 1) load(seg);
         uint32_t some = 0;                         // this lane's candidates, a bit each
@@ -181,7 +193,7 @@ __global__ __launch_bounds__(NT, GATED && WPR == 2 ? 3 : 4) void int8_rowwise_ke
   // 127 v / amax.  Plain rows: v and amax are first moved by a power of two so that the reciprocal stays
   // normal; a product and one correction.  SwiGLU: one product, rounded by adding 1.5 * 2^23 in the same
   // instruction (the code is then the low byte); the elements nearer to a border than fp32 can tell are
-  // evaluated again in fp64 below, those of a row so small that fp32 lost them all.  A factor of 0 gives
+  // evaluated again in fp64 below, all of them where fp32 may have lost some.  A factor of 0 gives
   // codes 0 (NaN converts to 0; in the sum it leaves a low byte that is not used).
   const float mv = amax < 0x1p-60f ? 0x1p64f : (amax > 0x1p60f ? 0x1p-64f : 1.0f);
   const float den = amax * mv, num = dead ? 0.0f : 127.0f * mv, rc = __builtin_amdgcn_rcpf(den);
@@ -222,7 +234,7 @@ __global__ __launch_bounds__(NT, GATED && WPR == 2 ? 3 : 4) void int8_rowwise_ke
     }
     if constexpr (GATED) {
       if (dead || !live) some = 0;
-      else if (tiny) some = (uint32_t)((1ull << (8 * NCH)) - 1);
+      else if (tiny || lost) some = (uint32_t)((1ull << (8 * NCH)) - 1);
       for (; some; some &= some - 1) {
         const int bit = __builtin_ctz(some);
         const int64_t c = seg * kSeg + 8 * (l + 64 * WPR * (bit >> 3)) + (bit & 7);

@@ -6,6 +6,7 @@ import torch
 
 import oracle
 from gpu_util import dev, host, require_gpu
+from workloads import f32_to_bf16_bits
 
 pytestmark = pytest.mark.gpu
 
@@ -35,3 +36,54 @@ def test_offsets_out_of_order_list_more_tiles_than_a_small_launch_counts(G, M):
         assert bool(((got[:-4096].view(M, -1).double() - a @ b).abs() <= 1e-5 * (a.abs() @ b.abs())).all())
     ref = (qx.double() @ qw.double().t().contiguous()) * sx.double()[:, None] * sw.double()
     assert bool(((y8[:-4096].view(M, N).double() - ref).abs() <= 2.0 ** -22 * ref.abs()).all())
+
+
+def _swiglu_codes(y):
+    """Float64 codes and scales of silu(gate) * up of bf16 bit patterns [R, 2C]."""
+    g, u = np.split(oracle.bf16_bits_to_f64(y), 2, axis=1)
+    with np.errstate(over="ignore"):
+        return oracle.int8_quantize_rows(g / (1 + np.exp(-g)) * u)
+
+
+def _check_swiglu(m, gates, ups):
+    y = f32_to_bf16_bits(np.concatenate([gates, ups], axis=1).astype(np.float32))
+    q, s = m.int8_quantize_swiglu_rowwise(dev(y).view(torch.bfloat16))
+    rq, rs = _swiglu_codes(y)
+    bad = np.flatnonzero((host(q) != rq).any(axis=1))
+    assert bad.size == 0, f"rows {bad[:5]}: {int((host(q) != rq).sum())} codes differ"
+    # both are a float64 value (off by a few 2^-52) rounded to fp32: at most one step apart
+    np.testing.assert_allclose(host(s), rs, rtol=2.0 ** -23, atol=2.0 ** -149)
+
+
+@pytest.mark.parametrize("C", [8, 264, 1408, 2048, 2056, 4104, 9000])
+def test_swiglu_saturated_gates_with_large_ups(C):
+    """e^-g overflows fp32, its reciprocal is subnormal, or g itself is, and an up of 1e3 to 1e38 makes an ordinary
+    value of it, beside ordinary and small ones: the maximum of the row, or a code, or next to nothing."""
+    m = require_gpu()
+    rng = np.random.default_rng(C)
+    R = 48
+    gates, ups = rng.normal(0, 1, (R, C)), rng.normal(0, 1, (R, C)) * 10.0 ** rng.uniform(-9, 0, (R, 1))
+    few = max(1, C // 64)
+    for r in range(R):
+        at = rng.choice(C, few, replace=False)
+        sign = rng.choice([-1.0, 1.0], few)
+        if r % 3 == 2:                               # gates near or below the smallest normal number
+            gates[r, at] = sign * 10.0 ** rng.uniform(-40, -37, few)
+            ups[r, at] = 10.0 ** rng.uniform(3, 38, few)
+        else:                                        # saturated gates; the value at most 1e3
+            g = rng.uniform(-170, -80, few)
+            gates[r, at] = g
+            ups[r, at] = sign * 10.0 ** np.minimum(rng.uniform(3, 38.4, few), 3 - np.log10(-g) - g / np.log(10))
+    _check_swiglu(m, gates, ups)
+
+
+def test_swiglu_saturated_gates_by_hand():
+    m = require_gpu()
+    gates = np.full((5, 8), 1.0)
+    ups = np.zeros((5, 8))
+    gates[0, :2], ups[0, :2] = (-90, 1), (1e32, 1e-6)
+    gates[1, :2], ups[1, :2] = (-88.5, -60), (2e6, 1e-4)
+    gates[2, :2], ups[2, :2] = (1, -89), (1, 9.97e37)
+    gates[3, :2], ups[3, :2] = (1e-39, 1), (3e38, 0.01)
+    gates[4, :2], ups[4, :2] = (-120, -87), (-3e38, 1e-20)
+    _check_swiglu(m, gates, ups)
