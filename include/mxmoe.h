@@ -502,7 +502,7 @@ mxmoe_status int8_grouped_gemm_fwd(const int8_t* qx, const float* sx, const int8
  * kernel arguments allow (48 tensors each):
  *   g' = c g;  m = b1 m + (1 - b1) g';  v = b2 v + (1 - b2) g'^2
  *   p = (1 - lr wd) p - lr (m / (1 - b1^t)) / (sqrt(v / (1 - b2^t)) + eps);  w = bf16(p)
- * in fp32, in place.  The gradients (gdt: f32 or bf16) are what the wgrad entry points write, and the bf16
+ * in fp32, in place (tables of more than 2^36 elements also take more launches).  The gradients (gdt: f32 or bf16) are what the wgrad entry points write, and the bf16
  * copies w what the quantisers and the bf16 GEMMs read.  state_bits 32: m, v are f32 and ms, vs unused.
  * state_bits 8: m, v are one byte per element with one f32 scale per 128 consecutive elements (ms, vs
  * [ceil(n / 128)]); all-zero codes and scales are zero moments:
@@ -514,7 +514,7 @@ mxmoe_status int8_grouped_gemm_fwd(const int8_t* qx, const float* sx, const int8
  * replays with the values given here, except those read on the device: *lr_dev (f32) replaces lr and
  * *step_dev (int64, >= 1) replaces step when not NULL, and *grad_scale (f32) is c (1 when NULL). */
 typedef struct {
-  int64_t n;          /* elements, >= 0 */
+  int64_t n;          /* elements, 0 .. 2^36 - 4096 */
   float* p;           /* weights, f32 [n] */
   void* w_bf16;       /* bf16 copy [n], or NULL */
   const void* g;      /* gradient [n], f32 or bf16 */

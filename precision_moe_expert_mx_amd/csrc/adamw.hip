@@ -19,6 +19,8 @@
 // 128 and meet for its two maxima by lane permutes; every byte is touched once, non-temporally.  Measured
 // on 235M elements with fp32 / bf16 gradients: fp32 moments 5.56 / 5.59 TB/s (1268 / 1177 us), 8-bit moments
 // 5.48 / 5.45 (777 / 695 us).
+#include <algorithm>
+
 #include "plain.h"
 
 namespace mxmoe {
@@ -242,6 +244,7 @@ __global__ __launch_bounds__(NT) void adamw_kernel(AdamwArgs p) {
 // Values of 8-bit moments: a lane's two groups of eight consecutive elements (8-byte reads, 16- or 32-byte
 // writes), 2048 elements apart.  Bound: HBM, 3 or 5 bytes per element.
 constexpr int kGroup = 8, kGroups = 2;
+static_assert(NT * kGroup * kGroups % 128 == 0, "whole scales");
 template <bool SECOND, bool BF16>
 __global__ __launch_bounds__(NT) void adamw_values_kernel(const uint8_t* __restrict__ q, const float* __restrict__ s,
                                                           int64_t n, void* __restrict__ out) {
@@ -296,7 +299,7 @@ __global__ __launch_bounds__(NT) void adamw_values_kernel(const uint8_t* __restr
 }  // namespace
 
 // 1024 elements while that leaves few blocks (small tensors: as many CUs as there are pieces), else 4096
-int32_t adamw_elements_per_block(int64_t total) { return total <= 4096 ? kIter : 4 * kIter; }
+int32_t adamw_elements_per_block(int64_t total) { return total <= 4096 ? kIter : kAdamwBlock; }
 
 hipError_t launch_adamw(const AdamwArgs& p, int blocks, bool eight, bool gbf16, hipStream_t st) {
   const dim3 g((unsigned)blocks), b(NT);
@@ -309,13 +312,18 @@ hipError_t launch_adamw(const AdamwArgs& p, int blocks, bool eight, bool gbf16, 
 
 hipError_t launch_adamw_values(const uint8_t* q, const float* s, int64_t n, bool second, bool bf16, void* out,
                                hipStream_t st) {
-  const int64_t per = NT * kGroup * kGroups, grid = (n + per - 1) / per;
-  if (grid > 0x7FFFFFFF) return hipErrorInvalidValue;
-  const dim3 g((unsigned)grid), b(NT);
-  if (second && bf16) hipLaunchKernelGGL((adamw_values_kernel<true, true>), g, b, 0, st, q, s, n, out);
-  else if (second) hipLaunchKernelGGL((adamw_values_kernel<true, false>), g, b, 0, st, q, s, n, out);
-  else if (bf16) hipLaunchKernelGGL((adamw_values_kernel<false, true>), g, b, 0, st, q, s, n, out);
-  else hipLaunchKernelGGL((adamw_values_kernel<false, false>), g, b, 0, st, q, s, n, out);
+  constexpr int64_t per = NT * kGroup * kGroups;             // (whole blocks of 128)
+  auto go = [&](auto kernel) {
+    for (int64_t i = 0; i < n; i += per * kMaxBlocks) {
+      const int64_t k = std::min(n - i, per * kMaxBlocks);
+      hipLaunchKernelGGL(kernel, dim3((unsigned)((k + per - 1) / per)), dim3(NT), 0, st, q + i, s + i / 128, k,
+                         (void*)((char*)out + i * (bf16 ? 2 : 4)));
+    }
+  };
+  if (second && bf16) go(adamw_values_kernel<true, true>);
+  else if (second) go(adamw_values_kernel<true, false>);
+  else if (bf16) go(adamw_values_kernel<false, true>);
+  else go(adamw_values_kernel<false, false>);
   return hipGetLastError();
 }
 

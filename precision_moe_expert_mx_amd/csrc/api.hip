@@ -868,8 +868,8 @@ mxmoe_status adamw_step(const mxmoe_adamw_tensor* tensors, int32_t count, mxmoe_
   int64_t total = 0;
   for (int32_t k = 0; k < count; ++k) {
     const mxmoe_adamw_tensor& t = tensors[k];
-    if (t.n < 0 || t.n > ((int64_t)1 << 40))
-      return fail(MXMOE_ERR_SHAPE, "%s: tensor %d has n = %lld", fn, (int)k, (long long)t.n);
+    if (t.n < 0 || t.n > kMaxBlocks * kAdamwBlock)
+      return fail(MXMOE_ERR_SHAPE, "%s: tensor %d has n = %lld, outside [0, 2^36 - 4096]", fn, (int)k, (long long)t.n);
     if (t.n == 0) continue;
     const void* need[4] = {t.p, t.g, t.m, t.v};
     for (const void* q : need) {
@@ -906,7 +906,7 @@ mxmoe_status adamw_step(const mxmoe_adamw_tensor* tensors, int32_t count, mxmoe_
     for (; k < count && p.count < kAdamwTensors; ++k) {
       if (tensors[k].n == 0) continue;
       const int64_t nb = (tensors[k].n + p.per - 1) / p.per;
-      if (blocks + nb > INT32_MAX) break;
+      if (blocks + nb > kMaxBlocks) break;
       p.t_[p.count] = tensors[k];
       p.first[p.count++] = (int32_t)blocks;
       blocks += nb;

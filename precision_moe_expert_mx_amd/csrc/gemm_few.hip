@@ -7,6 +7,7 @@
 // the registers of v_mfma_f32_16x16x32_bf16 / v_mfma_i32_16x16x64_i8 (lane l: column l % 16, 16 bytes at
 // 64 k + 16 (l / 16) of its row), eight loads in flight per wave and several workgroups per CU.  The rows
 // of X come the same way (they stay in L2).  An expert's rows are taken 32 at a time.
+#include <algorithm>
 #include <type_traits>
 
 #include "plain.h"
@@ -142,7 +143,7 @@ __global__ __launch_bounds__(NT) void few_rows_kernel(GemmArgs p, int blocks) {
 // (Rows that all reach one expert cost it more: 512 on one of 64 experts pass its weights, from L2, 16 times.)
 bool few_rows(const GemmArgs& p) {
   const int64_t columns = (p.N + 255) / 256;
-  if (min((int64_t)p.G, p.M) * columns <= 128) return p.M * p.N <= 3 << 16;
+  if (std::min((int64_t)p.G, p.M) * columns <= 128) return p.M * p.N <= 3 << 16;
   return p.M <= 8 * (int64_t)p.G && p.ldb >= 4096 && p.G * columns < 1024;
 }
 
@@ -152,7 +153,7 @@ hipError_t launch_few_rows_gemm(bool int8, const GemmArgs& p, hipStream_t st) {
   // one; 8 experts, N 4096, K 7168, 8 rows: 119 against 107).
   const int nc = p.M > 4 * (int64_t)p.G && p.G * p.N >= 32 * 4096 ? 2 : 1;
   const int64_t blocks = (p.N + 16 * nc - 1) / (16 * nc);
-  if (blocks * p.G > 0x7FFFFFFF) return hipErrorInvalidValue;
+  if (blocks * p.G > kMaxBlocks) return hipErrorInvalidValue;
   const dim3 g((unsigned)(blocks * p.G)), b(NT);
   if (int8 && nc == 2) hipLaunchKernelGGL((few_rows_kernel<true, 2>), g, b, 0, st, p, (int)blocks);
   else if (int8) hipLaunchKernelGGL((few_rows_kernel<true, 1>), g, b, 0, st, p, (int)blocks);

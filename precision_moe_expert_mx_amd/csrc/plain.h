@@ -6,6 +6,9 @@
 
 namespace mxmoe {
 
+// A launch has fewer than 2^32 threads (one of more starts a part of them, without an error): workgroups of 256.
+constexpr int64_t kMaxBlocks = (1 << 24) - 1;
+
 // plain operands: bf16 (all modes; leading dimensions in bytes), or int8 forward (sa, sb: fp32 row scales)
 hipError_t launch_dense_gemm(int mode, bool int8, const GemmArgs& a, hipStream_t st);
 // the same forward for few rows per expert, and whether a call is of that kind
@@ -32,7 +35,8 @@ struct AdamwArgs {
   const float* grad_scale;
 };
 static_assert(sizeof(AdamwArgs) <= 4096, "kernel arguments");
-// elements of a block, for `total` pieces of 1024 over all tensors
+// elements of a block (at most kAdamwBlock), for `total` pieces of 1024 over all tensors
+constexpr int32_t kAdamwBlock = 4096;
 int32_t adamw_elements_per_block(int64_t total);
 hipError_t launch_adamw(const AdamwArgs& p, int blocks, bool eight, bool gbf16, hipStream_t st);
 hipError_t launch_adamw_values(const uint8_t* q, const float* s, int64_t n, bool second, bool bf16, void* out,

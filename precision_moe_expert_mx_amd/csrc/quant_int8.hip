@@ -17,6 +17,8 @@
 // fit, and no memory access in the usual chain (a candidate's values are kept, not read again: 4.4 -> 6 TB/s).
 // Measured: 65536 x 7168 plain 6.3 TB/s; SwiGLU 65536 x 2048 5.6-6.0, 32768 x 8192 5.9, 49152 x 1408 4.7,
 // 49152 x 1024 3.4 (the work per row, not per element, counts there).
+#include <algorithm>
+
 #include "plain.h"
 
 namespace mxmoe {
@@ -252,9 +254,13 @@ hipError_t launch_int8_rowwise(const uint16_t* x, int64_t R, int64_t C, bool gat
   const int wpr = C <= 512 * kMaxChunks ? 1 : (C <= 1024 * kMaxChunks ? 2 : 4);
   const int nch = wpr == 1 ? (int)((C + 511) / 512) : kMaxChunks;
   const int64_t per = NT / 64 / wpr;
-  const int64_t grid = (R + per - 1) / per;
-  if (grid > 0x7FFFFFFF) return hipErrorInvalidValue;
-  auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(NT), 0, st, x, R, C, q, s); };
+  auto go = [&](auto kernel) {
+    for (int64_t r = 0; r < R; r += per * kMaxBlocks) {
+      const int64_t n = std::min(R - r, per * kMaxBlocks);
+      hipLaunchKernelGGL(kernel, dim3((unsigned)((n + per - 1) / per)), dim3(NT), 0, st, x + r * (gated ? 2 * C : C), n, C,
+                         q + r * C, s + r);
+    }
+  };
   if (gated) {
     if (wpr == 4) go(int8_rowwise_kernel<true, 4, 4>);
     else if (wpr == 2) go(int8_rowwise_kernel<true, 2, 4>);

@@ -87,3 +87,36 @@ def test_swiglu_saturated_gates_by_hand():
     gates[3, :2], ups[3, :2] = (1e-39, 1), (3e38, 0.01)
     gates[4, :2], ups[4, :2] = (-120, -87), (-3e38, 1e-20)
     _check_swiglu(m, gates, ups)
+
+
+def test_quantisers_of_more_rows_than_a_launch_has_workgroups():
+    m = require_gpu()
+    R, C = (1 << 26) + 1001, 8
+    x = torch.randint(0, 1 << 14, (R, 2 * C), device="cuda", dtype=torch.int16)      # finite magnitudes below 2
+    for fn, y in ((m.int8_quantize_rowwise, x[:, :C].contiguous()), (m.int8_quantize_swiglu_rowwise, x)):
+        q, s = fn(y)
+        for part in (slice(0, 9), slice((1 << 26) - 9, (1 << 26) + 9), slice(R - 9, R)):
+            q1, s1 = fn(y[part].contiguous())
+            assert torch.equal(q[part], q1) and torch.equal(s[part], s1)
+        del q, s
+
+
+def test_values_of_more_moments_than_a_launch_has_workgroups():
+    m = require_gpu()
+    n = (1 << 36) + 5001
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < 3.1 * n:
+        pytest.skip("needs 213 GB of GPU memory")
+    q = torch.empty(n, dtype=torch.uint8, device="cuda")
+    s = torch.empty(-(-n // 128), device="cuda")
+    out = torch.empty(n, dtype=torch.bfloat16, device="cuda")
+    k = 128 * 80 + n % 128
+    for part, scales in ((slice(0, 128 * 9), slice(0, 9)), (slice(n - k, n), slice(-81, None))):
+        q[part].random_(0, 127)                      # (no NaN codes)
+        s[scales].uniform_(0.5, 2)
+    for name in ("exp_avg", "exp_avg_sq"):
+        m.adamw_dequantize(q, s, name, "bf16", out=out)
+        for part, scales in ((slice(0, 128 * 9), slice(0, 9)), (slice(n - k, n), slice(-81, None))):
+            assert torch.equal(out[part], m.adamw_dequantize(q[part].clone(), s[scales].clone(), name, "bf16"))
+    del q, s, out
+    torch.cuda.empty_cache()
