@@ -31,6 +31,7 @@
 // lanes read 4 rows x 16 columns and each gets one column's 4 values), so no operand is ever transposed in
 // memory.  The row fragments of a tile alternate between the two row halves of the waves, and fragments
 // without valid rows are skipped, so that a tile of few rows costs what its rows do, 64 at a time.
+#include <algorithm>
 #include <type_traits>
 
 #include "grouped_tile.h"
@@ -727,8 +728,8 @@ hipError_t launch_tiles(const GemmArgs& p, int64_t tiles, int cus, hipStream_t s
   // Positions of a list of T tiles lie below 2 T + 8 (list_position and its chunk).  Whole rounds over the XCDs: a
   // workgroup then stays on one, so that its list positions grow, whatever the offsets hold (out of order they can
   // list more tiles than `tiles`).
-  const int64_t most = max(kXcd, cus * Shape<TD>::kPerCu / kXcd * kXcd);
-  const dim3 grid((unsigned)min(most, (2 * tiles + 8 + kXcd - 1) / kXcd * kXcd));
+  const int64_t most = std::max(kXcd, cus * Shape<TD>::kPerCu / kXcd * kXcd);
+  const dim3 grid((unsigned)std::min(most, (2 * tiles + 8 + kXcd - 1) / kXcd * kXcd));
   hipLaunchKernelGGL((dense_grouped_gemm_kernel<MODE, TYPE, TD>), grid, dim3(NT), 0, st, p);
   return hipGetLastError();
 }
@@ -742,7 +743,7 @@ hipError_t launch_mode(const GemmArgs& p, hipStream_t st) {
   auto count = [&](int64_t bm, bool most) -> int64_t {   // tiles of bm x bm outputs: at most, or about
     const int64_t ntc = ((MODE == kFwd ? p.N : p.K) + bm - 1) / bm;
     if (MODE == kWgrad) return p.G * ((p.N + bm - 1) / bm) * ntc;
-    return ((p.M + bm - 1) / bm + (most ? p.G : min((int64_t)p.G, p.M) / 2)) * ntc;
+    return ((p.M + bm - 1) / bm + (most ? p.G : std::min((int64_t)p.G, p.M) / 2)) * ntc;
   };
   // 128 x 128 tiles where 256 x 256 ones would leave CUs idle.  In units of a round of large tiles, c small ones per
   // CU take about 0.2 + 0.33 c; measured, 256 against 128, us (tiles): 7 experts of 5003 rows, N 1000, K 1120:
