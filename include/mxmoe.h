@@ -490,7 +490,9 @@ mxmoe_status int8_quantize_swiglu_rowwise(const void* y_bf16, int64_t R, int64_t
                                           void* stream);
 
 /* int8_grouped_gemm_fwd: Y[r, n] = (sum_k qx[r, k] qw[gN + n, k]) * sx[r] * sw[gN + n]: the sum is exact (int32),
- * then one fp32 conversion and two fp32 products (|err| <= 2^-22 |Y|, plus half a bf16 ulp for bf16 outputs).
+ * then one fp32 conversion and the products by sx and by sw in this order (|err| <= 2^-22 |Y|, plus 2^-149, plus half a
+ * bf16 ulp for bf16 outputs).  sum * sx has to stay in the fp32 range (with the scales of int8_quantize_rowwise, tokens
+ * below 1e31 do; a sum of zero gives zero for every finite sx and sw).
  * qx [M, K], qw [G*N, K] int8 (any codes, -128 included), sx [M], sw [G*N] f32.  K % 16 == 0, K < 131072 (the
  * int32 sum), N % 8 == 0, 1 <= G <= 1024; M == 0 is a no-op. */
 mxmoe_status int8_grouped_gemm_fwd(const int8_t* qx, const float* sx, const int8_t* qw, const float* sw,

@@ -681,7 +681,7 @@ struct Runner {
               const float4 c4 = col_scale[8 * j + 2 * q + (lane >> 5)];
               c = e == 0 ? c4.x : e == 1 ? c4.y : e == 2 ? c4.z : c4.w;
             }
-            return (float)acc[i][j][4 * q + e] * (row_scale[i] * c);
+            return (float)acc[i][j][4 * q + e] * row_scale[i] * c;
           } else {
             return acc[i][j][4 * q + e];
           }

@@ -112,7 +112,7 @@ __global__ __launch_bounds__(NT) void few_rows_kernel(GemmArgs p, int blocks) {
           const float sx = ((const float*)p.sa)[row];
           const float* sw = (const float*)p.sb + (int64_t)g * p.N + col;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) v[e] = (float)s[e] * (sx * sw[e]);
+          for (int e = 0; e < 4; ++e) v[e] = (float)s[e] * sx * sw[e];
         } else {
 #pragma unroll
           for (int e = 0; e < 4; ++e) v[e] = s[e];

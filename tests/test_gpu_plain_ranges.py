@@ -6,7 +6,7 @@ import torch
 
 import oracle
 from gpu_util import dev, host, require_gpu
-from workloads import f32_to_bf16_bits
+from workloads import f32_to_bf16_bits, routing_offsets
 
 pytestmark = pytest.mark.gpu
 
@@ -120,3 +120,31 @@ def test_values_of_more_moments_than_a_launch_has_workgroups():
             assert torch.equal(out[part], m.adamw_dequantize(q[part].clone(), s[scales].clone(), name, "bf16"))
     del q, s, out
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("sizes,N,K", [([1, 0, 2], 264, 4096), ([300, 5, 700], 520, 1008), ([1500, 1, 2000], 4104, 208)])
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_int8_scales_whose_product_leaves_fp32(sizes, N, K, dt):
+    """Scales whose product is subnormal or overflows while the output does not, and sums of zero beside them."""
+    m = require_gpu()
+    rng = np.random.default_rng(N)
+    offs = routing_offsets(np.asarray(sizes))
+    M, G = int(offs[-1]), len(sizes)
+    qx, qw = rng.integers(-128, 128, (M, K)).astype(np.int8), rng.integers(-128, 128, (G * N, K)).astype(np.int8)
+    qx[::3] = 0                                      # sums of zero
+    for top in (-41.0, 41.0):                        # log10 of the product of the scales
+        a = rng.uniform(8, 28, M)
+        sx = (10.0 ** (np.sign(top) * a)).astype(np.float32)
+        sw = (10.0 ** rng.uniform(0, 1, G * N) * 10.0 ** (top / 2)).astype(np.float32)
+        if top > 0:
+            qx[1::3], sx[1::3] = 0, 1e30             # (rows that are not zero would overflow)
+            qx[2::3], sx[2::3] = 0, 1e25
+        y = m.int8_grouped_gemm_fwd(dev(qx), dev(sx), dev(qw), dev(sw), dev(offs), N, dt)
+        ref = oracle.int8_gemm_fwd(qx, sx, qw, sw, offs, N)
+        ok = np.abs(ref) < 3e38
+        rel = 2.0 ** -22 + (2.0 ** -8 if dt == "bf16" else 0)
+        got = y.float().cpu().numpy().astype(np.float64)
+        # below the smallest normal number an output is off by half a subnormal step of its type
+        err = np.abs(got - ref)
+        tiny = 2.0 ** -149 if dt == "f32" else 2.0 ** -133
+        assert (err <= rel * np.abs(ref) + tiny)[ok].all()
