@@ -186,8 +186,9 @@ __global__ __launch_bounds__(NT) void adamw_kernel(AdamwArgs p) {
     for (int e = 0; e < kVec; ++e) {
       moments(m[e], v[e], g[e], c);
       // hardware square root and reciprocal (one unit in the last place each, of an update that is far
-      // smaller than the weight)
-      const float root = __builtin_amdgcn_sqrtf(v[e] * c.inv_bc2) + c.eps;
+      // smaller than the weight); the root takes subnormal numbers for zero, so a small v is moved up first
+      const bool small = v[e] < 0x1p-64f;
+      const float root = __builtin_amdgcn_sqrtf((small ? v[e] * 0x1p64f : v[e]) * c.inv_bc2) * (small ? 0x1p-32f : 1.0f) + c.eps;
       w[e] = fmaf(-c.step * m[e], __builtin_amdgcn_rcpf(root), w[e] * c.decay);
     }
     if constexpr (EIGHT) {

@@ -10,6 +10,8 @@ from workloads import f32_to_bf16_bits, routing_offsets
 
 pytestmark = pytest.mark.gpu
 
+U = 2.0 ** -24                     # half a step of fp32, relative
+
 
 @pytest.mark.parametrize("G,M", [(6, 6144), (7, 6272), (49, 768)])
 def test_offsets_out_of_order_list_more_tiles_than_a_small_launch_counts(G, M):
@@ -148,3 +150,29 @@ def test_int8_scales_whose_product_leaves_fp32(sizes, N, K, dt):
         err = np.abs(got - ref)
         tiny = 2.0 ** -149 if dt == "f32" else 2.0 ** -133
         assert (err <= rel * np.abs(ref) + tiny)[ok].all()
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("size,eps", [(1e-20, 1e-30), (3e-19, 2.0 ** -126), (1e-22, 1e-25), (1e-12, 1e-20)])
+def test_second_moment_below_the_smallest_normal_number(bits, size, eps):
+    """Gradients whose squares are subnormal: the update divides by their root, not by eps alone.  The moments are
+    the kernel's own fp32 operations; the update of those is off by its own 12 roundings (see the bound of
+    test_gpu_adamw) and the 2 of the first moment's product with the rate."""
+    m = require_gpu()
+    rng = np.random.default_rng(1)
+    n, lr, b1, b2 = 5000, 1e-2, 0.9, 0.95
+    f = np.float32
+    p0 = (0.02 * rng.standard_normal(n)).astype(f)
+    g = (size * rng.standard_normal(n)).astype(f)
+    p, zeros = dev(p0.copy()), lambda k, dt: torch.zeros(k, dtype=dt, device="cuda")  # noqa: E731
+    kind = torch.uint8 if bits == 8 else torch.float32
+    mom, sc = [zeros(n, kind) for _ in range(2)], [zeros(-(-n // 128), torch.float32) for _ in range(2)]
+    table = m.adamw_table([p], [dev(g)], [mom[0]], [mom[1]], exp_avg_scales=[sc[0]] if bits == 8 else None,
+                          exp_avg_sq_scales=[sc[1]] if bits == 8 else None)
+    m.adamw_step(table, 1, lr, beta1=b1, beta2=b2, eps=eps, weight_decay=0.0)
+    m1, v1 = (f(1 - b1) * g).astype(np.float64), (f(1 - b2) * g * g).astype(np.float64)
+    if bits == 32:
+        assert np.array_equal(host(mom[0]), m1.astype(f)) and np.array_equal(host(mom[1]), v1.astype(f))
+    update = lr * (m1 / (1 - b1)) / (np.sqrt(v1 / (1 - b2)) + eps)
+    err = np.abs(host(p).astype(np.float64) - (p0.astype(np.float64) - update))
+    assert (err <= 3 * U * (np.abs(p0) + np.abs(update)) + 14 * U * np.abs(update)).all()
