@@ -511,7 +511,8 @@ mxmoe_status int8_grouped_gemm_fwd(const int8_t* qx, const float* sx, const int8
  *   m: E4M3 codes, scale max(amax / 448, 2^-126)
  *   v: code c = 8 E + f > 0 stands for (1 + f / 8) 2^(E - 31), 0 for zero; scale max(vmax / 1.875, 2^-126)
  * rounded to nearest even, a v > 0 never to zero.  The update itself uses the moments before rounding.  A
- * gradient that is not finite makes its element, and with 8-bit moments its block's scales, not finite.
+ * gradient that is not finite makes its element, and with 8-bit moments its block's scales, not finite, and with them
+ * the block's other elements from the next step on.
  * The tensor table is read during the call (host memory); tensors must not overlap.  A captured call
  * replays with the values given here, except those read on the device: *lr_dev (f32) replaces lr and
  * *step_dev (int64, >= 1) replaces step when not NULL, and *grad_scale (f32) is c (1 when NULL). */

@@ -53,7 +53,7 @@ __device__ __forceinline__ void decode_m(uint32_t w, float s, float (&m)[4]) {
   m[0] = lo[0] * s; m[1] = lo[1] * s; m[2] = hi[0] * s; m[3] = hi[1] * s;
 }
 __device__ __forceinline__ float decode_v1(uint32_t c, float s) {
-  return c ? __uint_as_float((c + 96 * 8) << 20) * s : 0.0f;
+  return (c ? __uint_as_float((c + 96 * 8) << 20) : 0.0f) * s;     // (code 0 too: a scale that is not finite shows)
 }
 __device__ __forceinline__ void decode_v(uint32_t w, float s, float (&v)[4]) {
 #pragma unroll

@@ -176,3 +176,26 @@ def test_second_moment_below_the_smallest_normal_number(bits, size, eps):
     update = lr * (m1 / (1 - b1)) / (np.sqrt(v1 / (1 - b2)) + eps)
     err = np.abs(host(p).astype(np.float64) - (p0.astype(np.float64) - update))
     assert (err <= 3 * U * (np.abs(p0) + np.abs(update)) + 14 * U * np.abs(update)).all()
+
+
+def test_nonfinite_second_moment_shows_in_its_values():
+    """The element whose gradient was not finite has no finite moment, in its codes' values too, and stays so."""
+    m = require_gpu()
+    n = 600
+    z = lambda k, dt=torch.float32: torch.zeros(k, dtype=dt, device="cuda")  # noqa: E731
+    p, g = z(n), torch.randn(n, device="cuda")
+    q, s = [z(n, torch.uint8) for _ in range(2)], [z(5) for _ in range(2)]
+    g[200], g[450] = float("nan"), float("inf")
+    table = m.adamw_table([p], [g], [q[0]], [q[1]], exp_avg_scales=[s[0]], exp_avg_sq_scales=[s[1]])
+    m.adamw_step(table, 1, 1e-3)
+    for k, name in enumerate(("exp_avg", "exp_avg_sq")):
+        for dt in ("f32", "bf16"):
+            v = m.adamw_dequantize(q[k], s[k], name, dt).float().cpu().numpy()
+            assert not np.isfinite(v[[200, 450]]).any(), (name, dt)
+            for b in (0, 2, 4):                      # the other blocks of 128
+                assert np.isfinite(v[128 * b:128 * (b + 1)]).all()
+    g.normal_()
+    m.adamw_step(table, 2, 1e-3)
+    for k, name in enumerate(("exp_avg", "exp_avg_sq")):
+        v = m.adamw_dequantize(q[k], s[k], name).cpu().numpy()
+        assert not np.isfinite(v[[200, 450]]).any(), name
