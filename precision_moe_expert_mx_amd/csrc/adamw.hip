@@ -59,23 +59,32 @@ __device__ __forceinline__ void decode_v(uint32_t w, float s, float (&v)[4]) {
 #pragma unroll
   for (int e = 0; e < 4; ++e) v[e] = decode_v1((w >> (8 * e)) & 255u, s);
 }
-// a / s with r the rounded reciprocal of s: one correction of the product rounds correctly (Markstein).
-__device__ __forceinline__ float quotient(float a, float s, float r) {
-  const float q = a * r;
-  return fmaf(fmaf(-q, s, a), r, q);
-}
-__device__ __forceinline__ uint32_t encode_m(const float (&m)[4], float s, float inv) {
+// a / s with r the rounded reciprocal of s: one correction of the product rounds correctly (Markstein), if the
+// remainder is a normal number: small scales and what they divide are moved up by 2^64 (codes reach down to
+// 2^-32 s, and the remainder to 2^-48 of that).
+struct Divisor {
+  float up, s, r;
+  __device__ __forceinline__ explicit Divisor(float scale)
+      : up(scale < 0x1p-60f ? 0x1p64f : 1.0f), s(scale * up), r(1.0f / s) {}
+  __device__ __forceinline__ float quotient(float v) const {
+    const float a = v * up, q = a * r;
+    return fmaf(fmaf(-q, s, a), r, q);
+  }
+};
+__device__ __forceinline__ uint32_t encode_m(const float (&m)[4], float s) {
+  const Divisor d(s);
   float y[4];
 #pragma unroll
-  for (int e = 0; e < 4; ++e) y[e] = fminf(fmaxf(quotient(m[e], s, inv), -448.0f), 448.0f);
+  for (int e = 0; e < 4; ++e) y[e] = fminf(fmaxf(d.quotient(m[e]), -448.0f), 448.0f);
   int o = __builtin_amdgcn_cvt_pk_fp8_f32(y[0], y[1], 0, false);
   return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(y[2], y[3], o, true);
 }
-__device__ __forceinline__ uint32_t encode_v(const float (&v)[4], float s, float inv) {
+__device__ __forceinline__ uint32_t encode_v(const float (&v)[4], float s) {
+  const Divisor d(s);
   uint32_t w = 0;
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
-    const uint32_t bits = __float_as_uint(quotient(v[e], s, inv));
+    const uint32_t bits = __float_as_uint(d.quotient(v[e]));
     int c = (int)((bits + 0x7FFFFu + ((bits >> 20) & 1u)) >> 20) - 96 * 8;
     c = v[e] > 0.0f ? min(max(c, 1), 255) : 0;
     w |= (uint32_t)c << (8 * e);
@@ -207,8 +216,8 @@ __global__ __launch_bounds__(NT) void adamw_kernel(AdamwArgs p) {
       };
       ms = scale_of(am, 448.0f);
       vs = scale_of(av, kTop);
-      mq = encode_m(m, ms, 1.0f / ms);
-      vq = encode_v(v, vs, 1.0f / vs);
+      mq = encode_m(m, ms);
+      vq = encode_v(v, vs);
       if (left > 0 && (threadIdx.x & 31) == 0) {
         t.ms[i / 128] = ms;
         t.vs[i / 128] = vs;

@@ -199,3 +199,38 @@ def test_nonfinite_second_moment_shows_in_its_values():
     for k, name in enumerate(("exp_avg", "exp_avg_sq")):
         v = m.adamw_dequantize(q[k], s[k], name).cpu().numpy()
         assert not np.isfinite(v[[200, 450]]).any(), name
+
+
+@pytest.mark.parametrize("size", [1e-33, 1e-20, 3e-14, 1.0])
+def test_8_bit_codes_of_small_moments_equal_any_fp32_implementation(size):
+    """Gradients whose moments divided by their scale lie on a border between two codes or next to one: with b1 = b2 = 0
+    the moments are g and g * g, as near to borders as fp32 has them."""
+    m = require_gpu()
+    rng = np.random.default_rng(46)
+    f = np.float32
+    blocks = 400
+    g = np.zeros((blocks, 128), f)
+    g[:, 0] = size * (1 + rng.random(blocks))
+    smag, sv = (np.abs(g[:, 0]) * (f(1) / f(448))).astype(f), (g[:, 0] * g[:, 0] * (f(1) / f(1.875))).astype(f)
+    smag, sv = np.maximum(smag, f(2.0 ** -126)), np.maximum(sv, f(2.0 ** -126))
+    border_m = ((1 + (rng.integers(0, 8, (blocks, 64)) + 0.5) / 8) * 2.0 ** rng.integers(-6, 8, (blocks, 64))).astype(f)
+    border_v = ((1 + (rng.integers(0, 8, (blocks, 63)) + 0.5) / 8) * 2.0 ** rng.integers(-30, 0, (blocks, 63)))
+    g[:, 1:65] = border_m * smag[:, None] * rng.choice([-1, 1], (blocks, 64))
+    g[:, 65:] = np.sqrt(border_v * sv.astype(np.float64)[:, None])
+    g[:, 1:] = np.clip(g[:, 1:], -g[:, :1], g[:, :1])
+    g = g.reshape(-1)
+    z = lambda k, dt=torch.float32: torch.zeros(k, dtype=dt, device="cuda")  # noqa: E731
+    q, s = [z(g.size, torch.uint8) for _ in range(2)], [z(blocks) for _ in range(2)]
+    table = m.adamw_table([z(g.size)], [dev(g)], [q[0]], [q[1]], exp_avg_scales=[s[0]], exp_avg_sq_scales=[s[1]])
+    m.adamw_step(table, 1, 1e-3, beta1=0.0, beta2=0.0)
+    v = g * g
+    ms = np.maximum(np.abs(g).reshape(-1, 128).max(1) * (f(1) / f(448)), f(2.0 ** -126))
+    vs = np.maximum(v.reshape(-1, 128).max(1) * (f(1) / f(1.875)), f(2.0 ** -126))
+    assert np.array_equal(host(s[0]), ms) and np.array_equal(host(s[1]), vs)
+    mq = oracle.e4m3_encode(np.clip(g / np.repeat(ms, 128), -448, 448).astype(np.float64))
+    bits = (v / np.repeat(vs, 128)).view(np.uint32)
+    code = ((bits + 0x7FFFF + ((bits >> 20) & 1)) >> 20).astype(np.int64) - 96 * 8
+    vq = np.where(v > 0, np.clip(code, 1, 255), 0).astype(np.uint8)
+    for got, want in ((host(q[0]), mq), (host(q[1]), vq)):
+        got, want = np.where(got == 128, 0, got), np.where(want == 128, 0, want)     # (-0 and 0)
+        assert np.array_equal(got, want), int((got != want).sum())
