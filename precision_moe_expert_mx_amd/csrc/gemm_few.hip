@@ -132,17 +132,25 @@ __global__ __launch_bounds__(NT) void few_rows_kernel(GemmArgs p, int blocks) {
 }  // namespace
 
 // Few rows, for which this kernel's many small workgroups beat the tiled one.  With up to 128 tiles of 256 columns
-// of the experts that rows can reach: up to 3 2^16 outputs.  With more, the tiled kernel streams weights at 4 to 5.9
-// TB/s itself, and this one is faster on up to 8 rows per expert where a weight row has 4 KiB or more (each wave has a
-// quarter of it) and the layer has fewer than 1024 tiles.  Measured, this kernel against the tiled one, us, bf16 and
+// of the experts that rows can reach: up to 3 2^16 outputs and, since an expert's rows are taken one after the other, 64
+// rows per expert.  With more tiles, the tiled kernel streams weights at 4 to 5.9 TB/s itself, and this one is faster on
+// up to 8 rows per expert where a weight row has 4 KiB or more (each wave has a quarter of it) and the layer has fewer
+// than 1024 tiles.  Measured, this kernel against the tiled one, us, bf16 and
 // int8: one expert, N 4096, K 7168: 1 row 16 / 58 and 10 / 32, 48 rows 44 / 59 and 24 / 33; 2 experts, N 8192, K 4096:
 // 16 rows 31 / 56 and 19 / 22, 64 rows 71 / 56 and 36 / 22; 8 experts, N 4096, K 7168: 8 rows 59 / 96 and 34 / 52,
 // 64 rows 107 / 104 and 55 / 56; 64 experts, N 2816, K 2048: 48 rows 79 / 100 and 48 / 48, 384 rows 148 / 168 and
 // 80 / 73; N 2048, K 1408: 126 rows 67 / 61 and 40 / 37; 16 experts, N 16384, K 5120: 1 row 40 / 70 and 24 / 27,
 // 8 rows 219 / 184 and 113 / 100.
-// (Rows that all reach one expert cost it more: 512 on one of 64 experts pass its weights, from L2, 16 times.)
+// Narrow layers, bf16 and int8: one expert, N 128, K 7168: 64 rows 44 / 46 and 24 / 26, 96 rows 67 / 45 and 37 / 26,
+// 1536 rows 1090 / 56 and 583 / 24; N 512, K 512: 64 rows 6.3 / 8.3, 128 rows 9.5 / 8.3; 4 experts, N 256, K 7168: 192
+// rows 41 / 46, 256 rows 48 / 46, 512 rows 96 / 39; 8 experts, N 128, K 1024: 512 rows 8.3 / 11.6, 768 rows 12.2 / 11.6.
+// Rows that all reach one expert pass its weights, from L2, once per 32 of them, and the device alone knows their number:
+// at most 512 rows, so that this costs at most 16 passes (512 rows of one expert, N 128, K 7168: 364 us against 39; 64
+// experts, N 128, K 1024, 1536 rows evenly spread would be 8.6 against 13.7).  Over 420 random layers (uneven routing)
+// the two rules together choose 5% over the faster kernel's time, without the bounds on rows 24%.
 bool few_rows(const GemmArgs& p) {
   const int64_t columns = (p.N + 255) / 256;
+  if (p.M > std::min(64 * (int64_t)p.G, (int64_t)512)) return false;
   if (std::min((int64_t)p.G, p.M) * columns <= 128) return p.M * p.N <= 3 << 16;
   return p.M <= 8 * (int64_t)p.G && p.ldb >= 4096 && p.G * columns < 1024;
 }
@@ -153,8 +161,7 @@ hipError_t launch_few_rows_gemm(bool int8, const GemmArgs& p, hipStream_t st) {
   // one; 8 experts, N 4096, K 7168, 8 rows: 119 against 107).
   const int nc = p.M > 4 * (int64_t)p.G && p.G * p.N >= 32 * 4096 ? 2 : 1;
   const int64_t blocks = (p.N + 16 * nc - 1) / (16 * nc);
-  if (blocks * p.G > kMaxBlocks) return hipErrorInvalidValue;
-  const dim3 g((unsigned)(blocks * p.G)), b(NT);
+  const dim3 g((unsigned)(blocks * p.G)), b(NT);             // (at most 2^21 workgroups: 32768 columns, 1024 experts)
   if (int8 && nc == 2) hipLaunchKernelGGL((few_rows_kernel<true, 2>), g, b, 0, st, p, (int)blocks);
   else if (int8) hipLaunchKernelGGL((few_rows_kernel<true, 1>), g, b, 0, st, p, (int)blocks);
   else if (nc == 2) hipLaunchKernelGGL((few_rows_kernel<false, 2>), g, b, 0, st, p, (int)blocks);

@@ -234,3 +234,25 @@ def test_8_bit_codes_of_small_moments_equal_any_fp32_implementation(size):
     for got, want in ((host(q[0]), mq), (host(q[1]), vq)):
         got, want = np.where(got == 128, 0, got), np.where(want == 128, 0, want)     # (-0 and 0)
         assert np.array_equal(got, want), int((got != want).sum())
+
+
+@pytest.mark.parametrize("N", [8, 128, 264])
+@pytest.mark.parametrize("G,rows", [(1, 64), (1, 65), (1, 700), (8, 512), (8, 513), (8, 3000)])
+def test_narrow_layers_with_many_rows(G, N, rows):
+    """Either side of the choice between the kernels, evenly routed and all rows on one expert."""
+    m = require_gpu()
+    K = 2048
+    gen = torch.Generator(device="cuda").manual_seed(rows + N)
+    x = torch.randn(rows, K, device="cuda", generator=gen).bfloat16()
+    w = torch.randn(G * N, K, device="cuda", generator=gen).bfloat16()
+    (qx, sx), (qw, sw) = m.int8_quantize_rowwise(x), m.int8_quantize_rowwise(w)
+    even = [rows * g // G for g in range(G + 1)]
+    for offs in (even, [0] * ((G + 1) // 2) + [rows] * (G + 1 - (G + 1) // 2)):
+        o = torch.tensor(offs, dtype=torch.int32, device="cuda")
+        y, y8 = m.bf16_grouped_gemm_fwd(x, w, o, N).double(), m.int8_grouped_gemm_fwd(qx, sx, qw, sw, o, N).double()
+        for g in range(G):
+            r, c = slice(offs[g], offs[g + 1]), slice(g * N, (g + 1) * N)
+            a, b = x[r].double(), w[c].double().t().contiguous()
+            assert bool(((y[r] - a @ b).abs() <= 1e-5 * (a.abs() @ b.abs())).all())
+            ref = (qx[r].double() @ qw[c].double().t().contiguous()) * sx[r].double()[:, None] * sw[c].double()
+            assert bool(((y8[r] - ref).abs() <= 2.0 ** -22 * ref.abs()).all())
