@@ -458,8 +458,10 @@ mxmoe_status fp8bw_grouped_gemm_wgrad_fp8feed(const uint8_t* qdyT, const float* 
 
 /* ---------------------------------------------------------------- bf16 grouped GEMM
  * The three products of an expert layer straight from its row-major bf16 tensors: no quantisation, no
- * transposed copies, one launch each over every expert's real rows, fp32 sums
- * (|err| <= 1e-5 * sum |a b| per element, plus half a bf16 ulp for bf16 outputs).
+ * transposed copies, one launch each over every expert's real rows, one fp32 sum per output:
+ * |err| <= max(1e-5, 2^-25 L) * sum |a b| per element, L the length of the sum (K, N, or the expert's rows), plus half
+ * a bf16 ulp for bf16 outputs.  (The sum is rounded after every 8 products.  Products of both signs stay at a few 2^-24
+ * whatever L; equal ones, whose roundings all go one way, pass 1e-5 from L = 8192 on: 5e-5 at 65536, 2e-4 at 2^18.)
  *   fwd:   Y[r, n]     = sum_k X[r, k] W[gN + n, k]           y  [M, N]
  *   dgrad: dX[r, k]    = sum_n dY[r, n] W[gN + n, k]          dx [M, K]
  *   wgrad: dW[g, n, k] = sum_{r of g} dY[r, n] X[r, k]        dw [G, N, K], 0 for an expert without rows

@@ -256,3 +256,33 @@ def test_narrow_layers_with_many_rows(G, N, rows):
             assert bool(((y[r] - a @ b).abs() <= 1e-5 * (a.abs() @ b.abs())).all())
             ref = (qx[r].double() @ qw[c].double().t().contiguous()) * sx[r].double()[:, None] * sw[c].double()
             assert bool(((y8[r] - ref).abs() <= 2.0 ** -22 * ref.abs()).all())
+
+
+@pytest.mark.parametrize("L", [8192, 32768, 65537])
+@pytest.mark.parametrize("kind", ["equal", "one sign", "both signs"])
+def test_long_sums(L, kind):
+    """The three products of long contractions against float64: at most L / 8 roundings of 2^-24, taken fourfold for what
+    the instruction loses inside its 8 products.  (Equal products go past 1e-5: their roundings all go one way.)"""
+    m = require_gpu()
+    gen = torch.Generator(device="cuda").manual_seed(L)
+    n, c, Lk = 16, 24, L // 8 * 8
+
+    def make(rows, cols):
+        if kind == "equal":
+            return torch.full((rows, cols), 1 + 2.0 ** -7, device="cuda").bfloat16()
+        t = torch.randn(rows, cols, device="cuda", generator=gen)
+        return (t if kind == "both signs" else t.abs() + 0.1).bfloat16()
+
+    def check(got, a, b):
+        a, b = a.double(), b.double()
+        assert bool(((got.double() - a @ b).abs() <= max(1e-5, 2.0 ** -25 * L) * (a.abs() @ b.abs())).all())
+
+    offs = torch.tensor([0, 3, L + 3], dtype=torch.int32, device="cuda")
+    dy, x = make(L + 3, n), make(L + 3, c)
+    check(m.bf16_grouped_gemm_wgrad(dy, x, offs)[1], dy[3:].t().contiguous(), x[3:])
+    for rows in (5, 300):
+        o = torch.tensor([0, rows], dtype=torch.int32, device="cuda")
+        a, w = make(rows, Lk), make(n, Lk)
+        check(m.bf16_grouped_gemm_fwd(a, w, o, n), a, w.t().contiguous())
+        w = make(Lk, c)
+        check(m.bf16_grouped_gemm_dgrad(a, w, o, c), a, w)
