@@ -3,7 +3,8 @@
 Argument marshalling only: every step runs in the HIP library.  Tensors are torch tensors on the
 current HIP device (bf16 inputs may be given as torch.bfloat16 or as uint16/int16 bit patterns);
 outputs are allocated with torch when not passed in.  Calls are asynchronous on torch's current
-stream unless `stream` (a torch.cuda.Stream or a raw hipStream_t integer) is given.
+stream unless `stream` (a torch.cuda.Stream or a raw hipStream_t integer) is given; outputs that a call
+allocates then belong to that stream, as inside torch.cuda.stream(stream).
 
 The library must be built (``python -m precision_moe_expert_mx_amd.build``); importing this package
 without it raises, and there is no fallback path.
@@ -191,8 +192,18 @@ def _bf16_bits(x):
     raise TypeError(f"expected bfloat16 (or its 16-bit pattern), got {x.dtype}")
 
 
-def _empty(shape, dtype, like):
-    return _torch().empty(shape, dtype=dtype, device=like.device)
+def _empty(shape, dtype, like, stream=None):
+    """An output of a call on `stream`, from that stream's memory: the current stream may still be using blocks
+    that were freed on it."""
+    torch = _torch()
+    if stream is not None and like.is_cuda:
+        handle = _stream_handle(stream)
+        if handle != torch._C._cuda_getCurrentRawStream(like.get_device()):
+            if isinstance(stream, int):
+                stream = torch.cuda.ExternalStream(handle, like.device) if handle else torch.cuda.default_stream(like.device)
+            with torch.cuda.stream(stream):
+                return torch.empty(shape, dtype=dtype, device=like.device)
+    return torch.empty(shape, dtype=dtype, device=like.device)
 
 
 @functools.lru_cache(None)
@@ -216,18 +227,18 @@ def _call(entry, *args):
 
 
 # ---------------------------------------------------------------- MX quantisers
-def _rowwise_scales_out(R, C, tiled, like):
+def _rowwise_scales_out(R, C, tiled, like, stream):
     """A row-wise copy's scale buffer: [R, C / 32], or [C / 128, R, 4] in the tiled layout."""
     torch = _torch()
-    return _empty((C // 128, R, 4) if tiled else (R, C // 32), torch.uint8, like)
+    return _empty((C // 128, R, 4) if tiled else (R, C // 32), torch.uint8, like, stream)
 
 
 def _rowwise(name, tiled, x, q, s, stream):
     torch = _torch()
     x = _bf16_bits(x)
     R, C = x.shape
-    q = _empty((R, C), torch.uint8, x) if q is None else q
-    s = _rowwise_scales_out(R, C, tiled, x) if s is None else s
+    q = _empty((R, C), torch.uint8, x, stream) if q is None else q
+    s = _rowwise_scales_out(R, C, tiled, x, stream) if s is None else s
     _check(name, getattr(lib(), name)(_ptr(x), R, C, _ptr(q), _ptr(s), _stream_handle(stream)))
     return q, s
 
@@ -242,16 +253,16 @@ def mx_quantize_rowwise_tiled(x, q=None, s=None, stream=None) -> Tuple[object, o
     return _rowwise("mx_quantize_rowwise_tiled", True, x, q, s, stream)
 
 
-def _colwise_out(C, ld, tiled, like):
+def _colwise_out(C, ld, tiled, like, stream):
     """A column-wise code buffer: [C, ld] row-major, or [ld / 128, C, 128] in the tiled layout."""
     torch = _torch()
-    return _empty((ld // 128, C, 128) if tiled else (C, ld), torch.uint8, like)
+    return _empty((ld // 128, C, 128) if tiled else (C, ld), torch.uint8, like, stream)
 
 
-def _colwise_scales_out(C, ld, tiled, like):
+def _colwise_scales_out(C, ld, tiled, like, stream):
     """Its scale buffer: [C, ld / 32] row-major, or [ld / 128, C, 4] in the tiled layout."""
     torch = _torch()
-    return _empty((ld // 128, C, 4) if tiled else (C, ld // 32), torch.uint8, like)
+    return _empty((ld // 128, C, 4) if tiled else (C, ld // 32), torch.uint8, like, stream)
 
 
 def _colwise(name, tiled, x, offs, G, ld, qT, sT, stream):
@@ -262,8 +273,8 @@ def _colwise(name, tiled, x, offs, G, ld, qT, sT, stream):
         G = offs.numel() - 1
     if ld is None:
         ld = mx_colwise_ld(R, G if offs is not None else None)
-    qT = _colwise_out(C, ld, tiled, x) if qT is None else qT
-    sT = _colwise_scales_out(C, ld, tiled, x) if sT is None else sT
+    qT = _colwise_out(C, ld, tiled, x, stream) if qT is None else qT
+    sT = _colwise_scales_out(C, ld, tiled, x, stream) if sT is None else sT
     _check(name, getattr(lib(), name)(_ptr(x), R, C, _ptr(offs), G, _ptr(qT), _ptr(sT), ld, _stream_handle(stream)))
     return qT, sT
 
@@ -287,10 +298,10 @@ def _dual(name, tiled, x, offs, G, ld, row_idx, q, s, qT, sT, stream):
         G = offs.numel() - 1
     if ld is None:
         ld = mx_colwise_ld(R, G if offs is not None else None)
-    q = _empty((R, C), torch.uint8, x) if q is None else q
-    s = _rowwise_scales_out(R, C, tiled, x) if s is None else s
-    qT = _colwise_out(C, ld, tiled, x) if qT is None else qT
-    sT = _colwise_scales_out(C, ld, tiled, x) if sT is None else sT
+    q = _empty((R, C), torch.uint8, x, stream) if q is None else q
+    s = _rowwise_scales_out(R, C, tiled, x, stream) if s is None else s
+    qT = _colwise_out(C, ld, tiled, x, stream) if qT is None else qT
+    sT = _colwise_scales_out(C, ld, tiled, x, stream) if sT is None else sT
     _check(name, getattr(lib(), name)(_ptr(x), R, C, _ptr(row_idx), R_src, _ptr(offs), G, _ptr(q), _ptr(s), _ptr(qT),
                                       _ptr(sT), ld, _stream_handle(stream)))
     return q, s, qT, sT
@@ -317,7 +328,7 @@ def _fwd(name, qx, sx, qw, sw, offs, N, out_dtype, y, stream, fast):
     M, K = qx.shape
     G = offs.numel() - 1
     tdt, cdt = _out_dtype(out_dtype)
-    y = _empty((M, N), tdt, qx) if y is None else y
+    y = _empty((M, N), tdt, qx, stream) if y is None else y
     _check(*_call(_gemm(name, fast), _ptr(qx), _ptr(sx), _ptr(qw), _ptr(sw), _ptr(offs), G, M, N, K, _ptr(y), cdt,
                   _stream_handle(stream)))
     return y
@@ -339,18 +350,18 @@ def _swiglu(name, tiled, qx, sx, qw, sw, offs, N, y, qh, sh, h, with_h, colwise,
     M, K = qx.shape
     G = offs.numel() - 1
     H = N // 2
-    y = _empty((M, N), torch.bfloat16, qx) if y is None else y
-    qh = _empty((M, H), torch.uint8, qx) if qh is None else qh
-    sh = _rowwise_scales_out(M, H, tiled, qx) if sh is None else sh
+    y = _empty((M, N), torch.bfloat16, qx, stream) if y is None else y
+    qh = _empty((M, H), torch.uint8, qx, stream) if qh is None else qh
+    sh = _rowwise_scales_out(M, H, tiled, qx, stream) if sh is None else sh
     if with_h and h is None:
-        h = _empty((M, H), torch.float32, qx)
+        h = _empty((M, H), torch.float32, qx, stream)
     if colwise or tiled or qhT is not None:
         if qhT is not None:
             ldh = qhT.shape[0] * 128 if tiled else qhT.shape[1]
         elif ldh is None:
             ldh = mx_colwise_ld(M, G)
-        qhT = _colwise_out(H, ldh, tiled, qx) if qhT is None else qhT
-        shT = _colwise_scales_out(H, ldh, tiled, qx) if shT is None else shT
+        qhT = _colwise_out(H, ldh, tiled, qx, stream) if qhT is None else qhT
+        shT = _colwise_scales_out(H, ldh, tiled, qx, stream) if shT is None else shT
     _check(name, getattr(lib(), name)(
         _ptr(qx), _ptr(sx), _ptr(qw), _ptr(sw), _ptr(offs), G, M, N, K, _ptr(y), _ptr(qh), _ptr(sh), _ptr(h),
         _ptr(qhT), _ptr(shT), int(ldh or 0), _stream_handle(stream)))
@@ -396,7 +407,7 @@ def _dgrad(name, ldw, qdy, sdy, qwT, swT, offs, K, out_dtype, dx, stream, fast):
     M, N = qdy.shape
     G = offs.numel() - 1
     tdt, cdt = _out_dtype(out_dtype)
-    dx = _empty((M, K), tdt, qdy) if dx is None else dx
+    dx = _empty((M, K), tdt, qdy, stream) if dx is None else dx
     _check(*_call(_gemm(name, fast), _ptr(qdy), _ptr(sdy), _ptr(qwT), _ptr(swT), ldw, _ptr(offs), G, M, N, K,
                   _ptr(dx), cdt, _stream_handle(stream)))
     return dx
@@ -420,7 +431,7 @@ def mx_grouped_gemm_wgrad_tiled(qdyT, sdyT, qxT, sxT, offs, M: int, out_dtype: s
 def _wgrad(name, N, ld, K, qdyT, sdyT, qxT, sxT, offs, M, out_dtype, dw, stream, fast):
     G = offs.numel() - 1
     tdt, cdt = _out_dtype(out_dtype)
-    dw = _empty((G, N, K), tdt, qdyT) if dw is None else dw
+    dw = _empty((G, N, K), tdt, qdyT, stream) if dw is None else dw
     _check(*_call(_gemm(name, fast), _ptr(qdyT), _ptr(sdyT), _ptr(qxT), _ptr(sxT), ld, _ptr(offs), G, M, N, K,
                   _ptr(dw), cdt, _stream_handle(stream)))
     return dw
@@ -432,8 +443,8 @@ def mxfp4_quantize_rowwise(x, q=None, s=None, stream=None):
     torch = _torch()
     x = _bf16_bits(x)
     R, C = x.shape
-    q = _empty((R, C // 2), torch.uint8, x) if q is None else q
-    s = _empty((R, C // 32), torch.uint8, x) if s is None else s
+    q = _empty((R, C // 2), torch.uint8, x, stream) if q is None else q
+    s = _empty((R, C // 32), torch.uint8, x, stream) if s is None else s
     _check("mxfp4_quantize_rowwise", lib().mxfp4_quantize_rowwise(_ptr(x), R, C, _ptr(q), _ptr(s),
                                                                   _stream_handle(stream)))
     return q, s
@@ -448,8 +459,8 @@ def mxfp4_quantize_colwise(x, offs=None, G: int = 1, ld: Optional[int] = None, q
         G = offs.numel() - 1
     if ld is None:
         ld = mxfp4_colwise_ld(R, G if offs is not None else None)
-    qT = _empty((C, ld // 2), torch.uint8, x) if qT is None else qT
-    sT = _empty((C, ld // 32), torch.uint8, x) if sT is None else sT
+    qT = _empty((C, ld // 2), torch.uint8, x, stream) if qT is None else qT
+    sT = _empty((C, ld // 32), torch.uint8, x, stream) if sT is None else sT
     _check("mxfp4_quantize_colwise", lib().mxfp4_quantize_colwise(_ptr(x), R, C, _ptr(offs), G, _ptr(qT), _ptr(sT),
                                                                   ld, _stream_handle(stream)))
     return qT, sT
@@ -460,7 +471,7 @@ def mxfp4_grouped_gemm_fwd(qx, sx, qw, sw, offs, N: int, out_dtype: str = "f32",
     M, K = qx.shape[0], 2 * qx.shape[1]
     G = offs.numel() - 1
     tdt, cdt = _out_dtype(out_dtype)
-    y = _empty((M, N), tdt, qx) if y is None else y
+    y = _empty((M, N), tdt, qx, stream) if y is None else y
     _check("mxfp4_grouped_gemm_fwd", lib().mxfp4_grouped_gemm_fwd(_ptr(qx), _ptr(sx), _ptr(qw), _ptr(sw), _ptr(offs),
                                                                   G, M, N, K, _ptr(y), cdt, _stream_handle(stream)))
     return y
@@ -472,7 +483,7 @@ def mxfp4_grouped_gemm_dgrad(qdy, sdy, qwT, swT, offs, K: int, out_dtype: str = 
     ldw = 2 * qwT.shape[1]
     G = offs.numel() - 1
     tdt, cdt = _out_dtype(out_dtype)
-    dx = _empty((M, K), tdt, qdy) if dx is None else dx
+    dx = _empty((M, K), tdt, qdy, stream) if dx is None else dx
     _check("mxfp4_grouped_gemm_dgrad", lib().mxfp4_grouped_gemm_dgrad(_ptr(qdy), _ptr(sdy), _ptr(qwT), _ptr(swT), ldw,
                                                                       _ptr(offs), G, M, N, K, _ptr(dx), cdt,
                                                                       _stream_handle(stream)))
@@ -485,7 +496,7 @@ def mxfp4_grouped_gemm_wgrad(qdyT, sdyT, qxT, sxT, offs, M: int, out_dtype: str 
     K = qxT.shape[0]
     G = offs.numel() - 1
     tdt, cdt = _out_dtype(out_dtype)
-    dw = _empty((G, N, K), tdt, qdyT) if dw is None else dw
+    dw = _empty((G, N, K), tdt, qdyT, stream) if dw is None else dw
     _check("mxfp4_grouped_gemm_wgrad", lib().mxfp4_grouped_gemm_wgrad(_ptr(qdyT), _ptr(sdyT), _ptr(qxT), _ptr(sxT), ld,
                                                                       _ptr(offs), G, M, N, K, _ptr(dw), cdt,
                                                                       _stream_handle(stream)))
@@ -498,8 +509,8 @@ def fp8bw_quantize_act_1x128(x, q=None, s=None, stream=None, pow2: bool = False)
     torch = _torch()
     x = _bf16_bits(x)
     R, C = x.shape
-    q = _empty((R, C), torch.uint8, x) if q is None else q
-    s = _empty((R, C // 128), torch.float32, x) if s is None else s
+    q = _empty((R, C), torch.uint8, x, stream) if q is None else q
+    s = _empty((R, C // 128), torch.float32, x, stream) if s is None else s
     fn = "fp8bw_quantize_act_1x128" + ("_pow2" if pow2 else "")
     _check(fn, getattr(lib(), fn)(_ptr(x), R, C, _ptr(q), _ptr(s), _stream_handle(stream)))
     return q, s
@@ -512,10 +523,10 @@ def fp8bw_quantize_weight_128x128(w, q=None, s=None, qT=None, transposed: bool =
     torch = _torch()
     w = _bf16_bits(w)
     R, C = w.shape
-    q = _empty((R, C), torch.uint8, w) if q is None else q
-    s = _empty((R // 128, C // 128), torch.float32, w) if s is None else s
+    q = _empty((R, C), torch.uint8, w, stream) if q is None else q
+    s = _empty((R // 128, C // 128), torch.float32, w, stream) if s is None else s
     if transposed and qT is None:
-        qT = _empty((C, R), torch.uint8, w)
+        qT = _empty((C, R), torch.uint8, w, stream)
     fn = "fp8bw_quantize_weight_128x128" + ("_pow2" if pow2 else "")
     _check(fn, getattr(lib(), fn)(_ptr(w), R, C, _ptr(q), _ptr(s), _ptr(qT), _stream_handle(stream)))
     return (q, s) if qT is None else (q, s, qT)
@@ -525,7 +536,7 @@ def _bw_fwd(name, qx, sx, qw, sw, offs, N, out_dtype, y, stream, fast):
     M, K = qx.shape
     G = offs.numel() - 1
     tdt, cdt = _out_dtype(out_dtype)
-    y = _empty((M, N), tdt, qx) if y is None else y
+    y = _empty((M, N), tdt, qx, stream) if y is None else y
     _check(*_call(_gemm(name, fast), _ptr(qx), _ptr(sx), _ptr(qw), _ptr(sw), _ptr(offs), G, M, N, K, _ptr(y), cdt,
                   _stream_handle(stream)))
     return y
@@ -535,7 +546,7 @@ def _bw_dgrad(name, qdy, sdy, qwT, sw, offs, K, out_dtype, dx, stream, fast):
     M, N = qdy.shape
     G = offs.numel() - 1
     tdt, cdt = _out_dtype(out_dtype)
-    dx = _empty((M, K), tdt, qdy) if dx is None else dx
+    dx = _empty((M, K), tdt, qdy, stream) if dx is None else dx
     _check(*_call(_gemm(name, fast), _ptr(qdy), _ptr(sdy), _ptr(qwT), _ptr(sw), _ptr(offs), G, M, N, K, _ptr(dx),
                   cdt, _stream_handle(stream)))
     return dx
@@ -580,8 +591,8 @@ def fp8bw_quantize_colwise_128(x, offs=None, G: int = 1, ld: Optional[int] = Non
         G = offs.numel() - 1
     if ld is None:
         ld = fp8bw_colwise_ld_min(R, G) if offs is not None else 128 * ((R + 127) // 128)
-    qT = _empty((C, ld), torch.uint8, x) if qT is None else qT
-    sT = _empty((C, ld // 128), torch.float32, x) if sT is None else sT
+    qT = _empty((C, ld), torch.uint8, x, stream) if qT is None else qT
+    sT = _empty((C, ld // 128), torch.float32, x, stream) if sT is None else sT
     fn = "fp8bw_quantize_colwise_128" + ("_pow2" if pow2 else "")
     _check(fn, getattr(lib(), fn)(_ptr(x), R, C, _ptr(offs), G, _ptr(qT), _ptr(sT), ld, _stream_handle(stream)))
     return qT, sT
@@ -592,7 +603,7 @@ def _bw_wgrad(name, qdyT, sdyT, qxT, sxT, offs, M, out_dtype, dw, stream, fast):
     K = qxT.shape[0]
     G = offs.numel() - 1
     tdt, cdt = _out_dtype(out_dtype)
-    dw = _empty((G, N, K), tdt, qdyT) if dw is None else dw
+    dw = _empty((G, N, K), tdt, qdyT, stream) if dw is None else dw
     _check(*_call(_gemm(name, fast), _ptr(qdyT), _ptr(sdyT), _ptr(qxT), _ptr(sxT), ld, _ptr(offs), G, M, N, K,
                   _ptr(dw), cdt, _stream_handle(stream)))
     return dw
@@ -680,7 +691,7 @@ def _weights(name, w, dtypes, G, N, K):
 def _bf16_gemm(name, a, b, offs, shape, dims, out_dtype, out, stream):
     tdt, cdt = _out_dtype(out_dtype)
     if out is None:
-        out = _empty(shape, tdt, a)
+        out = _empty(shape, tdt, a, stream)
     else:
         _want("output", out, (tdt,), shape)
     _run(name, (a, b, offs, out), stream, a.data_ptr(), b.data_ptr(), offs.data_ptr(), *dims, out.data_ptr(), cdt)
@@ -720,8 +731,8 @@ def bf16_grouped_gemm_wgrad(dy, x, offs, out_dtype: str = "f32", dw=None, stream
 
 def _int8_rowwise(name, x, R, C, q, s, stream):
     torch = _torch()
-    q = _empty((R, C), torch.int8, x) if q is None else q
-    s = _empty((R,), torch.float32, x) if s is None else s
+    q = _empty((R, C), torch.int8, x, stream) if q is None else q
+    s = _empty((R,), torch.float32, x, stream) if s is None else s
     _want("q", q, (torch.int8,), (R, C))
     _want("s", s, (torch.float32,), (R,))
     _run(name, (x, q, s), stream, x.data_ptr(), R, C, q.data_ptr(), s.data_ptr())
@@ -755,7 +766,7 @@ def int8_grouped_gemm_fwd(qx, sx, qw, sw, offs, N: int, out_dtype: str = "f32", 
     _want("sw", sw, f32, (G, N) if sw.dim() == 2 else (G * N,))
     tdt, cdt = _out_dtype(out_dtype)
     if y is None:
-        y = _empty((M, N), tdt, qx)
+        y = _empty((M, N), tdt, qx, stream)
     else:
         _want("y", y, (tdt,), (M, N))
     _run("int8_grouped_gemm_fwd", (qx, sx, qw, sw, offs, y), stream, qx.data_ptr(), sx.data_ptr(), qw.data_ptr(),
@@ -878,7 +889,7 @@ def adamw_dequantize(q, s, moment: str, out_dtype: str = "f32", out=None, stream
     _want("s", s, (torch.float32,), ((q.numel() + 127) // 128,))
     tdt, cdt = _out_dtype(out_dtype)
     if out is None:
-        out = _empty(q.shape, tdt, q)
+        out = _empty(q.shape, tdt, q, stream)
     else:
         _want("out", out, (tdt,), q.shape)
     _run("adamw_dequantize", (q, s, out), stream, q.data_ptr(), s.data_ptr(), q.numel(), int(moment == "exp_avg_sq"),
