@@ -83,9 +83,9 @@ __device__ __forceinline__ int row_swz(int r) { return (r >> 1) & 7; }
 template <int TD>
 __device__ __forceinline__ int col_swz(int t) { return ((t & 3) | ((t >> 1) & 4)) & (2 * TD - 1); }
 
-// One operand of a wave: its share of a stage's loads (kLoads of 1 KiB, fewer of A in a tile of fewer
-// rows; load j of wave w fills the stage's 1 KiB piece kWaves j + w) as 32-bit lane offsets from a
-// wave-uniform base that moves by `step` bytes per stage, and its fragments' LDS offsets in a stage.
+// One operand of a wave: its share of a stage's loads (kLoads of 1 KiB; load j of wave w fills the stage's 1 KiB
+// piece kWaves j + w) as 32-bit lane offsets from a wave-uniform base that moves by `step` bytes per stage, and its
+// fragments' LDS offsets in a stage.
 template <bool COLS_, int STRIDE, int TD>       // STRIDE: rows (columns) from one fragment to the next
 struct Operand {
   static constexpr bool COLS = COLS_;
@@ -136,10 +136,10 @@ struct Operand {
       if (k >= lim) off[j] -= COLS ? k * ld : k;
     }
   }
-  static __device__ __forceinline__ void zero(int lane, int w, int loads, int lim, char* st) {
+  static __device__ __forceinline__ void zero(int lane, int w, int lim, char* st) {
 #pragma unroll
     for (int j = 0; j < kLoads; ++j)
-      if (j < loads && at(lane, w, j) >= lim) *(uint4*)(st + (kWaves * j + w) * 1024 + 16 * lane) = make_uint4(0, 0, 0, 0);
+      if (at(lane, w, j) >= lim) *(uint4*)(st + (kWaves * j + w) * 1024 + 16 * lane) = make_uint4(0, 0, 0, 0);
   }
 
   // Fragments start at row (column) r0 of the tile, a multiple of 32.
@@ -497,8 +497,8 @@ struct Runner {
   // A partial stage has landed everywhere: clear what lies past its end, before anyone reads it.
   __device__ __forceinline__ void clear(int lim, char* sa, char* sb) {
     const int lane = fresh_lane();
-    a.zero(lane, w, kLoads, A_COLS ? lim : lim * ES, sa);
-    b.zero(lane, w, kLoads, B_COLS ? lim : lim * ES, sb);
+    a.zero(lane, w, A_COLS ? lim : lim * ES, sa);
+    b.zero(lane, w, B_COLS ? lim : lim * ES, sb);
     lds_barrier();
   }
 

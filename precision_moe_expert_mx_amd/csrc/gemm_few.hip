@@ -2,7 +2,7 @@
 // or 8-bit integers:  Y[r, n] = sum_k X[r, k] W[gN + n, k]  (int8: times sx[r] sw[gN + n], exact int32 sum).
 //
 // Bound: HBM, every weight of an expert that a row reaches is read once: G_hit N K elements.  A tile of 256
-// columns per workgroup would leave most CUs idle, so a workgroup takes 16 columns of one expert and its
+// columns per workgroup would leave most CUs idle, so a workgroup takes 16 or 32 columns of one expert and its
 // four waves a quarter of the contraction each; their sums meet in LDS.  Weights go straight from memory to
 // the registers of v_mfma_f32_16x16x32_bf16 / v_mfma_i32_16x16x64_i8 (lane l: column l % 16, 16 bytes at
 // 64 k + 16 (l / 16) of its row), eight loads in flight per wave and several workgroups per CU.  The rows
