@@ -790,6 +790,8 @@ class AdamWTable:
 
     def __init__(self, entries, array, bits, grad_dtype, like):
         self.entries, self.array, self.bits, self.grad_dtype, self.like = entries, array, bits, grad_dtype, like
+        self.args = ctypes.addressof(array), len(array), grad_dtype, bits           # (of the C call)
+        self.weights = [t for row in entries for t in row[:2] if t is not None]     # (params and their copies)
 
 
 def adamw_table(params, grads, exp_avg, exp_avg_sq, weights=None, exp_avg_scales=None, exp_avg_sq_scales=None):
@@ -857,14 +859,17 @@ def adamw_step(table, step, lr, beta1: float = 0.9, beta2: float = 0.999, eps: f
 
     step (counted from 1) and lr are numbers, or GPU scalars (int64 / float32 tensors) that the kernel reads,
     for a step captured into a graph.  grad_scale: a float32 GPU scalar that multiplies every gradient
-    (clipping), or None."""
+    (clipping), or None.
+
+    The weights and their copies count as modified in place, so a backward pass that saved one before the step
+    raises; replays of a captured step cannot be noticed that way."""
     torch = _torch()
-    hyper = _AdamWHyper(0.0, float(beta1), float(beta2), float(eps), float(weight_decay), 1, None, None, None)
+    hyper = _AdamWHyper(0.0, beta1, beta2, eps, weight_decay, 1)
     scalars = []
     if isinstance(lr, torch.Tensor):
         scalars.append(("lr", lr, torch.float32, "lr_dev"))
     else:
-        hyper.lr = float(lr)
+        hyper.lr = lr
     if isinstance(step, torch.Tensor):
         scalars.append(("step", step, torch.int64, "step_dev"))
     else:
@@ -875,8 +880,9 @@ def adamw_step(table, step, lr, beta1: float = 0.9, beta2: float = 0.999, eps: f
         if t.dtype != dt or t.numel() != 1:
             raise TypeError(f"{name}: expected one {dt} on the GPU, got {t.dtype} of {t.numel()}")
         setattr(hyper, field, _ptr(t))
-    _run("adamw_step", (table.like, *[t for _, t, _, _ in scalars]), stream, ctypes.addressof(table.array),
-         len(table.array), table.grad_dtype, table.bits, ctypes.addressof(hyper))
+    _run("adamw_step", (table.like, *[t for _, t, _, _ in scalars]) if scalars else (table.like,), stream, *table.args,
+         ctypes.addressof(hyper))
+    torch.autograd.graph.increment_version(table.weights)
 
 
 def adamw_dequantize(q, s, moment: str, out_dtype: str = "f32", out=None, stream=None):

@@ -286,3 +286,23 @@ def test_long_sums(L, kind):
         check(m.bf16_grouped_gemm_fwd(a, w, o, n), a, w.t().contiguous())
         w = make(Lk, c)
         check(m.bf16_grouped_gemm_dgrad(a, w, o, c), a, w)
+
+
+def test_backward_with_weights_of_before_the_step_raises():
+    """The step is an in-place change that autograd knows of, of the weights and of their bf16 copies."""
+    m = require_gpu()
+    z = lambda: torch.zeros(256, device="cuda")  # noqa: E731
+    p, w, g = torch.ones(256, device="cuda"), torch.ones(256, dtype=torch.bfloat16, device="cuda"), torch.ones(256, device="cuda")
+    table = m.adamw_table([p], [g], [z()], [z()], weights=[w])
+    for saved in (p, w):
+        x = torch.ones_like(saved, requires_grad=True)
+        y = (x * saved).sum()                        # (saves the weight for x's gradient)
+        m.adamw_step(table, 1, 1e-3)
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            y.backward()
+        (x * saved).sum().backward()                 # one that ran after the step is fine
+        assert torch.equal(x.grad, saved)
+    with torch.inference_mode():                     # (tensors without a version)
+        p2, g2 = torch.ones(256, device="cuda"), torch.ones(256, device="cuda")
+        m.adamw_step(m.adamw_table([p2], [g2], [z()], [z()]), 1, 1e-3)
+    assert (p2 != 1).all()
