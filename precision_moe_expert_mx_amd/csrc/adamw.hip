@@ -17,8 +17,8 @@
 // Bound: HBM.  Bytes per element: weight 8, copy 2, gradient 4 or 2, moments 16 (fp32) or 4.06 (8 bits).
 // A lane owns four consecutive elements (16-byte accesses of the fp32 arrays), so 32 lanes hold a block of
 // 128 and meet for its two maxima by lane permutes; every byte is touched once, non-temporally.  Measured
-// on 235M elements with fp32 / bf16 gradients: fp32 moments 5.56 / 5.59 TB/s (1268 / 1177 us), 8-bit moments
-// 5.48 / 5.45 (777 / 695 us).
+// on 235M elements with fp32 / bf16 gradients: fp32 moments 5.5-5.65 TB/s both (1249-1274 / 1167-1189 us), 8-bit
+// moments 5.4-5.5 both (772-792 / 695-706 us).
 #include <algorithm>
 
 #include "plain.h"

@@ -23,8 +23,10 @@
 //
 // Bound: the matrix cores, and on random operands the chip's power, which sets their clock: of a stage's 2048
 // matrix clocks the loop takes 2300-2400 and a tile 13000 more (measured with GRBM_GUI_ACTIVE at K 1280 .. 10240),
-// at 1.7-1.9 GHz.  One product of 16384 x 16384 x 5120: forward 1400-1470 TFLOP/s, dgrad 1360-1400, wgrad
-// 1270-1390, int8 2500-2600 (the range is that of different cards).
+// at 1.7-1.9 GHz.  One product of 16384 x 16384 x 5120: forward 1380-1470 TFLOP/s, dgrad 1360-1400, wgrad
+// 1270-1390, int8 2500-2600 (the range is that of different cards).  Layers of many experts with short contractions
+// (64 of 768 rows, K 1408) keep the matrix cores busy for half of the clocks only: they wait for the first loads and the
+// epilogue of each tile, for a stage's loads, and for the workgroups with more whole tiles.
 //
 // An operand contiguous along t is staged as 256 rows of 128 bytes; one with t as its rows as 64 rows of 256
 // columns (512 bytes), which fragments are read from with the transposing LDS read (ds_read_b64_tr_b16: 16

@@ -14,9 +14,10 @@
 // and the conversion, by 1, 2 or 4 waves according to its length (at most 4 x 16 bytes per lane and
 // operand); rows of more than 8192 elements are read again.  With SwiGLU the chain of a row (loads, maximum,
 // one fp64 evaluation, conversion) has to hide behind the other rows of a CU: 128 registers, so that 16 waves
-// fit, and no memory access in the usual chain (a candidate's values are kept, not read again: 4.4 -> 6 TB/s).
-// Measured: 65536 x 7168 plain 6.3 TB/s; SwiGLU 65536 x 2048 5.6-6.0, 32768 x 8192 5.9, 49152 x 1408 4.7,
-// 49152 x 1024 3.4 (the work per row, not per element, counts there).
+// fit, and no memory access in the usual chain (a candidate's values are kept, not read again, a third faster).
+// Measured (the range is that of different cards and runs): 65536 x 7168 plain 5.7-6.3 TB/s; SwiGLU 32768 x 8192
+// 5.5-5.8, 32768 x 4096 5.1-5.2, 65536 x 2048 4.5-5.6, 49152 x 1408 4.2-4.7, 49152 x 1024 3.4-4.5, 200000 x 512
+// 4.0-4.2 (the work per row, not per element, counts in the short ones).
 #include <algorithm>
 
 #include "plain.h"
