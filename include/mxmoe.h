@@ -545,6 +545,106 @@ mxmoe_status adamw_step(const mxmoe_adamw_tensor* tensors, int32_t count, mxmoe_
 mxmoe_status adamw_dequantize(const uint8_t* q, const float* s, int64_t n, int32_t second_moment, void* out,
                               mxmoe_dtype odt, void* stream);
 
+/* ---------------------------------------------------------------- norm
+ * rmsnorm_fwd: the root-mean-square norm of R rows of C elements, with the addition of a block's output to the
+ * residual stream before it:
+ *   h = x + residual, added in fp32, rounded to the residual's type;  r = 1 / sqrt(mean_c h^2 + eps);  y = h r w
+ * x [R, C] (xdt), residual [R, C] (rdt) or NULL (then h = x, is not written, and rdt and h are ignored), w [C]
+ * (wdt), y [R, C] (ydt), h [R, C] (rdt; may be the residual's own buffer, every other output has its own).  The squares are summed
+ * in fp64, everything else is fp32.  C % 8 == 0, C <= 32768, 2^-126 <= eps <= 1e30; R == 0 is a no-op.
+ *
+ * int8_quantize_rmsnorm_rowwise: the same y as 8-bit integers with a scale per row, q int8 [R, C], s f32 [R], as
+ * int8_quantize_rowwise makes them, but in one rounding from the exact values: with v = h w (r cancels),
+ * q = round-to-nearest-even(127 v / amax) of the exact quotient, amax = max_c |v|, s = fl32(amax r / 127); an
+ * all-zero row has s = 1 and codes 0, a row with a NaN or an infinity a scale of NaN and codes 0.
+ *
+ * mx_quantize_rmsnorm_rowwise: the same y as E4M3 codes with a scale per 32, q [R, C], s E8M0 [R, C/32], as
+ * mx_quantize_rowwise makes them, in one rounding from y in fp64 (rows with a NaN or an infinity: codes and scales unspecified).  C % 32 == 0.
+ *
+ * y_bf16 of the two: y in bf16 as well (what the router reads), or NULL. */
+mxmoe_status rmsnorm_fwd(const void* x, mxmoe_dtype xdt, const void* residual, mxmoe_dtype rdt, const void* w,
+                         mxmoe_dtype wdt, int64_t R, int64_t C, double eps, void* y, mxmoe_dtype ydt, void* h,
+                         void* stream);
+mxmoe_status int8_quantize_rmsnorm_rowwise(const void* x, mxmoe_dtype xdt, const void* residual, mxmoe_dtype rdt,
+                                           const void* w, mxmoe_dtype wdt, int64_t R, int64_t C, double eps, int8_t* q,
+                                           float* s, void* y_bf16, void* h, void* stream);
+mxmoe_status mx_quantize_rmsnorm_rowwise(const void* x, mxmoe_dtype xdt, const void* residual, mxmoe_dtype rdt,
+                                         const void* w, mxmoe_dtype wdt, int64_t R, int64_t C, double eps, uint8_t* q,
+                                         uint8_t* s, void* y_bf16, void* h, void* stream);
+
+/* rmsnorm_bwd: gradients of rmsnorm_fwd's y with respect to h (which is that of x and of the residual) and w:
+ *   g = dy w;  dx = r (g - h r^2 mean_c(g h)) + dres;  dw = sum over the rows of dy h r
+ * dy [R, C] (dydt), h [R, C] (hdt) and dres [R, C] (hdt; the gradient that reaches h by another way, or NULL),
+ * dx [R, C] (hdt; may be dres' or dy's own buffer where the types are the same), dw f32 [C] or NULL (not needed).  dw is summed in a fixed order
+ * through `ws`, rmsnorm_bwd_workspace(R, C) bytes that the caller owns during the call (not read for dw == NULL).
+ * R == 0: dw = 0. */
+int64_t rmsnorm_bwd_workspace(int64_t R, int64_t C);
+mxmoe_status rmsnorm_bwd(const void* dy, mxmoe_dtype dydt, const void* h, mxmoe_dtype hdt, const void* w,
+                         mxmoe_dtype wdt, const void* dres, int64_t R, int64_t C, double eps, void* dx, float* dw,
+                         void* ws, void* stream);
+
+/* ---------------------------------------------------------------- routing
+ * moe_route_fwd: each token's `top` experts and their weights from router logits [T, E] (ldt):
+ *   p = softmax(logits) or sigmoid(logits) over all E experts
+ *   c = p + bias (bias f32 [E]: balances the choice only), or the logit itself where bias is NULL
+ *   of `groups` groups of E / groups consecutive experts, the keep_groups with the largest sum of their group_top
+ *   (1 or 2) largest c stay (groups 1: all)
+ *   ids [T, top] = the experts with the largest c, in falling order; equal c go to the lower index
+ *   weights f32 [T, top] = scale * p of the chosen, divided by their sum if renormalize (0 where that sum is 0)
+ * Both comparisons are those of fp64 values.  A logit of -infinity is an expert with p = 0.  A NaN
+ * ranks last (every c of a row of softmax scores with a bias is one if a logit is) and shows in the weights that contain it.  valid (bytes [T], or NULL): tokens with 0 are padding, with ids -1 and weights 0.
+ * 1 <= E <= 1024, 1 <= top <= 64, top <= E / groups * keep_groups, groups <= 64, T * top < 2^31.
+ *
+ * moe_sort: the chosen pairs in the order of their experts, for the `G` experts first .. first + G - 1 that are
+ * here (all, or one GPU's): offs [G + 1] with offs[0] = 0, row_idx [T * top] the token of each row, pos [T, top]
+ * the row of each pair.  Rows of an expert keep the order of their tokens.  Pairs of other experts and of
+ * negative ids have no row: their pos is -1, and row_idx is -1 from offs[G] on.  The forward and data-gradient products on
+ * such offs (offs[G] < M = T * top) leave the rows from offs[G] on as they were, and the weight gradients do not read them.  1 <= G <= 1024.
+ * ws: moe_sort_workspace(T * top, G) bytes that the caller owns during the call (NULL where that is 0).
+ *
+ * moe_route_sort: both at once (the same results); ws as in moe_sort.  first + G <= E.
+ *
+ * moe_route_bwd: dlogits [T, E] (ldt) from dweights f32 [T, top]; the choice itself has no gradient.  ids outside
+ * [0, E) add nothing. */
+typedef enum { MXMOE_SOFTMAX = 0, MXMOE_SIGMOID = 1 } mxmoe_score;
+mxmoe_status moe_route_fwd(const void* logits, mxmoe_dtype ldt, const float* bias, const uint8_t* valid, int64_t T,
+                           int32_t E, int32_t top, mxmoe_score score, int32_t groups, int32_t keep_groups,
+                           int32_t group_top, int32_t renormalize, double scale, int32_t* ids, float* weights,
+                           void* stream);
+int64_t moe_sort_workspace(int64_t pairs, int32_t G);
+mxmoe_status moe_sort(const int32_t* ids, int64_t T, int32_t top, int32_t G, int32_t first, int32_t* offs,
+                      int32_t* row_idx, int32_t* pos, void* ws, void* stream);
+mxmoe_status moe_route_sort(const void* logits, mxmoe_dtype ldt, const float* bias, const uint8_t* valid, int64_t T,
+                            int32_t E, int32_t top, mxmoe_score score, int32_t groups, int32_t keep_groups,
+                            int32_t group_top, int32_t renormalize, double scale, int32_t* ids, float* weights,
+                            int32_t G, int32_t first, int32_t* offs, int32_t* row_idx, int32_t* pos, void* ws,
+                            void* stream);
+mxmoe_status moe_route_bwd(const float* dweights, const int32_t* ids, const void* logits, mxmoe_dtype ldt, int64_t T,
+                           int32_t E, int32_t top, mxmoe_score score, int32_t renormalize, double scale, void* dlogits,
+                           void* stream);
+
+/* ---------------------------------------------------------------- rows out and back
+ * A pos [T, top] names the row of each of a token's pairs (moe_sort makes it); a value outside [0, M) is a pair without a row, and no
+ * two pairs have the same row.  1 <= top <= 64.
+ * moe_dispatch: xr[pos[t, k]] = x[t] for rows of row_bytes bytes (a multiple of 8: bf16, f32 or 8-bit codes), and
+ * sr[pos[t, k]] = scales[t] for rows of scale_bytes bytes (NULL, 0: none): x [T], xr [M].  Rows that no
+ * pair names stay as they were.
+ * moe_combine_fwd: out[t] = residual[t] + sum_k weights[t, k] y[pos[t, k]]: y [M, C] (ydt), weights f32 [T, top]
+ * (NULL: 1, which is moe_dispatch's backward), residual [T, C] (rdt, NULL: 0), out [T, C] (odt; may be the residual's own
+ * buffer where the types are the same); summed in fp32.
+ * moe_combine_bwd: dy[pos[t, k]] = weights[t, k] dout[t] and dweights[t, k] = sum_c dout[t, c] y[pos[t, k], c] (0 for a
+ * pair without a row): dout [T, C] (ddt), y [M, C] and dy [M, C] (ydt; dy may be y's own buffer), dweights f32 [T, top].  dy and dweights may be
+ * NULL (not needed), y too without dweights.  The residual's gradient is dout.  Rows of dy that no pair names stay as
+ * they were.  C % 8 == 0. */
+mxmoe_status moe_dispatch(const void* x, int64_t row_bytes, const void* scales, int64_t scale_bytes,
+                          const int32_t* pos, int64_t T, int32_t top, int64_t M, void* xr, void* sr, void* stream);
+mxmoe_status moe_combine_fwd(const void* y, mxmoe_dtype ydt, const int32_t* pos, const float* weights,
+                             const void* residual, mxmoe_dtype rdt, int64_t T, int32_t top, int64_t M, int64_t C,
+                             void* out, mxmoe_dtype odt, void* stream);
+mxmoe_status moe_combine_bwd(const void* dout, mxmoe_dtype ddt, const int32_t* pos, const float* weights, const void* y,
+                             mxmoe_dtype ydt, int64_t T, int32_t top, int64_t M, int64_t C, void* dy, float* dweights,
+                             void* stream);
+
 /* Opt-in offsets validator: copies offs to the host (synchronising `stream`)
  * and checks offs[0] == 0, non-decreasing, offs[G] == M.  Returns
  * MXMOE_ERR_OFFSETS with a message naming the first bad index. */

@@ -32,6 +32,9 @@ __all__ = [
     "bf16_grouped_gemm_fwd", "bf16_grouped_gemm_dgrad", "bf16_grouped_gemm_wgrad",
     "int8_quantize_rowwise", "int8_quantize_swiglu_rowwise", "int8_grouped_gemm_fwd",
     "AdamWTable", "adamw_table", "adamw_step", "adamw_dequantize",
+    "rmsnorm_fwd", "int8_quantize_rmsnorm_rowwise", "mx_quantize_rmsnorm_rowwise", "rmsnorm_bwd",
+    "moe_route_fwd", "moe_sort", "moe_route_sort", "moe_route_bwd",
+    "moe_dispatch", "moe_combine_fwd", "moe_combine_bwd",
     "EXPORTED_SYMBOLS",
 ]
 
@@ -44,6 +47,8 @@ _STATUS = {0: "OK", 1: "ERR_NULL", 2: "ERR_SHAPE", 3: "ERR_ALIGN", 4: "ERR_DTYPE
 _p = ctypes.c_void_p
 _i64 = ctypes.c_int64
 _i32 = ctypes.c_int32
+_int = ctypes.c_int
+_f64 = ctypes.c_double
 
 # name -> (restype, argtypes); mirrors include/mxmoe.h
 _SIGS = {
@@ -86,6 +91,20 @@ _SIGS = {
     "int8_grouped_gemm_fwd": (ctypes.c_int, [_p, _p, _p, _p, _p, _i32, _i64, _i64, _i64, _p, ctypes.c_int, _p]),
     "adamw_step": (ctypes.c_int, [_p, _i32, ctypes.c_int, _i32, _p, _p]),
     "adamw_dequantize": (ctypes.c_int, [_p, _p, _i64, _i32, _p, ctypes.c_int, _p]),
+    "rmsnorm_fwd": (_int, [_p, _int, _p, _int, _p, _int, _i64, _i64, _f64, _p, _int, _p, _p]),
+    "int8_quantize_rmsnorm_rowwise": (_int, [_p, _int, _p, _int, _p, _int, _i64, _i64, _f64, _p, _p, _p, _p, _p]),
+    "mx_quantize_rmsnorm_rowwise": (_int, [_p, _int, _p, _int, _p, _int, _i64, _i64, _f64, _p, _p, _p, _p, _p]),
+    "rmsnorm_bwd_workspace": (_i64, [_i64, _i64]),
+    "rmsnorm_bwd": (_int, [_p, _int, _p, _int, _p, _int, _p, _i64, _i64, _f64, _p, _p, _p, _p]),
+    "moe_route_fwd": (_int, [_p, _int, _p, _p, _i64, _i32, _i32, _int, _i32, _i32, _i32, _i32, _f64, _p, _p, _p]),
+    "moe_sort_workspace": (_i64, [_i64, _i32]),
+    "moe_sort": (_int, [_p, _i64, _i32, _i32, _i32, _p, _p, _p, _p, _p]),
+    "moe_route_sort": (_int, [_p, _int, _p, _p, _i64, _i32, _i32, _int, _i32, _i32, _i32, _i32, _f64, _p, _p, _i32, _i32,
+                              _p, _p, _p, _p, _p]),
+    "moe_route_bwd": (_int, [_p, _p, _p, _int, _i64, _i32, _i32, _int, _i32, _f64, _p, _p]),
+    "moe_dispatch": (_int, [_p, _i64, _p, _i64, _p, _i64, _i32, _i64, _p, _p, _p]),
+    "moe_combine_fwd": (_int, [_p, _int, _p, _p, _p, _int, _i64, _i32, _i64, _i64, _p, _int, _p]),
+    "moe_combine_bwd": (_int, [_p, _int, _p, _p, _p, _int, _i64, _i32, _i64, _i64, _p, _p, _p]),
 }
 # the 128-byte tiled layouts: the same arguments as the row-major entry points
 for _n in ("mx_quantize_rowwise", "mx_quantize_colwise", "mx_quantize_dual", "mx_grouped_gemm_fwd",
@@ -901,3 +920,321 @@ def adamw_dequantize(q, s, moment: str, out_dtype: str = "f32", out=None, stream
     _run("adamw_dequantize", (q, s, out), stream, q.data_ptr(), s.data_ptr(), q.numel(), int(moment == "exp_avg_sq"),
          out.data_ptr(), cdt)
     return out
+
+
+# ---------------------------------------------------------------- norm
+@functools.lru_cache(None)
+def _floats():
+    """The element types of the norm's and the rows' tensors, and their codes."""
+    torch = _torch()
+    return {torch.float32: MXMOE_F32, torch.bfloat16: MXMOE_BF16}
+
+
+def _norm_inputs(x, w, residual, h, stream):
+    """Checked arguments of a norm: the tensors, the C call's first arguments, its h."""
+    floats = _floats()
+    R, C = _rows("x", x, floats)
+    _want("w", w, floats, (C,))
+    if residual is None:
+        if h is not None:
+            raise ValueError("h goes with residual, and only with it")
+        return (x, w), (x.data_ptr(), floats[x.dtype], None, 0, w.data_ptr(), floats[w.dtype], R, C), None
+    _want("residual", residual, floats, (R, C))
+    if h is None:
+        h = _empty((R, C), residual.dtype, x, stream)
+    else:
+        _want("h", h, (residual.dtype,), (R, C))
+    return (x, w, residual, h), (x.data_ptr(), floats[x.dtype], residual.data_ptr(), floats[residual.dtype],
+                                 w.data_ptr(), floats[w.dtype], R, C), h
+
+
+def rmsnorm_fwd(x, w, eps: float = 1e-6, residual=None, out_dtype: str = "bf16", y=None, h=None, stream=None):
+    """Root-mean-square norm y [R, C] = h / sqrt(mean(h^2) + eps) * w of x [R, C], and with residual [R, C] of
+    h = x + residual rounded to the residual's type, which is returned too: y, or (y, h).
+
+    x, residual and w [C] are f32 or bf16 each.  h may be the residual itself (updated in place).  C % 8 == 0,
+    C <= 32768."""
+    tensors, args, h = _norm_inputs(x, w, residual, h, stream)
+    tdt, cdt = _out_dtype(out_dtype)
+    if y is None:
+        y = _empty(x.shape, tdt, x, stream)
+    else:
+        _want("y", y, (tdt,), x.shape)
+    _run("rmsnorm_fwd", (*tensors, y), stream, *args, eps, y.data_ptr(), cdt, None if h is None else h.data_ptr())
+    return y if h is None else (y, h)
+
+
+def _quantize_rmsnorm(name, x, w, eps, residual, with_y, q, s, h, y, stream, qdt, sdt, sshape):
+    tensors, args, h = _norm_inputs(x, w, residual, h, stream)
+    q = _empty(x.shape, qdt, x, stream) if q is None else q
+    s = _empty(sshape, sdt, x, stream) if s is None else s
+    _want("q", q, (qdt,), x.shape)
+    _want("s", s, (sdt,), sshape)
+    tensors += (q, s)
+    if y is not None or with_y:
+        bf16 = _torch().bfloat16
+        y = _empty(x.shape, bf16, x, stream) if y is None else y
+        _want("y", y, (bf16,), x.shape)
+        tensors += (y,)
+    _run(name, tensors, stream, *args, eps, q.data_ptr(), s.data_ptr(), None if y is None else y.data_ptr(),
+         None if h is None else h.data_ptr())
+    return (q, s) + (() if h is None else (h,)) + (() if y is None else (y,))
+
+
+def int8_quantize_rmsnorm_rowwise(x, w, eps: float = 1e-6, residual=None, with_y: bool = False, q=None, s=None, h=None,
+                                  y=None, stream=None):
+    """rmsnorm_fwd's y as 8-bit integers with a scale per row (as int8_quantize_rowwise's, in one rounding from the
+    exact values): (q int8 [R, C], s f32 [R]), then h with a residual, then y in bf16 with `with_y`."""
+    torch = _torch()
+    return _quantize_rmsnorm("int8_quantize_rmsnorm_rowwise", x, w, eps, residual, with_y, q, s, h, y, stream, torch.int8,
+                             torch.float32, x.shape[:1])
+
+
+def mx_quantize_rmsnorm_rowwise(x, w, eps: float = 1e-6, residual=None, with_y: bool = False, q=None, s=None, h=None,
+                                y=None, stream=None):
+    """rmsnorm_fwd's y as E4M3 codes with a scale per 32 (as mx_quantize_rowwise's, in one rounding from the exact
+    values): (q uint8 [R, C], s uint8 [R, C/32]), then h with a residual, then y in bf16 with `with_y`."""
+    u8 = _torch().uint8
+    return _quantize_rmsnorm("mx_quantize_rmsnorm_rowwise", x, w, eps, residual, with_y, q, s, h, y, stream, u8, u8,
+                             (*x.shape[:1], x.shape[-1] // 32))
+
+
+def rmsnorm_bwd(dy, h, w, eps: float = 1e-6, dres=None, dx=None, dw=None, need_dw: bool = True, stream=None):
+    """Gradients of rmsnorm_fwd's y with respect to h [R, C] (which is that of x and of the residual) and w:
+    (dx of h's type [R, C], dw f32 [C], or None without need_dw).
+
+    dy [R, C] f32 or bf16; dres, of h's type, is the gradient that reaches h by another way and is added (dx may be dres
+    itself)."""
+    torch = _torch()
+    floats = _floats()
+    R, C = _rows("h", h, floats)
+    _want("dy", dy, floats, (R, C))
+    _want("w", w, floats, (C,))
+    tensors = (dy, h, w)
+    if dres is not None:
+        _want("dres", dres, (h.dtype,), (R, C))
+        tensors += (dres,)
+    if dx is None:
+        dx = _empty((R, C), h.dtype, h, stream)
+    else:
+        _want("dx", dx, (h.dtype,), (R, C))
+    tensors += (dx,)
+    ws = None
+    if need_dw:
+        if dw is None:
+            dw = _empty((C,), torch.float32, h, stream)
+        else:
+            _want("dw", dw, (torch.float32,), (C,))
+        ws = _empty((max(0, lib().rmsnorm_bwd_workspace(R, C)),), torch.uint8, h, stream)
+        tensors += (dw,)
+    elif dw is not None:
+        raise ValueError("dw goes with need_dw")
+    _run("rmsnorm_bwd", tensors, stream, dy.data_ptr(), floats[dy.dtype], h.data_ptr(), floats[h.dtype], w.data_ptr(),
+         floats[w.dtype], None if dres is None else dres.data_ptr(), R, C, eps, dx.data_ptr(),
+         None if dw is None else dw.data_ptr(), None if ws is None else ws.data_ptr())
+    return dx, dw
+
+
+# ---------------------------------------------------------------- routing
+_SCORES = {"softmax": 0, "sigmoid": 1}
+
+
+def _score(score):
+    if score not in _SCORES:
+        raise ValueError(f"score: expected 'softmax' or 'sigmoid', got {score!r}")
+    return _SCORES[score]
+
+
+def _route(name, logits, top, score, bias, groups, keep_groups, group_top, renormalize, scale, valid, ids, weights, sort,
+           stream):
+    torch = _torch()
+    floats = _floats()
+    T, E = _rows("logits", logits, floats)
+    tensors = (logits,)
+    if bias is not None:
+        _want("bias", bias, (torch.float32,), (E,))
+        tensors += (bias,)
+    if valid is not None:
+        _want("valid", valid, (torch.bool, torch.uint8), (T,))
+        tensors += (valid,)
+    ids = _empty((T, top), torch.int32, logits, stream) if ids is None else ids
+    weights = _empty((T, top), torch.float32, logits, stream) if weights is None else weights
+    _want("ids", ids, (torch.int32,), (T, top))
+    _want("weights", weights, (torch.float32,), (T, top))
+    _run(name, (*tensors, ids, weights, *sort[0]), stream, logits.data_ptr(), floats[logits.dtype],
+         None if bias is None else bias.data_ptr(), None if valid is None else valid.data_ptr(), T, E, top, _score(score),
+         groups, groups if keep_groups is None else keep_groups, group_top, int(renormalize), scale, ids.data_ptr(),
+         weights.data_ptr(), *sort[1])
+    return ids, weights
+
+
+def moe_route_fwd(logits, top: int, score: str = "softmax", bias=None, groups: int = 1, keep_groups: Optional[int] = None,
+                  group_top: int = 1, renormalize: bool = True, scale: float = 1.0, valid=None, ids=None, weights=None,
+                  stream=None):
+    """The `top` experts of each token and their weights from router logits [T, E] (f32 or bf16): (ids int32 [T, top],
+    weights f32 [T, top]).
+
+    The choice goes by softmax or sigmoid scores, plus bias f32 [E] if given (which balances and does not weigh);
+    of `groups` groups of consecutive experts only the keep_groups with the largest sum of their group_top (1 or 2)
+    best stay.  Equal ones: the lower index.  Weights are the scores, divided by their sum if renormalize, times
+    scale.  valid (bool [T]): tokens that are False get ids of -1 and weights of 0."""
+    return _route("moe_route_fwd", logits, top, score, bias, groups, keep_groups, group_top, renormalize, scale, valid,
+                  ids, weights, ((), ()), stream)
+
+
+def _sort_outputs(T, top, G, first, offs, row_idx, pos, like, stream):
+    i32 = _torch().int32
+    offs = _empty((G + 1,), i32, like, stream) if offs is None else offs
+    row_idx = _empty((T * top,), i32, like, stream) if row_idx is None else row_idx
+    pos = _empty((T, top), i32, like, stream) if pos is None else pos
+    _want("offs", offs, (i32,), (G + 1,))
+    _want("row_idx", row_idx, (i32,), (T * top,))
+    _want("pos", pos, (i32,), (T, top))
+    need = lib().moe_sort_workspace(T * top, G)
+    ws = _empty((need,), _torch().uint8, like, stream) if need > 0 else None
+    return (offs, row_idx, pos), (G, first, offs.data_ptr(), row_idx.data_ptr(), pos.data_ptr(),
+                                  None if ws is None else ws.data_ptr()), ws
+
+
+def moe_sort(ids, G: int, first: int = 0, offs=None, row_idx=None, pos=None, stream=None):
+    """The chosen pairs ids int32 [T, top] by expert, for the G experts from `first` on that are here: (offs int32
+    [G+1], row_idx int32 [T*top] the token of each row, pos int32 [T, top] the row of each pair).
+
+    An expert's rows keep the order of their tokens.  Pairs of other experts and negative ids have no row: pos -1, and
+    row_idx is -1 from offs[G] on."""
+    T, top = _rows("ids", ids, (_torch().int32,))
+    out, args, ws = _sort_outputs(T, top, G, first, offs, row_idx, pos, ids, stream)
+    _run("moe_sort", (ids, *out), stream, ids.data_ptr(), T, top, *args)
+    return out
+
+
+def moe_route_sort(logits, top: int, G: Optional[int] = None, first: int = 0, score: str = "softmax", bias=None,
+                   groups: int = 1, keep_groups: Optional[int] = None, group_top: int = 1, renormalize: bool = True,
+                   scale: float = 1.0, valid=None, ids=None, weights=None, offs=None, row_idx=None, pos=None, stream=None):
+    """moe_route_fwd and moe_sort at once: (ids, weights, offs, row_idx, pos).  G: the experts here (all)."""
+    T, E = _rows("logits", logits, _floats())
+    out, args, ws = _sort_outputs(T, top, E if G is None else G, first, offs, row_idx, pos, logits, stream)
+    return (*_route("moe_route_sort", logits, top, score, bias, groups, keep_groups, group_top, renormalize, scale, valid,
+                    ids, weights, (out, args), stream), *out)
+
+
+def moe_route_bwd(dweights, ids, logits, score: str = "softmax", renormalize: bool = True, scale: float = 1.0,
+                  dlogits=None, stream=None):
+    """dlogits [T, E] (of the logits' type) from dweights f32 [T, top], with the forward call's ids and logits."""
+    torch = _torch()
+    floats = _floats()
+    T, E = _rows("logits", logits, floats)
+    _want("ids", ids, (torch.int32,), (T, None))
+    _want("dweights", dweights, (torch.float32,), ids.shape)
+    if dlogits is None:
+        dlogits = _empty((T, E), logits.dtype, logits, stream)
+    else:
+        _want("dlogits", dlogits, (logits.dtype,), (T, E))
+    _run("moe_route_bwd", (dweights, ids, logits, dlogits), stream, dweights.data_ptr(), ids.data_ptr(), logits.data_ptr(),
+         floats[logits.dtype], T, E, ids.shape[1], _score(score), int(renormalize), scale, dlogits.data_ptr())
+    return dlogits
+
+
+# ---------------------------------------------------------------- rows out and back
+def _pairs(pos, weights, T):
+    """Checked pos [T, top] and weights of the rows' entry points: top."""
+    torch = _torch()
+    _want("pos", pos, (torch.int32,), (T, None))
+    if weights is not None:
+        _want("weights", weights, (torch.float32,), pos.shape)
+    return pos.shape[1]
+
+
+def moe_dispatch(x, pos, scales=None, rows: Optional[int] = None, xr=None, sr=None, stream=None):
+    """Tokens' rows to their experts' places: xr[pos[t, k]] = x[t] for x [T, C] (bf16, f32, int8 or uint8) and pos int32
+    [T, top] (moe_sort's): xr [rows, C], rows T * top unless given.  With scales [T] or [T, S] of the rows (f32 or uint8)
+    also sr[pos[t, k]] = scales[t]: (xr, sr).  Rows that no pair names stay as they were."""
+    torch = _torch()
+    T, C = _rows("x", x, (torch.bfloat16, torch.float32, torch.int8, torch.uint8))
+    top = _pairs(pos, None, T)
+    M = (T * top if rows is None else rows) if xr is None else xr.shape[0]
+    if xr is None:
+        xr = _empty((M, C), x.dtype, x, stream)
+    else:
+        _want("xr", xr, (x.dtype,), (M, C))
+    if scales is None:
+        if sr is not None:
+            raise ValueError("sr goes with scales")
+        _run("moe_dispatch", (x, pos, xr), stream, x.data_ptr(), C * x.element_size(), None, 0, pos.data_ptr(), T, top, M,
+             xr.data_ptr(), None)
+        return xr
+    shape = scales.shape[1:]
+    _want("scales", scales, (torch.float32, torch.uint8), (T, *shape))
+    if sr is None:
+        sr = _empty((M, *shape), scales.dtype, x, stream)
+    else:
+        _want("sr", sr, (scales.dtype,), (M, *shape))
+    _run("moe_dispatch", (x, pos, scales, xr, sr), stream, x.data_ptr(), C * x.element_size(), scales.data_ptr(),
+         shape.numel() * scales.element_size(), pos.data_ptr(), T, top, M, xr.data_ptr(), sr.data_ptr())
+    return xr, sr
+
+
+def moe_combine_fwd(y, pos, weights=None, residual=None, out_dtype: str = "bf16", out=None, stream=None):
+    """Weighted sums of the tokens' rows: out [T, C] = residual + sum_k weights[t, k] y[pos[t, k]] for y [M, C], pos int32
+    [T, top] (moe_sort's; pairs without a row add nothing), weights f32 [T, top] (None: 1, which is moe_dispatch's
+    backward) and residual [T, C] (None: 0).  y and residual are f32 or bf16 each; out may be the residual itself."""
+    floats = _floats()
+    M, C = _rows("y", y, floats)
+    T = pos.shape[0]
+    top = _pairs(pos, weights, T)
+    tdt, cdt = _out_dtype(out_dtype)
+    tensors = (y, pos)
+    if weights is not None:
+        tensors += (weights,)
+    if residual is not None:
+        _want("residual", residual, floats, (T, C))
+        tensors += (residual,)
+    if out is None:
+        out = _empty((T, C), tdt, y, stream)
+    else:
+        _want("out", out, (tdt,), (T, C))
+    _run("moe_combine_fwd", (*tensors, out), stream, y.data_ptr(), floats[y.dtype], pos.data_ptr(),
+         None if weights is None else weights.data_ptr(), None if residual is None else residual.data_ptr(),
+         0 if residual is None else floats[residual.dtype], T, top, M, C, out.data_ptr(), cdt)
+    return out
+
+
+def moe_combine_bwd(dout, pos, weights=None, y=None, out_dtype: Optional[str] = None, rows: Optional[int] = None, dy=None,
+                    need_dy: bool = True, stream=None):
+    """Gradients of moe_combine_fwd's out [T, C] with respect to y and the weights: (dy [M, C] with dy[pos[t, k]] =
+    weights[t, k] dout[t], dweights f32 [T, top] with the products of dout[t] and y[pos[t, k]], 0 for a pair
+    without a row).
+
+    y [M, C]: the forward call's (without it dweights is None, and dy has `rows` rows, T * top unless given, of
+    out_dtype).  dy is of y's type and may be y itself; rows of it that no pair names stay as they were; it is None
+    without need_dy.  The residual's gradient is dout."""
+    torch = _torch()
+    floats = _floats()
+    T, C = _rows("dout", dout, floats)
+    top = _pairs(pos, weights, T)
+    tensors = (dout, pos)
+    if weights is not None:
+        tensors += (weights,)
+    dweights = None
+    if y is not None:
+        _want("y", y, floats, (None, C))
+        M, dt = y.shape[0], y.dtype
+        if out_dtype is not None and _out_dtype(out_dtype)[0] != dt:
+            raise TypeError(f"out_dtype: dy is of y's type, {dt}")
+        dweights = _empty((T, top), torch.float32, dout, stream)
+        tensors += (y, dweights)
+    else:
+        M = (T * top if rows is None else rows) if dy is None else dy.shape[0]
+        dt = _out_dtype("bf16" if out_dtype is None else out_dtype)[0] if dy is None or out_dtype is not None else dy.dtype
+    if need_dy:
+        if dy is None:
+            dy = _empty((M, C), dt, dout, stream)
+        else:
+            _want("dy", dy, (dt,) if dt in floats else tuple(floats), (M, C))
+        tensors += (dy,)
+    elif dy is not None:
+        raise ValueError("dy goes with need_dy")
+    _run("moe_combine_bwd", tensors, stream, dout.data_ptr(), floats[dout.dtype], pos.data_ptr(),
+         None if weights is None else weights.data_ptr(), None if y is None else y.data_ptr(), floats[dt], T, top, M, C,
+         None if dy is None else dy.data_ptr(), None if dweights is None else dweights.data_ptr())
+    return dy, dweights

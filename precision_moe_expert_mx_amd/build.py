@@ -11,7 +11,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libmxmoe.so")
 SOURCES = ["api.hip", "quant_mx.hip", "quant_bw.hip", "gemm_bw.hip", "gemm_mx.hip", "gemm_dense.hip", "gemm_few.hip",
-           "quant_int8.hip", "adamw.hip"]
+           "quant_int8.hip", "adamw.hip", "norm.hip", "route.hip", "rows.hip"]
 ARCH = "gfx950"
 
 

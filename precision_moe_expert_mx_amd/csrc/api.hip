@@ -8,7 +8,7 @@
 #include <mutex>
 #include <vector>
 
-#include "plain.h"
+#include "layer.h"
 
 using namespace mxmoe;
 
@@ -931,6 +931,279 @@ mxmoe_status adamw_dequantize(const uint8_t* q, const float* s, int64_t n, int32
   TRY(check_ptr(fn, "out", out, 16));
   TRY(check_device());
   return launched(launch_adamw_values(q, s, n, second_moment == 1, odt == MXMOE_BF16, out, (hipStream_t)stream), fn);
+}
+
+// ---- norm ------------------------------------------------------------------------------------
+static bool known(int dt) { return dt == MXMOE_F32 || dt == MXMOE_BF16; }
+
+static mxmoe_status check_norm(const char* fn, int64_t R, int64_t C, int64_t multiple, double eps) {
+  if (R < 0 || C <= 0 || C % multiple || C > kMaxNormRow)
+    return fail(MXMOE_ERR_SHAPE, "%s: need R >= 0, 0 < C <= %d, C %% %d == 0 (R=%lld C=%lld)", fn, (int)kMaxNormRow,
+                (int)multiple, (long long)R, (long long)C);
+  if (R > ((int64_t)1 << 40)) return fail(MXMOE_ERR_SHAPE, "%s: R too large", fn);
+  if (!(eps >= 0x1p-126 && eps <= 1e30)) return fail(MXMOE_ERR_SHAPE, "%s: need 2^-126 <= eps <= 1e30", fn);
+  return MXMOE_OK;
+}
+
+static mxmoe_status rmsnorm_impl(const char* fn, int out, const void* x, int xdt, const void* residual, int rdt,
+                                 const void* w, int wdt, int64_t R, int64_t C, double eps, void* y, int ydt, void* q,
+                                 void* s, void* h, void* stream) {
+  TRY(check_norm(fn, R, C, out == kNormMx ? 32 : 8, eps));
+  if (!known(xdt) || (residual && !known(rdt)) || !known(wdt) || !known(ydt))
+    return fail(MXMOE_ERR_DTYPE, "%s: unknown dtype (x %d, residual %d, w %d, y %d)", fn, xdt, rdt, wdt, ydt);
+  if (R == 0) return ok();
+  TRY(check_ptr(fn, "x", x, 16));
+  TRY(check_ptr(fn, "w", w, 16));
+  if (residual) {
+    TRY(check_ptr(fn, "residual", residual, 16));
+    TRY(check_ptr(fn, "h", h, 16));
+  }
+  if (out == kNormPlain || y) TRY(check_ptr(fn, "y", y, 16));
+  if (out != kNormPlain) {
+    TRY(check_ptr(fn, "q", q, 16));
+    TRY(check_ptr(fn, "s", s, 4));
+  }
+  TRY(check_device());
+  NormArgs a;
+  a.x = x; a.residual = residual; a.w = w; a.h = h; a.y = y; a.q = q; a.s = s;
+  a.R = R; a.C = C; a.eps = eps;
+  a.x_bf16 = xdt == MXMOE_BF16; a.r_bf16 = rdt == MXMOE_BF16; a.w_bf16 = wdt == MXMOE_BF16; a.y_bf16 = ydt == MXMOE_BF16;
+  return launched(launch_rmsnorm(out, a, (hipStream_t)stream), fn);
+}
+
+mxmoe_status rmsnorm_fwd(const void* x, mxmoe_dtype xdt, const void* residual, mxmoe_dtype rdt, const void* w,
+                         mxmoe_dtype wdt, int64_t R, int64_t C, double eps, void* y, mxmoe_dtype ydt, void* h,
+                         void* stream) {
+  return rmsnorm_impl("rmsnorm_fwd", kNormPlain, x, (int)xdt, residual, (int)rdt, w, (int)wdt, R, C, eps, y, (int)ydt,
+                      nullptr, nullptr, h, stream);
+}
+
+mxmoe_status int8_quantize_rmsnorm_rowwise(const void* x, mxmoe_dtype xdt, const void* residual, mxmoe_dtype rdt,
+                                           const void* w, mxmoe_dtype wdt, int64_t R, int64_t C, double eps, int8_t* q,
+                                           float* s, void* y_bf16, void* h, void* stream) {
+  return rmsnorm_impl("int8_quantize_rmsnorm_rowwise", kNormInt8, x, (int)xdt, residual, (int)rdt, w, (int)wdt, R, C,
+                      eps, y_bf16, MXMOE_BF16, q, s, h, stream);
+}
+
+mxmoe_status mx_quantize_rmsnorm_rowwise(const void* x, mxmoe_dtype xdt, const void* residual, mxmoe_dtype rdt,
+                                         const void* w, mxmoe_dtype wdt, int64_t R, int64_t C, double eps, uint8_t* q,
+                                         uint8_t* s, void* y_bf16, void* h, void* stream) {
+  return rmsnorm_impl("mx_quantize_rmsnorm_rowwise", kNormMx, x, (int)xdt, residual, (int)rdt, w, (int)wdt, R, C, eps,
+                      y_bf16, MXMOE_BF16, q, s, h, stream);
+}
+
+int64_t rmsnorm_bwd_workspace(int64_t R, int64_t C) {
+  if (R < 0 || C <= 0 || C % 8 || C > kMaxNormRow) return -1;
+  return rmsnorm_bwd_rows(R, C) * C * 4;
+}
+
+mxmoe_status rmsnorm_bwd(const void* dy, mxmoe_dtype dydt, const void* h, mxmoe_dtype hdt, const void* w,
+                         mxmoe_dtype wdt, const void* dres, int64_t R, int64_t C, double eps, void* dx, float* dw,
+                         void* ws, void* stream) {
+  const char* fn = "rmsnorm_bwd";
+  TRY(check_norm(fn, R, C, 8, eps));
+  if (!known((int)dydt) || !known((int)hdt) || !known((int)wdt))
+    return fail(MXMOE_ERR_DTYPE, "%s: unknown dtype (dy %d, h %d, w %d)", fn, (int)dydt, (int)hdt, (int)wdt);
+  if (dw) TRY(check_ptr(fn, "dw", dw, 16));
+  if (R == 0 && !dw) return ok();
+  if (R) {
+    TRY(check_ptr(fn, "dy", dy, 16));
+    TRY(check_ptr(fn, "h", h, 16));
+    TRY(check_ptr(fn, "w", w, 16));
+    TRY(check_ptr(fn, "dx", dx, 16));
+    if (dres) TRY(check_ptr(fn, "dres", dres, 16));
+    if (dw) TRY(check_ptr(fn, "ws", ws, 16));
+  }
+  TRY(check_device());
+  NormBwdArgs a;
+  a.dy = dy; a.h = h; a.w = w; a.dres = dres; a.dx = dx; a.dw = dw; a.ws = (float*)ws;
+  a.R = R; a.C = C; a.eps = eps;
+  a.dy_bf16 = dydt == MXMOE_BF16; a.h_bf16 = hdt == MXMOE_BF16; a.w_bf16 = wdt == MXMOE_BF16;
+  return launched(launch_rmsnorm_bwd(a, (hipStream_t)stream), fn);
+}
+
+// ---- routing ---------------------------------------------------------------------------------
+static mxmoe_status check_pairs(const char* fn, int64_t T, int32_t top) {
+  if (T < 0 || top < 1 || top > kMaxTop || T > INT32_MAX / top)
+    return fail(MXMOE_ERR_SHAPE, "%s: need T >= 0, 1 <= top <= %d, T * top < 2^31 (T=%lld top=%d)", fn, (int)kMaxTop,
+                (long long)T, (int)top);
+  return MXMOE_OK;
+}
+
+static mxmoe_status check_route(const char* fn, int64_t T, int32_t E, int32_t top, int ldt, int score, double scale) {
+  TRY(check_pairs(fn, T, top));
+  if (E < 1 || E > kMaxG || top > E)
+    return fail(MXMOE_ERR_SHAPE, "%s: need 1 <= E <= %d and top <= E (E=%d top=%d)", fn, (int)kMaxG, (int)E, (int)top);
+  if (!known(ldt)) return fail(MXMOE_ERR_DTYPE, "%s: unknown logits dtype %d", fn, ldt);
+  if (score != MXMOE_SOFTMAX && score != MXMOE_SIGMOID) return fail(MXMOE_ERR_DTYPE, "%s: unknown score %d", fn, score);
+  if (!(scale - scale == 0)) return fail(MXMOE_ERR_SHAPE, "%s: need a finite scale", fn);
+  return MXMOE_OK;
+}
+
+static mxmoe_status check_sort(const char* fn, int64_t P, int32_t G, int32_t first, const int32_t* offs,
+                               const int32_t* row_idx, const int32_t* pos, const void* ws) {
+  if (G < 1 || G > kMaxG || first < 0)
+    return fail(MXMOE_ERR_SHAPE, "%s: need 1 <= G <= %d and first >= 0 (G=%d first=%d)", fn, (int)kMaxG, (int)G, (int)first);
+  TRY(check_ptr(fn, "offs", offs, 4));
+  if (P) {
+    TRY(check_ptr(fn, "row_idx", row_idx, 4));
+    TRY(check_ptr(fn, "pos", pos, 4));
+  }
+  if (moe_sort_workspace(P, G)) TRY(check_ptr(fn, "ws", ws, 16));
+  return MXMOE_OK;
+}
+
+// moe_route_fwd, and moe_route_sort where sort is not null (its ids are filled in here)
+static mxmoe_status route_impl(const char* fn, const void* logits, int ldt, const float* bias, const uint8_t* valid,
+                               int64_t T, int32_t E, int32_t top, int score, int32_t groups, int32_t keep_groups,
+                               int32_t group_top, int32_t renormalize, double scale, int32_t* ids, float* weights,
+                               const SortArgs* sort, void* stream) {
+  TRY(check_route(fn, T, E, top, ldt, score, scale));
+  if (groups < 1 || groups > 64 || E % groups || keep_groups < 1 || keep_groups > groups ||
+      top > E / groups * keep_groups || group_top < 1 || group_top > 2)
+    return fail(MXMOE_ERR_SHAPE, "%s: need groups <= 64 that divide E, 1 <= keep_groups <= groups, top <= E / groups * "
+                "keep_groups, group_top 1 or 2 (E=%d top=%d groups=%d keep_groups=%d group_top=%d)", fn, (int)E, (int)top,
+                (int)groups, (int)keep_groups, (int)group_top);
+  if (sort) {
+    TRY(check_sort(fn, sort->P, sort->G, sort->first, sort->offs, sort->row_idx, sort->pos, sort->ws));
+    if (sort->first > E - sort->G)
+      return fail(MXMOE_ERR_SHAPE, "%s: first + G = %lld beyond E = %d", fn, (long long)sort->first + sort->G, (int)E);
+  }
+  if (bias) TRY(check_ptr(fn, "bias", bias, 4));
+  if (T == 0 && !sort) return ok();
+  if (T) {
+    TRY(check_ptr(fn, "logits", logits, 16));
+    TRY(check_ptr(fn, "ids", ids, 4));
+    TRY(check_ptr(fn, "weights", weights, 4));
+  }
+  TRY(check_device());
+  RouteArgs a;
+  a.logits = logits; a.bias = bias; a.valid = valid; a.T = T; a.E = E; a.top = top;
+  a.bf16 = ldt == MXMOE_BF16; a.sigmoid = score == MXMOE_SIGMOID; a.groups = groups; a.keep = keep_groups;
+  a.group_top = group_top; a.renorm = renormalize != 0; a.scale = scale; a.ids = ids; a.weights = weights;
+  hipError_t e = T ? launch_route_fwd(a, (hipStream_t)stream) : hipSuccess;
+  if (e == hipSuccess && sort) e = launch_sort(*sort, (hipStream_t)stream);
+  return launched(e, fn);
+}
+
+mxmoe_status moe_route_fwd(const void* logits, mxmoe_dtype ldt, const float* bias, const uint8_t* valid, int64_t T,
+                           int32_t E, int32_t top, mxmoe_score score, int32_t groups, int32_t keep_groups,
+                           int32_t group_top, int32_t renormalize, double scale, int32_t* ids, float* weights,
+                           void* stream) {
+  return route_impl("moe_route_fwd", logits, (int)ldt, bias, valid, T, E, top, (int)score, groups, keep_groups, group_top,
+                    renormalize, scale, ids, weights, nullptr, stream);
+}
+
+int64_t moe_sort_workspace(int64_t pairs, int32_t G) {
+  if (pairs < 0 || pairs > INT32_MAX || G < 1 || G > kMaxG) return -1;
+  const int64_t chunks = sort_chunks(pairs);
+  return chunks > 1 ? chunks * (G + 1) * 4 : 0;
+}
+
+mxmoe_status moe_sort(const int32_t* ids, int64_t T, int32_t top, int32_t G, int32_t first, int32_t* offs,
+                      int32_t* row_idx, int32_t* pos, void* ws, void* stream) {
+  const char* fn = "moe_sort";
+  TRY(check_pairs(fn, T, top));
+  TRY(check_sort(fn, T * top, G, first, offs, row_idx, pos, ws));
+  if (T) TRY(check_ptr(fn, "ids", ids, 4));
+  TRY(check_device());
+  const SortArgs a = {ids, T * top, top, G, first, offs, row_idx, pos, (int32_t*)ws};
+  return launched(launch_sort(a, (hipStream_t)stream), fn);
+}
+
+mxmoe_status moe_route_sort(const void* logits, mxmoe_dtype ldt, const float* bias, const uint8_t* valid, int64_t T,
+                            int32_t E, int32_t top, mxmoe_score score, int32_t groups, int32_t keep_groups,
+                            int32_t group_top, int32_t renormalize, double scale, int32_t* ids, float* weights,
+                            int32_t G, int32_t first, int32_t* offs, int32_t* row_idx, int32_t* pos, void* ws,
+                            void* stream) {
+  const char* fn = "moe_route_sort";
+  TRY(check_pairs(fn, T, top));
+  const SortArgs s = {ids, T * top, top, G, first, offs, row_idx, pos, (int32_t*)ws};
+  return route_impl(fn, logits, (int)ldt, bias, valid, T, E, top, (int)score, groups, keep_groups, group_top, renormalize,
+                    scale, ids, weights, &s, stream);
+}
+
+mxmoe_status moe_route_bwd(const float* dweights, const int32_t* ids, const void* logits, mxmoe_dtype ldt, int64_t T,
+                           int32_t E, int32_t top, mxmoe_score score, int32_t renormalize, double scale, void* dlogits,
+                           void* stream) {
+  const char* fn = "moe_route_bwd";
+  TRY(check_route(fn, T, E, top, (int)ldt, (int)score, scale));
+  if (T == 0) return ok();
+  TRY(check_ptr(fn, "dweights", dweights, 4));
+  TRY(check_ptr(fn, "ids", ids, 4));
+  TRY(check_ptr(fn, "logits", logits, 16));
+  TRY(check_ptr(fn, "dlogits", dlogits, 16));
+  TRY(check_device());
+  const RouteBwdArgs a = {dweights, ids, logits, dlogits, T, E, top, ldt == MXMOE_BF16, score == MXMOE_SIGMOID,
+                          renormalize != 0, (float)scale};
+  return launched(launch_route_bwd(a, (hipStream_t)stream), fn);
+}
+
+// ---- rows out and back -----------------------------------------------------------------------
+static mxmoe_status check_rows(const char* fn, int64_t T, int32_t top, int64_t M, int64_t C) {
+  TRY(check_pairs(fn, T, top));
+  if (M < 0 || M > INT32_MAX) return fail(MXMOE_ERR_SHAPE, "%s: need 0 <= M < 2^31 (M=%lld)", fn, (long long)M);
+  if (C <= 0 || C % 8 || C > INT32_MAX)
+    return fail(MXMOE_ERR_SHAPE, "%s: need rows of a multiple of 8, less than 2^31 (%lld)", fn, (long long)C);
+  return MXMOE_OK;
+}
+
+mxmoe_status moe_dispatch(const void* x, int64_t row_bytes, const void* scales, int64_t scale_bytes,
+                          const int32_t* pos, int64_t T, int32_t top, int64_t M, void* xr, void* sr, void* stream) {
+  const char* fn = "moe_dispatch";
+  TRY(check_rows(fn, T, top, M, row_bytes));
+  if (scales ? scale_bytes <= 0 || scale_bytes > INT32_MAX : scale_bytes != 0)
+    return fail(MXMOE_ERR_SHAPE, "%s: scale_bytes = %lld", fn, (long long)scale_bytes);
+  if (T == 0 || M == 0) return ok();
+  TRY(check_ptr(fn, "x", x, 16));
+  TRY(check_ptr(fn, "pos", pos, 4));
+  TRY(check_ptr(fn, "xr", xr, 16));
+  if (scales) {
+    TRY(check_ptr(fn, "scales", scales, 4));
+    TRY(check_ptr(fn, "sr", sr, 4));
+  }
+  TRY(check_device());
+  const DispatchArgs a = {(const uint8_t*)x, (const uint8_t*)scales, pos, (uint8_t*)xr, (uint8_t*)sr, T, M, row_bytes,
+                          scale_bytes, top};
+  return launched(launch_dispatch(a, (hipStream_t)stream), fn);
+}
+
+mxmoe_status moe_combine_fwd(const void* y, mxmoe_dtype ydt, const int32_t* pos, const float* weights,
+                             const void* residual, mxmoe_dtype rdt, int64_t T, int32_t top, int64_t M, int64_t C,
+                             void* out, mxmoe_dtype odt, void* stream) {
+  const char* fn = "moe_combine_fwd";
+  TRY(check_rows(fn, T, top, M, C));
+  if (!known((int)ydt) || (residual && !known((int)rdt)) || !known((int)odt))
+    return fail(MXMOE_ERR_DTYPE, "%s: unknown dtype (y %d, residual %d, out %d)", fn, (int)ydt, (int)rdt, (int)odt);
+  if (T == 0) return ok();
+  if (M) TRY(check_ptr(fn, "y", y, 16));
+  TRY(check_ptr(fn, "pos", pos, 4));
+  TRY(check_ptr(fn, "out", out, 16));
+  if (weights) TRY(check_ptr(fn, "weights", weights, 4));
+  if (residual) TRY(check_ptr(fn, "residual", residual, 16));
+  TRY(check_device());
+  const CombineArgs a = {y, pos, weights, residual, out, T, M, C, top, ydt == MXMOE_BF16, rdt == MXMOE_BF16,
+                         odt == MXMOE_BF16};
+  return launched(launch_combine_fwd(a, (hipStream_t)stream), fn);
+}
+
+mxmoe_status moe_combine_bwd(const void* dout, mxmoe_dtype ddt, const int32_t* pos, const float* weights, const void* y,
+                             mxmoe_dtype ydt, int64_t T, int32_t top, int64_t M, int64_t C, void* dy, float* dweights,
+                             void* stream) {
+  const char* fn = "moe_combine_bwd";
+  TRY(check_rows(fn, T, top, M, C));
+  if (!known((int)ddt) || !known((int)ydt))
+    return fail(MXMOE_ERR_DTYPE, "%s: unknown dtype (dout %d, y %d)", fn, (int)ddt, (int)ydt);
+  if (T == 0 || (!dy && !dweights)) return ok();
+  TRY(check_ptr(fn, "dout", dout, 16));
+  TRY(check_ptr(fn, "pos", pos, 4));
+  if (weights) TRY(check_ptr(fn, "weights", weights, 4));
+  if (dweights) TRY(check_ptr(fn, "dweights", dweights, 4));
+  if (M && dweights) TRY(check_ptr(fn, "y", y, 16));
+  if (M && dy) TRY(check_ptr(fn, "dy", dy, 16));
+  TRY(check_device());
+  const CombineBwdArgs a = {dout, pos, weights, y, dy, dweights, T, M, C, top, ddt == MXMOE_BF16, ydt == MXMOE_BF16};
+  return launched(launch_combine_bwd(a, (hipStream_t)stream), fn);
 }
 
 mxmoe_status mxmoe_check_offsets(const int32_t* offs, int32_t G, int64_t M, void* stream) {

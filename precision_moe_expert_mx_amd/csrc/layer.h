@@ -1,0 +1,182 @@
+// Internal launch declarations of the kernels around the experts' products: the norm before them, the choice and
+// the order of a token's experts, the rows' way out and back; arguments already validated.
+#pragma once
+
+#include "plain.h"
+
+namespace mxmoe {
+
+// Longest row of the norm (held in registers by at most 16 waves).
+constexpr int64_t kMaxNormRow = 32768;
+constexpr int32_t kMaxTop = 64;                   // choices of a token: one per lane
+
+enum NormOut { kNormPlain = 0, kNormInt8 = 1, kNormMx = 2 };
+struct NormArgs {
+  const void* x;
+  const void* residual;       // or null: then h is x itself and not written
+  const void* w;
+  void* h;
+  void* y;                    // plain: bf16 or f32; 8 bits: bf16, or null
+  void* q;                    // 8 bits
+  void* s;
+  int64_t R, C;
+  double eps;
+  int32_t x_bf16, r_bf16, w_bf16, y_bf16;
+};
+hipError_t launch_rmsnorm(int out, const NormArgs& a, hipStream_t st);
+
+struct NormBwdArgs {
+  const void* dy;
+  const void* h;
+  const void* w;
+  const void* dres;           // of h's type, or null
+  void* dx;                   // of h's type
+  float* dw;                  // or null
+  float* ws;                  // rmsnorm_bwd_rows(R, C) rows of C partial sums
+  int64_t R, C;
+  double eps;
+  int32_t dy_bf16, h_bf16, w_bf16;
+};
+int64_t rmsnorm_bwd_rows(int64_t R, int64_t C);
+hipError_t launch_rmsnorm_bwd(const NormBwdArgs& a, hipStream_t st);
+
+struct RouteArgs {
+  const void* logits;
+  const float* bias;          // or null
+  const uint8_t* valid;       // or null
+  int64_t T;
+  int32_t E, top, bf16, sigmoid, groups, keep, group_top, renorm;
+  double scale;
+  int32_t* ids;
+  float* weights;
+};
+hipError_t launch_route_fwd(const RouteArgs& a, hipStream_t st);
+
+struct RouteBwdArgs {
+  const float* dweights;
+  const int32_t* ids;
+  const void* logits;
+  void* dlogits;              // of the logits' type
+  int64_t T;
+  int32_t E, top, bf16, sigmoid, renorm;
+  float scale;
+};
+hipError_t launch_route_bwd(const RouteBwdArgs& a, hipStream_t st);
+
+struct SortArgs {
+  const int32_t* ids;
+  int64_t P;                  // pairs, T * top
+  int32_t top, G, first;
+  int32_t* offs;
+  int32_t* row_idx;
+  int32_t* pos;
+  int32_t* ws;                // sort_chunks(P) rows of G + 1 counts (not used for one chunk)
+};
+int64_t sort_chunks(int64_t P);
+hipError_t launch_sort(const SortArgs& a, hipStream_t st);
+
+struct DispatchArgs {
+  const uint8_t* x;
+  const uint8_t* scales;      // or null
+  const int32_t* pos;
+  uint8_t* xr;
+  uint8_t* sr;
+  int64_t T, M, row_bytes, scale_bytes;
+  int32_t top;
+};
+hipError_t launch_dispatch(const DispatchArgs& a, hipStream_t st);
+
+struct CombineArgs {
+  const void* y;
+  const int32_t* pos;
+  const float* weights;       // or null: all 1
+  const void* residual;       // or null
+  void* out;
+  int64_t T, M, C;
+  int32_t top, y_bf16, r_bf16, out_bf16;
+};
+hipError_t launch_combine_fwd(const CombineArgs& a, hipStream_t st);
+
+struct CombineBwdArgs {
+  const void* dout;
+  const int32_t* pos;
+  const float* weights;       // or null: all 1
+  const void* y;              // or null: no dweights
+  void* dy;                   // of y's type, or null
+  float* dweights;            // or null
+  int64_t T, M, C;
+  int32_t top, d_bf16, y_bf16;
+};
+hipError_t launch_combine_bwd(const CombineBwdArgs& a, hipStream_t st);
+
+// ---- shared device helpers ----------------------------------------------------------------------
+// Eight consecutive elements as they lie in memory: 16 bytes of bf16 or 32 of fp32.
+struct Raw8 {
+  uint4 a, b;
+};
+template <bool NT>
+__device__ __forceinline__ uint4 load16(const void* p) {
+  if constexpr (NT) return load16_nt((const uint4*)p);
+  return *(const uint4*)p;
+}
+template <bool NT = true>
+__device__ __forceinline__ void load8(Raw8& r, const void* base, int64_t at, bool bf16) {
+  if (bf16) {
+    r.a = load16<NT>((const uint16_t*)base + at);
+  } else {
+    r.a = load16<NT>((const float*)base + at);
+    r.b = load16<NT>((const float*)base + at + 4);
+  }
+}
+__device__ __forceinline__ void to_float8(const Raw8& r, bool bf16, float (&f)[8]) {
+  if (bf16) {
+    const uint32_t v[4] = {r.a.x, r.a.y, r.a.z, r.a.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[2 * i] = __uint_as_float(v[i] << 16);
+      f[2 * i + 1] = __uint_as_float(v[i] & 0xFFFF0000u);
+    }
+  } else {
+    const uint32_t v[8] = {r.a.x, r.a.y, r.a.z, r.a.w, r.b.x, r.b.y, r.b.z, r.b.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(v[i]);
+  }
+}
+// (hardware rounding: nearest even, a NaN stays one)
+__device__ __forceinline__ uint32_t bf16_pack(float a, float b) {
+  return __builtin_bit_cast(uint32_t, v2bf{(__bf16)a, (__bf16)b});
+}
+__device__ __forceinline__ uint4 bf16_pack8(const float (&f)[8]) {
+  return make_uint4(bf16_pack(f[0], f[1]), bf16_pack(f[2], f[3]), bf16_pack(f[4], f[5]), bf16_pack(f[6], f[7]));
+}
+__device__ __forceinline__ void store16_nt(void* p, uint4 v) {
+  __builtin_nontemporal_store(v4u_{v.x, v.y, v.z, v.w}, (v4u_*)p);
+}
+__device__ __forceinline__ void store8(void* base, int64_t at, bool bf16, const float (&f)[8]) {
+  if (bf16) {
+    store16_nt((uint16_t*)base + at, bf16_pack8(f));
+  } else {
+    float* p = (float*)base + at;
+    __builtin_nontemporal_store(v4f{f[0], f[1], f[2], f[3]}, (v4f*)p);
+    __builtin_nontemporal_store(v4f{f[4], f[5], f[6], f[7]}, (v4f*)(p + 4));
+  }
+}
+
+// Sums and maxima over a wave, the result in every lane.
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) v += __shfl_xor(v, d, 64);
+  return v;
+}
+__device__ __forceinline__ double wave_sum(double v) {
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) v += __shfl_xor(v, d, 64);
+  return v;
+}
+__device__ __forceinline__ double wave_max(double v) {
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) v = fmax(v, __shfl_xor(v, d, 64));
+  return v;
+}
+
+}  // namespace mxmoe

@@ -1,0 +1,407 @@
+// Root-mean-square norm of a residual stream on gfx950, with the addition of a block's output before it and its
+// result in bf16, fp32, 8-bit integers (a scale per row) or E4M3 (a scale per 32 elements); and its backward.
+//
+//   h = x + residual, rounded to the residual's type (it is stored, and what the backward pass reads is what is
+//   normalised here);   r = 1 / sqrt(mean_c h^2 + eps);   y = h r w
+//   int8:  v = h w,  q = round-to-nearest-even(127 v / max|v|),  s = fl32(max|v| r / 127)   (r cancels in the codes)
+//   E4M3:  e = max(floor(log2 max|y|) - 8, -127) of 32 elements,  q = E4M3(y 2^-e), saturating
+//   back:  g = dy w,  dx = r (g - h r^2 mean_c(g h)) + dres,  dw = sum over rows of dy h r
+//
+// The squares are summed in fp64, so that they neither overflow nor vanish and the codes are those of the
+// exact values.  8-bit codes are formed in one rounding from y, not from its bf16 value.
+#include <algorithm>
+
+#include "layer.h"
+
+namespace mxmoe {
+namespace {
+
+// ---- sums over the WPR waves of a row (every thread of the block meets the barriers) ------------
+template <int WPR, typename V>
+__device__ __forceinline__ V row_sum(V v, V* red) {
+  v = wave_sum(v);
+  if constexpr (WPR > 1) {
+    const int w = threadIdx.x >> 6;
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0) red[w] = v;
+    __syncthreads();
+    v = 0;
+#pragma unroll
+    for (int k = 0; k < WPR; ++k) v += red[w / WPR * WPR + k];
+  }
+  return v;
+}
+template <int WPR>
+__device__ __forceinline__ double row_max(double v, double* red) {
+  v = wave_max(v);
+  if constexpr (WPR > 1) {
+    const int w = threadIdx.x >> 6;
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0) red[w] = v;
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < WPR; ++k) v = fmax(v, red[w / WPR * WPR + k]);
+  }
+  return v;
+}
+// 1 / sqrt(m) of a positive m in fp64: the hardware's estimate and two Newton steps (0 of infinity, which they would
+// make a NaN of).
+__device__ __forceinline__ double rsqrt64(double m) {
+  if (m == __builtin_inf()) return 0;
+  double r = __builtin_amdgcn_rsq(m);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) r = fma(0.5 * r, fma(-m * r, r, 1.0), r);
+  return r;
+}
+// y in fp32 so that a second rounding to fewer bits gives what one rounding of y would: cut off towards zero, the
+// last bit set where anything was cut ("round to odd").
+__device__ __forceinline__ float round_to_odd(double y) {
+  const float f = (float)y;
+  const double back = (double)f;
+  if (back == y || y != y) return f;
+  uint32_t u = __float_as_uint(f);
+  if (fabs(back) > fabs(y)) --u;
+  return __uint_as_float(u | 1u);
+}
+
+// Waves of a row (WPR) and chunks of 8 elements per lane (NCH).  Rows past R of the last block repeat row R - 1
+// without storing.
+template <int OUT, int WPR, int NCH>
+__global__ __launch_bounds__(WPR > 4 ? 64 * WPR : 256) void rmsnorm_kernel(NormArgs p) {
+  constexpr int NT = WPR > 4 ? 64 * WPR : 256;
+  __shared__ double red[NT / 64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t row_raw = (int64_t)blockIdx.x * (NT / 64 / WPR) + wave / WPR;
+  const bool live = row_raw < p.R;
+  const int64_t row = live ? row_raw : p.R - 1;
+  const int64_t C = p.C, at0 = row * C;
+  const int l = 64 * (wave % WPR) + lane;
+  const bool x_bf16 = p.x_bf16, r_bf16 = p.r_bf16, w_bf16 = p.w_bf16;
+
+  float h[NCH][8];
+  {
+    Raw8 x[NCH], r[NCH];
+#pragma unroll
+    for (int k = 0; k < NCH; ++k) {
+      const int64_t c = 8 * (l + 64 * WPR * k);
+      x[k].a = x[k].b = r[k].a = r[k].b = make_uint4(0, 0, 0, 0);
+      if (c < C) {
+        load8(x[k], p.x, at0 + c, x_bf16);
+        if (p.residual) load8(r[k], p.residual, at0 + c, r_bf16);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < NCH; ++k) {
+      to_float8(x[k], x_bf16, h[k]);
+      if (p.residual) {
+        float f[8];
+        to_float8(r[k], r_bf16, f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          h[k][e] += f[e];
+          if (r_bf16) h[k][e] = (float)(__bf16)h[k][e];
+        }
+        const int64_t c = 8 * (l + 64 * WPR * k);
+        if (live && c < C) store8(p.h, at0 + c, r_bf16, h[k]);
+      }
+    }
+  }
+  double sum = 0;
+#pragma unroll
+  for (int k = 0; k < NCH; ++k)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sum = fma((double)h[k][e], (double)h[k][e], sum);
+  sum = row_sum<WPR>(sum, red);
+  const double r64 = rsqrt64(sum / (double)C + p.eps);
+  const float r32 = (float)r64;
+
+  auto weight = [&](int k, float (&w)[8]) {
+    const int64_t c = 8 * (l + 64 * WPR * k);
+    Raw8 t;
+    t.a = t.b = make_uint4(0, 0, 0, 0);
+    if (c < C) load8<false>(t, p.w, c, w_bf16);
+    to_float8(t, w_bf16, w);
+  };
+
+  if constexpr (OUT == kNormInt8) {
+    double amax = 0;
+    bool nan = false;                              // (fmax drops a NaN)
+#pragma unroll
+    for (int k = 0; k < NCH; ++k) {
+      float w[8];
+      weight(k, w);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const double v = (double)h[k][e] * (double)w[e];
+        amax = fmax(amax, fabs(v));
+        nan |= v != v;
+      }
+    }
+    if (nan) amax = __builtin_inf();
+    amax = row_max<WPR>(amax, red);
+    const bool finite = amax < __builtin_inf() && sum < __builtin_inf();
+    const bool zero = amax == 0;
+    if (live && l == 0) ((float*)p.s)[row] = zero && finite ? 1.0f : finite ? (float)(amax * r64 / 127.0) : __builtin_nanf("");
+    const bool dead = zero || !finite;
+    const double inv = dead ? 0.0 : 127.0 / amax;
+#pragma unroll
+    for (int k = 0; k < NCH; ++k) {
+      const int64_t c = 8 * (l + 64 * WPR * k);
+      float w[8], y[8];
+      weight(k, w);
+      uint32_t code[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const double v = (double)h[k][e] * (double)w[e];
+        // a product with the rounded reciprocal is within 2^-52 of the quotient: where it is that near to a tie, divide
+        const double t = v * inv;
+        double n = rint(t);
+        if (fabs(t - n) > 0.5 - 1e-12) n = rint(127.0 * v / amax);
+        code[e] = dead ? 0u : (uint32_t)(int)n & 255u;
+        y[e] = h[k][e] * r32 * w[e];
+      }
+      if (live && c < C) {
+        store8_nt((uint2*)((int8_t*)p.q + at0 + c),
+                  make_uint2(code[0] | code[1] << 8 | code[2] << 16 | code[3] << 24,
+                             code[4] | code[5] << 8 | code[6] << 16 | code[7] << 24));
+        if (p.y) store8(p.y, at0 + c, true, y);
+      }
+    }
+  } else if constexpr (OUT == kNormMx) {
+#pragma unroll
+    for (int k = 0; k < NCH; ++k) {
+      const int64_t c = 8 * (l + 64 * WPR * k);
+      float w[8], y[8], o[8];
+      weight(k, w);
+      uint32_t m = 0;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        o[e] = round_to_odd((double)h[k][e] * (double)w[e] * r64);
+        m = max(m, __float_as_uint(o[e]) & 0x7FFFFFFFu);
+        y[e] = h[k][e] * r32 * w[e];
+      }
+      m = quad_max(m);                             // 4 lanes hold a block of 32
+      const int e8 = max((int)(m >> 23) - 135, -127);
+      const float scale = __uint_as_float((uint32_t)(e8 + 127) << 23);
+      const float lim = __uint_as_float(((uint32_t)(e8 + 135) << 23) | 0x600000u);   // 448 * 2^e8
+      if (live && c < C) {
+        store8_nt((uint2*)((uint8_t*)p.q + at0 + c),
+                  make_uint2(cvt4_f32_e4m3_scaled(o[0], o[1], o[2], o[3], lim, scale),
+                             cvt4_f32_e4m3_scaled(o[4], o[5], o[6], o[7], lim, scale)));
+        if ((lane & 3) == 0) ((uint8_t*)p.s)[row * (C / 32) + c / 32] = (uint8_t)(e8 + 127);
+        if (p.y) store8(p.y, at0 + c, true, y);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < NCH; ++k) {
+      const int64_t c = 8 * (l + 64 * WPR * k);
+      float w[8], y[8];
+      weight(k, w);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) y[e] = h[k][e] * r32 * w[e];
+      if (live && c < C) store8(p.y, at0 + c, p.y_bf16, y);
+    }
+  }
+}
+
+// ---- backward ----------------------------------------------------------------------------------
+// A block takes rows blockIdx.x, blockIdx.x + gridDim.x, ... (times its rows at once), keeps the weights and its part of
+// dw in registers, and writes that part to its row of the workspace; a second launch adds the parts up.
+template <int WPR, int NCH>
+__global__ __launch_bounds__(WPR > 4 ? 64 * WPR : 256) void rmsnorm_bwd_kernel(NormBwdArgs p) {
+  constexpr int NT = WPR > 4 ? 64 * WPR : 256, RPB = NT / 64 / WPR;
+  __shared__ double red64[NT / 64];
+  __shared__ float red[NT / 64];
+  __shared__ float part[RPB > 1 ? RPB - 1 : 1][RPB > 1 ? 512 * WPR * NCH : 1];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, sub = wave / WPR;
+  const int64_t C = p.C;
+  const int l = 64 * (wave % WPR) + lane;
+  const bool dy_bf16 = p.dy_bf16, h_bf16 = p.h_bf16;
+  float w[NCH][8], acc[NCH][8];
+#pragma unroll
+  for (int k = 0; k < NCH; ++k) {
+    const int64_t c = 8 * (l + 64 * WPR * k);
+    Raw8 t;
+    t.a = t.b = make_uint4(0, 0, 0, 0);
+    if (c < C) load8<false>(t, p.w, c, p.w_bf16);
+    to_float8(t, p.w_bf16, w[k]);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) acc[k][e] = 0;
+  }
+  for (int64_t r0 = (int64_t)blockIdx.x * RPB; r0 < p.R; r0 += (int64_t)gridDim.x * RPB) {
+    const bool live = r0 + sub < p.R;
+    const int64_t at0 = (live ? r0 + sub : p.R - 1) * C;
+    Raw8 a[NCH], b[NCH], d[NCH];
+#pragma unroll
+    for (int k = 0; k < NCH; ++k) {
+      const int64_t c = 8 * (l + 64 * WPR * k);
+      a[k].a = a[k].b = b[k].a = b[k].b = d[k].a = d[k].b = make_uint4(0, 0, 0, 0);
+      if (c < C) {
+        load8(a[k], p.dy, at0 + c, dy_bf16);
+        load8(b[k], p.h, at0 + c, h_bf16);
+        if (p.dres) load8(d[k], p.dres, at0 + c, h_bf16);
+      }
+    }
+    float dy[NCH][8], h[NCH][8];
+    double sum = 0;
+    float dot = 0;
+#pragma unroll
+    for (int k = 0; k < NCH; ++k) {
+      to_float8(a[k], dy_bf16, dy[k]);
+      to_float8(b[k], h_bf16, h[k]);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        sum = fma((double)h[k][e], (double)h[k][e], sum);
+        dot = fmaf(dy[k][e] * w[k][e], h[k][e], dot);
+      }
+    }
+    sum = row_sum<WPR>(sum, red64);
+    dot = row_sum<WPR>(dot, red);
+    const float r = (float)rsqrt64(sum / (double)C + p.eps);
+    const float back = dot * r * r / (float)C;
+#pragma unroll
+    for (int k = 0; k < NCH; ++k) {
+      const int64_t c = 8 * (l + 64 * WPR * k);
+      float dx[8], f[8];
+      to_float8(d[k], h_bf16, f);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        dx[e] = fmaf(r, fmaf(-h[k][e], back, dy[k][e] * w[k][e]), f[e]);
+        if (live) acc[k][e] = fmaf(dy[k][e], h[k][e] * r, acc[k][e]);
+      }
+      if (live && c < C) store8(p.dx, at0 + c, h_bf16, dx);
+    }
+  }
+  if (!p.dw) return;
+  if constexpr (RPB > 1) {
+    if (sub > 0) {
+#pragma unroll
+      for (int k = 0; k < NCH; ++k)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) part[sub - 1][8 * (l + 64 * WPR * k) + e] = acc[k][e];
+    }
+    __syncthreads();
+    if (sub > 0) return;
+#pragma unroll
+    for (int s = 1; s < RPB; ++s)
+#pragma unroll
+      for (int k = 0; k < NCH; ++k)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc[k][e] += part[s - 1][8 * (l + 64 * WPR * k) + e];
+  }
+#pragma unroll
+  for (int k = 0; k < NCH; ++k) {
+    const int64_t c = 8 * (l + 64 * WPR * k);
+    if (c < C) {
+      float* o = p.ws + (int64_t)blockIdx.x * C + c;
+      *(float4*)o = make_float4(acc[k][0], acc[k][1], acc[k][2], acc[k][3]);
+      *(float4*)(o + 4) = make_float4(acc[k][4], acc[k][5], acc[k][6], acc[k][7]);
+    }
+  }
+}
+
+// dw[c] = sum over `rows` rows of the parts, in a fixed order: 64 columns per block, its 16 waves take every 16th row.
+__global__ __launch_bounds__(1024) void column_sum_kernel(const float* ws, int rows, int64_t C, float* dw) {
+  __shared__ float part[16][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t c = (int64_t)blockIdx.x * 64 + lane;
+  float s = 0;
+  if (c < C)
+    for (int r = wave; r < rows; r += 16) s += ws[r * C + c];
+  part[wave][lane] = s;
+  __syncthreads();
+  if (wave == 0 && c < C) {
+    s = 0;
+#pragma unroll
+    for (int k = 0; k < 16; ++k) s += part[k][lane];
+    dw[c] = s;
+  }
+}
+
+constexpr int kBwdBlocks = 512;
+
+// waves of a row and chunks per lane of the backward kernel
+int bwd_waves(int64_t C) { return C <= 2048 ? 1 : C <= 8192 ? 4 : 16; }
+
+}  // namespace
+
+template <int OUT>
+static hipError_t launch_rmsnorm_out(const NormArgs& a, hipStream_t st) {
+  const int64_t C = a.C;
+  // few rows: a row over 16 waves
+  const int wpr = C > 8192 || (a.R <= 512 && C > 2048) ? 16 : C > 2048 ? 4 : 1;
+  const int nch = (int)((C + 512 * wpr - 1) / (512 * wpr));
+  const int64_t per = wpr == 1 ? 4 : 1;
+  auto go = [&](auto kernel) {
+    for (int64_t r = 0; r < a.R; r += per * (kMaxBlocks / 4)) {
+      NormArgs p = a;
+      const int64_t xs = a.x_bf16 ? 2 : 4, rs = a.r_bf16 ? 2 : 4, ys = a.y_bf16 ? 2 : 4;
+      p.R = std::min(a.R - r, per * (kMaxBlocks / 4));
+      p.x = (const uint8_t*)a.x + r * C * xs;
+      if (a.residual) {
+        p.residual = (const uint8_t*)a.residual + r * C * rs;
+        p.h = (uint8_t*)a.h + r * C * rs;
+      }
+      if (a.y) p.y = (uint8_t*)a.y + r * C * ys;
+      if (a.q) p.q = (uint8_t*)a.q + r * C;
+      if (a.s) p.s = (uint8_t*)a.s + r * (OUT == kNormInt8 ? 4 : C / 32);
+      hipLaunchKernelGGL(kernel, dim3((unsigned)((p.R + per - 1) / per)), dim3(wpr > 4 ? 64 * wpr : 256), 0, st, p);
+    }
+  };
+  if (wpr == 1) {
+    if (nch == 1) go(rmsnorm_kernel<OUT, 1, 1>);
+    else if (nch == 2) go(rmsnorm_kernel<OUT, 1, 2>);
+    else if (nch == 3) go(rmsnorm_kernel<OUT, 1, 3>);
+    else go(rmsnorm_kernel<OUT, 1, 4>);
+  } else if (wpr == 4) {
+    if (nch == 2) go(rmsnorm_kernel<OUT, 4, 2>);
+    else if (nch == 3) go(rmsnorm_kernel<OUT, 4, 3>);
+    else go(rmsnorm_kernel<OUT, 4, 4>);
+  } else {
+    if (nch == 1) go(rmsnorm_kernel<OUT, 16, 1>);
+    else if (nch == 2) go(rmsnorm_kernel<OUT, 16, 2>);
+    else go(rmsnorm_kernel<OUT, 16, 4>);
+  }
+  return hipGetLastError();
+}
+
+hipError_t launch_rmsnorm(int out, const NormArgs& a, hipStream_t st) {
+  return out == kNormInt8 ? launch_rmsnorm_out<kNormInt8>(a, st)
+         : out == kNormMx ? launch_rmsnorm_out<kNormMx>(a, st)
+                          : launch_rmsnorm_out<kNormPlain>(a, st);
+}
+
+int64_t rmsnorm_bwd_rows(int64_t R, int64_t C) {
+  const int per = bwd_waves(C) == 1 ? 4 : 1;
+  return std::min<int64_t>((R + per - 1) / per, kBwdBlocks);
+}
+
+hipError_t launch_rmsnorm_bwd(const NormBwdArgs& a, hipStream_t st) {
+  const int wpr = bwd_waves(a.C), nch = (int)((a.C + 512 * wpr - 1) / (512 * wpr));
+  const int blocks = (int)rmsnorm_bwd_rows(a.R, a.C);
+  auto go = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, dim3(blocks), dim3(wpr > 4 ? 64 * wpr : 256), 0, st, a);
+  };
+  if (blocks) {
+    if (wpr == 1) {
+      if (nch == 1) go(rmsnorm_bwd_kernel<1, 1>);
+      else if (nch == 2) go(rmsnorm_bwd_kernel<1, 2>);
+      else if (nch == 3) go(rmsnorm_bwd_kernel<1, 3>);
+      else go(rmsnorm_bwd_kernel<1, 4>);
+    } else if (wpr == 4) {
+      if (nch == 2) go(rmsnorm_bwd_kernel<4, 2>);
+      else if (nch == 3) go(rmsnorm_bwd_kernel<4, 3>);
+      else go(rmsnorm_bwd_kernel<4, 4>);
+    } else {
+      if (nch == 2) go(rmsnorm_bwd_kernel<16, 2>);
+      else if (nch == 3) go(rmsnorm_bwd_kernel<16, 3>);
+      else go(rmsnorm_bwd_kernel<16, 4>);
+    }
+  }
+  if (a.dw)
+    hipLaunchKernelGGL(column_sum_kernel, dim3((unsigned)((a.C + 63) / 64)), dim3(1024), 0, st, a.ws, blocks, a.C, a.dw);
+  return hipGetLastError();
+}
+
+}  // namespace mxmoe
