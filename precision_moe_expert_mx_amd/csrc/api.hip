@@ -1081,9 +1081,7 @@ static mxmoe_status route_impl(const char* fn, const void* logits, int ldt, cons
   a.logits = logits; a.bias = bias; a.valid = valid; a.T = T; a.E = E; a.top = top;
   a.bf16 = ldt == MXMOE_BF16; a.sigmoid = score == MXMOE_SIGMOID; a.groups = groups; a.keep = keep_groups;
   a.group_top = group_top; a.renorm = renormalize != 0; a.scale = scale; a.ids = ids; a.weights = weights;
-  hipError_t e = T ? launch_route_fwd(a, (hipStream_t)stream) : hipSuccess;
-  if (e == hipSuccess && sort) e = launch_sort(*sort, (hipStream_t)stream);
-  return launched(e, fn);
+  return launched(launch_route(a, sort, (hipStream_t)stream), fn);
 }
 
 mxmoe_status moe_route_fwd(const void* logits, mxmoe_dtype ldt, const float* bias, const uint8_t* valid, int64_t T,
@@ -1096,8 +1094,7 @@ mxmoe_status moe_route_fwd(const void* logits, mxmoe_dtype ldt, const float* bia
 
 int64_t moe_sort_workspace(int64_t pairs, int32_t G) {
   if (pairs < 0 || pairs > INT32_MAX || G < 1 || G > kMaxG) return -1;
-  const int64_t chunks = sort_chunks(pairs);
-  return chunks > 1 ? chunks * (G + 1) * 4 : 0;
+  return sort_workspace(pairs, G);
 }
 
 mxmoe_status moe_sort(const int32_t* ids, int64_t T, int32_t top, int32_t G, int32_t first, int32_t* offs,
@@ -1107,7 +1104,7 @@ mxmoe_status moe_sort(const int32_t* ids, int64_t T, int32_t top, int32_t G, int
   TRY(check_sort(fn, T * top, G, first, offs, row_idx, pos, ws));
   if (T) TRY(check_ptr(fn, "ids", ids, 4));
   TRY(check_device());
-  const SortArgs a = {ids, T * top, top, G, first, offs, row_idx, pos, (int32_t*)ws};
+  const SortArgs a = {ids, T * top, top, G, first, offs, row_idx, pos, (uint16_t*)ws, 0, 0, 0};
   return launched(launch_sort(a, (hipStream_t)stream), fn);
 }
 
@@ -1118,7 +1115,7 @@ mxmoe_status moe_route_sort(const void* logits, mxmoe_dtype ldt, const float* bi
                             void* stream) {
   const char* fn = "moe_route_sort";
   TRY(check_pairs(fn, T, top));
-  const SortArgs s = {ids, T * top, top, G, first, offs, row_idx, pos, (int32_t*)ws};
+  const SortArgs s = {ids, T * top, top, G, first, offs, row_idx, pos, (uint16_t*)ws, 0, 0, 0};
   return route_impl(fn, logits, (int)ldt, bias, valid, T, E, top, (int)score, groups, keep_groups, group_top, renormalize,
                     scale, ids, weights, &s, stream);
 }

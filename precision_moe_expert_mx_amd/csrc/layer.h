@@ -50,7 +50,6 @@ struct RouteArgs {
   int32_t* ids;
   float* weights;
 };
-hipError_t launch_route_fwd(const RouteArgs& a, hipStream_t st);
 
 struct RouteBwdArgs {
   const float* dweights;
@@ -70,10 +69,13 @@ struct SortArgs {
   int32_t* offs;
   int32_t* row_idx;
   int32_t* pos;
-  int32_t* ws;                // sort_chunks(P) rows of G + 1 counts (not used for one chunk)
+  uint16_t* ws;               // counts per chunk and bucket (sort_workspace bytes)
+  int32_t chunks, chunk_pairs, block_chunks;       // (set by the launches)
 };
-int64_t sort_chunks(int64_t P);
-hipError_t launch_sort(const SortArgs& a, hipStream_t st);
+int64_t sort_workspace(int64_t P, int32_t G);
+hipError_t launch_sort(SortArgs a, hipStream_t st);
+// and where sort is not null its pairs sorted (of the ids that are written here)
+hipError_t launch_route(const RouteArgs& a, const SortArgs* sort, hipStream_t st);
 
 struct DispatchArgs {
   const uint8_t* x;

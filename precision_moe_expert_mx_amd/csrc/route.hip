@@ -16,7 +16,9 @@ namespace mxmoe {
 namespace {
 
 constexpr int kSortThreads = 1024, kSortWaves = kSortThreads / 64;
-constexpr int kSortChunk = 8192;                  // pairs of a block
+constexpr int kSortChunk = 4096;                  // pairs that one block places without counts
+constexpr int kPlacePairs = 4096;                 // pairs of a block otherwise
+constexpr int kCountBlocks = 512;                 // blocks that count, unless their chunks pass 65535 pairs
 constexpr int kMaxExperts = 1024;
 
 __device__ __forceinline__ float load_logit(const void* base, int64_t at, bool bf16) {
@@ -27,21 +29,28 @@ __device__ __forceinline__ double sigmoid64(double x) {
   return (x >= 0 ? 1.0 : e) / (1.0 + e);
 }
 
-// A wave per token, NE logits per lane (expert e = lane + 64 j).
-template <int NE>
-__global__ __launch_bounds__(256) void route_kernel(RouteArgs p) {
-  __shared__ double sc[4][64 * NE];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t t = (int64_t)blockIdx.x * 4 + wave;
-  if (t >= p.T) return;
-  const int E = p.E, top = p.top;
-  if (p.valid && !p.valid[t]) {
-    if (lane < top) {
-      p.ids[t * top + lane] = -1;
-      p.weights[t * top + lane] = 0;
-    }
-    return;
+
+struct Choice {
+  int id;
+  float w;
+};
+// The weight of lane k's choice from its score w (renormalised softmax scores are a softmax over the chosen).
+__device__ __forceinline__ float weight_in_fp64(const RouteArgs& p, int64_t t, int id, double w) {
+  const bool chosen = (int)(threadIdx.x & 63) < p.top;
+  if (p.renorm && !p.sigmoid) {
+    const double xk = chosen ? (double)load_logit(p.logits, t * p.E + id, p.bf16) : -__builtin_inf();
+    const double xm = wave_max(xk);
+    w = xk != xk ? xk : xm == -__builtin_inf() ? 0.0 : xk == xm ? 1.0 : exp(xk - xm);
   }
+  const double total = p.renorm ? wave_sum(chosen ? w : 0.0) : 1.0;
+  return total == 0 ? 0.0f : (float)(p.scale * w / total);
+}
+
+// One token by a whole wave, everything in fp64, NE logits per lane (expert e = lane + 64 j): the definition as it stands,
+// for calls outside the other kernel's range.  Returns expert k and its weight in lane k < top.
+template <int NE>
+__device__ __forceinline__ Choice route_in_fp64(const RouteArgs& p, int64_t t, double* sc) {
+  const int lane = threadIdx.x & 63, E = p.E, top = p.top;
   double x[NE], c[NE];
   double m = -__builtin_inf();
 #pragma unroll
@@ -61,25 +70,25 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs p) {
     sum += pr[j];
   }
   sum = wave_sum(sum);
+  uint32_t open = 0;                               // experts that may be chosen, a bit per j
 #pragma unroll
   for (int j = 0; j < NE; ++j) {
     const int e = lane + 64 * j;
     if (!p.sigmoid) pr[j] = sum == 0 ? 0.0 : pr[j] / sum;
     c[j] = e < E ? (p.bias ? pr[j] + (double)p.bias[e] : x[j]) : -__builtin_inf();
     if (!(c[j] == c[j])) c[j] = -__builtin_inf();  // a NaN ranks last
+    open |= (e < E ? 1u : 0u) << j;
   }
-  uint32_t open = 0;                               // experts that may be chosen, a bit per j
-#pragma unroll
-  for (int j = 0; j < NE; ++j) open |= (lane + 64 * j < E ? 1u : 0u) << j;
   if (p.groups > 1) {
     const int size = E / p.groups;
+    __builtin_amdgcn_wave_barrier();
 #pragma unroll
-    for (int j = 0; j < NE; ++j) sc[wave][lane + 64 * j] = c[j];
+    for (int j = 0; j < NE; ++j) sc[lane + 64 * j] = c[j];
     __builtin_amdgcn_wave_barrier();
     double g1 = -__builtin_inf(), g2 = g1;
     if (lane < p.groups)
       for (int i = 0; i < size; ++i) {
-        const double v = sc[wave][lane * size + i];
+        const double v = sc[lane * size + i];
         g2 = fmax(g2, fmin(g1, v));
         g1 = fmax(g1, v);
       }
@@ -124,12 +133,99 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs p) {
       w = bp;
     }
   }
-  double total = 1;
-  if (p.renorm) total = wave_sum(lane < top ? w : 0.0);
-  if (lane < top) {
-    p.ids[t * top + lane] = id;
-    p.weights[t * top + lane] = total == 0 ? 0.0f : (float)(p.scale * w / total);
+  return {id, weight_in_fp64(p, t, id, w)};
+}
+
+// Every token that way, a wave each.
+template <int NE>
+__global__ __launch_bounds__(256) void route_wave_kernel(RouteArgs p) {
+  __shared__ double sc[4][64 * NE];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t t = (int64_t)blockIdx.x * 4 + wave;
+  if (t >= p.T) return;
+  Choice c = {-1, 0.0f};
+  if (!p.valid || p.valid[t]) c = route_in_fp64<NE>(p, t, sc[wave]);
+  if (lane < p.top) {
+    p.ids[t * p.top + lane] = c.id;
+    p.weights[t * p.top + lane] = c.w;
   }
+}
+
+// The choice of one token in few registers (lane k returns expert k), for what the kernel with some lanes per token leaves:
+// scores are formed again wherever they are needed.
+__device__ __forceinline__ int route_again(const RouteArgs& p, int64_t t) {
+  const int lane = threadIdx.x & 63, E = p.E, top = p.top;
+  const int64_t row = t * E;
+  double m = -__builtin_inf(), sum = 0;
+  if (!p.sigmoid) {
+#pragma unroll 1
+    for (int e = lane; e < E; e += 64) m = fmax(m, (double)load_logit(p.logits, row + e, p.bf16));
+    m = wave_max(m);
+#pragma unroll 1
+    for (int e = lane; e < E; e += 64) {
+      const double x = load_logit(p.logits, row + e, p.bf16);
+      sum += x == m ? (m == -__builtin_inf() ? 0.0 : 1.0) : exp(x - m);
+    }
+    sum = wave_sum(sum);
+  }
+  auto score = [&](int e) {
+    const double x = load_logit(p.logits, row + e, p.bf16);
+    if (p.sigmoid) return sigmoid64(x);
+    return sum == 0 ? 0.0 : (x == m ? 1.0 : exp(x - m)) / sum;
+  };
+  auto rank_by = [&](int e) {
+    const double c = p.bias ? score(e) + (double)p.bias[e] : (double)load_logit(p.logits, row + e, p.bf16);
+    return c == c ? c : -__builtin_inf();          // a NaN ranks last
+  };
+  uint64_t kept = ~0ull;
+  const int size = E / p.groups;
+  if (p.groups > 1) {
+    double g1 = -__builtin_inf(), g2 = g1;
+    if (lane < p.groups)
+#pragma unroll 1
+      for (int i = 0; i < size; ++i) {
+        const double v = rank_by(lane * size + i);
+        g2 = fmax(g2, fmin(g1, v));
+        g1 = fmax(g1, v);
+      }
+    const double mine = p.group_top == 2 && size > 1 ? g1 + g2 : g1;
+    int rank = 0;
+#pragma unroll 1
+    for (int g = 0; g < p.groups; ++g) {
+      const double other = __shfl(mine, g, 64);
+      rank += other > mine || (other == mine && g < lane);
+    }
+    kept = __ballot(lane < p.groups && rank < p.keep);
+  }
+  int id = 0, last = -1;
+  double bar = __builtin_inf();
+#pragma unroll 1
+  for (int k = 0; k < top; ++k) {                  // the first behind the last one, in the order of c and index
+    double best = -__builtin_inf();
+    int at = INT32_MAX;
+#pragma unroll 1
+    for (int e = lane; e < E; e += 64) {
+      if (!(kept >> (e / size) & 1)) continue;
+      const double c = rank_by(e);
+      if ((c < bar || (c == bar && e > last)) && (c > best || at == INT32_MAX)) {
+        best = c;
+        at = e;
+      }
+    }
+#pragma unroll 1
+    for (int d = 1; d < 64; d <<= 1) {
+      const double ob = __shfl_xor(best, d, 64);
+      const int oa = __shfl_xor(at, d, 64);
+      if (ob > best || (ob == best && oa < at)) {
+        best = ob;
+        at = oa;
+      }
+    }
+    bar = best;
+    last = at;
+    if (lane == k) id = at;
+  }
+  return id;
 }
 
 // dlogits from dweights: a wave per token.
@@ -219,109 +315,741 @@ __global__ __launch_bounds__(256) void route_bwd_kernel(RouteBwdArgs p) {
 }
 
 // ---- sort --------------------------------------------------------------------------------------
-__device__ __forceinline__ int bucket(const SortArgs& p, int64_t i) {
-  const int64_t e = (int64_t)p.ids[i] - p.first;
-  return p.ids[i] >= 0 && e >= 0 && e < p.G ? (int)e : p.G;       // G: pairs that no expert here takes
+// Pairs in chunks: a first launch counts each chunk's pairs per bucket (the experts here, and one for all other pairs),
+// a second one places them, some chunks per block.
+__device__ __forceinline__ int bucket(const SortArgs& p, int32_t id) {
+  const int64_t e = (int64_t)id - p.first;
+  return id >= 0 && e >= 0 && e < p.G ? (int)e : p.G;
 }
+__device__ __forceinline__ int64_t count_pitch(int G) { return (G + 8) / 8 * 8; }      // of the counts, 16-byte rows
 
 __global__ __launch_bounds__(kSortThreads) void sort_count_kernel(SortArgs p) {
   __shared__ int32_t cnt[kMaxExperts + 1];
   for (int e = threadIdx.x; e <= p.G; e += kSortThreads) cnt[e] = 0;
   __syncthreads();
-  const int64_t i0 = (int64_t)blockIdx.x * kSortChunk, i1 = min(i0 + kSortChunk, p.P);
-  for (int64_t i = i0 + threadIdx.x; i < i1; i += kSortThreads) atomicAdd(&cnt[bucket(p, i)], 1);
+  const int64_t i0 = (int64_t)blockIdx.x * p.chunk_pairs, i1 = min(i0 + p.chunk_pairs, p.P);
+  for (int64_t i = i0 + threadIdx.x; i < i1; i += kSortThreads) atomicAdd(&cnt[bucket(p, p.ids[i])], 1);
   __syncthreads();
-  for (int e = threadIdx.x; e <= p.G; e += kSortThreads) p.ws[blockIdx.x * (int64_t)(p.G + 1) + e] = cnt[e];
+  for (int e = threadIdx.x; e <= p.G; e += kSortThreads) p.ws[blockIdx.x * count_pitch(p.G) + e] = (uint16_t)cnt[e];
 }
 
-// A block places its chunk's pairs: the start of each bucket (over all chunks), plus the earlier chunks' pairs of it, plus
-// those of earlier waves of the chunk; a wave takes its pairs 64 at a time in order, and lanes of one bucket find
-// their rank by matching its number bit by bit.
-__global__ __launch_bounds__(kSortThreads) void sort_place_kernel(SortArgs p) {
-  __shared__ int32_t next[kSortWaves][kMaxExperts + 1];
-  __shared__ int32_t base[kMaxExperts + 2];
+// Shared memory of a block of NW waves that places pairs in nb buckets.
+template <int NW>
+struct PlaceLds {
+  int32_t* next;                                   // [NW][nb] each wave's pairs of a bucket, then its next row there
+  int32_t* before;                                 // [nb]
+  int32_t* total;                                  // [nb]
+  int32_t* sums;                                   // [NW]
+  static constexpr int words(int nb) { return (NW + 2) * nb + NW; }
+  __device__ __forceinline__ PlaceLds(int32_t* at, int nb)
+      : next(at), before(next + NW * nb), total(before + nb), sums(total + nb) {}
+};
+
+// Places pairs i0 .. i1 (their ids at ids[i - i0]): a bucket's start (over all pairs), plus the earlier chunks' pairs of it,
+// plus those of earlier waves of the block; a wave takes its pairs 64 at a time in order, and lanes of one bucket
+// find their rank by matching its number bit by bit.  COUNTED: chunk0 of p.chunks chunks are before i0; otherwise these are
+// all pairs.  The chain of memory accesses is the time of this: a block's ids are read once (up to four per lane), together
+// with the counts.
+template <int NW, bool COUNTED>
+__device__ __forceinline__ void place(const SortArgs& p, const int32_t* ids, int64_t i0, int64_t i1, int chunk0, bool first,
+                                      const PlaceLds<NW>& s) {
+  constexpr int NT = 64 * NW, HELD = 4;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, tid = threadIdx.x;
-  const int nb = p.G + 1, chunks = gridDim.x;
-  const int64_t i0 = (int64_t)blockIdx.x * kSortChunk, i1 = min(i0 + kSortChunk, p.P);
-  const int64_t per = (i1 - i0 + kSortThreads - 1) / kSortThreads * 64;         // pairs of a wave
+  const int nb = p.G + 1;
+  const int64_t per = (i1 - i0 + NT - 1) / NT * 64;          // pairs of a wave
   const int64_t w0 = min(i0 + wave * per, i1), w1 = min(w0 + per, i1);
-  for (int e = lane; e < nb; e += 64) next[wave][e] = 0;
-  __syncthreads();
-  for (int64_t i = w0 + lane; i < w1; i += 64) atomicAdd(&next[wave][bucket(p, i)], 1);
-  __syncthreads();
-  // totals over all chunks, then their exclusive sum
-  for (int e = tid; e < nb; e += kSortThreads) {
-    int32_t before = 0, all = 0;
-    if (chunks == 1) {
-      for (int w = 0; w < kSortWaves; ++w) all += next[w][e];
-    } else {
-      for (int k = 0; k < chunks; ++k) {
-        const int32_t n = p.ws[k * (int64_t)nb + e];
-        before += k < (int)blockIdx.x ? n : 0;
-        all += n;
-      }
-    }
-    base[e] = all;
-    // (the waves' starts relative to the bucket's)
-    for (int w = 0; w < kSortWaves; ++w) {
-      const int32_t n = next[w][e];
-      next[w][e] = before;
-      before += n;
-    }
-  }
-  __syncthreads();
-  if (wave == 0) {
-    int32_t carry = 0;
-    for (int e0 = 0; e0 < nb; e0 += 64) {
-      const int e = e0 + lane;
-      const int32_t n = e < nb ? base[e] : 0;
-      int32_t incl = n;
+  const bool held = per <= 64 * HELD;
+  int32_t b[HELD];                                           // buckets, -1 past the end
+  auto load = [&](int64_t at) {
 #pragma unroll
-      for (int d = 1; d < 64; d <<= 1) {
-        const int32_t o = __shfl_up(incl, d, 64);
-        if (lane >= d) incl += o;
+    for (int k = 0; k < HELD; ++k) {
+      const int64_t i = at + 64 * k + lane;
+      b[k] = i < w1 ? bucket(p, ids[i - i0]) : -1;
+    }
+  };
+  load(w0);
+  for (int e = lane; e < nb; e += 64) s.next[wave * nb + e] = 0;
+  if constexpr (COUNTED) {
+    for (int e = tid; e < nb; e += NT) s.before[e] = s.total[e] = 0;
+    __syncthreads();
+    // 8 counts per load, the chunks split over the block, 16 loads of a thread in flight
+    const int pitch = (int)count_pitch(p.G), cols = pitch / 8, parts = max(1, min(NT / cols, (p.chunks + 15) / 16));
+    const int col = tid % cols, part = tid / cols;
+    if (part < parts) {
+      int32_t n0[8] = {0, 0, 0, 0, 0, 0, 0, 0}, n1[8] = {0, 0, 0, 0, 0, 0, 0, 0};       // before, all
+      for (int k0 = part; k0 < p.chunks; k0 += 16 * parts) {
+        uint4 v[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int k = k0 + i * parts;
+          v[i] = k < p.chunks ? *(const uint4*)(p.ws + (int64_t)k * pitch + 8 * col) : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const bool earlier = k0 + i * parts < chunk0;
+          const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            n1[2 * j] += w[j] & 0xFFFF;
+            n1[2 * j + 1] += w[j] >> 16;
+            n0[2 * j] += earlier ? w[j] & 0xFFFF : 0;
+            n0[2 * j + 1] += earlier ? w[j] >> 16 : 0;
+          }
+        }
       }
-      if (e < nb) base[e] = carry + incl - n;
-      carry += __shfl(incl, 63, 64);
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (8 * col + j < nb) {
+          if (n1[j]) atomicAdd(&s.total[8 * col + j], n1[j]);
+          if (n0[j]) atomicAdd(&s.before[8 * col + j], n0[j]);
+        }
+    }
+  }
+  for (int64_t at = w0;;) {
+#pragma unroll
+    for (int k = 0; k < HELD; ++k)
+      if (b[k] >= 0) atomicAdd(&s.next[wave * nb + b[k]], 1);
+    at += 64 * HELD;
+    if (at >= w1) break;
+    load(at);
+  }
+  __syncthreads();
+  // exclusive sum of the buckets' totals: NT buckets at a time
+  int32_t carry = 0;
+  for (int e0 = 0; e0 < nb; e0 += NT) {
+    const int e = e0 + tid;
+    int32_t n = 0;
+    if (e < nb) {
+      if constexpr (COUNTED) n = s.total[e];
+      else
+#pragma unroll
+        for (int w = 0; w < NW; ++w) n += s.next[w * nb + e];
+    }
+    int32_t incl = n;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int32_t o = __shfl_up(incl, d, 64);
+      if (lane >= d) incl += o;
+    }
+    if (e0) __syncthreads();
+    if (lane == 63) s.sums[wave] = incl;
+    __syncthreads();
+    int32_t start = carry + incl - n;
+    for (int w = 0; w < NW; ++w) {
+      if (w < wave) start += s.sums[w];
+      carry += s.sums[w];
+    }
+    if (e < nb) {
+      if (first) p.offs[e] = start;
+      if constexpr (COUNTED) start += s.before[e];
+      int32_t m[NW];
+#pragma unroll
+      for (int w = 0; w < NW; ++w) m[w] = s.next[w * nb + e];
+#pragma unroll
+      for (int w = 0; w < NW; ++w) {
+        s.next[w * nb + e] = start;
+        start += m[w];
+      }
     }
   }
   __syncthreads();
-  if (blockIdx.x == 0)
-    for (int e = tid; e < nb; e += kSortThreads) p.offs[e] = base[e];
-  int bits = 1;
-  while ((1 << bits) < nb) ++bits;
-  for (int64_t i = w0 + lane; i - lane < w1; i += 64) {
-    const bool in = i < w1;
-    const int b = in ? bucket(p, i) : -1;
-    uint64_t same = __ballot(in);
-    for (int k = 0; k < bits; ++k) {
-      const uint64_t set = __ballot(b >> k & 1);
-      same &= b >> k & 1 ? set : ~set;
-    }
-    const int rank = __popcll(same & ((1ull << lane) - 1));
-    if (in) {
-      const int32_t at = base[b] + next[wave][b] + rank;
+  const int bits = 32 - __builtin_clz(nb);         // (bucket numbers are below 2^bits)
+  if (!held) load(w0);
+  for (int64_t at = w0; at < w1;) {
+#pragma unroll
+    for (int k = 0; k < HELD; ++k) {
+      uint64_t same = __ballot(b[k] >= 0);
+      if (!same) break;
+      for (int j = 0; j < bits; ++j) {
+        const uint64_t set = __ballot(b[k] >> j & 1);
+        same &= b[k] >> j & 1 ? set : ~set;
+      }
+      const int rank = __popcll(same & ((1ull << lane) - 1));
+      if (b[k] >= 0) {
+        const int32_t row = s.next[wave * nb + b[k]] + rank;
+        __builtin_amdgcn_wave_barrier();
+        if (rank == 0) s.next[wave * nb + b[k]] += __popcll(same);
+        const int64_t i = at + 64 * k + lane;
+        p.pos[i] = b[k] < p.G ? row : -1;
+        p.row_idx[row] = b[k] < p.G ? (int32_t)((uint32_t)i / (uint32_t)p.top) : -1;
+      }
       __builtin_amdgcn_wave_barrier();
-      if (rank == 0) next[wave][b] += __popcll(same);
-      p.pos[i] = b < p.G ? at : -1;
-      p.row_idx[at] = b < p.G ? (int32_t)(i / p.top) : -1;
     }
-    __builtin_amdgcn_wave_barrier();
+    at += 64 * HELD;
+    if (at < w1) load(at);
+  }
+}
+
+template <bool COUNTED>
+__global__ __launch_bounds__(kSortThreads) void sort_place_kernel(SortArgs p) {
+  __shared__ int32_t lds[PlaceLds<kSortWaves>::words(kMaxExperts + 1)];
+  const PlaceLds<kSortWaves> s(lds, p.G + 1);
+  const int64_t n = COUNTED ? (int64_t)p.block_chunks * p.chunk_pairs : p.P, i0 = blockIdx.x * n;
+  place<kSortWaves, COUNTED>(p, p.ids + i0, i0, min(i0 + n, p.P), (int)blockIdx.x * p.block_chunks, blockIdx.x == 0, s);
+}
+
+// ---- some lanes per token ------------------------------------------------------------------------
+// L lanes hold a token, NE consecutive experts each.  An expert's key is 32 bits: its c, as an integer that orders like it,
+// above the bits of its index (inverted, so that equal c go to the lower one).  A lane sorts its LS largest keys by
+// a network in registers; lanes then merge their lists pairwise (the larger half of two sorted lists is one maximum
+// per entry, fed by a lane permute), until all lanes of the token hold its LS >= top largest in order.
+//   bf16 logits without a bias: the 16 bits of the logit, exact.
+//   fp32 logits without a bias: the difference to the largest in steps of 2^-20 (2^-18 for 1024 experts).  The steps keep the
+//   order, so only logits within one step are in doubt.
+//   with a bias: c from fp32, in steps of 2^-23 of the power of two above A = max(1, max|c|).  A sigmoid is off by at
+//   most 4 * 2^-24 (p (1 - p) times its exponential's 2 |x| + 2, one rounding of the sum, two of the reciprocal), the
+//   addition by A 2^-24: with the roundings of the difference 5 steps for each of two, so 16 are in doubt.  A softmax
+//   score is off by at most 30 * 2^-24 (its own exponential 3, the sum's terms and 22 additions): 40 steps.
+// Two experts in doubt are settled if they are alike (the same logit and bias: equal c, the index decides); a token that
+// has others, next to each other in its list or across its end, is evaluated in fp64 by its wave.
+constexpr int kRouteThreads = 512, kRouteWaves = kRouteThreads / 64;
+
+template <int N>
+__device__ __forceinline__ void order2(uint32_t (&a)[N], int i, int j) {
+  const uint32_t hi = max(a[i], a[j]);
+  a[j] = min(a[i], a[j]);
+  a[i] = hi;
+}
+// Batcher's odd-even merge sort, descending.
+template <int N>
+__device__ __forceinline__ void sort_desc(uint32_t (&a)[N]) {
+#pragma unroll
+  for (int p = 1; p < N; p *= 2)
+#pragma unroll
+    for (int k = p; k >= 1; k /= 2)
+#pragma unroll
+      for (int j = k % p; j + k < N; j += 2 * k)
+#pragma unroll
+        for (int i = 0; i < k; ++i)
+          if (i + j + k < N && (i + j) / (2 * p) == (i + j + k) / (2 * p)) order2(a, i + j, i + j + k);
+}
+template <int N>
+__device__ __forceinline__ void merge_desc(uint32_t (&a)[N]) {          // of a bitonic sequence
+#pragma unroll
+  for (int d = N / 2; d >= 1; d /= 2)
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (!(i & d)) order2(a, i, i + d);
+}
+// Lane exchange within a token, step S: neighbours of 2, 4, 8, 16, 32, 64 lanes.
+template <int S>
+__device__ __forceinline__ uint32_t partner(uint32_t v) {
+  if constexpr (S == 0) return __builtin_amdgcn_update_dpp(0, (int)v, 0xB1, 0xF, 0xF, true);
+  else if constexpr (S == 1) return __builtin_amdgcn_update_dpp(0, (int)v, 0x4E, 0xF, 0xF, true);
+  else if constexpr (S == 2) return __builtin_amdgcn_update_dpp(0, (int)v, 0x141, 0xF, 0xF, true);
+  else if constexpr (S == 3) return __builtin_amdgcn_update_dpp(0, (int)v, 0x140, 0xF, 0xF, true);
+  else return (uint32_t)__shfl_xor((int)v, S == 4 ? 16 : 32, 64);
+}
+template <int L, int S = 0, typename F>
+__device__ __forceinline__ float over(float v, F f) {                   // reduction over a token's lanes
+  if constexpr ((1 << S) < L) return over<L, S + 1>(f(v, __uint_as_float(partner<S>(__float_as_uint(v)))), f);
+  else return v;
+}
+template <int L>
+__device__ __forceinline__ float max_over(float v) { return over<L>(v, [](float a, float b) { return fmaxf(a, b); }); }
+template <int L>
+__device__ __forceinline__ float sum_over(float v) { return over<L>(v, [](float a, float b) { return a + b; }); }
+template <int L, int LS, int S = 0>
+__device__ __forceinline__ void merge_over(uint32_t (&a)[LS]) {
+  if constexpr ((1 << S) < L) {
+    uint32_t b[LS];
+#pragma unroll
+    for (int i = 0; i < LS; ++i) b[i] = partner<S>(a[LS - 1 - i]);
+#pragma unroll
+    for (int i = 0; i < LS; ++i) a[i] = max(a[i], b[i]);
+    merge_desc(a);
+    merge_over<L, LS, S + 1>(a);
+  }
+}
+// Scores in fp32: e^(x - m) of a softmax (1 of the largest, also an infinite one), the sigmoid.
+__device__ __forceinline__ float relative_exp(float x, float m) { return x == m ? 1.0f : __expf(x - m); }
+__device__ __forceinline__ float sigmoid32(float x) { return __builtin_amdgcn_rcpf(1.0f + __expf(-x)); }
+
+constexpr int log2_of(int n) { return n <= 1 ? 0 : 1 + log2_of(n / 2); }
+
+// N consecutive logits of a row from `at` on, those from E on -infinity.
+template <int N>
+__device__ __forceinline__ void load_logits(const void* base, int64_t row, int at, int E, bool bf16, float (&x)[N]) {
+  static_assert(N % 4 == 0, "");
+  if (E % 4 == 0) {                                // (rows of whole 16 bytes in fp32, 8 in bf16)
+#pragma unroll
+    for (int j = 0; j < N; j += 4) {
+      uint4 v = make_uint4(0xFF800000u, 0xFF800000u, 0xFF800000u, 0xFF800000u);
+      if (at + j < E) {
+        if (bf16) {
+          const uint2 w = *(const uint2*)((const uint16_t*)base + row + at + j);
+          v = make_uint4(w.x << 16, w.x & 0xFFFF0000u, w.y << 16, w.y & 0xFFFF0000u);
+        } else {
+          v = *(const uint4*)((const float*)base + row + at + j);
+        }
+      }
+      x[j] = __uint_as_float(v.x);
+      x[j + 1] = __uint_as_float(v.y);
+      x[j + 2] = __uint_as_float(v.z);
+      x[j + 3] = __uint_as_float(v.w);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < N; ++j) x[j] = at + j < E ? load_logit(base, row + at + j, bf16) : -__builtin_inff();
+  }
+}
+
+enum SortMode { kNoSort = 0, kCount = 1, kSortHere = 2 };
+enum RouteKind { kBf16 = 0, kF32 = 1, kBiased = 2 };         // (of the keys; the last takes both types of logits)
+
+// A lane's part of a token: logits, keys, and what the token's lanes have in common.
+template <int L, int NE, int KIND>
+struct Part {
+  static constexpr bool biased = KIND == kBiased, exact = KIND == kBf16;
+  static constexpr int B = log2_of(L * NE), SB = B > 8 ? 32 - B : 24;
+  static constexpr uint32_t kIndex = (1u << B) - 1, kSteps = (1u << SB) - 1;
+  float x[NE];
+  uint32_t key[NE];
+  float mx, total;                                 // the largest logit; a softmax's sum (1 where it is not needed)
+  float far;                                       // biased: largest |c|, at least 1
+  bool odd;                                        // a token that keys say nothing about
+
+  static __device__ __forceinline__ bool is_bf16(const RouteArgs& p) { return biased ? p.bf16 : exact; }
+  static __device__ __forceinline__ uint32_t within(const RouteArgs& p) { return !biased ? 0 : p.sigmoid ? 16 : 40; }
+  // expert of a key (0 .. L * NE - 1)
+  static __device__ __forceinline__ int expert(uint32_t k) { return (int)(kIndex - (k & kIndex)); }
+  __device__ __forceinline__ float c_of(int j, bool sigmoid, const float* bias) const {
+    if constexpr (!biased) return x[j];
+    return (sigmoid ? sigmoid32(x[j]) : relative_exp(x[j], mx) * (1.0f / total)) + bias[j];
+  }
+  __device__ __forceinline__ void load(const RouteArgs& p, int64_t row, int at, const float* bias) {
+    const int E = p.E;
+    const bool sigmoid = p.sigmoid;
+    load_logits<NE>(p.logits, row, at, E, is_bf16(p), x);
+    mx = -__builtin_inff();
+#pragma unroll
+    for (int j = 0; j < NE; ++j) mx = fmaxf(mx, x[j]);       // (drops NaN)
+    mx = max_over<L>(mx);
+    odd = mx == -__builtin_inff();
+    total = 1;
+    if (!sigmoid && (biased || !p.renorm)) {
+      float s = 0;
+#pragma unroll
+      for (int j = 0; j < NE; ++j) s += relative_exp(x[j], mx);        // (0 past E)
+      total = sum_over<L>(s);
+    }
+    float c[NE], m = mx, step = (float)(1u << (SB - 4));
+    if constexpr (biased) {
+      far = 1;
+      m = -__builtin_inff();
+      int n = E - at;                              // (not a constant of the tokens' loop: 16 masks would be kept)
+      asm("" : "+v"(n));
+      float worst = 0;
+#pragma unroll
+      for (int j = 0; j < NE; ++j) {
+        c[j] = c_of(j, sigmoid, bias);
+        const float a = j < n ? fabsf(c[j]) : 0.0f;
+        worst = a < 1e30f ? fmaxf(worst, a) : __builtin_inff();
+        c[j] = j < n ? c[j] : -__builtin_inff();
+        m = fmaxf(m, c[j]);
+      }
+      odd |= !(worst < 1e30f);
+      far = fmaxf(far, worst);
+      far = max_over<L>(far);
+      m = max_over<L>(m);
+      // steps per unit: 2^(SB - 1) over the power of two above far
+      step = __uint_as_float((uint32_t)(SB - 1 + 254 - ((__float_as_uint(far) >> 23) + 1)) << 23);
+    } else {
+#pragma unroll
+      for (int j = 0; j < NE; ++j) c[j] = x[j];
+    }
+#pragma unroll
+    for (int j = 0; j < NE; ++j) {
+      const uint32_t low = kIndex - (uint32_t)(at + j);
+      if constexpr (exact) {
+        const float v = c[j] == c[j] ? c[j] + 0.0f : -__builtin_inff();        // (-0 like 0, a NaN last)
+        const uint32_t u = __float_as_uint(v) >> 16;
+        key[j] = ((u ^ ((u & 0x8000u) ? 0xFFFFu : 0x8000u)) << 16) | low;
+      } else {
+        const float d = c[j] == m ? (float)kSteps : fmaxf(fmaf(c[j] - m, step, (float)kSteps), 0.0f);    // (a NaN: 0)
+        key[j] = (uint32_t)d << B | low;
+      }
+      // (past E: -infinity, and a higher index than any expert's)
+    }
+  }
+  // The token's N largest keys in order, in every lane.
+  template <int N>
+  __device__ __forceinline__ void largest(uint32_t (&best)[N], bool kept) const {
+#pragma unroll
+    for (int i = 0; i < N; ++i) best[i] = i < NE ? key[i < NE ? i : 0] : 0;
+    sort_desc(best);
+#pragma unroll
+    for (int b = N; b < NE; b += N) {
+      uint32_t more[N];
+#pragma unroll
+      for (int i = 0; i < N; ++i) more[i] = b + i < NE ? key[b + i < NE ? b + i : 0] : 0;
+      sort_desc(more);
+#pragma unroll
+      for (int i = 0; i < N; ++i) best[i] = max(best[i], more[N - 1 - i]);
+      merge_desc(best);
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) best[i] = kept ? best[i] : 0;
+    merge_over<L, N>(best);
+  }
+};
+// A group's score from its lanes' two largest: `lanes` lanes, this one's group being g.
+template <typename V>
+__device__ __forceinline__ V group_score(V g1, V g2, int lane, int sub, int g, int lanes, bool two) {
+  const V a1 = g1, a2 = g2;
+  for (int i = 1; i < lanes; ++i) {
+    const int from = lane - sub + g * lanes + (sub - g * lanes + i) % lanes;
+    const V o1 = __shfl(a1, from, 64), o2 = __shfl(a2, from, 64);
+    g2 = fmax(fmin(g1, o1), fmax(g2, o2));
+    g1 = fmax(g1, o1);
+  }
+  return two ? g1 + g2 : g1;
+}
+// Entry sub of a list, and entry n - 1.
+template <int N>
+__device__ __forceinline__ void pick(const uint32_t (&list)[N], int sub, int n, uint32_t& mine, uint32_t& last) {
+  mine = last = list[0];
+#pragma unroll
+  for (int i = 1; i < N; ++i) {
+    if (sub == i) mine = list[i];
+    if (i < n) last = list[i];
+  }
+}
+
+// Choices of the tokens with rows at `row` (one per L lanes) as fp64 orders them: the groups in fp64, then the 16 largest keys
+// in the order of their c in fp64, which is right if what is behind them is out of the doubt's reach; else the token is left to
+// the whole wave.  Lane k of a token returns choice k.
+template <int L, int NE, int KIND>
+__device__ __forceinline__ int second_look(const RouteArgs& p, int64_t t, bool real) {
+  typedef Part<L, NE, KIND> P;
+  constexpr int W = 16;
+  const int lane = threadIdx.x & 63, sub = lane & (L - 1), lane0 = lane - sub, E = p.E, at = sub * NE, end = min(at + NE, E);
+  const int64_t row = t * E;
+  const bool bf16 = P::is_bf16(p), sigmoid = p.sigmoid;
+  uint32_t entry, bar, behind;
+  double mx;
+  bool odd;
+  {
+    float bias[P::biased ? NE : 1];
+    if constexpr (P::biased) {
+#pragma unroll
+      for (int j = 0; j < NE; ++j) bias[j] = at + j < E ? p.bias[at + j] : 0.0f;
+    }
+    P part;
+    part.load(p, row, at, bias);
+    mx = part.mx;
+    odd = part.odd;
+    double sum = 1;
+    if (P::biased && !sigmoid) {
+      sum = 0;
+#pragma unroll 1
+      for (int e = at; e < end; ++e) {
+        const double v = load_logit(p.logits, row + e, bf16);
+        sum += v == mx ? 1.0 : exp(v - mx);
+      }
+#pragma unroll
+      for (int d = 1; d < L; d <<= 1) sum += __shfl_xor(sum, d, 64);
+    }
+    auto in_fp64 = [&](int e) {
+      double v = load_logit(p.logits, row + e, bf16);
+      if constexpr (P::biased)
+        v = (sigmoid ? sigmoid64(v) : (v == mx ? 1.0 : exp(v - mx)) / sum) + (double)p.bias[e];
+      return v == v ? v : -__builtin_inf();
+    };
+    bool kept = true;
+    if (p.groups > 1) {
+      const int size = E / p.groups, lanes = size / NE, g = sub / lanes;
+      double g1 = -__builtin_inf(), g2 = g1;
+#pragma unroll 1
+      for (int e = at; e < end; ++e) {
+        const double v = in_fp64(e);
+        g2 = fmax(g2, fmin(g1, v));
+        g1 = fmax(g1, v);
+      }
+      const double score = group_score(g1, g2, lane, sub, g, lanes, p.group_top == 2 && size > 1);
+      int rank = 0;
+      for (int o = 0; o < p.groups; ++o) {
+        const double other = __shfl(score, lane0 + o * lanes, 64);
+        rank += other > score || (other == score && o < g);
+      }
+      kept = rank < p.keep;
+    }
+    uint32_t list[W];
+    part.template largest<W>(list, kept);
+    pick(list, sub, p.top, entry, bar);
+    behind = list[W - 1];
+    const bool there = sub < W && entry != 0 && P::expert(entry) < E;
+    const int ide = there ? P::expert(entry) : 0;
+    const double ce = in_fp64(ide);
+    int rank = 0;
+#pragma unroll 1
+    for (int i = 0; i < W; ++i) {
+      const double o = __shfl(ce, lane0 + i, 64);
+      const int io = __shfl(ide, lane0 + i, 64), to = __shfl((int)there, lane0 + i, 64);
+      rank += to && (o > ce || (o == ce && io < ide));
+    }
+    // (entries that are not there are the last, so that every lane has a target of its own)
+    entry = (uint32_t)__builtin_amdgcn_ds_permute(4 * (lane0 + (there ? rank : sub)), ide);
+  }
+  int id = (int)entry;
+  const bool settled = !odd && bar != 0 && (P::exact || behind == 0 || (bar >> P::B) > (behind >> P::B) + P::within(p));
+  const uint64_t left = __ballot(real && !settled);
+#pragma unroll 1
+  for (int k = 0; k < 64 / L; ++k) {
+    if (!(left >> (k * L) & (L == 64 ? ~0ull : (1ull << (L & 63)) - 1))) continue;
+    const int64_t tk = __shfl((int)t, k * L, 64);            // (T < 2^31)
+    const int ci = __shfl(route_again(p, tk), sub, 64);      // (lane i of the wave has choice i)
+    if (lane / L == k) id = ci;
+  }
+  return id;
+}
+
+template <int L, int NE, int LS, int KIND>
+__global__ __launch_bounds__(kRouteThreads) __attribute__((amdgpu_waves_per_eu(4))) void route_kernel(RouteArgs p, SortArgs q, int mode, int iters) {
+  typedef Part<L, NE, KIND> P;
+  constexpr int TPW = 64 / L;
+  constexpr int kTokens = kRouteWaves * TPW;       // of the block at a time
+  constexpr int kBatch = 64 / TPW;                 // rounds whose tokens in doubt have a bit each
+  extern __shared__ int32_t cnt[];                 // the counts, or the ids and what places them
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, sub = lane & (L - 1);
+  const int E = p.E, top = p.top, at = sub * NE;
+  const bool bf16 = P::is_bf16(p), sigmoid = p.sigmoid, chosen = sub < top;
+  if (mode == kCount) {
+    for (int e = threadIdx.x; e <= q.G; e += kRouteThreads) cnt[e] = 0;
+    __syncthreads();
+  }
+  float bias[P::biased ? NE : 1];
+  if constexpr (P::biased) {
+#pragma unroll
+    for (int j = 0; j < NE; ++j) bias[j] = at + j < E ? p.bias[at + j] : 0.0f;
+  }
+  const int64_t first = (int64_t)blockIdx.x * iters * kTokens + wave * TPW + lane / L;       // token of round 0
+  // a token's choices, with their logits and its softmax
+  auto write = [&](int64_t t, bool live, int id, float xk, float mx, float total) {
+    float w;
+    if (p.renorm) {
+      // relative to the largest chosen logit, so that no sum vanishes
+      const float xm = max_over<L>(chosen ? xk : -__builtin_inff());
+      float v = 0;
+      if (chosen && xm == -__builtin_inff()) {
+        v = xk == xk ? 0.0f : xk;
+      } else if (chosen) {
+        if (sigmoid) v = __expf(fminf(xk, 0.0f) - fminf(xm, 0.0f)) * __builtin_amdgcn_rcpf(1.0f + __expf(-fabsf(xk)));
+        else v = relative_exp(xk, xm);
+      }
+      const float s = sum_over<L>(v);
+      w = s == 0 || (sigmoid && xm < -745.2f && s == s) ? 0.0f : v / s;
+    } else {
+      w = sigmoid ? sigmoid32(xk) : mx == -__builtin_inff() && xk == xk ? 0.0f : relative_exp(xk, mx) / total;
+    }
+    if (chosen && t < p.T) {
+      id = live ? id : -1;
+      p.ids[t * top + sub] = id;
+      p.weights[t * top + sub] = live ? w * (float)p.scale : 0.0f;
+      if (mode == kCount) atomicAdd(&cnt[bucket(q, id)], 1);
+      if (mode == kSortHere) cnt[t * top + sub] = id;
+    }
+  };
+  for (int it0 = 0; it0 < iters; it0 += kBatch) {
+    uint64_t later = 0;                            // tokens in doubt, TPW bits per round
+    for (int it = it0; it < min(it0 + kBatch, iters); ++it) {
+      const int64_t t = first + (int64_t)it * kTokens, tr = min(t, p.T - 1);
+      if (t - lane / L >= p.T) break;
+      const bool live = t < p.T && (!p.valid || p.valid[tr]);
+      P part;
+      part.load(p, tr * E, at, bias);
+      bool doubt = part.odd, kept = true;
+      if (p.groups > 1) {
+        // a group is the experts of `lanes` lanes
+        const int size = E / p.groups, lanes = size / NE, g = sub / lanes;
+        float g1 = -__builtin_inff(), g2 = g1;
+#pragma unroll
+        for (int j = 0; j < NE; ++j) {
+          const float c = part.c_of(j, sigmoid, bias), v = c == c ? c : -__builtin_inff();
+          g2 = fmaxf(g2, fminf(g1, v));
+          g1 = fmaxf(g1, v);
+        }
+        const bool two = p.group_top == 2 && size > 1;
+        const float score = group_score(g1, g2, lane, sub, g, lanes, two);
+        // biased values and sums are rounded (without a bias only sums are): what is nearer than that is in doubt
+        const float tol = P::biased ? 128 * 0x1p-24f * part.far : two ? 8 * 0x1p-24f * fmaxf(fabsf(g1), fabsf(g2)) : -1.0f;
+        int rank = 0;
+        for (int o = 0; o < p.groups; ++o) {
+          const float other = __shfl(score, lane - sub + o * lanes, 64);
+          rank += other > score || (other == score && o < g);
+          doubt |= tol >= 0 && at < E && o != g && !(fabsf(other - score) > tol && fabsf(other - score) < __builtin_inff());
+        }
+        kept = rank < p.keep;
+      }
+      uint32_t best[LS], mine, last;
+      part.template largest<LS>(best, kept);
+      pick(best, sub, top, mine, last);            // lane k of the token takes choice k
+      const int id = P::expert(mine), idk = chosen && id < E ? id : 0;
+      const float xk = load_logit(p.logits, tr * E + idk, bf16);
+      if constexpr (!P::exact) {
+        constexpr int B = P::B;
+        const int idl = min(P::expert(last), E - 1);
+        const float bk = P::biased ? p.bias[idk] : 0.0f;
+        const float xl = load_logit(p.logits, tr * E + idl, bf16), bl = P::biased ? p.bias[idl] : 0.0f;
+        const uint32_t q_last = last >> B, q_mine = mine >> B, within = P::within(p);
+        // neighbours in the list
+        const uint32_t q_prev = (uint32_t)__shfl_up((int)q_mine, 1, 64);
+        const float x_prev = __shfl_up(xk, 1, 64), b_prev = __shfl_up(bk, 1, 64);
+        doubt |= chosen && sub > 0 && q_prev - q_mine <= within && !(x_prev == xk && b_prev == bk);
+        // the end of the list: as many experts as are chosen, apart from those like the last
+        const uint32_t bar = q_last > within ? q_last - within : 0;
+        int extra = chosen && !(xk == xl && bk == bl) ? -1 : 0;
+#pragma unroll
+        for (int j = 0; j < NE; ++j)
+          extra += kept && (part.key[j] >> B) >= bar &&
+                           !(part.x[j] == xl && (!P::biased || bias[P::biased ? j : 0] == bl))
+                       ? 1
+                       : 0;
+        doubt |= sum_over<L>((float)extra) != 0.0f || q_last == 0;     // (as all of -infinity are)
+      } else {
+        doubt |= last == 0;
+      }
+      const uint64_t need = __ballot(doubt && live);
+      uint32_t bits = 0;                           // the wave's tokens in doubt
+#pragma unroll
+      for (int k = 0; k < TPW; ++k)
+        bits |= (need >> (k * L) & (L == 64 ? ~0ull : (1ull << (L & 63)) - 1)) ? 1u << k : 0u;
+      later |= (uint64_t)bits << (TPW * (it - it0));
+      write(bits >> (lane / L) & 1 ? p.T : t, live, id, xk, part.mx, part.total);
+    }
+    // tokens in doubt, as many at a time as the wave holds
+    while (later) {
+      int64_t t = 0;
+      bool real = false;
+#pragma unroll
+      for (int k = 0; k < TPW; ++k) {
+        if (later) {
+          const int bit = __builtin_ctzll(later);
+          if (lane / L == k) {
+            t = first - lane / L + (int64_t)(it0 + bit / TPW) * kTokens + bit % TPW;
+            real = true;
+          }
+          later &= later - 1;
+        }
+      }
+      const int id = second_look<L, NE, KIND>(p, t, real);
+      const float xk = load_logit(p.logits, t * E + (chosen ? id : 0), bf16);
+      float mx = -__builtin_inff(), total = 1;
+      if (!sigmoid && !p.renorm) {
+        float x[NE], s = 0;
+        load_logits<NE>(p.logits, t * E, at, E, bf16, x);
+#pragma unroll
+        for (int j = 0; j < NE; ++j) mx = fmaxf(mx, x[j]);
+        mx = max_over<L>(mx);
+#pragma unroll
+        for (int j = 0; j < NE; ++j) s += relative_exp(x[j], mx);
+        total = sum_over<L>(s);
+      }
+      write(real ? t : p.T, true, id, xk, mx, total);
+    }
+  }
+  if (mode == kCount) {
+    __syncthreads();
+    for (int e = threadIdx.x; e <= q.G; e += kRouteThreads) q.ws[blockIdx.x * count_pitch(q.G) + e] = (uint16_t)cnt[e];
+  } else if (mode == kSortHere) {
+    __syncthreads();
+    place<kRouteWaves, false>(q, cnt, 0, q.P, 0, true, PlaceLds<kRouteWaves>(cnt + q.P, q.G + 1));
   }
 }
 
 }  // namespace
 
-hipError_t launch_route_fwd(const RouteArgs& a, hipStream_t st) {
-  const int ne = (a.E + 63) / 64;
+namespace {
+
+// The launch of a lanes-per-token kernel; -1 lanes: the call is outside their range (more choices than a list holds, or groups
+// that are not whole lanes), and every token takes a wave.
+struct RouteShape {
+  int lanes, experts;                              // lanes of a token, experts of a lane
+};
+RouteShape route_shape(const RouteArgs& a) {
+  RouteShape s = {a.E <= 256 ? 16 : a.E <= 512 ? 32 : 64, a.E <= 64 ? 4 : a.E <= 128 ? 8 : 16};
+  if (a.top > 16 || (a.groups > 1 && a.E / a.groups % s.experts)) s.lanes = -1;
+  return s;
+}
+
+template <int L, int NE>
+void go_route(const RouteArgs& a, const SortArgs& q, int mode, int iters, unsigned blocks, hipStream_t st) {
+  size_t lds = 0;
+  if (mode == kCount) lds = 4 * (q.G + 1);
+  if (mode == kSortHere) lds = 4 * (q.P + PlaceLds<kRouteWaves>::words(q.G + 1));
   auto go = [&](auto kernel) {
-    hipLaunchKernelGGL(kernel, dim3((unsigned)((a.T + 3) / 4)), dim3(256), 0, st, a);
+    hipLaunchKernelGGL(kernel, dim3(blocks), dim3(kRouteThreads), lds, st, a, q, mode, iters);
   };
-  if (ne <= 1) go(route_kernel<1>);
-  else if (ne <= 2) go(route_kernel<2>);
-  else if (ne <= 4) go(route_kernel<4>);
-  else if (ne <= 8) go(route_kernel<8>);
-  else go(route_kernel<16>);
+  if (a.bias) a.top <= 8 ? go(route_kernel<L, NE, 8, kBiased>) : go(route_kernel<L, NE, 16, kBiased>);
+  else if (a.bf16) a.top <= 8 ? go(route_kernel<L, NE, 8, kBf16>) : go(route_kernel<L, NE, 16, kBf16>);
+  else a.top <= 8 ? go(route_kernel<L, NE, 8, kF32>) : go(route_kernel<L, NE, 16, kF32>);
+}
+
+void launch_place(SortArgs q, hipStream_t st) {
+  // a block per 4096 pairs or so
+  q.block_chunks = q.chunks ? std::max(1, kPlacePairs / q.chunk_pairs) : 0;
+  const unsigned blocks = q.chunks ? (unsigned)((q.chunks + q.block_chunks - 1) / q.block_chunks) : 1;
+  hipLaunchKernelGGL(q.chunks ? sort_place_kernel<true> : sort_place_kernel<false>, dim3(blocks), dim3(kSortThreads), 0, st, q);
+}
+
+}  // namespace
+
+// (the counts of either launch_sort or launch_route fit)
+int64_t sort_workspace(int64_t P, int32_t G) {
+  if (P <= kSortChunk) return 0;
+  return std::max<int64_t>(kCountBlocks, P / 32768 + 1) * ((G + 8) / 8 * 8) * 2;
+}
+
+hipError_t launch_sort(SortArgs q, hipStream_t st) {
+  q.chunks = 0;
+  if (q.P > kSortChunk) {
+    q.chunk_pairs = (int)std::min<int64_t>(std::max<int64_t>(1024, (q.P + kCountBlocks * 64 - 1) / (kCountBlocks * 64) * 64), 65472);
+    q.chunks = (int)((q.P + q.chunk_pairs - 1) / q.chunk_pairs);
+    hipLaunchKernelGGL(sort_count_kernel, dim3(q.chunks), dim3(kSortThreads), 0, st, q);
+  }
+  launch_place(q, st);
+  return hipGetLastError();
+}
+
+hipError_t launch_route(const RouteArgs& a, const SortArgs* sort, hipStream_t st) {
+  const RouteShape s = route_shape(a);
+  if (s.lanes < 0) {
+    const int ne = (a.E + 63) / 64;
+    auto go = [&](auto kernel) {
+      if (a.T) hipLaunchKernelGGL(kernel, dim3((unsigned)((a.T + 3) / 4)), dim3(256), 0, st, a);
+    };
+    if (ne <= 1) go(route_wave_kernel<1>);
+    else if (ne <= 2) go(route_wave_kernel<2>);
+    else if (ne <= 4) go(route_wave_kernel<4>);
+    else if (ne <= 8) go(route_wave_kernel<8>);
+    else go(route_wave_kernel<16>);
+    return sort ? launch_sort(*sort, st) : hipGetLastError();
+  }
+  SortArgs q = {};
+  if (sort) q = *sort;
+  const int tokens = kRouteWaves * 64 / s.lanes;   // of a block at a time
+  const int64_t all = (a.T + tokens - 1) / tokens;
+  int mode = kNoSort;
+  int64_t iters = 1;
+  if (sort && all <= 2) {
+    mode = kSortHere;
+    iters = 2;
+  } else if (sort && q.P > kSortChunk) {
+    mode = kCount;
+    iters = std::min<int64_t>((all + kCountBlocks - 1) / kCountBlocks, 65535 / (tokens * a.top));
+  }
+  const int64_t blocks = std::max<int64_t>(1, (all + iters - 1) / iters);
+  if (mode == kCount) {
+    q.chunk_pairs = (int)(tokens * iters * a.top);
+    q.chunks = (int)blocks;
+  }
+  auto go = [&](auto f) { f(a, q, mode, (int)iters, (unsigned)blocks, st); };
+  if (s.experts == 4) go(go_route<16, 4>);
+  else if (s.experts == 8) go(go_route<16, 8>);
+  else if (s.lanes == 16) go(go_route<16, 16>);
+  else if (s.lanes == 32) go(go_route<32, 16>);
+  else go(go_route<64, 16>);
+  if (sort && mode != kSortHere) launch_place(q, st);
   return hipGetLastError();
 }
 
@@ -335,15 +1063,6 @@ hipError_t launch_route_bwd(const RouteBwdArgs& a, hipStream_t st) {
   else if (ne <= 4) go(route_bwd_kernel<4>);
   else if (ne <= 8) go(route_bwd_kernel<8>);
   else go(route_bwd_kernel<16>);
-  return hipGetLastError();
-}
-
-int64_t sort_chunks(int64_t P) { return std::max<int64_t>(1, (P + kSortChunk - 1) / kSortChunk); }
-
-hipError_t launch_sort(const SortArgs& a, hipStream_t st) {
-  const unsigned chunks = (unsigned)sort_chunks(a.P);
-  if (chunks > 1) hipLaunchKernelGGL(sort_count_kernel, dim3(chunks), dim3(kSortThreads), 0, st, a);
-  hipLaunchKernelGGL(sort_place_kernel, dim3(chunks), dim3(kSortThreads), 0, st, a);
   return hipGetLastError();
 }
 
