@@ -228,92 +228,6 @@ __device__ __forceinline__ int route_again(const RouteArgs& p, int64_t t) {
   return id;
 }
 
-// dlogits from dweights: a wave per token.
-//   softmax, renormalised (w' = w / scale): dl_k = scale w'_k (dw_k - D),  D = sum_k w'_k dw_k, 0 elsewhere
-//   sigmoid, renormalised: the same times (1 - p_k);   sigmoid: dl_k = scale dw_k p_k (1 - p_k)
-//   softmax: dl_e = p_e (scale dw_e [e chosen] - scale sum_k p_k dw_k)
-template <int NE>
-__global__ __launch_bounds__(256) void route_bwd_kernel(RouteBwdArgs p) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t t = (int64_t)blockIdx.x * 4 + wave;
-  if (t >= p.T) return;
-  const int E = p.E, top = p.top;
-  int id = -1;
-  float dw = 0, xk = -__builtin_inff();
-  if (lane < top) {
-    id = p.ids[t * top + lane];
-    if (id < 0 || id >= E) id = -1;
-    if (id >= 0) {
-      dw = p.dweights[t * top + lane];
-      xk = load_logit(p.logits, t * E + id, p.bf16);
-    }
-  }
-  float m = xk;
-  float x[NE], sum = 0;
-  const bool all = !p.sigmoid && !p.renorm;
-  if (all) {
-#pragma unroll
-    for (int j = 0; j < NE; ++j) {
-      const int e = lane + 64 * j;
-      x[j] = e < E ? load_logit(p.logits, t * E + e, p.bf16) : -__builtin_inff();
-      m = fmaxf(m, x[j]);
-    }
-  }
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) m = fmaxf(m, __shfl_xor(m, d, 64));
-  // relative to the largest, as in the forward pass
-  auto rel = [&](float v) { return v == m ? (m == -__builtin_inff() ? 0.0f : 1.0f) : expf(v - m); };
-  float v = 0;                                     // of lane k: its choice's gradient
-  float shared = 0;
-  if (all) {
-#pragma unroll
-    for (int j = 0; j < NE; ++j) {
-      x[j] = lane + 64 * j < E ? rel(x[j]) : 0.0f;
-      sum += x[j];
-    }
-    sum = wave_sum(sum);
-    const float inv = sum == 0 ? 0.0f : 1.0f / sum;
-#pragma unroll
-    for (int j = 0; j < NE; ++j) x[j] *= inv;
-    const float pk = id >= 0 ? rel(xk) * inv : 0.0f;
-    v = p.scale * dw * pk;
-    shared = wave_sum(v);
-  } else {
-    // sigmoid(x) = e^min(x, 0) / (1 + e^-|x|); relative to the largest, so that none of a sum vanishes
-    float pk = 0, q = 0;
-    if (id >= 0) {
-      const float en = expf(-fabsf(xk));
-      q = (xk >= 0 ? en : 1.0f) / (1.0f + en);     // 1 - p
-      pk = p.sigmoid ? (p.renorm ? expf(fminf(xk, 0.0f) - fminf(m, 0.0f)) / (1.0f + en) : (xk >= 0 ? 1.0f : en) / (1.0f + en))
-                     : rel(xk);
-      if (p.sigmoid && p.renorm && m < -745.2f) pk = 0;          // (a sum of 0 in fp64: weights of 0)
-    }
-    if (!p.sigmoid) q = 1.0f;
-    if (p.renorm) {
-      const float s = wave_sum(pk);
-      pk = s == 0 ? 0.0f : pk / s;
-      const float d = wave_sum(pk * dw);
-      v = p.scale * pk * (dw - d) * q;
-    } else {
-      v = p.scale * dw * pk * q;
-    }
-  }
-#pragma unroll
-  for (int j = 0; j < NE; ++j) {
-    const int e = lane + 64 * j;
-    float o = all ? -x[j] * shared : 0.0f;
-    for (int k = 0; k < top; ++k) {
-      const int ik = __shfl(id, k, 64);
-      const float vk = __shfl(v, k, 64);
-      if (ik == e) o += vk;
-    }
-    if (e < E) {
-      if (p.bf16) ((__bf16*)p.dlogits)[t * E + e] = (__bf16)o;
-      else ((float*)p.dlogits)[t * E + e] = o;
-    }
-  }
-}
-
 // ---- sort --------------------------------------------------------------------------------------
 // Pairs in chunks: a first launch counts each chunk's pairs per bucket (the experts here, and one for all other pairs),
 // a second one places them, some chunks per block.
@@ -337,12 +251,12 @@ __global__ __launch_bounds__(kSortThreads) void sort_count_kernel(SortArgs p) {
 template <int NW>
 struct PlaceLds {
   int32_t* next;                                   // [NW][nb] each wave's pairs of a bucket, then its next row there
-  int32_t* before;                                 // [nb]
-  int32_t* total;                                  // [nb]
+  int32_t* before;                                 // [8][ceil(nb / 8)], bucket e at (e % 8, e / 8)
+  int32_t* total;                                  // the same
   int32_t* sums;                                   // [NW]
-  static constexpr int words(int nb) { return (NW + 2) * nb + NW; }
+  static constexpr int words(int nb) { return NW * nb + 2 * ((nb + 7) / 8 * 8) + NW; }
   __device__ __forceinline__ PlaceLds(int32_t* at, int nb)
-      : next(at), before(next + NW * nb), total(before + nb), sums(total + nb) {}
+      : next(at), before(next + NW * nb), total(before + (nb + 7) / 8 * 8), sums(total + (nb + 7) / 8 * 8) {}
 };
 
 // Places pairs i0 .. i1 (their ids at ids[i - i0]): a bucket's start (over all pairs), plus the earlier chunks' pairs of it,
@@ -370,22 +284,22 @@ __device__ __forceinline__ void place(const SortArgs& p, const int32_t* ids, int
   load(w0);
   for (int e = lane; e < nb; e += 64) s.next[wave * nb + e] = 0;
   if constexpr (COUNTED) {
-    for (int e = tid; e < nb; e += NT) s.before[e] = s.total[e] = 0;
+    for (int e = tid; e < (nb + 7) / 8 * 8; e += NT) s.before[e] = s.total[e] = 0;
     __syncthreads();
-    // 8 counts per load, the chunks split over the block, 16 loads of a thread in flight
-    const int pitch = (int)count_pitch(p.G), cols = pitch / 8, parts = max(1, min(NT / cols, (p.chunks + 15) / 16));
+    // 8 counts per load, the chunks split over the block, 10 loads of a thread in flight
+    const int pitch = (int)count_pitch(p.G), cols = pitch / 8, parts = max(1, min(NT / cols, (p.chunks + 9) / 10));
     const int col = tid % cols, part = tid / cols;
     if (part < parts) {
       int32_t n0[8] = {0, 0, 0, 0, 0, 0, 0, 0}, n1[8] = {0, 0, 0, 0, 0, 0, 0, 0};       // before, all
-      for (int k0 = part; k0 < p.chunks; k0 += 16 * parts) {
-        uint4 v[16];
+      for (int k0 = part; k0 < p.chunks; k0 += 10 * parts) {
+        uint4 v[10];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
+        for (int i = 0; i < 10; ++i) {
           const int k = k0 + i * parts;
           v[i] = k < p.chunks ? *(const uint4*)(p.ws + (int64_t)k * pitch + 8 * col) : make_uint4(0, 0, 0, 0);
         }
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
+        for (int i = 0; i < 10; ++i) {
           const bool earlier = k0 + i * parts < chunk0;
           const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
 #pragma unroll
@@ -398,11 +312,10 @@ __device__ __forceinline__ void place(const SortArgs& p, const int32_t* ids, int
         }
       }
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (8 * col + j < nb) {
-          if (n1[j]) atomicAdd(&s.total[8 * col + j], n1[j]);
-          if (n0[j]) atomicAdd(&s.before[8 * col + j], n0[j]);
-        }
+      for (int j = 0; j < 8; ++j) {
+        if (n1[j]) atomicAdd(&s.total[j * cols + col], n1[j]);
+        if (n0[j]) atomicAdd(&s.before[j * cols + col], n0[j]);
+      }
     }
   }
   for (int64_t at = w0;;) {
@@ -420,7 +333,7 @@ __device__ __forceinline__ void place(const SortArgs& p, const int32_t* ids, int
     const int e = e0 + tid;
     int32_t n = 0;
     if (e < nb) {
-      if constexpr (COUNTED) n = s.total[e];
+      if constexpr (COUNTED) n = s.total[(e & 7) * ((nb + 7) / 8) + (e >> 3)];
       else
 #pragma unroll
         for (int w = 0; w < NW; ++w) n += s.next[w * nb + e];
@@ -441,7 +354,7 @@ __device__ __forceinline__ void place(const SortArgs& p, const int32_t* ids, int
     }
     if (e < nb) {
       if (first) p.offs[e] = start;
-      if constexpr (COUNTED) start += s.before[e];
+      if constexpr (COUNTED) start += s.before[(e & 7) * ((nb + 7) / 8) + (e >> 3)];
       int32_t m[NW];
 #pragma unroll
       for (int w = 0; w < NW; ++w) m[w] = s.next[w * nb + e];
@@ -453,22 +366,25 @@ __device__ __forceinline__ void place(const SortArgs& p, const int32_t* ids, int
     }
   }
   __syncthreads();
-  const int bits = 32 - __builtin_clz(nb);         // (bucket numbers are below 2^bits)
   if (!held) load(w0);
   for (int64_t at = w0; at < w1;) {
+    uint64_t same[HELD];                           // lanes of the same bucket, of each of the pairs held
+#pragma unroll
+    for (int k = 0; k < HELD; ++k) same[k] = __ballot(b[k] >= 0);
+    for (int j = 0; nb >> j; ++j)                  // (bucket numbers are at most nb - 1)
+#pragma unroll
+      for (int k = 0; k < HELD; ++k) {
+        const bool bit = b[k] >> j & 1;
+        const uint64_t set = __ballot(bit);
+        same[k] &= bit ? set : ~set;
+      }
 #pragma unroll
     for (int k = 0; k < HELD; ++k) {
-      uint64_t same = __ballot(b[k] >= 0);
-      if (!same) break;
-      for (int j = 0; j < bits; ++j) {
-        const uint64_t set = __ballot(b[k] >> j & 1);
-        same &= b[k] >> j & 1 ? set : ~set;
-      }
-      const int rank = __popcll(same & ((1ull << lane) - 1));
+      const int rank = __popcll(same[k] & ((1ull << lane) - 1));
       if (b[k] >= 0) {
         const int32_t row = s.next[wave * nb + b[k]] + rank;
         __builtin_amdgcn_wave_barrier();
-        if (rank == 0) s.next[wave * nb + b[k]] += __popcll(same);
+        if (rank == 0) s.next[wave * nb + b[k]] += __popcll(same[k]);
         const int64_t i = at + 64 * k + lane;
         p.pos[i] = b[k] < p.G ? row : -1;
         p.row_idx[row] = b[k] < p.G ? (int32_t)((uint32_t)i / (uint32_t)p.top) : -1;
@@ -957,6 +873,109 @@ __global__ __launch_bounds__(kRouteThreads) __attribute__((amdgpu_waves_per_eu(4
   }
 }
 
+// dlogits from dweights, L lanes per token and NE experts per lane (4 consecutive ones of every 4 L); lane k < top has choice k.
+//   softmax, renormalised (w' = w / scale): dl_k = scale w'_k (dw_k - D),  D = sum_k w'_k dw_k, 0 elsewhere
+//   sigmoid, renormalised: the same times (1 - p_k);   sigmoid: dl_k = scale dw_k p_k (1 - p_k)
+//   softmax: dl_e = p_e (scale dw_e [e chosen] - scale sum_k p_k dw_k)
+// Bound: HBM; only the last reads more than the chosen logits.
+template <int L, int NE>
+__global__ __launch_bounds__(256) void route_bwd_kernel(RouteBwdArgs p) {
+  const int lane = threadIdx.x & 63, sub = lane & (L - 1), lane0 = lane - sub;
+  const int64_t t0 = ((int64_t)blockIdx.x * 4 + (threadIdx.x >> 6)) * (64 / L);
+  if (t0 >= p.T) return;
+  const int E = p.E, top = p.top;
+  const int64_t t = t0 + lane / L, tr = min(t, p.T - 1), row = tr * E;
+  const bool whole = E % 4 == 0, bf16 = p.bf16, all = !p.sigmoid && !p.renorm;
+  int id = -1;
+  float dw = 0, xk = -__builtin_inff();
+  if (sub < top) {
+    id = p.ids[tr * top + sub];
+    if (id < 0 || id >= E) id = -1;
+    if (id >= 0) {
+      dw = p.dweights[tr * top + sub];
+      xk = load_logit(p.logits, row + id, bf16);
+    }
+  }
+  float o[NE];
+  float m = xk;
+  if (all) {
+#pragma unroll
+    for (int j = 0; j < NE; j += 4) {
+      float x[4];
+      load_logits<4>(p.logits, row, 4 * sub + L * j, E, bf16, x);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        o[j + i] = x[i];
+        m = fmaxf(m, x[i]);
+      }
+    }
+  }
+  m = max_over<L>(m);
+  // relative to the largest, as in the forward pass
+  auto rel = [&](float v) { return m == -__builtin_inff() ? 0.0f : relative_exp(v, m); };
+  float v = 0;                                     // of lane k: its choice's gradient
+  float shared = 0;
+  if (all) {
+    float sum = 0;
+#pragma unroll
+    for (int j = 0; j < NE; ++j) {
+      o[j] = rel(o[j]);
+      sum += o[j];
+    }
+    sum = sum_over<L>(sum);
+    const float inv = sum == 0 ? 0.0f : 1.0f / sum;
+    v = id >= 0 ? p.scale * dw * (rel(xk) * inv) : 0.0f;
+    shared = sum_over<L>(v) * -inv;
+  } else {
+    // sigmoid(x) = e^min(x, 0) / (1 + e^-|x|); relative to the largest, so that none of a sum vanishes
+    float pk = 0, q = 1;
+    if (id >= 0) {
+      if (p.sigmoid) {
+        const float en = __expf(-fabsf(xk)), inv = 1.0f / (1.0f + en);
+        q = (xk >= 0 ? en : 1.0f) * inv;           // 1 - p
+        pk = (p.renorm ? __expf(fminf(xk, 0.0f) - fminf(m, 0.0f)) : xk >= 0 ? 1.0f : en) * inv;
+        if (p.renorm && m < -745.2f) pk = 0;       // (a sum of 0 in fp64: weights of 0)
+      } else {
+        pk = rel(xk);
+      }
+    }
+    if (p.renorm) {
+      const float s = sum_over<L>(pk);
+      pk = s == 0 ? 0.0f : pk / s;
+      const float d = sum_over<L>(pk * dw);
+      v = p.scale * pk * (dw - d) * q;
+    } else {
+      v = p.scale * dw * pk * q;
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < NE; ++j) o[j] = all ? o[j] * shared : 0.0f;
+  for (int k = 0; k < top; ++k) {
+    const int at = __shfl(id, lane0 + k, 64) - 4 * sub;
+    const float vk = __shfl(v, lane0 + k, 64);
+#pragma unroll
+    for (int j = 0; j < NE; ++j) o[j] += at == L * (j & ~3) + (j & 3) ? vk : 0.0f;
+  }
+  if (t >= p.T) return;
+#pragma unroll
+  for (int j = 0; j < NE; j += 4) {
+    const int e = 4 * sub + L * j;
+    if (whole) {
+      if (e < E) {
+        if (bf16) store8_nt((uint2*)((uint16_t*)p.dlogits + row + e), make_uint2(bf16_pack(o[j], o[j + 1]), bf16_pack(o[j + 2], o[j + 3])));
+        else __builtin_nontemporal_store(v4f{o[j], o[j + 1], o[j + 2], o[j + 3]}, (v4f*)((float*)p.dlogits + row + e));
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (e + i < E) {
+          if (bf16) ((__bf16*)p.dlogits)[row + e + i] = (__bf16)o[j + i];
+          else ((float*)p.dlogits)[row + e + i] = o[j + i];
+        }
+    }
+  }
+}
+
 }  // namespace
 
 namespace {
@@ -1054,15 +1073,14 @@ hipError_t launch_route(const RouteArgs& a, const SortArgs* sort, hipStream_t st
 }
 
 hipError_t launch_route_bwd(const RouteBwdArgs& a, hipStream_t st) {
-  const int ne = (a.E + 63) / 64;
-  auto go = [&](auto kernel) {
-    hipLaunchKernelGGL(kernel, dim3((unsigned)((a.T + 3) / 4)), dim3(256), 0, st, a);
+  auto go = [&](auto kernel, int tokens) {
+    hipLaunchKernelGGL(kernel, dim3((unsigned)((a.T + 4 * tokens - 1) / (4 * tokens))), dim3(256), 0, st, a);
   };
-  if (ne <= 1) go(route_bwd_kernel<1>);
-  else if (ne <= 2) go(route_bwd_kernel<2>);
-  else if (ne <= 4) go(route_bwd_kernel<4>);
-  else if (ne <= 8) go(route_bwd_kernel<8>);
-  else go(route_bwd_kernel<16>);
+  if (a.top > 16 || a.E > 512) go(route_bwd_kernel<64, 16>, 1);
+  else if (a.E <= 64) go(route_bwd_kernel<16, 4>, 4);
+  else if (a.E <= 128) go(route_bwd_kernel<16, 8>, 4);
+  else if (a.E <= 256) go(route_bwd_kernel<16, 16>, 4);
+  else go(route_bwd_kernel<32, 16>, 2);
   return hipGetLastError();
 }
 
