@@ -112,36 +112,59 @@ struct CombineBwdArgs {
 hipError_t launch_combine_bwd(const CombineBwdArgs& a, hipStream_t st);
 
 // ---- shared device helpers ----------------------------------------------------------------------
-// Eight consecutive elements as they lie in memory: 16 bytes of bf16 or 32 of fp32.
+// Eight consecutive elements as they lie in memory: 16 bytes of bf16 or 32 of fp32, of a type known when compiling (BF16) or not.
+enum { kAny = -1 };
+template <int BF16 = kAny>
 struct Raw8 {
   uint4 a, b;
+};
+template <>
+struct Raw8<1> {
+  uint4 a;
 };
 template <bool NT>
 __device__ __forceinline__ uint4 load16(const void* p) {
   if constexpr (NT) return load16_nt((const uint4*)p);
   return *(const uint4*)p;
 }
-template <bool NT = true>
-__device__ __forceinline__ void load8(Raw8& r, const void* base, int64_t at, bool bf16) {
-  if (bf16) {
+template <bool NT = true, int BF16>
+__device__ __forceinline__ void load8(Raw8<BF16>& r, const void* base, int64_t at, bool bf16) {
+  if constexpr (BF16 == 1) {
     r.a = load16<NT>((const uint16_t*)base + at);
   } else {
-    r.a = load16<NT>((const float*)base + at);
-    r.b = load16<NT>((const float*)base + at + 4);
+    if (BF16 != 0 && bf16) {
+      r.a = load16<NT>((const uint16_t*)base + at);
+    } else {
+      r.a = load16<NT>((const float*)base + at);
+      r.b = load16<NT>((const float*)base + at + 4);
+    }
   }
 }
-__device__ __forceinline__ void to_float8(const Raw8& r, bool bf16, float (&f)[8]) {
-  if (bf16) {
-    const uint32_t v[4] = {r.a.x, r.a.y, r.a.z, r.a.w};
+template <int BF16>
+__device__ __forceinline__ void clear8(Raw8<BF16>& r) {
+  r.a = make_uint4(0, 0, 0, 0);
+  if constexpr (BF16 != 1) r.b = make_uint4(0, 0, 0, 0);
+}
+__device__ __forceinline__ void bf16_to_float8(uint4 a, float (&f)[8]) {
+  const uint32_t v[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      f[2 * i] = __uint_as_float(v[i] << 16);
-      f[2 * i + 1] = __uint_as_float(v[i] & 0xFFFF0000u);
-    }
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = __uint_as_float(v[i] << 16);
+    f[2 * i + 1] = __uint_as_float(v[i] & 0xFFFF0000u);
+  }
+}
+template <int BF16>
+__device__ __forceinline__ void to_float8(const Raw8<BF16>& r, bool bf16, float (&f)[8]) {
+  if constexpr (BF16 == 1) {
+    bf16_to_float8(r.a, f);
   } else {
-    const uint32_t v[8] = {r.a.x, r.a.y, r.a.z, r.a.w, r.b.x, r.b.y, r.b.z, r.b.w};
+    if (BF16 != 0 && bf16) {
+      bf16_to_float8(r.a, f);
+    } else {
+      const uint32_t v[8] = {r.a.x, r.a.y, r.a.z, r.a.w, r.b.x, r.b.y, r.b.z, r.b.w};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(v[i]);
+      for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(v[i]);
+    }
   }
 }
 // (hardware rounding: nearest even, a NaN stays one)

@@ -53,8 +53,24 @@ __device__ __forceinline__ double rsqrt64(double m) {
   for (int i = 0; i < 2; ++i) r = fma(0.5 * r, fma(-m * r, r, 1.0), r);
   return r;
 }
-// y in fp32 so that a second rounding to fewer bits gives what one rounding of y would: cut off towards zero, the
-// last bit set where anything was cut ("round to odd").
+// Maximum over a row of magnitude bits.
+template <int WPR>
+__device__ __forceinline__ uint32_t row_max_bits(uint32_t v, uint32_t* red) {
+  v = hex_max(v);
+  v = max(v, (uint32_t)__shfl_xor((int)v, 16, 64));
+  v = max(v, (uint32_t)__shfl_xor((int)v, 32, 64));
+  if constexpr (WPR > 1) {
+    const int w = threadIdx.x >> 6;
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0) red[w] = v;
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < WPR; ++k) v = max(v, red[w / WPR * WPR + k]);
+  }
+  return v;
+}
+// A value in fp32 so that a second rounding to fewer bits gives what one rounding of it would: cut off towards zero, the
+// last bit set where anything was cut ("round to odd").  Of y, and of y + e with |e| of a few units of y.
 __device__ __forceinline__ float round_to_odd(double y) {
   const float f = (float)y;
   const double back = (double)f;
@@ -63,28 +79,42 @@ __device__ __forceinline__ float round_to_odd(double y) {
   if (fabs(back) > fabs(y)) --u;
   return __uint_as_float(u | 1u);
 }
+__device__ __forceinline__ float round_to_odd(float big, float small) {
+#pragma clang fp contract(off)
+  const float y = big + small, e = small - (y - big);        // (exact)
+  const uint32_t u = __float_as_uint(y) - ((__float_as_uint(y) ^ __float_as_uint(e)) >> 31);
+  return copysignf(e != 0 ? __uint_as_float(u | 1u) : y, big);         // (-0 stays)
+}
+// h w r that way, r = r_hi + r_lo: the errors of both products and r_lo's part, exact or to 2^-46 of the value.
+__device__ __forceinline__ float product_to_odd(float h, float w, float r_hi, float r_lo) {
+#pragma clang fp contract(off)
+  const float v = h * w, v_lo = fmaf(h, w, -v), y = v * r_hi;
+  return round_to_odd(y, fmaf(v_lo, r_hi, fmaf(v, r_lo, fmaf(v, r_hi, -y))));
+}
 
-// Waves of a row (WPR) and chunks of 8 elements per lane (NCH).  Rows past R of the last block repeat row R - 1
-// without storing.
-template <int OUT, int WPR, int NCH>
+// Waves of a row (WPR) and chunks of 8 elements per lane (NCH); BF16: x and the residual (if any) are bf16, else each is what the
+// arguments say.  Rows past R of the last block repeat row R - 1 without storing.
+template <int OUT, int WPR, int NCH, bool BF16>
 __global__ __launch_bounds__(WPR > 4 ? 64 * WPR : 256) void rmsnorm_kernel(NormArgs p) {
   constexpr int NT = WPR > 4 ? 64 * WPR : 256;
   __shared__ double red[NT / 64];
+  __shared__ uint32_t red32[NT / 64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t row_raw = (int64_t)blockIdx.x * (NT / 64 / WPR) + wave / WPR;
   const bool live = row_raw < p.R;
   const int64_t row = live ? row_raw : p.R - 1;
   const int64_t C = p.C, at0 = row * C;
   const int l = 64 * (wave % WPR) + lane;
-  const bool x_bf16 = p.x_bf16, r_bf16 = p.r_bf16, w_bf16 = p.w_bf16;
+  const bool x_bf16 = BF16 || p.x_bf16, r_bf16 = BF16 || p.r_bf16, w_bf16 = p.w_bf16;
 
   float h[NCH][8];
   {
-    Raw8 x[NCH], r[NCH];
+    Raw8<BF16 ? 1 : kAny> x[NCH], r[NCH];
 #pragma unroll
     for (int k = 0; k < NCH; ++k) {
       const int64_t c = 8 * (l + 64 * WPR * k);
-      x[k].a = x[k].b = r[k].a = r[k].b = make_uint4(0, 0, 0, 0);
+      clear8(x[k]);
+      clear8(r[k]);
       if (c < C) {
         load8(x[k], p.x, at0 + c, x_bf16);
         if (p.residual) load8(r[k], p.residual, at0 + c, r_bf16);
@@ -117,68 +147,96 @@ __global__ __launch_bounds__(WPR > 4 ? 64 * WPR : 256) void rmsnorm_kernel(NormA
 
   auto weight = [&](int k, float (&w)[8]) {
     const int64_t c = 8 * (l + 64 * WPR * k);
-    Raw8 t;
-    t.a = t.b = make_uint4(0, 0, 0, 0);
+    Raw8<> t;
+    clear8(t);
     if (c < C) load8<false>(t, p.w, c, w_bf16);
     to_float8(t, w_bf16, w);
   };
 
   if constexpr (OUT == kNormInt8) {
-    double amax = 0;
-    bool nan = false;                              // (fmax drops a NaN)
+    // v = h w in fp32 (exact where both are bf16); the magnitude bits of a float order like its value, a NaN's above all
+    const bool exact = w_bf16 && (p.residual ? r_bf16 : x_bf16);
+    uint32_t m = 0;
 #pragma unroll
     for (int k = 0; k < NCH; ++k) {
       float w[8];
       weight(k, w);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const double v = (double)h[k][e] * (double)w[e];
-        amax = fmax(amax, fabs(v));
-        nan |= v != v;
-      }
+      for (int e = 0; e < 8; ++e) m = max(m, __float_as_uint(h[k][e] * w[e]) & 0x7FFFFFFFu);
     }
-    if (nan) amax = __builtin_inf();
-    amax = row_max<WPR>(amax, red);
-    const bool finite = amax < __builtin_inf() && sum < __builtin_inf();
-    const bool zero = amax == 0;
-    if (live && l == 0) ((float*)p.s)[row] = zero && finite ? 1.0f : finite ? (float)(amax * r64 / 127.0) : __builtin_nanf("");
-    const bool dead = zero || !finite;
-    const double inv = dead ? 0.0 : 127.0 / amax;
+    m = row_max_bits<WPR>(m, red32);
+    const float amax = __uint_as_float(m);
+    const bool finite = m < 0x7F800000u && sum < __builtin_inf();
+    // the exact maximum, where the product was rounded or too small for that: of those that round to it
+    double amax64 = (double)amax;
+    const bool tiny = amax < 1e-30f;
+    if (!exact || tiny) {
+      double some = 0;
+#pragma unroll
+      for (int k = 0; k < NCH; ++k) {
+        float w[8];
+        weight(k, w);
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (tiny || fabsf(h[k][e] * w[e]) == amax) some = fmax(some, fabs((double)h[k][e] * (double)w[e]));
+      }
+      amax64 = row_max<WPR>(some, red);
+    }
+    const bool zero = amax64 == 0, dead = zero || !finite;
+    if (live && l == 0) ((float*)p.s)[row] = !finite ? __builtin_nanf("") : zero ? 1.0f : (float)(amax64 * r64 / 127.0);
+    const float factor = dead || tiny ? 0.0f : 127.0f / amax;
 #pragma unroll
     for (int k = 0; k < NCH; ++k) {
       const int64_t c = 8 * (l + 64 * WPR * k);
-      float w[8], y[8];
+      float w[8];
       weight(k, w);
-      uint32_t code[8];
+      uint32_t code[8], near = tiny && !dead ? 0xFFu : 0u;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const double v = (double)h[k][e] * (double)w[e];
-        // a product with the rounded reciprocal is within 2^-52 of the quotient: where it is that near to a tie, divide
-        const double t = v * inv;
-        double n = rint(t);
-        if (fabs(t - n) > 0.5 - 1e-12) n = rint(127.0 * v / amax);
+        // four roundings: within 127 * 4 * 2^-24 = 3e-5 of the quotient
+        const float t = h[k][e] * w[e] * factor, n = rintf(t);
+        near |= fabsf(t - n) > 0.5f - 4e-5f ? 1u << e : 0u;
         code[e] = dead ? 0u : (uint32_t)(int)n & 255u;
-        y[e] = h[k][e] * r32 * w[e];
+      }
+      if (dead) near = 0;
+      if (__ballot(near != 0)) {                   // beside a border between two codes: of the exact quotient
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (near >> e & 1) code[e] = (uint32_t)(int)rint(127.0 * ((double)h[k][e] * (double)w[e]) / amax64) & 255u;
       }
       if (live && c < C) {
         store8_nt((uint2*)((int8_t*)p.q + at0 + c),
                   make_uint2(code[0] | code[1] << 8 | code[2] << 16 | code[3] << 24,
                              code[4] | code[5] << 8 | code[6] << 16 | code[7] << 24));
-        if (p.y) store8(p.y, at0 + c, true, y);
+        if (p.y) {
+          float y[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) y[e] = h[k][e] * r32 * w[e];
+          store8(p.y, at0 + c, true, y);
+        }
       }
     }
   } else if constexpr (OUT == kNormMx) {
+    const float r_lo = (float)(r64 - (double)r32);
 #pragma unroll
     for (int k = 0; k < NCH; ++k) {
       const int64_t c = 8 * (l + 64 * WPR * k);
-      float w[8], y[8], o[8];
+      float w[8], o[8];
       weight(k, w);
       uint32_t m = 0;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        o[e] = round_to_odd((double)h[k][e] * (double)w[e] * r64);
+        o[e] = product_to_odd(h[k][e], w[e], r32, r_lo);
         m = max(m, __float_as_uint(o[e]) & 0x7FFFFFFFu);
-        y[e] = h[k][e] * r32 * w[e];
+      }
+      // where a block's largest value is so small that errors are lost (or a product is not a number): from fp64
+      if (__ballot(quad_max(m) - 1u < 0x17800000u - 1u || quad_max(m) >= 0x7F800000u)) {   // (0, 2^-80), or inf
+        m = 0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          o[e] = round_to_odd((double)h[k][e] * (double)w[e] * r64);
+          m = max(m, __float_as_uint(o[e]) & 0x7FFFFFFFu);
+        }
       }
       m = quad_max(m);                             // 4 lanes hold a block of 32
       const int e8 = max((int)(m >> 23) - 135, -127);
@@ -189,7 +247,12 @@ __global__ __launch_bounds__(WPR > 4 ? 64 * WPR : 256) void rmsnorm_kernel(NormA
                   make_uint2(cvt4_f32_e4m3_scaled(o[0], o[1], o[2], o[3], lim, scale),
                              cvt4_f32_e4m3_scaled(o[4], o[5], o[6], o[7], lim, scale)));
         if ((lane & 3) == 0) ((uint8_t*)p.s)[row * (C / 32) + c / 32] = (uint8_t)(e8 + 127);
-        if (p.y) store8(p.y, at0 + c, true, y);
+        if (p.y) {
+          float y[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) y[e] = h[k][e] * r32 * w[e];
+          store8(p.y, at0 + c, true, y);
+        }
       }
     }
   } else {
@@ -208,7 +271,8 @@ __global__ __launch_bounds__(WPR > 4 ? 64 * WPR : 256) void rmsnorm_kernel(NormA
 // ---- backward ----------------------------------------------------------------------------------
 // A block takes rows blockIdx.x, blockIdx.x + gridDim.x, ... (times its rows at once), keeps the weights and its part of
 // dw in registers, and writes that part to its row of the workspace; a second launch adds the parts up.
-template <int WPR, int NCH>
+// BF16: dy, h and dres are bf16, else each is what the arguments say.
+template <int WPR, int NCH, bool BF16>
 __global__ __launch_bounds__(WPR > 4 ? 64 * WPR : 256) void rmsnorm_bwd_kernel(NormBwdArgs p) {
   constexpr int NT = WPR > 4 ? 64 * WPR : 256, RPB = NT / 64 / WPR;
   __shared__ double red64[NT / 64];
@@ -217,13 +281,13 @@ __global__ __launch_bounds__(WPR > 4 ? 64 * WPR : 256) void rmsnorm_bwd_kernel(N
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, sub = wave / WPR;
   const int64_t C = p.C;
   const int l = 64 * (wave % WPR) + lane;
-  const bool dy_bf16 = p.dy_bf16, h_bf16 = p.h_bf16;
+  const bool dy_bf16 = BF16 || p.dy_bf16, h_bf16 = BF16 || p.h_bf16;
   float w[NCH][8], acc[NCH][8];
 #pragma unroll
   for (int k = 0; k < NCH; ++k) {
     const int64_t c = 8 * (l + 64 * WPR * k);
-    Raw8 t;
-    t.a = t.b = make_uint4(0, 0, 0, 0);
+    Raw8<> t;
+    clear8(t);
     if (c < C) load8<false>(t, p.w, c, p.w_bf16);
     to_float8(t, p.w_bf16, w[k]);
 #pragma unroll
@@ -232,28 +296,30 @@ __global__ __launch_bounds__(WPR > 4 ? 64 * WPR : 256) void rmsnorm_bwd_kernel(N
   for (int64_t r0 = (int64_t)blockIdx.x * RPB; r0 < p.R; r0 += (int64_t)gridDim.x * RPB) {
     const bool live = r0 + sub < p.R;
     const int64_t at0 = (live ? r0 + sub : p.R - 1) * C;
-    Raw8 a[NCH], b[NCH], d[NCH];
+    Raw8<BF16 ? 1 : kAny> a[NCH], b[NCH], d[NCH];
 #pragma unroll
     for (int k = 0; k < NCH; ++k) {
       const int64_t c = 8 * (l + 64 * WPR * k);
-      a[k].a = a[k].b = b[k].a = b[k].b = d[k].a = d[k].b = make_uint4(0, 0, 0, 0);
+      clear8(a[k]);
+      clear8(b[k]);
+      clear8(d[k]);
       if (c < C) {
         load8(a[k], p.dy, at0 + c, dy_bf16);
         load8(b[k], p.h, at0 + c, h_bf16);
         if (p.dres) load8(d[k], p.dres, at0 + c, h_bf16);
       }
     }
-    float dy[NCH][8], h[NCH][8];
     double sum = 0;
     float dot = 0;
 #pragma unroll
     for (int k = 0; k < NCH; ++k) {
-      to_float8(a[k], dy_bf16, dy[k]);
-      to_float8(b[k], h_bf16, h[k]);
+      float dy[8], h[8];
+      to_float8(a[k], dy_bf16, dy);
+      to_float8(b[k], h_bf16, h);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        sum = fma((double)h[k][e], (double)h[k][e], sum);
-        dot = fmaf(dy[k][e] * w[k][e], h[k][e], dot);
+        sum = fma((double)h[e], (double)h[e], sum);
+        dot = fmaf(dy[e] * w[k][e], h[e], dot);
       }
     }
     sum = row_sum<WPR>(sum, red64);
@@ -263,12 +329,17 @@ __global__ __launch_bounds__(WPR > 4 ? 64 * WPR : 256) void rmsnorm_bwd_kernel(N
 #pragma unroll
     for (int k = 0; k < NCH; ++k) {
       const int64_t c = 8 * (l + 64 * WPR * k);
-      float dx[8], f[8];
+      float dx[8], f[8], dy[8], h[8];
+      // (the raw values are unpacked again rather than kept)
+      asm("" : "+v"(a[k].a.x), "+v"(a[k].a.y), "+v"(a[k].a.z), "+v"(a[k].a.w), "+v"(b[k].a.x), "+v"(b[k].a.y), "+v"(b[k].a.z),
+          "+v"(b[k].a.w));
+      to_float8(a[k], dy_bf16, dy);
+      to_float8(b[k], h_bf16, h);
       to_float8(d[k], h_bf16, f);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        dx[e] = fmaf(r, fmaf(-h[k][e], back, dy[k][e] * w[k][e]), f[e]);
-        if (live) acc[k][e] = fmaf(dy[k][e], h[k][e] * r, acc[k][e]);
+        dx[e] = fmaf(r, fmaf(-h[e], back, dy[e] * w[k][e]), f[e]);
+        if (live) acc[k][e] = fmaf(dy[e], h[e] * r, acc[k][e]);
       }
       if (live && c < C) store8(p.dx, at0 + c, h_bf16, dx);
     }
@@ -349,20 +420,23 @@ static hipError_t launch_rmsnorm_out(const NormArgs& a, hipStream_t st) {
       hipLaunchKernelGGL(kernel, dim3((unsigned)((p.R + per - 1) / per)), dim3(wpr > 4 ? 64 * wpr : 256), 0, st, p);
     }
   };
+  const bool bf16 = a.x_bf16 && (!a.residual || a.r_bf16);
+#define GO(WPR, NCH) bf16 ? go(rmsnorm_kernel<OUT, WPR, NCH, true>) : go(rmsnorm_kernel<OUT, WPR, NCH, false>)
   if (wpr == 1) {
-    if (nch == 1) go(rmsnorm_kernel<OUT, 1, 1>);
-    else if (nch == 2) go(rmsnorm_kernel<OUT, 1, 2>);
-    else if (nch == 3) go(rmsnorm_kernel<OUT, 1, 3>);
-    else go(rmsnorm_kernel<OUT, 1, 4>);
+    if (nch == 1) GO(1, 1);
+    else if (nch == 2) GO(1, 2);
+    else if (nch == 3) GO(1, 3);
+    else GO(1, 4);
   } else if (wpr == 4) {
-    if (nch == 2) go(rmsnorm_kernel<OUT, 4, 2>);
-    else if (nch == 3) go(rmsnorm_kernel<OUT, 4, 3>);
-    else go(rmsnorm_kernel<OUT, 4, 4>);
+    if (nch == 2) GO(4, 2);
+    else if (nch == 3) GO(4, 3);
+    else GO(4, 4);
   } else {
-    if (nch == 1) go(rmsnorm_kernel<OUT, 16, 1>);
-    else if (nch == 2) go(rmsnorm_kernel<OUT, 16, 2>);
-    else go(rmsnorm_kernel<OUT, 16, 4>);
+    if (nch == 1) GO(16, 1);
+    else if (nch == 2) GO(16, 2);
+    else GO(16, 4);
   }
+#undef GO
   return hipGetLastError();
 }
 
@@ -384,20 +458,23 @@ hipError_t launch_rmsnorm_bwd(const NormBwdArgs& a, hipStream_t st) {
     hipLaunchKernelGGL(kernel, dim3(blocks), dim3(wpr > 4 ? 64 * wpr : 256), 0, st, a);
   };
   if (blocks) {
+    const bool bf16 = a.dy_bf16 && a.h_bf16;
+#define GO(WPR, NCH) bf16 ? go(rmsnorm_bwd_kernel<WPR, NCH, true>) : go(rmsnorm_bwd_kernel<WPR, NCH, false>)
     if (wpr == 1) {
-      if (nch == 1) go(rmsnorm_bwd_kernel<1, 1>);
-      else if (nch == 2) go(rmsnorm_bwd_kernel<1, 2>);
-      else if (nch == 3) go(rmsnorm_bwd_kernel<1, 3>);
-      else go(rmsnorm_bwd_kernel<1, 4>);
+      if (nch == 1) GO(1, 1);
+      else if (nch == 2) GO(1, 2);
+      else if (nch == 3) GO(1, 3);
+      else GO(1, 4);
     } else if (wpr == 4) {
-      if (nch == 2) go(rmsnorm_bwd_kernel<4, 2>);
-      else if (nch == 3) go(rmsnorm_bwd_kernel<4, 3>);
-      else go(rmsnorm_bwd_kernel<4, 4>);
+      if (nch == 2) GO(4, 2);
+      else if (nch == 3) GO(4, 3);
+      else GO(4, 4);
     } else {
-      if (nch == 2) go(rmsnorm_bwd_kernel<16, 2>);
-      else if (nch == 3) go(rmsnorm_bwd_kernel<16, 3>);
-      else go(rmsnorm_bwd_kernel<16, 4>);
+      if (nch == 2) GO(16, 2);
+      else if (nch == 3) GO(16, 3);
+      else GO(16, 4);
     }
+#undef GO
   }
   if (a.dw)
     hipLaunchKernelGGL(column_sum_kernel, dim3((unsigned)((a.C + 63) / 64)), dim3(1024), 0, st, a.ws, blocks, a.C, a.dw);

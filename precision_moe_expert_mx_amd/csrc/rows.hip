@@ -53,7 +53,7 @@ __global__ __launch_bounds__(NT) void combine_kernel(CombineArgs p) {
   const int64_t t = i / per, c = 8 * (i - t * per);
   float acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
   if (p.residual) {
-    Raw8 r;
+    Raw8<> r;
     load8(r, p.residual, t * p.C + c, p.r_bf16);
     to_float8(r, p.r_bf16, acc);
   }
@@ -62,7 +62,7 @@ __global__ __launch_bounds__(NT) void combine_kernel(CombineArgs p) {
     const int64_t r = p.pos[t * p.top + k];
     if (r < 0 || r >= p.M) continue;
     const float w = p.weights ? p.weights[t * p.top + k] : 1.0f;
-    Raw8 y;
+    Raw8<> y;
     float f[8];
     load8(y, p.y, r * p.C + c, p.y_bf16);
     to_float8(y, p.y_bf16, f);
@@ -86,7 +86,7 @@ __global__ __launch_bounds__(NT) void combine_bwd_kernel(CombineBwdArgs p) {
     float dot = 0;
     if (here)
       for (int64_t c = 8 * lane; c < p.C; c += 512) {
-        Raw8 d, y;
+        Raw8<> d, y;
         float g[8], f[8];
         load8<false>(d, p.dout, t * p.C + c, p.d_bf16);
         to_float8(d, p.d_bf16, g);
