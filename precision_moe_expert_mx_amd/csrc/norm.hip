@@ -70,7 +70,7 @@ __device__ __forceinline__ uint32_t row_max_bits(uint32_t v, uint32_t* red) {
   return v;
 }
 // A value in fp32 so that a second rounding to fewer bits gives what one rounding of it would: cut off towards zero, the
-// last bit set where anything was cut ("round to odd").  Of y, and of y + e with |e| of a few units of y.
+// last bit set where anything was cut ("round to odd").
 __device__ __forceinline__ float round_to_odd(double y) {
   const float f = (float)y;
   const double back = (double)f;
@@ -79,19 +79,6 @@ __device__ __forceinline__ float round_to_odd(double y) {
   if (fabs(back) > fabs(y)) --u;
   return __uint_as_float(u | 1u);
 }
-__device__ __forceinline__ float round_to_odd(float big, float small) {
-#pragma clang fp contract(off)
-  const float y = big + small, e = small - (y - big);        // (exact)
-  const uint32_t u = __float_as_uint(y) - ((__float_as_uint(y) ^ __float_as_uint(e)) >> 31);
-  return copysignf(e != 0 ? __uint_as_float(u | 1u) : y, big);         // (-0 stays)
-}
-// h w r that way, r = r_hi + r_lo: the errors of both products and r_lo's part, exact or to 2^-46 of the value.
-__device__ __forceinline__ float product_to_odd(float h, float w, float r_hi, float r_lo) {
-#pragma clang fp contract(off)
-  const float v = h * w, v_lo = fmaf(h, w, -v), y = v * r_hi;
-  return round_to_odd(y, fmaf(v_lo, r_hi, fmaf(v, r_lo, fmaf(v, r_hi, -y))));
-}
-
 // Waves of a row (WPR) and chunks of 8 elements per lane (NCH); BF16: x and the residual (if any) are bf16, else each is what the
 // arguments say.  Rows past R of the last block repeat row R - 1 without storing.
 template <int OUT, int WPR, int NCH, bool BF16>
@@ -113,9 +100,11 @@ __global__ __launch_bounds__(WPR > 4 ? 64 * WPR : 256) void rmsnorm_kernel(NormA
 #pragma unroll
     for (int k = 0; k < NCH; ++k) {
       const int64_t c = 8 * (l + 64 * WPR * k);
-      clear8(x[k]);
-      clear8(r[k]);
-      if (c < C) {
+      if (k == NCH - 1) {                          // (the others are whole)
+        clear8(x[k]);
+        clear8(r[k]);
+      }
+      if (k < NCH - 1 || c < C) {
         load8(x[k], p.x, at0 + c, x_bf16);
         if (p.residual) load8(r[k], p.residual, at0 + c, r_bf16);
       }
@@ -148,8 +137,8 @@ __global__ __launch_bounds__(WPR > 4 ? 64 * WPR : 256) void rmsnorm_kernel(NormA
   auto weight = [&](int k, float (&w)[8]) {
     const int64_t c = 8 * (l + 64 * WPR * k);
     Raw8<> t;
-    clear8(t);
-    if (c < C) load8<false>(t, p.w, c, w_bf16);
+    if (k == NCH - 1) clear8(t);
+    if (k < NCH - 1 || c < C) load8<false>(t, p.w, c, w_bf16);
     to_float8(t, w_bf16, w);
   };
 
@@ -184,30 +173,34 @@ __global__ __launch_bounds__(WPR > 4 ? 64 * WPR : 256) void rmsnorm_kernel(NormA
     }
     const bool zero = amax64 == 0, dead = zero || !finite;
     if (live && l == 0) ((float*)p.s)[row] = !finite ? __builtin_nanf("") : zero ? 1.0f : (float)(amax64 * r64 / 127.0);
+    // a factor of 0 gives codes 0 (a NaN too, in the sum below: its low byte is not used)
     const float factor = dead || tiny ? 0.0f : 127.0f / amax;
+    constexpr float kMagic = 12582912.0f;          // 1.5 * 2^23: the low byte of the sum is the code
 #pragma unroll
     for (int k = 0; k < NCH; ++k) {
       const int64_t c = 8 * (l + 64 * WPR * k);
       float w[8];
       weight(k, w);
-      uint32_t code[8], near = tiny && !dead ? 0xFFu : 0u;
+      uint32_t code[8], near = 0;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        // four roundings: within 127 * 4 * 2^-24 = 3e-5 of the quotient
-        const float t = h[k][e] * w[e] * factor, n = rintf(t);
-        near |= fabsf(t - n) > 0.5f - 4e-5f ? 1u << e : 0u;
-        code[e] = dead ? 0u : (uint32_t)(int)n & 255u;
+        // the product, the maximum, the factor and this sum: within 127 * 4 * 2^-24 = 3e-5 of the quotient
+        const float v = h[k][e] * w[e], m = fmaf(v, factor, kMagic), n = m - kMagic;
+        if (__ballot(fabsf(fmaf(v, factor, -n)) > 0.5f - 4e-5f)) near |= 1u << e;
+        code[e] = __float_as_uint(m);
       }
-      if (dead) near = 0;
-      if (__ballot(near != 0)) {                   // beside a border between two codes: of the exact quotient
+      if (tiny) near = 0xFF;
+      if (near && !dead) {                         // beside a border between two codes: of the exact quotient
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-          if (near >> e & 1) code[e] = (uint32_t)(int)rint(127.0 * ((double)h[k][e] * (double)w[e]) / amax64) & 255u;
+          if (near >> e & 1) code[e] = (uint32_t)(int)rint(127.0 * ((double)h[k][e] * (double)w[e]) / amax64);
       }
       if (live && c < C) {
-        store8_nt((uint2*)((int8_t*)p.q + at0 + c),
-                  make_uint2(code[0] | code[1] << 8 | code[2] << 16 | code[3] << 24,
-                             code[4] | code[5] << 8 | code[6] << 16 | code[7] << 24));
+        auto pack = [&](int e) {                   // the low bytes of four
+          const uint32_t lo = __builtin_amdgcn_perm(code[e + 1], code[e], 0x0C0C0400u);
+          return lo | __builtin_amdgcn_perm(code[e + 3], code[e + 2], 0x0C0C0400u) << 16;
+        };
+        store8_nt((uint2*)((int8_t*)p.q + at0 + c), dead ? make_uint2(0, 0) : make_uint2(pack(0), pack(4)));
         if (p.y) {
           float y[8];
 #pragma unroll
@@ -217,28 +210,35 @@ __global__ __launch_bounds__(WPR > 4 ? 64 * WPR : 256) void rmsnorm_kernel(NormA
       }
     }
   } else if constexpr (OUT == kNormMx) {
-    const float r_lo = (float)(r64 - (double)r32);
+    // y in fp32 is within 2 units (three roundings) of the exact value: that moves a code only where y is that near to a
+    // tie of E4M3, whose 20 bits below the code are 0x80000, and a scale only where the maximum is that near to a power
+    // of two.  There, and for what falls below the normal codes (2^-15 of the maximum, or scales that are not normal), y is
+    // formed again in fp64 and rounded so that the code's rounding is the only one.
 #pragma unroll
     for (int k = 0; k < NCH; ++k) {
       const int64_t c = 8 * (l + 64 * WPR * k);
       float w[8], o[8];
       weight(k, w);
-      uint32_t m = 0;
+      uint32_t m = 0, least = 0xFFFFFFFFu, nearest = 0xFFFFFFFFu;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        o[e] = product_to_odd(h[k][e], w[e], r32, r_lo);
-        m = max(m, __float_as_uint(o[e]) & 0x7FFFFFFFu);
+        o[e] = h[k][e] * w[e] * r32;
+        const uint32_t u = __float_as_uint(o[e]) & 0x7FFFFFFFu;
+        m = max(m, u);
+        least = min(least, u - 1);                 // (a zero is no small value)
+        nearest = min(nearest, (u - (0x80000u - 4)) & 0xFFFFFu);
       }
-      // where a block's largest value is so small that errors are lost (or a product is not a number): from fp64
-      if (__ballot(quad_max(m) - 1u < 0x17800000u - 1u || quad_max(m) >= 0x7F800000u)) {   // (0, 2^-80), or inf
+      m = quad_max(m);                             // 4 lanes hold a block of 32
+      const bool again = nearest <= 8 || ((m + 4) & 0x7FFFFFu) <= 8 || m >= 0x7F800000u || (m != 0 && (m < 0x08000000u || least < m - 0x07000000u));
+      if (__ballot(again)) {
         m = 0;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           o[e] = round_to_odd((double)h[k][e] * (double)w[e] * r64);
           m = max(m, __float_as_uint(o[e]) & 0x7FFFFFFFu);
         }
+        m = quad_max(m);
       }
-      m = quad_max(m);                             // 4 lanes hold a block of 32
       const int e8 = max((int)(m >> 23) - 135, -127);
       const float scale = __uint_as_float((uint32_t)(e8 + 127) << 23);
       const float lim = __uint_as_float(((uint32_t)(e8 + 135) << 23) | 0x600000u);   // 448 * 2^e8
@@ -300,10 +300,14 @@ __global__ __launch_bounds__(WPR > 4 ? 64 * WPR : 256) void rmsnorm_bwd_kernel(N
 #pragma unroll
     for (int k = 0; k < NCH; ++k) {
       const int64_t c = 8 * (l + 64 * WPR * k);
-      clear8(a[k]);
-      clear8(b[k]);
-      clear8(d[k]);
-      if (c < C) {
+      if (k == NCH - 1) {                          // (the others are whole)
+        clear8(a[k]);
+        clear8(b[k]);
+        clear8(d[k]);
+      } else if (!p.dres) {
+        clear8(d[k]);
+      }
+      if (k < NCH - 1 || c < C) {
         load8(a[k], p.dy, at0 + c, dy_bf16);
         load8(b[k], p.h, at0 + c, h_bf16);
         if (p.dres) load8(d[k], p.dres, at0 + c, h_bf16);
@@ -434,6 +438,7 @@ static hipError_t launch_rmsnorm_out(const NormArgs& a, hipStream_t st) {
   } else {
     if (nch == 1) GO(16, 1);
     else if (nch == 2) GO(16, 2);
+    else if (nch == 3) GO(16, 3);
     else GO(16, 4);
   }
 #undef GO
