@@ -187,21 +187,29 @@ __device__ __forceinline__ void store8(void* base, int64_t at, bool bf16, const 
   }
 }
 
-// Sums and maxima over a wave, the result in every lane.
-__device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) v += __shfl_xor(v, d, 64);
-  return v;
+// Sums and maxima over a wave, the result in every lane: lane permutes within 16 lanes, then across them.
+template <int CTRL>
+__device__ __forceinline__ float dpp(float v) {
+  return __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(v), CTRL, 0xF, 0xF, true));
 }
-__device__ __forceinline__ double wave_sum(double v) {
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) v += __shfl_xor(v, d, 64);
-  return v;
+template <int CTRL>
+__device__ __forceinline__ double dpp(double v) {
+  const uint64_t u = (uint64_t)__double_as_longlong(v);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)u, CTRL, 0xF, 0xF, true);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(u >> 32), CTRL, 0xF, 0xF, true);
+  return __longlong_as_double((long long)((uint64_t)hi << 32 | lo));
 }
-__device__ __forceinline__ double wave_max(double v) {
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) v = fmax(v, __shfl_xor(v, d, 64));
-  return v;
+template <typename V, typename F>
+__device__ __forceinline__ V over_wave(V v, F f) {
+  v = f(v, dpp<0xB1>(v));                          // neighbours of 2, 4 (quad permutes), 8, 16 (mirrors)
+  v = f(v, dpp<0x4E>(v));
+  v = f(v, dpp<0x141>(v));
+  v = f(v, dpp<0x140>(v));
+  v = f(v, __shfl_xor(v, 16, 64));
+  return f(v, __shfl_xor(v, 32, 64));
 }
+__device__ __forceinline__ float wave_sum(float v) { return over_wave(v, [](float a, float b) { return a + b; }); }
+__device__ __forceinline__ double wave_sum(double v) { return over_wave(v, [](double a, double b) { return a + b; }); }
+__device__ __forceinline__ double wave_max(double v) { return over_wave(v, [](double a, double b) { return fmax(a, b); }); }
 
 }  // namespace mxmoe

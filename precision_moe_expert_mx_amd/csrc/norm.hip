@@ -167,7 +167,7 @@ __global__ __launch_bounds__(WPR > 4 ? 64 * WPR : 256) void rmsnorm_kernel(NormA
         weight(k, w);
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-          if (tiny || fabsf(h[k][e] * w[e]) == amax) some = fmax(some, fabs((double)h[k][e] * (double)w[e]));
+          if (__ballot(tiny || fabsf(h[k][e] * w[e]) == amax)) some = fmax(some, fabs((double)h[k][e] * (double)w[e]));
       }
       amax64 = row_max<WPR>(some, red);
     }
@@ -210,9 +210,9 @@ __global__ __launch_bounds__(WPR > 4 ? 64 * WPR : 256) void rmsnorm_kernel(NormA
       }
     }
   } else if constexpr (OUT == kNormMx) {
-    // y in fp32 is within 2 units (three roundings) of the exact value: that moves a code only where y is that near to a
+    // y in fp32 is within 3 units (three roundings) of the exact value: that moves a code only where y is that near to a
     // tie of E4M3, whose 20 bits below the code are 0x80000, and a scale only where the maximum is that near to a power
-    // of two.  There, and for what falls below the normal codes (2^-15 of the maximum, or scales that are not normal), y is
+    // of two.  There, and for what falls below the normal codes (2^-14 of the maximum, or scales that are not normal), y is
     // formed again in fp64 and rounded so that the code's rounding is the only one.
 #pragma unroll
     for (int k = 0; k < NCH; ++k) {
@@ -275,8 +275,10 @@ __global__ __launch_bounds__(WPR > 4 ? 64 * WPR : 256) void rmsnorm_kernel(NormA
 template <int WPR, int NCH, bool BF16>
 __global__ __launch_bounds__(WPR > 4 ? 64 * WPR : 256) void rmsnorm_bwd_kernel(NormBwdArgs p) {
   constexpr int NT = WPR > 4 ? 64 * WPR : 256, RPB = NT / 64 / WPR;
-  __shared__ double red64[NT / 64];
-  __shared__ float red[NT / 64];
+  // where that fits into the registers of two waves per SIMD
+  constexpr bool PREFETCH = BF16 && WPR <= 4;
+  __shared__ double red64[2][NT / 64];
+  __shared__ float red[2][NT / 64];
   __shared__ float part[RPB > 1 ? RPB - 1 : 1][RPB > 1 ? 512 * WPR * NCH : 1];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, sub = wave / WPR;
   const int64_t C = p.C;
@@ -293,60 +295,96 @@ __global__ __launch_bounds__(WPR > 4 ? 64 * WPR : 256) void rmsnorm_bwd_kernel(N
 #pragma unroll
     for (int e = 0; e < 8; ++e) acc[k][e] = 0;
   }
-  for (int64_t r0 = (int64_t)blockIdx.x * RPB; r0 < p.R; r0 += (int64_t)gridDim.x * RPB) {
-    const bool live = r0 + sub < p.R;
-    const int64_t at0 = (live ? r0 + sub : p.R - 1) * C;
+  // a row's chunks as they lie in memory; the next row's are loaded while this one's sums are formed
+  struct Row {
     Raw8<BF16 ? 1 : kAny> a[NCH], b[NCH], d[NCH];
+  };
+  auto load = [&](Row& x, int64_t r0) {
+    const int64_t at0 = min(r0 + sub, p.R - 1) * C;
 #pragma unroll
     for (int k = 0; k < NCH; ++k) {
       const int64_t c = 8 * (l + 64 * WPR * k);
       if (k == NCH - 1) {                          // (the others are whole)
-        clear8(a[k]);
-        clear8(b[k]);
-        clear8(d[k]);
+        clear8(x.a[k]);
+        clear8(x.b[k]);
+        clear8(x.d[k]);
       } else if (!p.dres) {
-        clear8(d[k]);
+        clear8(x.d[k]);
       }
       if (k < NCH - 1 || c < C) {
-        load8(a[k], p.dy, at0 + c, dy_bf16);
-        load8(b[k], p.h, at0 + c, h_bf16);
-        if (p.dres) load8(d[k], p.dres, at0 + c, h_bf16);
+        load8(x.a[k], p.dy, at0 + c, dy_bf16);
+        load8(x.b[k], p.h, at0 + c, h_bf16);
+        if (p.dres) load8(x.d[k], p.dres, at0 + c, h_bf16);
       }
     }
+  };
+  const int64_t step = (int64_t)gridDim.x * RPB;
+  int parity = 0;
+  auto row = [&](Row& x, Row& next, int64_t r0) {
+    const bool live = r0 + sub < p.R;
+    if (PREFETCH && r0 + step < p.R) load(next, r0 + step);
     double sum = 0;
     float dot = 0;
 #pragma unroll
     for (int k = 0; k < NCH; ++k) {
       float dy[8], h[8];
-      to_float8(a[k], dy_bf16, dy);
-      to_float8(b[k], h_bf16, h);
+      to_float8(x.a[k], dy_bf16, dy);
+      to_float8(x.b[k], h_bf16, h);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         sum = fma((double)h[e], (double)h[e], sum);
         dot = fmaf(dy[e] * w[k][e], h[e], dot);
       }
     }
-    sum = row_sum<WPR>(sum, red64);
-    dot = row_sum<WPR>(dot, red);
+    sum = wave_sum(sum);
+    dot = wave_sum(dot);
+    if constexpr (WPR > 1) {                       // (two rows' sums in turn: one barrier each)
+      if (lane == 0) {
+        red64[parity][wave] = sum;
+        red[parity][wave] = dot;
+      }
+      __syncthreads();
+      sum = 0;
+      dot = 0;
+#pragma unroll
+      for (int k = 0; k < WPR; ++k) {
+        sum += red64[parity][sub * WPR + k];
+        dot += red[parity][sub * WPR + k];
+      }
+      parity ^= 1;
+    }
     const float r = (float)rsqrt64(sum / (double)C + p.eps);
     const float back = dot * r * r / (float)C;
+    const int64_t at0 = min(r0 + sub, p.R - 1) * C;
 #pragma unroll
     for (int k = 0; k < NCH; ++k) {
       const int64_t c = 8 * (l + 64 * WPR * k);
       float dx[8], f[8], dy[8], h[8];
       // (the raw values are unpacked again rather than kept)
-      asm("" : "+v"(a[k].a.x), "+v"(a[k].a.y), "+v"(a[k].a.z), "+v"(a[k].a.w), "+v"(b[k].a.x), "+v"(b[k].a.y), "+v"(b[k].a.z),
-          "+v"(b[k].a.w));
-      to_float8(a[k], dy_bf16, dy);
-      to_float8(b[k], h_bf16, h);
-      to_float8(d[k], h_bf16, f);
+      asm("" : "+v"(x.a[k].a.x), "+v"(x.a[k].a.y), "+v"(x.a[k].a.z), "+v"(x.a[k].a.w), "+v"(x.b[k].a.x), "+v"(x.b[k].a.y),
+          "+v"(x.b[k].a.z), "+v"(x.b[k].a.w));
+      to_float8(x.a[k], dy_bf16, dy);
+      to_float8(x.b[k], h_bf16, h);
+      to_float8(x.d[k], h_bf16, f);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         dx[e] = fmaf(r, fmaf(-h[e], back, dy[e] * w[k][e]), f[e]);
         if (live) acc[k][e] = fmaf(dy[e], h[e] * r, acc[k][e]);
       }
-      if (live && c < C) store8(p.dx, at0 + c, h_bf16, dx);
+      if (live && (k < NCH - 1 || c < C)) store8(p.dx, at0 + c, h_bf16, dx);
     }
+    if (!PREFETCH && r0 + step < p.R) load(next, r0 + step);
+  };
+  int64_t r0 = (int64_t)blockIdx.x * RPB;
+  Row x, y;
+  load(x, r0);
+  if constexpr (PREFETCH) {
+    for (; r0 < p.R; r0 += 2 * step) {
+      row(x, y, r0);
+      if (r0 + step < p.R) row(y, x, r0 + step);
+    }
+  } else {
+    for (; r0 < p.R; r0 += step) row(x, x, r0);
   }
   if (!p.dw) return;
   if constexpr (RPB > 1) {
@@ -383,7 +421,13 @@ __global__ __launch_bounds__(1024) void column_sum_kernel(const float* ws, int r
   const int64_t c = (int64_t)blockIdx.x * 64 + lane;
   float s = 0;
   if (c < C)
-    for (int r = wave; r < rows; r += 16) s += ws[r * C + c];
+    for (int r0 = wave; r0 < rows; r0 += 16 * 16) {          // 16 loads in flight
+      float v[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) v[i] = r0 + 16 * i < rows ? ws[(int64_t)(r0 + 16 * i) * C + c] : 0.0f;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) s += v[i];
+    }
   part[wave][lane] = s;
   __syncthreads();
   if (wave == 0 && c < C) {
@@ -405,7 +449,7 @@ template <int OUT>
 static hipError_t launch_rmsnorm_out(const NormArgs& a, hipStream_t st) {
   const int64_t C = a.C;
   // few rows: a row over 16 waves
-  const int wpr = C > 8192 || (a.R <= 512 && C > 2048) ? 16 : C > 2048 ? 4 : 1;
+  const int wpr = C > 8192 || (a.R <= 512 && C > 2048) ? 16 : C > 2048 || (a.R <= 512 && C > 512) ? 4 : 1;
   const int nch = (int)((C + 512 * wpr - 1) / (512 * wpr));
   const int64_t per = wpr == 1 ? 4 : 1;
   auto go = [&](auto kernel) {
@@ -432,7 +476,8 @@ static hipError_t launch_rmsnorm_out(const NormArgs& a, hipStream_t st) {
     else if (nch == 3) GO(1, 3);
     else GO(1, 4);
   } else if (wpr == 4) {
-    if (nch == 2) GO(4, 2);
+    if (nch == 1) GO(4, 1);
+    else if (nch == 2) GO(4, 2);
     else if (nch == 3) GO(4, 3);
     else GO(4, 4);
   } else {
