@@ -177,13 +177,19 @@ __device__ __forceinline__ uint4 bf16_pack8(const float (&f)[8]) {
 __device__ __forceinline__ void store16_nt(void* p, uint4 v) {
   __builtin_nontemporal_store(v4u_{v.x, v.y, v.z, v.w}, (v4u_*)p);
 }
+template <bool NT = true>
+__device__ __forceinline__ void store16(void* p, uint4 v) {
+  if constexpr (NT) store16_nt(p, v);
+  else *(uint4*)p = v;
+}
+template <bool NT = true>
 __device__ __forceinline__ void store8(void* base, int64_t at, bool bf16, const float (&f)[8]) {
   if (bf16) {
-    store16_nt((uint16_t*)base + at, bf16_pack8(f));
+    store16<NT>((uint16_t*)base + at, bf16_pack8(f));
   } else {
     float* p = (float*)base + at;
-    __builtin_nontemporal_store(v4f{f[0], f[1], f[2], f[3]}, (v4f*)p);
-    __builtin_nontemporal_store(v4f{f[4], f[5], f[6], f[7]}, (v4f*)(p + 4));
+    store16<NT>(p, make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3])));
+    store16<NT>(p + 4, make_uint4(__float_as_uint(f[4]), __float_as_uint(f[5]), __float_as_uint(f[6]), __float_as_uint(f[7])));
   }
 }
 

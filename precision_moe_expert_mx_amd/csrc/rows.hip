@@ -6,6 +6,10 @@
 //   backward:  dy[pos[t, k]] = w[t, k] dout[t],  dw[t, k] = sum_c dout[t, c] y[pos[t, k], c]
 //   The backward of dispatch is combine without weights.  A pos outside [0, M) is a pair that is not here: it adds
 //   nothing, gets no row, and its dw is 0.  Rows that no pair names stay as they were.
+//
+// Bound: HBM.  Every row is read once and written once; rows that go to the experts' products are stored so that they may
+// stay in the caches (8192 tokens with 6 rows of 2048: dispatch 46 -> 40 us, backward 82 -> 70; 131072 rows of 7168 the
+// same either way), the sums are not read again so soon and pass them by (46 us against 50).
 #include <algorithm>
 
 #include "layer.h"
@@ -22,19 +26,29 @@ template <> struct Unit<8> { typedef v2u_ type; };
 template <> struct Unit<4> { typedef uint32_t type; };
 template <> struct Unit<1> { typedef uint8_t type; };
 
-// A thread per unit of V bytes of a token's row, and per unit of S bytes of its scales.
+// Thread i's token and unit of `per` units a token, for fewer than 2^32 threads.
+__device__ __forceinline__ void split(uint32_t i, uint32_t per, int64_t& t, uint32_t& u) {
+  const uint32_t q = i / per;
+  t = q;
+  u = i - q * per;
+}
+
+// A thread per unit of V bytes of a token's row, and per unit of S bytes of its scales: a row is read once and written
+// `top` times.
 template <int V, int S>
-__global__ __launch_bounds__(NT) void dispatch_kernel(DispatchArgs p, int64_t units, int64_t per) {
-  const int64_t i = (int64_t)blockIdx.x * NT + threadIdx.x;
-  if (i >= p.T * per) return;
-  const int64_t t = i / per, u = i - t * per;
+__global__ __launch_bounds__(NT) void dispatch_kernel(DispatchArgs p, uint32_t units, uint32_t per) {
+  const uint32_t i = blockIdx.x * NT + threadIdx.x;
+  int64_t t;
+  uint32_t u;
+  split(i, per, t, u);
+  if (t >= p.T) return;
   const int32_t* pos = p.pos + t * p.top;
   if (u < units) {
     typedef typename Unit<V>::type T;
     const T v = __builtin_nontemporal_load((const T*)(p.x + t * p.row_bytes) + u);
     for (int k = 0; k < p.top; ++k) {
       const int64_t r = pos[k];
-      if (r >= 0 && r < p.M) __builtin_nontemporal_store(v, (T*)(p.xr + r * p.row_bytes) + u);
+      if (r >= 0 && r < p.M) ((T*)(p.xr + r * p.row_bytes))[u] = v;
     }
   } else {
     typedef typename Unit<S>::type T;
@@ -46,65 +60,114 @@ __global__ __launch_bounds__(NT) void dispatch_kernel(DispatchArgs p, int64_t un
   }
 }
 
-// A thread per 8 elements of a token's sum.
+// A thread per 8 elements of a token's sum, the loads of K choices in flight together; BF16: y's type.
+template <int K, bool BF16>
 __global__ __launch_bounds__(NT) void combine_kernel(CombineArgs p) {
-  const int64_t i = (int64_t)blockIdx.x * NT + threadIdx.x, per = p.C / 8;
-  if (i >= p.T * per) return;
-  const int64_t t = i / per, c = 8 * (i - t * per);
-  float acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-  if (p.residual) {
-    Raw8<> r;
-    load8(r, p.residual, t * p.C + c, p.r_bf16);
-    to_float8(r, p.r_bf16, acc);
-  }
+  const uint32_t i = blockIdx.x * NT + threadIdx.x;
+  int64_t t;
+  uint32_t u;
+  split(i, (uint32_t)(p.C / 8), t, u);
+  if (t >= p.T) return;
+  const int64_t c = 8 * (int64_t)u, at = t * p.top;
+  Raw8<> res;
+  if (p.residual) load8(res, p.residual, t * p.C + c, p.r_bf16);
   float sum[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-  for (int k = 0; k < p.top; ++k) {
-    const int64_t r = p.pos[t * p.top + k];
-    if (r < 0 || r >= p.M) continue;
-    const float w = p.weights ? p.weights[t * p.top + k] : 1.0f;
-    Raw8<> y;
-    float f[8];
-    load8(y, p.y, r * p.C + c, p.y_bf16);
-    to_float8(y, p.y_bf16, f);
+  for (int k0 = 0; k0 < p.top; k0 += K) {
+    Raw8<BF16> y[K];
+    float w[K];
+    bool here[K];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) sum[e] = fmaf(w, f[e], sum[e]);
+    for (int k = 0; k < K; ++k) {
+      const int64_t r = k0 + k < p.top ? p.pos[at + k0 + k] : -1;
+      here[k] = r >= 0 && r < p.M;
+      w[k] = 1;
+      if (here[k]) {
+        load8(y[k], p.y, r * p.C + c, BF16);
+        if (p.weights) w[k] = p.weights[at + k0 + k];
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      if (!here[k]) continue;
+      float f[8];
+      to_float8(y[k], BF16, f);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sum[e] = fmaf(w[k], f[e], sum[e]);
+    }
   }
+  if (p.residual) {
+    float f[8];
+    to_float8(res, p.r_bf16, f);
 #pragma unroll
-  for (int e = 0; e < 8; ++e) acc[e] += sum[e];
-  store8(p.out, t * p.C + c, p.out_bf16, acc);
+    for (int e = 0; e < 8; ++e) sum[e] += f[e];
+  }
+  store8(p.out, t * p.C + c, p.out_bf16, sum);
 }
 
-// A wave per token.
+// WPT waves per token; a lane takes 8 elements of dout and of K rows of y at a time.  BF16: dout and y are bf16, else each is
+// what the arguments say.
+template <int WPT, int K, bool BF16>
 __global__ __launch_bounds__(NT) void combine_bwd_kernel(CombineBwdArgs p) {
-  const int lane = threadIdx.x & 63;
-  const int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (t >= p.T) return;
-  for (int k = 0; k < p.top; ++k) {
-    const int64_t r = p.pos[t * p.top + k];
-    const bool here = r >= 0 && r < p.M;
-    const float w = p.weights ? p.weights[t * p.top + k] : 1.0f;
-    float dot = 0;
-    if (here)
-      for (int64_t c = 8 * lane; c < p.C; c += 512) {
-        Raw8<> d, y;
-        float g[8], f[8];
-        load8<false>(d, p.dout, t * p.C + c, p.d_bf16);
-        to_float8(d, p.d_bf16, g);
-        if (p.dweights) {
-          load8(y, p.y, r * p.C + c, p.y_bf16);
-          to_float8(y, p.y_bf16, f);
+  __shared__ float red[NT / 64][K];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, sub = wave % WPT;
+  const int64_t t_raw = (int64_t)blockIdx.x * (NT / 64 / WPT) + wave / WPT;
+  if (WPT == 1 && t_raw >= p.T) return;
+  const int64_t t = min(t_raw, p.T - 1), at = t * p.top;     // (WPT 4: a block per token)
+  const bool d_bf16 = BF16 || p.d_bf16, y_bf16 = BF16 || p.y_bf16, dots = p.dweights != nullptr;
+  for (int k0 = 0; k0 < p.top; k0 += K) {
+    int64_t row[K];                          // or -1
+    float w[K], dot[K];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) dot = fmaf(g[e], f[e], dot);
+    for (int k = 0; k < K; ++k) {
+      const int64_t r = k0 + k < p.top ? p.pos[at + k0 + k] : -1;
+      row[k] = r < p.M ? r : -1;
+      w[k] = p.weights && row[k] >= 0 ? p.weights[at + k0 + k] : 1.0f;
+      dot[k] = 0;
+    }
+    for (int64_t c = 8 * (lane + 64 * sub); c < p.C; c += 512 * WPT) {
+      Raw8<BF16 ? 1 : kAny> d, y[K];
+      float g[8];
+      load8<false>(d, p.dout, t * p.C + c, d_bf16);
+      if (dots) {
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+          if (row[k] >= 0) load8(y[k], p.y, row[k] * p.C + c, y_bf16);
+      }
+      to_float8(d, d_bf16, g);
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        if (row[k] < 0) continue;
+        float f[8];
+        if (dots) {
+          to_float8(y[k], y_bf16, f);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) dot[k] = fmaf(g[e], f[e], dot[k]);
         }
         if (p.dy) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) g[e] *= w;
-          store8(p.dy, r * p.C + c, p.y_bf16, g);
+          for (int e = 0; e < 8; ++e) f[e] = w[k] * g[e];
+          store8<false>(p.dy, row[k] * p.C + c, y_bf16, f);
         }
       }
-    if (p.dweights) {
-      dot = wave_sum(dot);
-      if (lane == 0) p.dweights[t * p.top + k] = dot;
+    }
+    if (dots) {
+      float mine = 0;                              // lane k: the sum of choice k
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        const float s = wave_sum(dot[k]);
+        if (lane == k) mine = s;
+      }
+      if constexpr (WPT > 1) {
+        __syncthreads();
+        if (lane < K) red[wave][lane] = mine;
+        __syncthreads();
+        if (lane < K) {
+          mine = 0;
+#pragma unroll
+          for (int v = 0; v < WPT; ++v) mine += red[v][lane];
+        }
+      }
+      if (sub == 0 && lane < K && k0 + lane < p.top) p.dweights[at + k0 + lane] = mine;
     }
   }
 }
@@ -115,14 +178,15 @@ hipError_t launch_dispatch(const DispatchArgs& a, hipStream_t st) {
   const int v = a.row_bytes % 16 ? 8 : 16, s = a.scale_bytes % 4 ? 1 : 4;
   const int64_t units = a.row_bytes / v, per = units + (a.scales ? a.scale_bytes / s : 0);
   auto go = [&](auto kernel) {
-    const int64_t step = std::max<int64_t>(1, kMaxBlocks * NT / per);         // tokens of a launch
+    const int64_t step = std::max<int64_t>(1, kMaxBlocks * NT / per);         // tokens of a launch (fewer than 2^32 threads)
     for (int64_t t = 0; t < a.T; t += step) {
       DispatchArgs p = a;
       p.T = std::min(step, a.T - t);
       p.x += t * a.row_bytes;
       p.pos += t * a.top;
       if (a.scales) p.scales += t * a.scale_bytes;
-      hipLaunchKernelGGL(kernel, dim3((unsigned)((p.T * per + NT - 1) / NT)), dim3(NT), 0, st, p, units, per);
+      hipLaunchKernelGGL(kernel, dim3((unsigned)((p.T * per + NT - 1) / NT)), dim3(NT), 0, st, p, (uint32_t)units,
+                         (uint32_t)per);
     }
   };
   if (v == 16) s == 4 ? go(dispatch_kernel<16, 4>) : go(dispatch_kernel<16, 1>);
@@ -132,6 +196,8 @@ hipError_t launch_dispatch(const DispatchArgs& a, hipStream_t st) {
 
 hipError_t launch_combine_fwd(const CombineArgs& a, hipStream_t st) {
   const int64_t per = a.C / 8, step = std::max<int64_t>(1, kMaxBlocks * NT / per);
+  auto kernel = a.y_bf16 ? (a.top <= 4 ? combine_kernel<4, true> : combine_kernel<8, true>)
+                         : (a.top <= 4 ? combine_kernel<4, false> : combine_kernel<8, false>);
   for (int64_t t = 0; t < a.T; t += step) {
     CombineArgs p = a;
     p.T = std::min(step, a.T - t);
@@ -139,13 +205,21 @@ hipError_t launch_combine_fwd(const CombineArgs& a, hipStream_t st) {
     if (a.weights) p.weights += t * a.top;
     if (a.residual) p.residual = (const uint8_t*)a.residual + t * a.C * (a.r_bf16 ? 2 : 4);
     p.out = (uint8_t*)a.out + t * a.C * (a.out_bf16 ? 2 : 4);
-    hipLaunchKernelGGL(combine_kernel, dim3((unsigned)((p.T * per + NT - 1) / NT)), dim3(NT), 0, st, p);
+    hipLaunchKernelGGL(kernel, dim3((unsigned)((p.T * per + NT - 1) / NT)), dim3(NT), 0, st, p);
   }
   return hipGetLastError();
 }
 
 hipError_t launch_combine_bwd(const CombineBwdArgs& a, hipStream_t st) {
-  const int64_t step = 4 * kMaxBlocks;
+  // long rows over 4 waves (8192 tokens, 6 rows of 2048 each: 97 -> 82 us; rows of 1024: 55 -> 57)
+  const int wpt = a.C > 1024 ? 4 : 1;
+  const int64_t per = 4 / wpt, step = per * kMaxBlocks;
+  const bool bf16 = a.d_bf16 && a.y_bf16;
+  auto pick = [&](auto four, auto one) { return wpt == 4 ? four : one; };
+  auto kernel = a.top <= 4 ? (bf16 ? pick(combine_bwd_kernel<4, 4, true>, combine_bwd_kernel<1, 4, true>)
+                                   : pick(combine_bwd_kernel<4, 4, false>, combine_bwd_kernel<1, 4, false>))
+                           : (bf16 ? pick(combine_bwd_kernel<4, 8, true>, combine_bwd_kernel<1, 8, true>)
+                                   : pick(combine_bwd_kernel<4, 8, false>, combine_bwd_kernel<1, 8, false>));
   for (int64_t t = 0; t < a.T; t += step) {
     CombineBwdArgs p = a;
     p.T = std::min(step, a.T - t);
@@ -153,7 +227,7 @@ hipError_t launch_combine_bwd(const CombineBwdArgs& a, hipStream_t st) {
     if (a.weights) p.weights += t * a.top;
     if (a.dweights) p.dweights += t * a.top;
     p.dout = (const uint8_t*)a.dout + t * a.C * (a.d_bf16 ? 2 : 4);
-    hipLaunchKernelGGL(combine_bwd_kernel, dim3((unsigned)((p.T + 3) / 4)), dim3(NT), 0, st, p);
+    hipLaunchKernelGGL(kernel, dim3((unsigned)((p.T + per - 1) / per)), dim3(NT), 0, st, p);
   }
   return hipGetLastError();
 }
