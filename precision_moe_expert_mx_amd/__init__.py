@@ -663,9 +663,27 @@ def _run(name, tensors, stream, *args):
         stream = _C._cuda_getCurrentRawStream(index)
     elif not isinstance(stream, int):
         stream = stream.cuda_stream
-    status = getattr(lib(), name)(*args, stream)
+    status = (_entries.get(name) or _entry(name))(*args, stream)
     if status:
         _check(name, status)
+
+
+_entries = {}
+
+
+def _entry(name):
+    """Entry point `name` of the library, looked up once."""
+    return _entries.setdefault(name, getattr(lib(), name))
+
+
+def _out(t, name, shape, dtype, like, stream):
+    """An output: the tensor given, checked, or a new one."""
+    if t is not None:
+        _want(name, t, (dtype,), shape)
+        return t
+    if stream is None:
+        return like.new_empty(shape, dtype=dtype)
+    return _empty(shape, dtype, like, stream)
 
 
 def _want(name, t, dtypes, shape):
@@ -940,10 +958,7 @@ def _norm_inputs(x, w, residual, h, stream):
             raise ValueError("h goes with residual, and only with it")
         return (x, w), (x.data_ptr(), floats[x.dtype], None, 0, w.data_ptr(), floats[w.dtype], R, C), None
     _want("residual", residual, floats, (R, C))
-    if h is None:
-        h = _empty((R, C), residual.dtype, x, stream)
-    else:
-        _want("h", h, (residual.dtype,), (R, C))
+    h = _out(h, "h", (R, C), residual.dtype, x, stream)
     return (x, w, residual, h), (x.data_ptr(), floats[x.dtype], residual.data_ptr(), floats[residual.dtype],
                                  w.data_ptr(), floats[w.dtype], R, C), h
 
@@ -956,25 +971,18 @@ def rmsnorm_fwd(x, w, eps: float = 1e-6, residual=None, out_dtype: str = "bf16",
     C <= 32768."""
     tensors, args, h = _norm_inputs(x, w, residual, h, stream)
     tdt, cdt = _out_dtype(out_dtype)
-    if y is None:
-        y = _empty(x.shape, tdt, x, stream)
-    else:
-        _want("y", y, (tdt,), x.shape)
+    y = _out(y, "y", x.shape, tdt, x, stream)
     _run("rmsnorm_fwd", (*tensors, y), stream, *args, eps, y.data_ptr(), cdt, None if h is None else h.data_ptr())
     return y if h is None else (y, h)
 
 
 def _quantize_rmsnorm(name, x, w, eps, residual, with_y, q, s, h, y, stream, qdt, sdt, sshape):
     tensors, args, h = _norm_inputs(x, w, residual, h, stream)
-    q = _empty(x.shape, qdt, x, stream) if q is None else q
-    s = _empty(sshape, sdt, x, stream) if s is None else s
-    _want("q", q, (qdt,), x.shape)
-    _want("s", s, (sdt,), sshape)
+    q = _out(q, "q", x.shape, qdt, x, stream)
+    s = _out(s, "s", sshape, sdt, x, stream)
     tensors += (q, s)
     if y is not None or with_y:
-        bf16 = _torch().bfloat16
-        y = _empty(x.shape, bf16, x, stream) if y is None else y
-        _want("y", y, (bf16,), x.shape)
+        y = _out(y, "y", x.shape, _torch().bfloat16, x, stream)
         tensors += (y,)
     _run(name, tensors, stream, *args, eps, q.data_ptr(), s.data_ptr(), None if y is None else y.data_ptr(),
          None if h is None else h.data_ptr())
@@ -1014,18 +1022,12 @@ def rmsnorm_bwd(dy, h, w, eps: float = 1e-6, dres=None, dx=None, dw=None, need_d
     if dres is not None:
         _want("dres", dres, (h.dtype,), (R, C))
         tensors += (dres,)
-    if dx is None:
-        dx = _empty((R, C), h.dtype, h, stream)
-    else:
-        _want("dx", dx, (h.dtype,), (R, C))
+    dx = _out(dx, "dx", (R, C), h.dtype, h, stream)
     tensors += (dx,)
     ws = None
     if need_dw:
-        if dw is None:
-            dw = _empty((C,), torch.float32, h, stream)
-        else:
-            _want("dw", dw, (torch.float32,), (C,))
-        ws = _empty((max(0, lib().rmsnorm_bwd_workspace(R, C)),), torch.uint8, h, stream)
+        dw = _out(dw, "dw", (C,), torch.float32, h, stream)
+        ws = _out(None, "ws", (max(0, lib().rmsnorm_bwd_workspace(R, C)),), torch.uint8, h, stream)
         tensors += (dw,)
     elif dw is not None:
         raise ValueError("dw goes with need_dw")
@@ -1057,10 +1059,8 @@ def _route(name, logits, top, score, bias, groups, keep_groups, group_top, renor
     if valid is not None:
         _want("valid", valid, (torch.bool, torch.uint8), (T,))
         tensors += (valid,)
-    ids = _empty((T, top), torch.int32, logits, stream) if ids is None else ids
-    weights = _empty((T, top), torch.float32, logits, stream) if weights is None else weights
-    _want("ids", ids, (torch.int32,), (T, top))
-    _want("weights", weights, (torch.float32,), (T, top))
+    ids = _out(ids, "ids", (T, top), torch.int32, logits, stream)
+    weights = _out(weights, "weights", (T, top), torch.float32, logits, stream)
     _run(name, (*tensors, ids, weights, *sort[0]), stream, logits.data_ptr(), floats[logits.dtype],
          None if bias is None else bias.data_ptr(), None if valid is None else valid.data_ptr(), T, E, top, _score(score),
          groups, groups if keep_groups is None else keep_groups, group_top, int(renormalize), scale, ids.data_ptr(),
@@ -1084,14 +1084,11 @@ def moe_route_fwd(logits, top: int, score: str = "softmax", bias=None, groups: i
 
 def _sort_outputs(T, top, G, first, offs, row_idx, pos, like, stream):
     i32 = _torch().int32
-    offs = _empty((G + 1,), i32, like, stream) if offs is None else offs
-    row_idx = _empty((T * top,), i32, like, stream) if row_idx is None else row_idx
-    pos = _empty((T, top), i32, like, stream) if pos is None else pos
-    _want("offs", offs, (i32,), (G + 1,))
-    _want("row_idx", row_idx, (i32,), (T * top,))
-    _want("pos", pos, (i32,), (T, top))
+    offs = _out(offs, "offs", (G + 1,), i32, like, stream)
+    row_idx = _out(row_idx, "row_idx", (T * top,), i32, like, stream)
+    pos = _out(pos, "pos", (T, top), i32, like, stream)
     need = lib().moe_sort_workspace(T * top, G)
-    ws = _empty((need,), _torch().uint8, like, stream) if need > 0 else None
+    ws = _out(None, "ws", (need,), _torch().uint8, like, stream) if need > 0 else None
     return (offs, row_idx, pos), (G, first, offs.data_ptr(), row_idx.data_ptr(), pos.data_ptr(),
                                   None if ws is None else ws.data_ptr()), ws
 
@@ -1126,10 +1123,7 @@ def moe_route_bwd(dweights, ids, logits, score: str = "softmax", renormalize: bo
     T, E = _rows("logits", logits, floats)
     _want("ids", ids, (torch.int32,), (T, None))
     _want("dweights", dweights, (torch.float32,), ids.shape)
-    if dlogits is None:
-        dlogits = _empty((T, E), logits.dtype, logits, stream)
-    else:
-        _want("dlogits", dlogits, (logits.dtype,), (T, E))
+    dlogits = _out(dlogits, "dlogits", (T, E), logits.dtype, logits, stream)
     _run("moe_route_bwd", (dweights, ids, logits, dlogits), stream, dweights.data_ptr(), ids.data_ptr(), logits.data_ptr(),
          floats[logits.dtype], T, E, ids.shape[1], _score(score), int(renormalize), scale, dlogits.data_ptr())
     return dlogits
@@ -1153,10 +1147,7 @@ def moe_dispatch(x, pos, scales=None, rows: Optional[int] = None, xr=None, sr=No
     T, C = _rows("x", x, (torch.bfloat16, torch.float32, torch.int8, torch.uint8))
     top = _pairs(pos, None, T)
     M = (T * top if rows is None else rows) if xr is None else xr.shape[0]
-    if xr is None:
-        xr = _empty((M, C), x.dtype, x, stream)
-    else:
-        _want("xr", xr, (x.dtype,), (M, C))
+    xr = _out(xr, "xr", (M, C), x.dtype, x, stream)
     if scales is None:
         if sr is not None:
             raise ValueError("sr goes with scales")
@@ -1165,10 +1156,7 @@ def moe_dispatch(x, pos, scales=None, rows: Optional[int] = None, xr=None, sr=No
         return xr
     shape = scales.shape[1:]
     _want("scales", scales, (torch.float32, torch.uint8), (T, *shape))
-    if sr is None:
-        sr = _empty((M, *shape), scales.dtype, x, stream)
-    else:
-        _want("sr", sr, (scales.dtype,), (M, *shape))
+    sr = _out(sr, "sr", (M, *shape), scales.dtype, x, stream)
     _run("moe_dispatch", (x, pos, scales, xr, sr), stream, x.data_ptr(), C * x.element_size(), scales.data_ptr(),
          shape.numel() * scales.element_size(), pos.data_ptr(), T, top, M, xr.data_ptr(), sr.data_ptr())
     return xr, sr
@@ -1189,10 +1177,7 @@ def moe_combine_fwd(y, pos, weights=None, residual=None, out_dtype: str = "bf16"
     if residual is not None:
         _want("residual", residual, floats, (T, C))
         tensors += (residual,)
-    if out is None:
-        out = _empty((T, C), tdt, y, stream)
-    else:
-        _want("out", out, (tdt,), (T, C))
+    out = _out(out, "out", (T, C), tdt, y, stream)
     _run("moe_combine_fwd", (*tensors, out), stream, y.data_ptr(), floats[y.dtype], pos.data_ptr(),
          None if weights is None else weights.data_ptr(), None if residual is None else residual.data_ptr(),
          0 if residual is None else floats[residual.dtype], T, top, M, C, out.data_ptr(), cdt)
@@ -1221,16 +1206,15 @@ def moe_combine_bwd(dout, pos, weights=None, y=None, out_dtype: Optional[str] = 
         M, dt = y.shape[0], y.dtype
         if out_dtype is not None and _out_dtype(out_dtype)[0] != dt:
             raise TypeError(f"out_dtype: dy is of y's type, {dt}")
-        dweights = _empty((T, top), torch.float32, dout, stream)
+        dweights = _out(None, "dweights", (T, top), torch.float32, dout, stream)
         tensors += (y, dweights)
     else:
         M = (T * top if rows is None else rows) if dy is None else dy.shape[0]
         dt = _out_dtype("bf16" if out_dtype is None else out_dtype)[0] if dy is None or out_dtype is not None else dy.dtype
     if need_dy:
-        if dy is None:
-            dy = _empty((M, C), dt, dout, stream)
-        else:
-            _want("dy", dy, (dt,) if dt in floats else tuple(floats), (M, C))
+        if dt not in floats:
+            raise TypeError(f"dy: expected float32 or bfloat16, got {dt}")
+        dy = _out(dy, "dy", (M, C), dt, dout, stream)
         tensors += (dy,)
     elif dy is not None:
         raise ValueError("dy goes with need_dy")
