@@ -18,7 +18,7 @@ namespace {
 constexpr int kSortThreads = 1024, kSortWaves = kSortThreads / 64;
 constexpr int kSortChunk = 4096;                  // pairs that one block places without counts
 constexpr int kPlacePairs = 4096;                 // pairs of a block otherwise
-constexpr int kCountBlocks = 512;                 // blocks that count, unless their chunks pass 65535 pairs
+constexpr int kCountBlocks = 256;                 // blocks that count, unless their chunks pass 65535 pairs
 constexpr int kMaxExperts = 1024;
 
 __device__ __forceinline__ float load_logit(const void* base, int64_t at, bool bf16) {
@@ -418,7 +418,8 @@ __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(SortArgs p) {
 //   score is off by at most 30 * 2^-24 (its own exponential 3, the sum's terms and 22 additions): 40 steps.
 // Two experts in doubt are settled if they are alike (the same logit and bias: equal c, the index decides); a token that
 // has others, next to each other in its list or across its end, is evaluated in fp64 by its wave.
-constexpr int kRouteThreads = 512, kRouteWaves = kRouteThreads / 64;
+constexpr int kRouteThreads = 1024;               // at most
+constexpr int kHereWaves = 8;                     // of the block that sorts its own pairs
 
 template <int N>
 __device__ __forceinline__ void order2(uint32_t (&a)[N], int i, int j) {
@@ -531,7 +532,7 @@ struct Part {
   static __device__ __forceinline__ int expert(uint32_t k) { return (int)(kIndex - (k & kIndex)); }
   __device__ __forceinline__ float c_of(int j, bool sigmoid, const float* bias) const {
     if constexpr (!biased) return x[j];
-    return (sigmoid ? sigmoid32(x[j]) : relative_exp(x[j], mx) * (1.0f / total)) + bias[j];
+    return (sigmoid ? sigmoid32(x[j]) : __expf(x[j] - mx) * (1.0f / total)) + bias[j];
   }
   __device__ __forceinline__ void load(const RouteArgs& p, int64_t row, int at, const float* bias) {
     const int E = p.E;
@@ -541,12 +542,12 @@ struct Part {
 #pragma unroll
     for (int j = 0; j < NE; ++j) mx = fmaxf(mx, x[j]);       // (drops NaN)
     mx = max_over<L>(mx);
-    odd = mx == -__builtin_inff();
+    odd = !(fabsf(mx) < __builtin_inff());
     total = 1;
     if (!sigmoid && (biased || !p.renorm)) {
       float s = 0;
 #pragma unroll
-      for (int j = 0; j < NE; ++j) s += relative_exp(x[j], mx);        // (0 past E)
+      for (int j = 0; j < NE; ++j) s += __expf(x[j] - mx);   // (0 past E)
       total = sum_over<L>(s);
     }
     float c[NE], m = mx, step = (float)(1u << (SB - 4));
@@ -582,8 +583,7 @@ struct Part {
         const uint32_t u = __float_as_uint(v) >> 16;
         key[j] = ((u ^ ((u & 0x8000u) ? 0xFFFFu : 0x8000u)) << 16) | low;
       } else {
-        const float d = c[j] == m ? (float)kSteps : fmaxf(fmaf(c[j] - m, step, (float)kSteps), 0.0f);    // (a NaN: 0)
-        key[j] = (uint32_t)d << B | low;
+        key[j] = (uint32_t)fmaxf(fmaf(c[j] - m, step, (float)kSteps), 0.0f) << B | low;      // (a NaN: 0)
       }
       // (past E: -infinity, and a higher index than any expert's)
     }
@@ -724,14 +724,14 @@ template <int L, int NE, int LS, int KIND>
 __global__ __launch_bounds__(kRouteThreads) __attribute__((amdgpu_waves_per_eu(4))) void route_kernel(RouteArgs p, SortArgs q, int mode, int iters) {
   typedef Part<L, NE, KIND> P;
   constexpr int TPW = 64 / L;
-  constexpr int kTokens = kRouteWaves * TPW;       // of the block at a time
+  const int threads = blockDim.x, tokens = threads / L;      // of the block at a time
   constexpr int kBatch = 64 / TPW;                 // rounds whose tokens in doubt have a bit each
   extern __shared__ int32_t cnt[];                 // the counts, or the ids and what places them
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, sub = lane & (L - 1);
   const int E = p.E, top = p.top, at = sub * NE;
   const bool bf16 = P::is_bf16(p), sigmoid = p.sigmoid, chosen = sub < top;
   if (mode == kCount) {
-    for (int e = threadIdx.x; e <= q.G; e += kRouteThreads) cnt[e] = 0;
+    for (int e = threadIdx.x; e <= q.G; e += threads) cnt[e] = 0;
     __syncthreads();
   }
   float bias[P::biased ? NE : 1];
@@ -739,7 +739,7 @@ __global__ __launch_bounds__(kRouteThreads) __attribute__((amdgpu_waves_per_eu(4
 #pragma unroll
     for (int j = 0; j < NE; ++j) bias[j] = at + j < E ? p.bias[at + j] : 0.0f;
   }
-  const int64_t first = (int64_t)blockIdx.x * iters * kTokens + wave * TPW + lane / L;       // token of round 0
+  const int64_t first = (int64_t)blockIdx.x * iters * tokens + wave * TPW + lane / L;       // token of round 0
   // a token's choices, with their logits and its softmax
   auto write = [&](int64_t t, bool live, int id, float xk, float mx, float total) {
     float w;
@@ -769,7 +769,7 @@ __global__ __launch_bounds__(kRouteThreads) __attribute__((amdgpu_waves_per_eu(4
   for (int it0 = 0; it0 < iters; it0 += kBatch) {
     uint64_t later = 0;                            // tokens in doubt, TPW bits per round
     for (int it = it0; it < min(it0 + kBatch, iters); ++it) {
-      const int64_t t = first + (int64_t)it * kTokens, tr = min(t, p.T - 1);
+      const int64_t t = first + (int64_t)it * tokens, tr = min(t, p.T - 1);
       if (t - lane / L >= p.T) break;
       const bool live = t < p.T && (!p.valid || p.valid[tr]);
       P part;
@@ -812,16 +812,20 @@ __global__ __launch_bounds__(kRouteThreads) __attribute__((amdgpu_waves_per_eu(4
         const uint32_t q_prev = (uint32_t)__shfl_up((int)q_mine, 1, 64);
         const float x_prev = __shfl_up(xk, 1, 64), b_prev = __shfl_up(bk, 1, 64);
         doubt |= chosen && sub > 0 && q_prev - q_mine <= within && !(x_prev == xk && b_prev == bk);
-        // the end of the list: as many experts as are chosen, apart from those like the last
-        const uint32_t bar = q_last > within ? q_last - within : 0;
-        int extra = chosen && !(xk == xl && bk == bl) ? -1 : 0;
+        // the end of the list: no more experts than are chosen, or the others are like the last
+        const uint32_t bar = q_last > within ? (q_last - within) << B : 0;
+        int n = 0;
 #pragma unroll
-        for (int j = 0; j < NE; ++j)
-          extra += kept && (part.key[j] >> B) >= bar &&
-                           !(part.x[j] == xl && (!P::biased || bias[P::biased ? j : 0] == bl))
-                       ? 1
-                       : 0;
-        doubt |= sum_over<L>((float)extra) != 0.0f || q_last == 0;     // (as all of -infinity are)
+        for (int j = 0; j < NE; ++j) n += part.key[j] >= bar ? 1 : 0;
+        const bool more = sum_over<L>(kept ? (float)n : 0.0f) != (float)top;
+        if (__ballot(more)) {
+          int extra = chosen && !(xk == xl && bk == bl) ? -1 : 0;
+#pragma unroll
+          for (int j = 0; j < NE; ++j)
+            extra += kept && part.key[j] >= bar && !(part.x[j] == xl && (!P::biased || bias[P::biased ? j : 0] == bl)) ? 1 : 0;
+          doubt |= sum_over<L>((float)extra) != 0.0f;
+        }
+        doubt |= q_last == 0;                      // (as all of -infinity are)
       } else {
         doubt |= last == 0;
       }
@@ -842,7 +846,7 @@ __global__ __launch_bounds__(kRouteThreads) __attribute__((amdgpu_waves_per_eu(4
         if (later) {
           const int bit = __builtin_ctzll(later);
           if (lane / L == k) {
-            t = first - lane / L + (int64_t)(it0 + bit / TPW) * kTokens + bit % TPW;
+            t = first - lane / L + (int64_t)(it0 + bit / TPW) * tokens + bit % TPW;
             real = true;
           }
           later &= later - 1;
@@ -866,10 +870,10 @@ __global__ __launch_bounds__(kRouteThreads) __attribute__((amdgpu_waves_per_eu(4
   }
   if (mode == kCount) {
     __syncthreads();
-    for (int e = threadIdx.x; e <= q.G; e += kRouteThreads) q.ws[blockIdx.x * count_pitch(q.G) + e] = (uint16_t)cnt[e];
+    for (int e = threadIdx.x; e <= q.G; e += threads) q.ws[blockIdx.x * count_pitch(q.G) + e] = (uint16_t)cnt[e];
   } else if (mode == kSortHere) {
     __syncthreads();
-    place<kRouteWaves, false>(q, cnt, 0, q.P, 0, true, PlaceLds<kRouteWaves>(cnt + q.P, q.G + 1));
+    place<kHereWaves, false>(q, cnt, 0, q.P, 0, true, PlaceLds<kHereWaves>(cnt + q.P, q.G + 1));
   }
 }
 
@@ -991,13 +995,16 @@ RouteShape route_shape(const RouteArgs& a) {
   return s;
 }
 
+// Shared memory of a block that sorts its own pairs.
+size_t here_bytes(const SortArgs& q) { return 4 * (q.P + PlaceLds<kHereWaves>::words(q.G + 1)); }
+
 template <int L, int NE>
-void go_route(const RouteArgs& a, const SortArgs& q, int mode, int iters, unsigned blocks, hipStream_t st) {
+void go_route(const RouteArgs& a, const SortArgs& q, int mode, int iters, unsigned blocks, int threads, hipStream_t st) {
   size_t lds = 0;
   if (mode == kCount) lds = 4 * (q.G + 1);
-  if (mode == kSortHere) lds = 4 * (q.P + PlaceLds<kRouteWaves>::words(q.G + 1));
+  if (mode == kSortHere) lds = here_bytes(q);
   auto go = [&](auto kernel) {
-    hipLaunchKernelGGL(kernel, dim3(blocks), dim3(kRouteThreads), lds, st, a, q, mode, iters);
+    hipLaunchKernelGGL(kernel, dim3(blocks), dim3(threads), lds, st, a, q, mode, iters);
   };
   if (a.bias) a.top <= 8 ? go(route_kernel<L, NE, 8, kBiased>) : go(route_kernel<L, NE, 16, kBiased>);
   else if (a.bf16) a.top <= 8 ? go(route_kernel<L, NE, 8, kBf16>) : go(route_kernel<L, NE, 16, kBf16>);
@@ -1046,23 +1053,25 @@ hipError_t launch_route(const RouteArgs& a, const SortArgs* sort, hipStream_t st
   }
   SortArgs q = {};
   if (sort) q = *sort;
-  const int tokens = kRouteWaves * 64 / s.lanes;   // of a block at a time
-  const int64_t all = (a.T + tokens - 1) / tokens;
-  int mode = kNoSort;
+  // blocks of 4 waves, or of 8 or 16 where there would be more than kCountBlocks (one per CU) otherwise
+  int threads = 256, mode = kNoSort;
+  auto rounds = [&] { return (a.T + threads / s.lanes - 1) / (threads / s.lanes); };
+  while (threads < kRouteThreads && rounds() > kCountBlocks) threads *= 2;
   int64_t iters = 1;
-  if (sort && all <= 2) {
+  if (sort && a.T <= 2 * 64 * kHereWaves / s.lanes && here_bytes(q) <= 60000) {
     mode = kSortHere;
+    threads = 64 * kHereWaves;
     iters = 2;
   } else if (sort && q.P > kSortChunk) {
     mode = kCount;
-    iters = std::min<int64_t>((all + kCountBlocks - 1) / kCountBlocks, 65535 / (tokens * a.top));
+    iters = std::min<int64_t>((rounds() + kCountBlocks - 1) / kCountBlocks, 65535 / (threads / s.lanes * a.top));
   }
-  const int64_t blocks = std::max<int64_t>(1, (all + iters - 1) / iters);
+  const int64_t blocks = std::max<int64_t>(1, (rounds() + iters - 1) / iters);
   if (mode == kCount) {
-    q.chunk_pairs = (int)(tokens * iters * a.top);
+    q.chunk_pairs = (int)(threads / s.lanes * iters * a.top);
     q.chunks = (int)blocks;
   }
-  auto go = [&](auto f) { f(a, q, mode, (int)iters, (unsigned)blocks, st); };
+  auto go = [&](auto f) { f(a, q, mode, (int)iters, (unsigned)blocks, threads, st); };
   if (s.experts == 4) go(go_route<16, 4>);
   else if (s.experts == 8) go(go_route<16, 8>);
   else if (s.lanes == 16) go(go_route<16, 16>);
