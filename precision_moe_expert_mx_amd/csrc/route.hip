@@ -17,7 +17,7 @@ namespace {
 
 constexpr int kSortThreads = 1024, kSortWaves = kSortThreads / 64;
 constexpr int kSortChunk = 4096;                  // pairs that one block places without counts
-constexpr int kPlacePairs = 4096;                 // pairs of a block otherwise
+constexpr int kPlacePairs = 1024;                 // pairs of a block otherwise, if that makes at most kCountBlocks blocks
 constexpr int kCountBlocks = 256;                 // blocks that count, unless their chunks pass 65535 pairs
 constexpr int kMaxExperts = 1024;
 
@@ -273,22 +273,30 @@ __device__ __forceinline__ void place(const SortArgs& p, const int32_t* ids, int
   const int64_t per = (i1 - i0 + NT - 1) / NT * 64;          // pairs of a wave
   const int64_t w0 = min(i0 + wave * per, i1), w1 = min(w0 + per, i1);
   const bool held = per <= 64 * HELD;
-  int32_t b[HELD];                                           // buckets, -1 past the end
-  auto load = [&](int64_t at) {
+  int32_t b[HELD];                                           // ids, then buckets, -1 past the end
+  auto fetch = [&](int64_t at) {
 #pragma unroll
     for (int k = 0; k < HELD; ++k) {
       const int64_t i = at + 64 * k + lane;
-      b[k] = i < w1 ? bucket(p, ids[i - i0]) : -1;
+      b[k] = i < w1 ? ids[i - i0] : 0;
     }
   };
-  load(w0);
+  auto sort_in = [&](int64_t at) {
+#pragma unroll
+    for (int k = 0; k < HELD; ++k) b[k] = at + 64 * k + lane < w1 ? bucket(p, b[k]) : -1;
+  };
+  auto load = [&](int64_t at) {
+    fetch(at);
+    sort_in(at);
+  };
+  fetch(w0);
   for (int e = lane; e < nb; e += 64) s.next[wave * nb + e] = 0;
   if constexpr (COUNTED) {
-    for (int e = tid; e < (nb + 7) / 8 * 8; e += NT) s.before[e] = s.total[e] = 0;
-    __syncthreads();
-    // 8 counts per load, the chunks split over the block, 10 loads of a thread in flight
+    // 8 counts per load, the chunks split over the block, 10 loads of a thread in flight (with its ids')
     const int pitch = (int)count_pitch(p.G), cols = pitch / 8, parts = max(1, min(NT / cols, (p.chunks + 9) / 10));
     const int col = tid % cols, part = tid / cols;
+    for (int e = tid; e < 8 * cols; e += NT) s.before[e] = s.total[e] = 0;
+    __syncthreads();
     if (part < parts) {
       int32_t n0[8] = {0, 0, 0, 0, 0, 0, 0, 0}, n1[8] = {0, 0, 0, 0, 0, 0, 0, 0};       // before, all
       for (int k0 = part; k0 < p.chunks; k0 += 10 * parts) {
@@ -296,7 +304,7 @@ __device__ __forceinline__ void place(const SortArgs& p, const int32_t* ids, int
 #pragma unroll
         for (int i = 0; i < 10; ++i) {
           const int k = k0 + i * parts;
-          v[i] = k < p.chunks ? *(const uint4*)(p.ws + (int64_t)k * pitch + 8 * col) : make_uint4(0, 0, 0, 0);
+          v[i] = k < p.chunks ? *(const uint4*)(p.ws + (uint32_t)(k * pitch + 8 * col)) : make_uint4(0, 0, 0, 0);
         }
 #pragma unroll
         for (int i = 0; i < 10; ++i) {
@@ -318,6 +326,7 @@ __device__ __forceinline__ void place(const SortArgs& p, const int32_t* ids, int
       }
     }
   }
+  sort_in(w0);
   for (int64_t at = w0;;) {
 #pragma unroll
     for (int k = 0; k < HELD; ++k)
@@ -1012,8 +1021,7 @@ void go_route(const RouteArgs& a, const SortArgs& q, int mode, int iters, unsign
 }
 
 void launch_place(SortArgs q, hipStream_t st) {
-  // a block per 4096 pairs or so
-  q.block_chunks = q.chunks ? std::max(1, kPlacePairs / q.chunk_pairs) : 0;
+  q.block_chunks = q.chunks ? (int)std::max<int64_t>(1, std::max<int64_t>(kPlacePairs, q.P / kCountBlocks) / q.chunk_pairs) : 0;
   const unsigned blocks = q.chunks ? (unsigned)((q.chunks + q.block_chunks - 1) / q.block_chunks) : 1;
   hipLaunchKernelGGL(q.chunks ? sort_place_kernel<true> : sort_place_kernel<false>, dim3(blocks), dim3(kSortThreads), 0, st, q);
 }
