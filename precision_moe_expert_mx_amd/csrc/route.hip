@@ -493,15 +493,16 @@ __device__ __forceinline__ float sigmoid32(float x) { return __builtin_amdgcn_rc
 
 constexpr int log2_of(int n) { return n <= 1 ? 0 : 1 + log2_of(n / 2); }
 
-// N consecutive logits of a row from `at` on, those from E on -infinity.
+// N consecutive logits of a row from `at` on, those from `end` on -infinity.  whole: four at a time lie on 16 bytes in fp32, 8 in
+// bf16, and none of them is past the end alone.
 template <int N>
-__device__ __forceinline__ void load_logits(const void* base, int64_t row, int at, int E, bool bf16, float (&x)[N]) {
+__device__ __forceinline__ void load_logits(const void* base, int64_t row, int at, int end, bool whole, bool bf16, float (&x)[N]) {
   static_assert(N % 4 == 0, "");
-  if (E % 4 == 0) {                                // (rows of whole 16 bytes in fp32, 8 in bf16)
+  if (whole) {
 #pragma unroll
     for (int j = 0; j < N; j += 4) {
       uint4 v = make_uint4(0xFF800000u, 0xFF800000u, 0xFF800000u, 0xFF800000u);
-      if (at + j < E) {
+      if (at + j < end) {
         if (bf16) {
           const uint2 w = *(const uint2*)((const uint16_t*)base + row + at + j);
           v = make_uint4(w.x << 16, w.x & 0xFFFF0000u, w.y << 16, w.y & 0xFFFF0000u);
@@ -516,8 +517,29 @@ __device__ __forceinline__ void load_logits(const void* base, int64_t row, int a
     }
   } else {
 #pragma unroll
-    for (int j = 0; j < N; ++j) x[j] = at + j < E ? load_logit(base, row + at + j, bf16) : -__builtin_inff();
+    for (int j = 0; j < N; ++j) x[j] = at + j < end ? load_logit(base, row + at + j, bf16) : -__builtin_inff();
   }
+}
+
+// The experts of a token's lane `sub`: at .. end - 1, at most NE of them and of one group, which is that of `lanes` lanes (all
+// of them without groups).
+struct Span {
+  int at, end, lanes, group;
+  bool whole;                                      // for load_logits
+  bool ragged;                                     // some lanes before the last one have fewer than NE
+};
+template <int NE>
+__device__ __forceinline__ Span span_of(const RouteArgs& p, int sub) {
+  const int size = p.E / p.groups;
+  Span s;
+  s.lanes = (size + NE - 1) / NE;
+  s.group = sub / s.lanes;
+  const bool in = s.group < p.groups;
+  s.at = in ? s.group * size + (sub - s.group * s.lanes) * NE : p.E;
+  s.end = in ? min(s.at + NE, (s.group + 1) * size) : p.E;
+  s.whole = p.E % 4 == 0 && size % 4 == 0;
+  s.ragged = p.groups > 1 && size % NE;
+  return s;
 }
 
 enum SortMode { kNoSort = 0, kCount = 1, kSortHere = 2 };
@@ -543,10 +565,10 @@ struct Part {
     if constexpr (!biased) return x[j];
     return (sigmoid ? sigmoid32(x[j]) : __expf(x[j] - mx) * (1.0f / total)) + bias[j];
   }
-  __device__ __forceinline__ void load(const RouteArgs& p, int64_t row, int at, const float* bias) {
-    const int E = p.E;
+  __device__ __forceinline__ void load(const RouteArgs& p, int64_t row, const Span& span, const float* bias) {
+    const int at = span.at;
     const bool sigmoid = p.sigmoid;
-    load_logits<NE>(p.logits, row, at, E, is_bf16(p), x);
+    load_logits<NE>(p.logits, row, at, span.end, span.whole, is_bf16(p), x);
     mx = -__builtin_inff();
 #pragma unroll
     for (int j = 0; j < NE; ++j) mx = fmaxf(mx, x[j]);       // (drops NaN)
@@ -563,7 +585,7 @@ struct Part {
     if constexpr (biased) {
       far = 1;
       m = -__builtin_inff();
-      int n = E - at;                              // (not a constant of the tokens' loop: 16 masks would be kept)
+      int n = span.end - at;                       // (not a constant of the tokens' loop: 16 masks would be kept)
       asm("" : "+v"(n));
       float worst = 0;
 #pragma unroll
@@ -595,6 +617,12 @@ struct Part {
         key[j] = (uint32_t)fmaxf(fmaf(c[j] - m, step, (float)kSteps), 0.0f) << B | low;      // (a NaN: 0)
       }
       // (past E: -infinity, and a higher index than any expert's)
+    }
+    if (span.ragged) {                             // (past the end of a group: the index of one in the next)
+      int n = span.end - at;
+      asm("" : "+v"(n));
+#pragma unroll
+      for (int j = 0; j < NE; ++j) key[j] = j < n ? key[j] : 0;
     }
   }
   // The token's N largest keys in order, in every lane.
@@ -648,7 +676,9 @@ template <int L, int NE, int KIND>
 __device__ __forceinline__ int second_look(const RouteArgs& p, int64_t t, bool real) {
   typedef Part<L, NE, KIND> P;
   constexpr int W = 16;
-  const int lane = threadIdx.x & 63, sub = lane & (L - 1), lane0 = lane - sub, E = p.E, at = sub * NE, end = min(at + NE, E);
+  const int lane = threadIdx.x & 63, sub = lane & (L - 1), lane0 = lane - sub, E = p.E;
+  const Span span = span_of<NE>(p, sub);
+  const int at = span.at, end = span.end;
   const int64_t row = t * E;
   const bool bf16 = P::is_bf16(p), sigmoid = p.sigmoid;
   uint32_t entry, bar, behind;
@@ -658,10 +688,10 @@ __device__ __forceinline__ int second_look(const RouteArgs& p, int64_t t, bool r
     float bias[P::biased ? NE : 1];
     if constexpr (P::biased) {
 #pragma unroll
-      for (int j = 0; j < NE; ++j) bias[j] = at + j < E ? p.bias[at + j] : 0.0f;
+      for (int j = 0; j < NE; ++j) bias[j] = at + j < end ? p.bias[at + j] : -__builtin_inff();
     }
     P part;
-    part.load(p, row, at, bias);
+    part.load(p, row, span, bias);
     mx = part.mx;
     odd = part.odd;
     double sum = 1;
@@ -683,7 +713,7 @@ __device__ __forceinline__ int second_look(const RouteArgs& p, int64_t t, bool r
     };
     bool kept = true;
     if (p.groups > 1) {
-      const int size = E / p.groups, lanes = size / NE, g = sub / lanes;
+      const int size = E / p.groups, lanes = span.lanes, g = span.group;
       double g1 = -__builtin_inf(), g2 = g1;
 #pragma unroll 1
       for (int e = at; e < end; ++e) {
@@ -737,7 +767,8 @@ __global__ __launch_bounds__(kRouteThreads) __attribute__((amdgpu_waves_per_eu(4
   constexpr int kBatch = 64 / TPW;                 // rounds whose tokens in doubt have a bit each
   extern __shared__ int32_t cnt[];                 // the counts, or the ids and what places them
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, sub = lane & (L - 1);
-  const int E = p.E, top = p.top, at = sub * NE;
+  const int E = p.E, top = p.top;
+  const Span span = span_of<NE>(p, sub);
   const bool bf16 = P::is_bf16(p), sigmoid = p.sigmoid, chosen = sub < top;
   if (mode == kCount) {
     for (int e = threadIdx.x; e <= q.G; e += threads) cnt[e] = 0;
@@ -746,7 +777,7 @@ __global__ __launch_bounds__(kRouteThreads) __attribute__((amdgpu_waves_per_eu(4
   float bias[P::biased ? NE : 1];
   if constexpr (P::biased) {
 #pragma unroll
-    for (int j = 0; j < NE; ++j) bias[j] = at + j < E ? p.bias[at + j] : 0.0f;
+    for (int j = 0; j < NE; ++j) bias[j] = span.at + j < span.end ? p.bias[span.at + j] : -__builtin_inff();
   }
   const int64_t first = (int64_t)blockIdx.x * iters * tokens + wave * TPW + lane / L;       // token of round 0
   // a token's choices, with their logits and its softmax
@@ -782,11 +813,10 @@ __global__ __launch_bounds__(kRouteThreads) __attribute__((amdgpu_waves_per_eu(4
       if (t - lane / L >= p.T) break;
       const bool live = t < p.T && (!p.valid || p.valid[tr]);
       P part;
-      part.load(p, tr * E, at, bias);
+      part.load(p, tr * E, span, bias);
       bool doubt = part.odd, kept = true;
       if (p.groups > 1) {
-        // a group is the experts of `lanes` lanes
-        const int size = E / p.groups, lanes = size / NE, g = sub / lanes;
+        const int size = E / p.groups, lanes = span.lanes, g = span.group;
         float g1 = -__builtin_inff(), g2 = g1;
 #pragma unroll
         for (int j = 0; j < NE; ++j) {
@@ -802,7 +832,7 @@ __global__ __launch_bounds__(kRouteThreads) __attribute__((amdgpu_waves_per_eu(4
         for (int o = 0; o < p.groups; ++o) {
           const float other = __shfl(score, lane - sub + o * lanes, 64);
           rank += other > score || (other == score && o < g);
-          doubt |= tol >= 0 && at < E && o != g && !(fabsf(other - score) > tol && fabsf(other - score) < __builtin_inff());
+          doubt |= tol >= 0 && g < p.groups && o != g && !(fabsf(other - score) > tol && fabsf(other - score) < __builtin_inff());
         }
         kept = rank < p.keep;
       }
@@ -866,7 +896,7 @@ __global__ __launch_bounds__(kRouteThreads) __attribute__((amdgpu_waves_per_eu(4
       float mx = -__builtin_inff(), total = 1;
       if (!sigmoid && !p.renorm) {
         float x[NE], s = 0;
-        load_logits<NE>(p.logits, t * E, at, E, bf16, x);
+        load_logits<NE>(p.logits, t * E, span.at, span.end, span.whole, bf16, x);
 #pragma unroll
         for (int j = 0; j < NE; ++j) mx = fmaxf(mx, x[j]);
         mx = max_over<L>(mx);
@@ -915,7 +945,7 @@ __global__ __launch_bounds__(256) void route_bwd_kernel(RouteBwdArgs p) {
 #pragma unroll
     for (int j = 0; j < NE; j += 4) {
       float x[4];
-      load_logits<4>(p.logits, row, 4 * sub + L * j, E, bf16, x);
+      load_logits<4>(p.logits, row, 4 * sub + L * j, E, whole, bf16, x);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         o[j + i] = x[i];
@@ -993,15 +1023,16 @@ __global__ __launch_bounds__(256) void route_bwd_kernel(RouteBwdArgs p) {
 
 namespace {
 
-// The launch of a lanes-per-token kernel; -1 lanes: the call is outside their range (more choices than a list holds, or groups
-// that are not whole lanes), and every token takes a wave.
+// The launch of a lanes-per-token kernel; -1 lanes: the call is outside their range (more choices than a list holds, or more than
+// 64 lanes of experts with every group on lanes of its own), and every token takes a wave.
 struct RouteShape {
   int lanes, experts;                              // lanes of a token, experts of a lane
 };
 RouteShape route_shape(const RouteArgs& a) {
-  RouteShape s = {a.E <= 256 ? 16 : a.E <= 512 ? 32 : 64, a.E <= 64 ? 4 : a.E <= 128 ? 8 : 16};
-  if (a.top > 16 || (a.groups > 1 && a.E / a.groups % s.experts)) s.lanes = -1;
-  return s;
+  if (a.top <= 16)
+    for (const RouteShape s : {RouteShape{16, 4}, {16, 8}, {16, 16}, {32, 16}, {64, 16}})
+      if ((a.E / a.groups + s.experts - 1) / s.experts * a.groups <= s.lanes) return s;
+  return {-1, 0};
 }
 
 // Shared memory of a block that sorts its own pairs.

@@ -104,6 +104,26 @@ def test_ties_go_to_the_lower_index(score, with_bias, E, groups, keep):
         check_route(m, logits.to(dt), 8, score, bias, groups, keep, 2 if with_bias else 1)
 
 
+@pytest.mark.parametrize("E,groups,keep,top", [(200, 4, 2, 8), (96, 8, 3, 10), (160, 8, 3, 6), (60, 60, 7, 5), (21, 3, 2, 4),
+                                               (30, 5, 1, 6), (510, 2, 1, 9), (77, 7, 7, 3), (900, 9, 4, 12), (14, 7, 3, 6),
+                                               (250, 25, 6, 16), (1000, 8, 2, 8)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_groups_of_any_size(E, groups, keep, top, score):
+    """Groups that end inside a lane's experts, with different and with few distinct values, some of them -infinity."""
+    m = require_gpu()
+    g = torch.Generator(device="cuda").manual_seed(E + groups)
+    T = 90
+    real = torch.randn((T, E), generator=g, device="cuda")
+    few = torch.randint(-2, 3, (T, E), generator=g, device="cuda").float()
+    masked = real.masked_fill(torch.rand((T, E), generator=g, device="cuda") < 0.5, -torch.inf)
+    bias = 0.2 * torch.randn(E, generator=g, device="cuda")
+    for x in (real, few, masked):
+        for dt in DT.values():
+            for b in (None, bias, torch.zeros_like(bias)):
+                for group_top in (1, 2):
+                    check_route(m, x.to(dt), top, score, b, groups, keep, group_top, renorm=group_top == 1)
+
+
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("with_bias", [False, True])
 def test_nearly_equal_scores(score, with_bias):
