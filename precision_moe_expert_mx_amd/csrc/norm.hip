@@ -155,11 +155,10 @@ __global__ __launch_bounds__(WPR > 4 ? 64 * WPR : 256) void rmsnorm_kernel(NormA
     }
     m = row_max_bits<WPR>(m, red32);
     const float amax = __uint_as_float(m);
-    const bool finite = m < 0x7F800000u && sum < __builtin_inf();
-    // the exact maximum, where the product was rounded or too small for that: of those that round to it
+    // the exact maximum, where the product was rounded: of those that round to it; of all where fp32 does not hold them
     double amax64 = (double)amax;
-    const bool tiny = amax < 1e-30f;
-    if (!exact || tiny) {
+    const bool outside = amax < 1e-30f || m >= 0x7F800000u;
+    if (!exact || outside) {
       double some = 0;
 #pragma unroll
       for (int k = 0; k < NCH; ++k) {
@@ -167,14 +166,18 @@ __global__ __launch_bounds__(WPR > 4 ? 64 * WPR : 256) void rmsnorm_kernel(NormA
         weight(k, w);
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-          if (__ballot(tiny || fabsf(h[k][e] * w[e]) == amax)) some = fmax(some, fabs((double)h[k][e] * (double)w[e]));
+          if (__ballot(outside || fabsf(h[k][e] * w[e]) == amax)) {
+            const double v = fabs((double)h[k][e] * (double)w[e]);
+            some = fmax(some, v == v ? v : __builtin_inf());
+          }
       }
       amax64 = row_max<WPR>(some, red);
     }
+    const bool finite = amax64 < __builtin_inf() && sum < __builtin_inf();
     const bool zero = amax64 == 0, dead = zero || !finite;
     if (live && l == 0) ((float*)p.s)[row] = !finite ? __builtin_nanf("") : zero ? 1.0f : (float)(amax64 * r64 / 127.0);
     // a factor of 0 gives codes 0 (a NaN too, in the sum below: its low byte is not used)
-    const float factor = dead || tiny ? 0.0f : 127.0f / amax;
+    const float factor = dead || outside ? 0.0f : 127.0f / amax;
     constexpr float kMagic = 12582912.0f;          // 1.5 * 2^23: the low byte of the sum is the code
 #pragma unroll
     for (int k = 0; k < NCH; ++k) {
@@ -189,7 +192,7 @@ __global__ __launch_bounds__(WPR > 4 ? 64 * WPR : 256) void rmsnorm_kernel(NormA
         if (__ballot(fabsf(fmaf(v, factor, -n)) > 0.5f - 4e-5f)) near |= 1u << e;
         code[e] = __float_as_uint(m);
       }
-      if (tiny) near = 0xFF;
+      if (outside) near = 0xFF;
       if (near && !dead) {                         // beside a border between two codes: of the exact quotient
 #pragma unroll
         for (int e = 0; e < 8; ++e)
@@ -277,8 +280,7 @@ __global__ __launch_bounds__(WPR > 4 ? 64 * WPR : 256) void rmsnorm_bwd_kernel(N
   constexpr int NT = WPR > 4 ? 64 * WPR : 256, RPB = NT / 64 / WPR;
   // where that fits into the registers of two waves per SIMD
   constexpr bool PREFETCH = BF16 && WPR <= 4;
-  __shared__ double red64[2][NT / 64];
-  __shared__ float red[2][NT / 64];
+  __shared__ double red[2][2][NT / 64];
   __shared__ float part[RPB > 1 ? RPB - 1 : 1][RPB > 1 ? 512 * WPR * NCH : 1];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, sub = wave / WPR;
   const int64_t C = p.C;
@@ -323,8 +325,7 @@ __global__ __launch_bounds__(WPR > 4 ? 64 * WPR : 256) void rmsnorm_bwd_kernel(N
   auto row = [&](Row& x, Row& next, int64_t r0) {
     const bool live = r0 + sub < p.R;
     if (PREFETCH && r0 + step < p.R) load(next, r0 + step);
-    double sum = 0;
-    float dot = 0;
+    double sum = 0, dot = 0;                       // (both of products that fp32 might not hold)
 #pragma unroll
     for (int k = 0; k < NCH; ++k) {
       float dy[8], h[8];
@@ -333,28 +334,28 @@ __global__ __launch_bounds__(WPR > 4 ? 64 * WPR : 256) void rmsnorm_bwd_kernel(N
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         sum = fma((double)h[e], (double)h[e], sum);
-        dot = fmaf(dy[e] * w[k][e], h[e], dot);
+        dot = fma((double)(dy[e] * w[k][e]), (double)h[e], dot);
       }
     }
     sum = wave_sum(sum);
     dot = wave_sum(dot);
     if constexpr (WPR > 1) {                       // (two rows' sums in turn: one barrier each)
       if (lane == 0) {
-        red64[parity][wave] = sum;
-        red[parity][wave] = dot;
+        red[parity][0][wave] = sum;
+        red[parity][1][wave] = dot;
       }
       __syncthreads();
       sum = 0;
       dot = 0;
 #pragma unroll
       for (int k = 0; k < WPR; ++k) {
-        sum += red64[parity][sub * WPR + k];
-        dot += red[parity][sub * WPR + k];
+        sum += red[parity][0][sub * WPR + k];
+        dot += red[parity][1][sub * WPR + k];
       }
       parity ^= 1;
     }
-    const float r = (float)rsqrt64(sum / (double)C + p.eps);
-    const float back = dot * r * r / (float)C;
+    const double r64 = rsqrt64(sum / (double)C + p.eps);
+    const float r = (float)r64, back = (float)(dot * r64 / (double)C);
     const int64_t at0 = min(r0 + sub, p.R - 1) * C;
 #pragma unroll
     for (int k = 0; k < NCH; ++k) {
@@ -368,8 +369,9 @@ __global__ __launch_bounds__(WPR > 4 ? 64 * WPR : 256) void rmsnorm_bwd_kernel(N
       to_float8(x.d[k], h_bf16, f);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        dx[e] = fmaf(r, fmaf(-h[e], back, dy[e] * w[k][e]), f[e]);
-        if (live) acc[k][e] = fmaf(dy[e], h[e] * r, acc[k][e]);
+        const float n = h[e] * r;
+        dx[e] = fmaf(r, fmaf(-n, back, dy[e] * w[k][e]), f[e]);
+        if (live) acc[k][e] = fmaf(dy[e], n, acc[k][e]);
       }
       if (live && (k < NCH - 1 || c < C)) store8(p.dx, at0 + c, h_bf16, dx);
     }

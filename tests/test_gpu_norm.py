@@ -137,6 +137,33 @@ def test_magnitudes():
             assert np.array_equal(q.cpu().numpy(), rq) and np.array_equal(s.cpu().numpy(), rs)
 
 
+def test_products_beyond_fp32():
+    """h w, and g h in the backward pass, pass the largest fp32 value where the results do not."""
+    m = require_gpu()
+    for C in (256, 4096):
+        x, _, w = make(4, C, "bf16", None, "f32", seed=4, std=1e37)
+        w *= 100
+        x[1] *= 1e-37
+        for wk in (w, w.to(DT["bf16"])):
+            q, s = m.int8_quantize_rmsnorm_rowwise(x, wk, 1e-6)
+            rq, rs = oracle.rmsnorm_int8(f64(x), f64(wk), 1e-6)
+            assert np.array_equal(q.cpu().numpy(), rq)
+            check(s, rs, 1.001 * U * rs, "scales")
+        wk = w.clone()
+        wk[3] = float("inf")
+        x[2, 3] = 0
+        q, s = m.int8_quantize_rmsnorm_rowwise(x, wk, 1e-6)
+        assert s.isnan().all() and not q.any()
+        x, _, w = make(4, C, "f32", None, "f32", seed=4, std=3e36)
+        dy = 20 * x / x.abs().max()                    # (a sum of products of one sign: it does pass it)
+        dx, dw = m.rmsnorm_bwd(dy, x, w, 1e-6)
+        args = f64(dy), f64(x), f64(w), 1e-6, None
+        rx, rw = oracle.rmsnorm_bwd(*args)
+        tx, tw = bwd_tolerance(*args, rx, "f32")
+        check(dx, rx, tx, "dx")
+        check(dw, rw, tw, "dw")
+
+
 def test_rows_with_nan_or_infinity():
     m = require_gpu()
     x, _, w = make(6, 1024, "bf16", None, "bf16")
