@@ -94,7 +94,11 @@ __global__ __launch_bounds__(WPR > 4 ? 64 * WPR : 256) void rmsnorm_kernel(NormA
   const int l = 64 * (wave % WPR) + lane;
   const bool x_bf16 = BF16 || p.x_bf16, r_bf16 = BF16 || p.r_bf16, w_bf16 = p.w_bf16;
 
-  float h[NCH][8];
+  Raw8<BF16> h[NCH];                               // (bf16 rows stay packed: half the registers)
+  Raw8<> wr[NCH];
+  float v[OUT == kNormInt8 ? NCH : 1][8];
+  uint32_t mk[NCH], m = 0;
+  double sum = 0;
   {
     Raw8<BF16 ? 1 : kAny> x[NCH], r[NCH];
 #pragma unroll
@@ -103,74 +107,90 @@ __global__ __launch_bounds__(WPR > 4 ? 64 * WPR : 256) void rmsnorm_kernel(NormA
       if (k == NCH - 1) {                          // (the others are whole)
         clear8(x[k]);
         clear8(r[k]);
+        clear8(wr[k]);
       }
       if (k < NCH - 1 || c < C) {
         load8(x[k], p.x, at0 + c, x_bf16);
         if (p.residual) load8(r[k], p.residual, at0 + c, r_bf16);
+        load8<false>(wr[k], p.w, c, w_bf16);
       }
     }
 #pragma unroll
     for (int k = 0; k < NCH; ++k) {
-      to_float8(x[k], x_bf16, h[k]);
+      float f[8];
+      to_float8(x[k], x_bf16, f);
       if (p.residual) {
-        float f[8];
-        to_float8(r[k], r_bf16, f);
+        float g[8];
+        to_float8(r[k], r_bf16, g);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          h[k][e] += f[e];
-          if (r_bf16) h[k][e] = (float)(__bf16)h[k][e];
+          f[e] += g[e];
+          if (r_bf16) f[e] = (float)(__bf16)f[e];
         }
         const int64_t c = 8 * (l + 64 * WPR * k);
-        if (live && c < C) store8(p.h, at0 + c, r_bf16, h[k]);
+        if (live && c < C) store8(p.h, at0 + c, r_bf16, f);
+      }
+      if constexpr (BF16) {
+        h[k].a = p.residual ? bf16_pack8(f) : x[k].a;
+      } else {
+        h[k].a = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+        h[k].b = make_uint4(__float_as_uint(f[4]), __float_as_uint(f[5]), __float_as_uint(f[6]), __float_as_uint(f[7]));
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sum = fma((double)f[e], (double)f[e], sum);
+      if constexpr (OUT == kNormInt8) {
+        // v = h w in fp32 (exact where both are bf16); the magnitude bits of a float order like its value, a NaN's above all
+        float w[8];
+        to_float8(wr[k], w_bf16, w);
+        mk[k] = 0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          v[k][e] = f[e] * w[e];
+          mk[k] = max(mk[k], __float_as_uint(v[k][e]) & 0x7FFFFFFFu);
+        }
+        m = max(m, mk[k]);
       }
     }
   }
-  double sum = 0;
-#pragma unroll
-  for (int k = 0; k < NCH; ++k)
-#pragma unroll
-    for (int e = 0; e < 8; ++e) sum = fma((double)h[k][e], (double)h[k][e], sum);
   sum = row_sum<WPR>(sum, red);
   const double r64 = rsqrt64(sum / (double)C + p.eps);
   const float r32 = (float)r64;
-
-  auto weight = [&](int k, float (&w)[8]) {
-    const int64_t c = 8 * (l + 64 * WPR * k);
-    Raw8<> t;
-    if (k == NCH - 1) clear8(t);
-    if (k < NCH - 1 || c < C) load8<false>(t, p.w, c, w_bf16);
-    to_float8(t, w_bf16, w);
+  // h and w of chunk k (again: unpacked where they are used, not kept)
+  auto values = [&](int k, float (&f)[8], float (&w)[8]) {
+    if constexpr (BF16) asm("" : "+v"(h[k].a.x), "+v"(h[k].a.y), "+v"(h[k].a.z), "+v"(h[k].a.w));
+    to_float8(h[k], BF16, f);
+    if constexpr (OUT == kNormInt8) {              // (seldom: from memory)
+      const int64_t c = 8 * (l + 64 * WPR * k);
+      Raw8<> t;
+      if (k == NCH - 1) clear8(t);
+      if (k < NCH - 1 || c < C) load8<false>(t, p.w, c, w_bf16);
+      to_float8(t, w_bf16, w);
+    } else {
+      to_float8(wr[k], w_bf16, w);
+    }
   };
 
   if constexpr (OUT == kNormInt8) {
-    // v = h w in fp32 (exact where both are bf16); the magnitude bits of a float order like its value, a NaN's above all
     const bool exact = w_bf16 && (p.residual ? r_bf16 : x_bf16);
-    uint32_t m = 0;
-#pragma unroll
-    for (int k = 0; k < NCH; ++k) {
-      float w[8];
-      weight(k, w);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) m = max(m, __float_as_uint(h[k][e] * w[e]) & 0x7FFFFFFFu);
-    }
     m = row_max_bits<WPR>(m, red32);
     const float amax = __uint_as_float(m);
-    // the exact maximum, where the product was rounded: of those that round to it; of all where fp32 does not hold them
+    // the exact maximum, where the product was rounded: of the lanes' eights with one that rounds to it; of all where fp32 does
+    // not hold them
     double amax64 = (double)amax;
     const bool outside = amax < 1e-30f || m >= 0x7F800000u;
     if (!exact || outside) {
       double some = 0;
 #pragma unroll
-      for (int k = 0; k < NCH; ++k) {
-        float w[8];
-        weight(k, w);
+      for (int k = 0; k < NCH; ++k)
+        if (__ballot(outside || mk[k] == m)) {
+          float f[8], w[8];
+          values(k, f, w);
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (__ballot(outside || fabsf(h[k][e] * w[e]) == amax)) {
-            const double v = fabs((double)h[k][e] * (double)w[e]);
-            some = fmax(some, v == v ? v : __builtin_inf());
+          for (int e = 0; e < 8; ++e) {
+            const double u = fabs((double)f[e] * (double)w[e]);
+            some = fmax(some, u == u ? u : __builtin_inf());
           }
-      }
+        }
       amax64 = row_max<WPR>(some, red);
     }
     const bool finite = amax64 < __builtin_inf() && sum < __builtin_inf();
@@ -179,24 +199,26 @@ __global__ __launch_bounds__(WPR > 4 ? 64 * WPR : 256) void rmsnorm_kernel(NormA
     // a factor of 0 gives codes 0 (a NaN too, in the sum below: its low byte is not used)
     const float factor = dead || outside ? 0.0f : 127.0f / amax;
     constexpr float kMagic = 12582912.0f;          // 1.5 * 2^23: the low byte of the sum is the code
+    constexpr float kNear = 0.5f - 4e-5f;
 #pragma unroll
     for (int k = 0; k < NCH; ++k) {
       const int64_t c = 8 * (l + 64 * WPR * k);
-      float w[8];
-      weight(k, w);
-      uint32_t code[8], near = 0;
+      uint32_t code[8];
+      float nearest = 0, off[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         // the product, the maximum, the factor and this sum: within 127 * 4 * 2^-24 = 3e-5 of the quotient
-        const float v = h[k][e] * w[e], m = fmaf(v, factor, kMagic), n = m - kMagic;
-        if (__ballot(fabsf(fmaf(v, factor, -n)) > 0.5f - 4e-5f)) near |= 1u << e;
-        code[e] = __float_as_uint(m);
+        const float q = fmaf(v[k][e], factor, kMagic), n = q - kMagic;
+        off[e] = fabsf(fmaf(v[k][e], factor, -n));
+        nearest = fmaxf(nearest, off[e]);
+        code[e] = __float_as_uint(q);
       }
-      if (outside) near = 0xFF;
-      if (near && !dead) {                         // beside a border between two codes: of the exact quotient
+      if (__ballot(outside || nearest > kNear) && !dead) {   // beside a border between two codes: of the exact quotient
+        float f[8], w[8];
+        values(k, f, w);
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-          if (near >> e & 1) code[e] = (uint32_t)(int)rint(127.0 * ((double)h[k][e] * (double)w[e]) / amax64);
+          if (outside || off[e] > kNear) code[e] = (uint32_t)(int)rint(127.0 * ((double)f[e] * (double)w[e]) / amax64);
       }
       if (live && c < C) {
         auto pack = [&](int e) {                   // the low bytes of four
@@ -205,9 +227,10 @@ __global__ __launch_bounds__(WPR > 4 ? 64 * WPR : 256) void rmsnorm_kernel(NormA
         };
         store8_nt((uint2*)((int8_t*)p.q + at0 + c), dead ? make_uint2(0, 0) : make_uint2(pack(0), pack(4)));
         if (p.y) {
-          float y[8];
+          float f[8], w[8], y[8];
+          values(k, f, w);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) y[e] = h[k][e] * r32 * w[e];
+          for (int e = 0; e < 8; ++e) y[e] = f[e] * r32 * w[e];
           store8(p.y, at0 + c, true, y);
         }
       }
@@ -220,24 +243,26 @@ __global__ __launch_bounds__(WPR > 4 ? 64 * WPR : 256) void rmsnorm_kernel(NormA
 #pragma unroll
     for (int k = 0; k < NCH; ++k) {
       const int64_t c = 8 * (l + 64 * WPR * k);
-      float w[8], o[8];
-      weight(k, w);
-      uint32_t m = 0, least = 0xFFFFFFFFu, nearest = 0xFFFFFFFFu;
+      float f[8], w[8], o[8], top = 0;
+      values(k, f, w);
+      uint32_t least = 0xFFFFFFFFu, nearest = 0xFFFFFFFFu;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        o[e] = h[k][e] * w[e] * r32;
-        const uint32_t u = __float_as_uint(o[e]) & 0x7FFFFFFFu;
-        m = max(m, u);
-        least = min(least, u - 1);                 // (a zero is no small value)
-        nearest = min(nearest, (u - (0x80000u - 4)) & 0xFFFFFu);
+        o[e] = f[e] * w[e] * r32;
+        const uint32_t u = __float_as_uint(o[e]);
+        top = fmaxf(top, fabsf(o[e]));
+        least = min(least, (u << 1) - 1);          // (without the sign; a zero is no small value)
+        nearest = min(nearest, (u << 12) - ((0x80000u - 4) << 12));        // (of the 20 bits)
       }
-      m = quad_max(m);                             // 4 lanes hold a block of 32
-      const bool again = nearest <= 8 || ((m + 4) & 0x7FFFFFu) <= 8 || m >= 0x7F800000u || (m != 0 && (m < 0x08000000u || least < m - 0x07000000u));
+      m = quad_max(__float_as_uint(top));           // 4 lanes hold a block of 32
+      const bool again = nearest <= 8u << 12 || ((m + 4) & 0x7FFFFFu) <= 8 || m >= 0x7F800000u ||
+                         (m != 0 && (m < 0x08000000u || least >> 1 < m - 0x07000000u));
       if (__ballot(again)) {
         m = 0;
+        values(k, f, w);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          o[e] = round_to_odd((double)h[k][e] * (double)w[e] * r64);
+          o[e] = round_to_odd((double)f[e] * (double)w[e] * r64);
           m = max(m, __float_as_uint(o[e]) & 0x7FFFFFFFu);
         }
         m = quad_max(m);
@@ -246,14 +271,22 @@ __global__ __launch_bounds__(WPR > 4 ? 64 * WPR : 256) void rmsnorm_kernel(NormA
       const float scale = __uint_as_float((uint32_t)(e8 + 127) << 23);
       const float lim = __uint_as_float(((uint32_t)(e8 + 135) << 23) | 0x600000u);   // 448 * 2^e8
       if (live && c < C) {
-        store8_nt((uint2*)((uint8_t*)p.q + at0 + c),
-                  make_uint2(cvt4_f32_e4m3_scaled(o[0], o[1], o[2], o[3], lim, scale),
-                             cvt4_f32_e4m3_scaled(o[4], o[5], o[6], o[7], lim, scale)));
+        uint32_t q[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          auto sat = [&](int e) { return __builtin_amdgcn_fmed3f(o[4 * i + e], -lim, lim); };
+          v2s b = v2s{0, 0};
+          b = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(b, sat(0), sat(1), scale, false);
+          b = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(b, sat(2), sat(3), scale, true);
+          q[i] = __builtin_bit_cast(uint32_t, b);
+        }
+        store8_nt((uint2*)((uint8_t*)p.q + at0 + c), make_uint2(q[0], q[1]));
         if ((lane & 3) == 0) ((uint8_t*)p.s)[row * (C / 32) + c / 32] = (uint8_t)(e8 + 127);
         if (p.y) {
           float y[8];
+          values(k, f, w);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) y[e] = h[k][e] * r32 * w[e];
+          for (int e = 0; e < 8; ++e) y[e] = f[e] * r32 * w[e];
           store8(p.y, at0 + c, true, y);
         }
       }
@@ -262,10 +295,10 @@ __global__ __launch_bounds__(WPR > 4 ? 64 * WPR : 256) void rmsnorm_kernel(NormA
 #pragma unroll
     for (int k = 0; k < NCH; ++k) {
       const int64_t c = 8 * (l + 64 * WPR * k);
-      float w[8], y[8];
-      weight(k, w);
+      float f[8], w[8], y[8];
+      values(k, f, w);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) y[e] = h[k][e] * r32 * w[e];
+      for (int e = 0; e < 8; ++e) y[e] = f[e] * r32 * w[e];
       if (live && c < C) store8(p.y, at0 + c, p.y_bf16, y);
     }
   }
