@@ -211,10 +211,11 @@ hipError_t launch_combine_fwd(const CombineArgs& a, hipStream_t st) {
 }
 
 hipError_t launch_combine_bwd(const CombineBwdArgs& a, hipStream_t st) {
-  // long rows over 4 waves (8192 tokens, 6 rows of 2048 each: 97 -> 82 us; rows of 1024: 55 -> 57)
-  const int wpt = a.C > 1024 ? 4 : 1;
-  const int64_t per = 4 / wpt, step = per * kMaxBlocks;
+  // long rows over 4 waves (bf16, 8192 tokens with 6 rows each of 2048: 97 -> 82 us; of 1408: 50 -> 55, of 1024: 55 -> 57; fp32,
+  // 5003 tokens with 3 rows of 1112: 44 -> 39, 8192 with 6 of 1280: 122 -> 131)
   const bool bf16 = a.d_bf16 && a.y_bf16;
+  const int wpt = a.C > (bf16 ? 1536 : 1024) ? 4 : 1;
+  const int64_t per = 4 / wpt, step = per * kMaxBlocks;
   auto pick = [&](auto four, auto one) { return wpt == 4 ? four : one; };
   auto kernel = a.top <= 4 ? (bf16 ? pick(combine_bwd_kernel<4, 4, true>, combine_bwd_kernel<1, 4, true>)
                                    : pick(combine_bwd_kernel<4, 4, false>, combine_bwd_kernel<1, 4, false>))
