@@ -8,7 +8,16 @@
 //   back:  g = dy w,  dx = r (g - h r^2 mean_c(g h)) + dres,  dw = sum over rows of dy h r
 //
 // The squares are summed in fp64, so that they neither overflow nor vanish and the codes are those of the
-// exact values.  8-bit codes are formed in one rounding from y, not from its bf16 value.
+// exact values.  8-bit codes are formed in one rounding from y, not from its bf16 value; y itself is fp32 (h r w, each product
+// rounded), rounded once more to bf16.
+//
+// Bound: HBM.  A row is read once and held in registers by one, four or sixteen waves, as it lies in memory (a lane with 32
+// elements then fits into 110 registers instead of 170, four waves per SIMD instead of two); no row comes from memory
+// twice.  65536 rows of 7168, bf16, in us and TB/s: y 311, 6.0; y and h of two inputs 640, 5.9; int8 310, 4.5 (with h 545, 6.0; with
+// fp32 weights 377: its exact maximum needs a second look); E4M3 348, 4.1 (with h 540, 6.1).  The two alone are bound by their
+// instructions (12 per code and 4 per square, at 4 clocks per wave), which is why codes come from fp32 and only what lies beside
+// a border between two codes is formed in fp64 (all in fp64: E4M3 of 8192 x 5120 with h 83 us, now 51).  A few rows
+// take 3.5 to 5 us, a launch and the chain of load, sum and store.
 #include <algorithm>
 
 #include "layer.h"
@@ -306,13 +315,15 @@ __global__ __launch_bounds__(WPR > 4 ? 64 * WPR : 256) void rmsnorm_kernel(NormA
 
 // ---- backward ----------------------------------------------------------------------------------
 // A block takes rows blockIdx.x, blockIdx.x + gridDim.x, ... (times its rows at once), keeps the weights and its part of
-// dw in registers, and writes that part to its row of the workspace; a second launch adds the parts up.
+// dw in registers, and writes that part to its row of the workspace; a second launch adds the parts up, in a fixed order (no
+// atomics: the same bits each time).  Bound: HBM, 65536 rows of 7168 with dres in 660 us (5.7 TB/s) and 5 us for the parts.
+// Two blocks of four waves per CU load one row while the other's sums are formed (512 blocks against 256 and 1024: 658, 755 and
+// 677 us there, 8192 x 5120 59, 73 and 63; a prefetch of the next row inside a block changed nothing, 658 and 662).  Blocks
+// of 16 waves fill a CU's registers by themselves (4096 x 16384: 256 blocks 96 us, 512 101).
 // BF16: dy, h and dres are bf16, else each is what the arguments say.
 template <int WPR, int NCH, bool BF16>
 __global__ __launch_bounds__(WPR > 4 ? 64 * WPR : 256) void rmsnorm_bwd_kernel(NormBwdArgs p) {
   constexpr int NT = WPR > 4 ? 64 * WPR : 256, RPB = NT / 64 / WPR;
-  // where that fits into the registers of two waves per SIMD
-  constexpr bool PREFETCH = BF16 && WPR <= 4;
   __shared__ double red[2][2][NT / 64];
   __shared__ float part[RPB > 1 ? RPB - 1 : 1][RPB > 1 ? 512 * WPR * NCH : 1];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, sub = wave / WPR;
@@ -330,11 +341,11 @@ __global__ __launch_bounds__(WPR > 4 ? 64 * WPR : 256) void rmsnorm_bwd_kernel(N
 #pragma unroll
     for (int e = 0; e < 8; ++e) acc[k][e] = 0;
   }
-  // a row's chunks as they lie in memory; the next row's are loaded while this one's sums are formed
+  // a row's chunks as they lie in memory
   struct Row {
     Raw8<BF16 ? 1 : kAny> a[NCH], b[NCH], d[NCH];
-  };
-  auto load = [&](Row& x, int64_t r0) {
+  } x;
+  auto load = [&](int64_t r0) {
     const int64_t at0 = min(r0 + sub, p.R - 1) * C;
 #pragma unroll
     for (int k = 0; k < NCH; ++k) {
@@ -355,9 +366,9 @@ __global__ __launch_bounds__(WPR > 4 ? 64 * WPR : 256) void rmsnorm_bwd_kernel(N
   };
   const int64_t step = (int64_t)gridDim.x * RPB;
   int parity = 0;
-  auto row = [&](Row& x, Row& next, int64_t r0) {
+  for (int64_t r0 = (int64_t)blockIdx.x * RPB; r0 < p.R; r0 += step) {
     const bool live = r0 + sub < p.R;
-    if (PREFETCH && r0 + step < p.R) load(next, r0 + step);
+    load(r0);
     double sum = 0, dot = 0;                       // (both of products that fp32 might not hold)
 #pragma unroll
     for (int k = 0; k < NCH; ++k) {
@@ -408,18 +419,6 @@ __global__ __launch_bounds__(WPR > 4 ? 64 * WPR : 256) void rmsnorm_bwd_kernel(N
       }
       if (live && (k < NCH - 1 || c < C)) store8(p.dx, at0 + c, h_bf16, dx);
     }
-    if (!PREFETCH && r0 + step < p.R) load(next, r0 + step);
-  };
-  int64_t r0 = (int64_t)blockIdx.x * RPB;
-  Row x, y;
-  load(x, r0);
-  if constexpr (PREFETCH) {
-    for (; r0 < p.R; r0 += 2 * step) {
-      row(x, y, r0);
-      if (r0 + step < p.R) row(y, x, r0 + step);
-    }
-  } else {
-    for (; r0 < p.R; r0 += step) row(x, x, r0);
   }
   if (!p.dw) return;
   if constexpr (RPB > 1) {
@@ -473,8 +472,6 @@ __global__ __launch_bounds__(1024) void column_sum_kernel(const float* ws, int r
   }
 }
 
-constexpr int kBwdBlocks = 512;
-
 // waves of a row and chunks per lane of the backward kernel
 int bwd_waves(int64_t C) { return C <= 2048 ? 1 : C <= 8192 ? 4 : 16; }
 
@@ -483,8 +480,9 @@ int bwd_waves(int64_t C) { return C <= 2048 ? 1 : C <= 8192 ? 4 : 16; }
 template <int OUT>
 static hipError_t launch_rmsnorm_out(const NormArgs& a, hipStream_t st) {
   const int64_t C = a.C;
-  // few rows: a row over 16 waves
-  const int wpr = C > 8192 || (a.R <= 512 && C > 2048) ? 16 : C > 2048 || (a.R <= 512 && C > 512) ? 4 : 1;
+  // A lane holds at most 32 elements.  Few rows go over four waves too (int8, rows of 2048: 512 of them 5.7 -> 4.5 us, 1024 of
+  // them 7.2 -> 5.7; 2048 rows to bf16 6.4 -> 7.2); sixteen are no faster than four there (64 rows of 7168: 5.0 and 5.2 us).
+  const int wpr = C > 8192 ? 16 : C > 2048 || (a.R <= 1024 && C > 512) ? 4 : 1;
   const int nch = (int)((C + 512 * wpr - 1) / (512 * wpr));
   const int64_t per = wpr == 1 ? 4 : 1;
   auto go = [&](auto kernel) {
@@ -516,8 +514,7 @@ static hipError_t launch_rmsnorm_out(const NormArgs& a, hipStream_t st) {
     else if (nch == 3) GO(4, 3);
     else GO(4, 4);
   } else {
-    if (nch == 1) GO(16, 1);
-    else if (nch == 2) GO(16, 2);
+    if (nch == 2) GO(16, 2);
     else if (nch == 3) GO(16, 3);
     else GO(16, 4);
   }
@@ -533,7 +530,7 @@ hipError_t launch_rmsnorm(int out, const NormArgs& a, hipStream_t st) {
 
 int64_t rmsnorm_bwd_rows(int64_t R, int64_t C) {
   const int per = bwd_waves(C) == 1 ? 4 : 1;
-  return std::min<int64_t>((R + per - 1) / per, kBwdBlocks);
+  return std::min<int64_t>((R + per - 1) / per, bwd_waves(C) == 16 ? 256 : 512);
 }
 
 hipError_t launch_rmsnorm_bwd(const NormBwdArgs& a, hipStream_t st) {
