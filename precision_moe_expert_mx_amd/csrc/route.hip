@@ -8,6 +8,12 @@
 //   how an exponential is rounded.
 //
 //   pairs (token, choice), in this order, sorted by expert (stable): offs, the token of each row, the row of each pair
+//
+// Bound: not HBM, but the instructions of the choice (with many tokens) and the chain of one token's steps (with few).  So
+// scores are fp32, several lanes take a token, keys are sorted in registers, and fp64 decides only what fp32 leaves in doubt (every
+// token in fp64, a wave each: 65536 tokens over 256 experts 228 us, now 28; their logits take 12 us to read).
+// 8192 tokens over 256 experts in 8 groups, sigmoid with a bias: 30 us, of which the second look of the few tokens in doubt is
+// half; 8 tokens of 64 experts, with the order of their rows: 5.4 us in one launch.
 #include <algorithm>
 
 #include "layer.h"
@@ -16,9 +22,13 @@ namespace mxmoe {
 namespace {
 
 constexpr int kSortThreads = 1024, kSortWaves = kSortThreads / 64;
-constexpr int kSortChunk = 4096;                  // pairs that one block places without counts
-constexpr int kPlacePairs = 1024;                 // pairs of a block otherwise, if that makes at most kCountBlocks blocks
-constexpr int kCountBlocks = 256;                 // blocks that count, unless their chunks pass 65535 pairs
+// Pairs that one block places without counts (4000 pairs: 5.7 us, against 2.2 and 6.9 in two launches; 8000: 9.0 against 2.6 and 7.0).
+constexpr int kSortChunk = 4096;
+// Pairs of a block otherwise, if that makes at most kCountBlocks blocks (65536 pairs over 256 experts: 8.8 us, 4096 per block 9.7).
+constexpr int kPlacePairs = 1024;
+// Blocks that count, unless their chunks pass 65535 pairs, one per CU: every block that places reads all counts.  65536 tokens
+// over 256 experts, routed and placed: 28 and 12 us; 128 blocks 47 and 11, 512 blocks 33 and 26.
+constexpr int kCountBlocks = 256;
 constexpr int kMaxExperts = 1024;
 
 __device__ __forceinline__ float load_logit(const void* base, int64_t at, bool bf16) {
@@ -1025,6 +1035,8 @@ namespace {
 
 // The launch of a lanes-per-token kernel; -1 lanes: the call is outside their range (more choices than a list holds, or more than
 // 64 lanes of experts with every group on lanes of its own), and every token takes a wave.
+// As few lanes as hold the experts at 16 each, and 16 lanes at least (8192 tokens over 256 experts: 16 lanes 9.9 us, 32 lanes
+// 11.7; 65536 tokens 28 and 53).  Lists of 8 for up to 8 choices, else of 16 (for 8 choices: 28 and 36).
 struct RouteShape {
   int lanes, experts;                              // lanes of a token, experts of a lane
 };
@@ -1092,15 +1104,17 @@ hipError_t launch_route(const RouteArgs& a, const SortArgs* sort, hipStream_t st
   }
   SortArgs q = {};
   if (sort) q = *sort;
-  // blocks of 4 waves, or of 8 or 16 where there would be more than kCountBlocks (one per CU) otherwise
+  // blocks of 4 waves, or of 8 or 16 where there would be more than kCountBlocks (one per CU) otherwise: few blocks to count and few
+  // counts to read back
   int threads = 256, mode = kNoSort;
   auto rounds = [&] { return (a.T + threads / s.lanes - 1) / (threads / s.lanes); };
   while (threads < kRouteThreads && rounds() > kCountBlocks) threads *= 2;
   int64_t iters = 1;
-  if (sort && a.T <= 2 * 64 * kHereWaves / s.lanes && here_bytes(q) <= 60000) {
+  // the tokens of one round of a block (8 of 64 experts: 5.7 us, against 3.6 and 3.5 for two launches, 8 of 256 7.3 against 4.6 and
+  // 4.0; in two rounds 64 of 256 took 11.2 against 5.4 and 4.4)
+  if (sort && a.T <= 64 * kHereWaves / s.lanes && here_bytes(q) <= 60000) {
     mode = kSortHere;
     threads = 64 * kHereWaves;
-    iters = 2;
   } else if (sort && q.P > kSortChunk) {
     mode = kCount;
     iters = std::min<int64_t>((rounds() + kCountBlocks - 1) / kCountBlocks, 65535 / (threads / s.lanes * a.top));
