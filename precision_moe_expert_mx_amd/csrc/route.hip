@@ -12,8 +12,8 @@
 // Bound: not HBM, but the instructions of the choice (with many tokens) and the chain of one token's steps (with few).  So
 // scores are fp32, several lanes take a token, keys are sorted in registers, and fp64 decides only what fp32 leaves in doubt (every
 // token in fp64, a wave each: 65536 tokens over 256 experts 228 us, now 28; their logits take 12 us to read).
-// 8192 tokens over 256 experts in 8 groups, sigmoid with a bias: 30 us, of which the second look of the few tokens in doubt is
-// half; 8 tokens of 64 experts, with the order of their rows: 5.4 us in one launch.
+// 8192 tokens over 256 experts in 8 groups, sigmoid with a bias: 22 us, of which the second look of the few tokens in doubt is
+// half (12 without it, timed alone); 8 tokens of 64 experts, with the order of their rows: 5.4 us in one launch.
 #include <algorithm>
 
 #include "layer.h"
@@ -431,13 +431,16 @@ __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(SortArgs p) {
 //   bf16 logits without a bias: the 16 bits of the logit, exact.
 //   fp32 logits without a bias: the difference to the largest in steps of 2^-20 (2^-18 for 1024 experts).  The steps keep the
 //   order, so only logits within one step are in doubt.
-//   with a bias: c from fp32, in steps of 2^-23 of the power of two above A = max(1, max|c|).  A sigmoid is off by at
-//   most 4 * 2^-24 (p (1 - p) times its exponential's 2 |x| + 2, one rounding of the sum, two of the reciprocal), the
-//   addition by A 2^-24: with the roundings of the difference 5 steps for each of two, so 16 are in doubt.  A softmax
-//   score is off by at most 30 * 2^-24 (its own exponential 3, the sum's terms and 22 additions): 40 steps.
+//   with a bias: c from fp32, in steps of 2^-23 of the power of two above A = max(largest p, max|c|), for a sigmoid
+//   max(1, max|c|).  A sigmoid is off by at most 4 * 2^-24 (p (1 - p) times its exponential's 2 |x| + 2, one rounding of
+//   the sum, two of the reciprocal), the addition by A 2^-24: with the roundings of the difference 5 steps for each of two, so 16
+//   are in doubt.  A softmax score is off by at most 30 * 2^-24 of the largest (its own exponential 3, the sum's terms and 22
+//   additions): 40 steps.
 // Two experts in doubt are settled if they are alike (the same logit and bias: equal c, the index decides); a token that
 // has others, next to each other in its list or across its end, is evaluated in fp64 by its wave.
-constexpr int kRouteThreads = 1024;               // at most
+// Threads of a block, at most: 16 waves of up to 128 registers, or with a bias 8 waves of more (with 128 they spill: 65536 tokens over
+// 256 experts 109 us, now 77; 8 tokens 8.6 and 5.9).
+constexpr int route_threads(bool biased) { return biased ? 512 : 1024; }
 constexpr int kHereWaves = 8;                     // of the block that sorts its own pairs
 
 template <int N>
@@ -564,7 +567,7 @@ struct Part {
   float x[NE];
   uint32_t key[NE];
   float mx, total;                                 // the largest logit; a softmax's sum (1 where it is not needed)
-  float far;                                       // biased: largest |c|, at least 1
+  float far;                                       // biased: A
   bool odd;                                        // a token that keys say nothing about
 
   static __device__ __forceinline__ bool is_bf16(const RouteArgs& p) { return biased ? p.bf16 : exact; }
@@ -593,7 +596,7 @@ struct Part {
     }
     float c[NE], m = mx, step = (float)(1u << (SB - 4));
     if constexpr (biased) {
-      far = 1;
+      far = sigmoid ? 1.0f : 1.0f / total;
       m = -__builtin_inff();
       int n = span.end - at;                       // (not a constant of the tokens' loop: 16 masks would be kept)
       asm("" : "+v"(n));
@@ -745,13 +748,14 @@ __device__ __forceinline__ int second_look(const RouteArgs& p, int64_t t, bool r
     behind = list[W - 1];
     const bool there = sub < W && entry != 0 && P::expert(entry) < E;
     const int ide = there ? P::expert(entry) : 0;
-    const double ce = in_fp64(ide);
+    const double ce = there ? in_fp64(ide) : -__builtin_inf();
+    const int ie = there ? ide : INT32_MAX;
     int rank = 0;
-#pragma unroll 1
+#pragma unroll 4
     for (int i = 0; i < W; ++i) {
       const double o = __shfl(ce, lane0 + i, 64);
-      const int io = __shfl(ide, lane0 + i, 64), to = __shfl((int)there, lane0 + i, 64);
-      rank += to && (o > ce || (o == ce && io < ide));
+      const int io = __shfl(ie, lane0 + i, 64);
+      rank += o > ce || (o == ce && io < ie);
     }
     // (entries that are not there are the last, so that every lane has a target of its own)
     entry = (uint32_t)__builtin_amdgcn_ds_permute(4 * (lane0 + (there ? rank : sub)), ide);
@@ -770,7 +774,7 @@ __device__ __forceinline__ int second_look(const RouteArgs& p, int64_t t, bool r
 }
 
 template <int L, int NE, int LS, int KIND>
-__global__ __launch_bounds__(kRouteThreads) __attribute__((amdgpu_waves_per_eu(4))) void route_kernel(RouteArgs p, SortArgs q, int mode, int iters) {
+__global__ __launch_bounds__(route_threads(KIND == kBiased)) void route_kernel(RouteArgs p, SortArgs q, int mode, int iters) {
   typedef Part<L, NE, KIND> P;
   constexpr int TPW = 64 / L;
   const int threads = blockDim.x, tokens = threads / L;      // of the block at a time
@@ -837,14 +841,18 @@ __global__ __launch_bounds__(kRouteThreads) __attribute__((amdgpu_waves_per_eu(4
         const bool two = p.group_top == 2 && size > 1;
         const float score = group_score(g1, g2, lane, sub, g, lanes, two);
         // biased values and sums are rounded (without a bias only sums are): what is nearer than that is in doubt
-        const float tol = P::biased ? 128 * 0x1p-24f * part.far : two ? 8 * 0x1p-24f * fmaxf(fabsf(g1), fabsf(g2)) : -1.0f;
         int rank = 0;
         for (int o = 0; o < p.groups; ++o) {
           const float other = __shfl(score, lane - sub + o * lanes, 64);
           rank += other > score || (other == score && o < g);
-          doubt |= tol >= 0 && g < p.groups && o != g && !(fabsf(other - score) > tol && fabsf(other - score) < __builtin_inff());
         }
         kept = rank < p.keep;
+        if (P::biased || two) {                    // (of the least that stays and the largest that does not)
+          const float stay = -max_over<L>(kept && g < p.groups ? -score : -__builtin_inff());
+          const float leave = max_over<L>(!kept && g < p.groups ? score : -__builtin_inff());
+          const float tol = P::biased ? 128 * 0x1p-24f * part.far : 8 * 0x1p-24f * fmaxf(fabsf(stay), leave == -__builtin_inff() ? 0.0f : fabsf(leave));
+          doubt |= p.keep < p.groups && !(stay - leave > tol);
+        }
       }
       uint32_t best[LS], mine, last;
       part.template largest<LS>(best, kept);
@@ -1108,7 +1116,7 @@ hipError_t launch_route(const RouteArgs& a, const SortArgs* sort, hipStream_t st
   // counts to read back
   int threads = 256, mode = kNoSort;
   auto rounds = [&] { return (a.T + threads / s.lanes - 1) / (threads / s.lanes); };
-  while (threads < kRouteThreads && rounds() > kCountBlocks) threads *= 2;
+  while (threads < route_threads(a.bias) && rounds() > kCountBlocks) threads *= 2;
   int64_t iters = 1;
   // the tokens of one round of a block (8 of 64 experts: 5.7 us, against 3.6 and 3.5 for two launches, 8 of 256 7.3 against 4.6 and
   // 4.0; in two rounds 64 of 256 took 11.2 against 5.4 and 4.4)
