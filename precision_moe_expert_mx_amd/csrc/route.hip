@@ -938,7 +938,8 @@ __global__ __launch_bounds__(route_threads(KIND == kBiased)) void route_kernel(R
 //   softmax, renormalised (w' = w / scale): dl_k = scale w'_k (dw_k - D),  D = sum_k w'_k dw_k, 0 elsewhere
 //   sigmoid, renormalised: the same times (1 - p_k);   sigmoid: dl_k = scale dw_k p_k (1 - p_k)
 //   softmax: dl_e = p_e (scale dw_e [e chosen] - scale sum_k p_k dw_k)
-// Bound: HBM; only the last reads more than the chosen logits.
+// Bound: HBM; only the last reads more than the chosen logits (65536 tokens, 256 experts in fp32: 25 us, 5.4 TB/s; a wave per token
+// took 64).
 template <int L, int NE>
 __global__ __launch_bounds__(256) void route_bwd_kernel(RouteBwdArgs p) {
   const int lane = threadIdx.x & 63, sub = lane & (L - 1), lane0 = lane - sub;

@@ -9,7 +9,8 @@
 //
 // Bound: HBM.  Every row is read once and written once; rows that go to the experts' products are stored so that they may
 // stay in the caches (8192 tokens with 6 rows of 2048: dispatch 46 -> 40 us, backward 82 -> 70; 131072 rows of 7168 the
-// same either way), the sums are not read again so soon and pass them by (46 us against 50).
+// same either way), the sums are not read again so soon and pass them by (46 us against 50).  16384 tokens with 8 rows of 7168:
+// sums onto the residual 385 us (6.1 TB/s), backward 785 (5.1); 8192 of them dispatched in 194 us (5.4).
 #include <algorithm>
 
 #include "layer.h"
