@@ -144,6 +144,20 @@ def test_nearly_equal_scores(score, with_bias):
 
 
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,top,groups,keep,group_top", [(64, 6, 1, None, 1), (256, 8, 1, None, 1), (256, 8, 8, 4, 2),
+                                                         (160, 6, 8, 3, 1), (1024, 12, 16, 4, 2)])
+def test_scores_that_the_bias_makes_nearly_equal(score, E, top, groups, keep, group_top):
+    """A bias that takes the first token's scores back to zero but for its own rounding, and tokens near that one: all
+    experts, and all groups, lie within the error of fp32, far above that of fp64 (their distances are about 2^-24 p / E)."""
+    m = require_gpu()
+    g = torch.Generator(device="cuda").manual_seed(E + groups)
+    first = torch.randn((1, E), generator=g, device="cuda")
+    bias = -torch.from_numpy(oracle.route_scores(f64(first), score)[0]).float().cuda()
+    near = first + torch.randn((40, E), generator=g, device="cuda") * torch.logspace(-8, -2, 40, device="cuda")[:, None]
+    check_route(m, torch.cat([first, near]), top, score, bias, groups, keep, group_top)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 def test_masks_infinities_and_padding(score):
     m = require_gpu()
     g = torch.Generator(device="cuda").manual_seed(8)
