@@ -430,7 +430,8 @@ __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(SortArgs p) {
 // per entry, fed by a lane permute), until all lanes of the token hold its LS >= top largest in order.
 //   bf16 logits without a bias: the 16 bits of the logit, exact.
 //   fp32 logits without a bias: the difference to the largest in steps of 2^-20 (2^-18 for 1024 experts).  The steps keep the
-//   order, so only logits within one step are in doubt.
+//   order, so only logits within one step are in doubt, and those that lie 16 or more below the largest: they share the least
+//   step, 1.  0 is the key of no expert.
 //   with a bias: c from fp32, in steps of 2^-23 of the power of two above A = max(largest p, max|c|), for a sigmoid
 //   max(1, max|c|).  A sigmoid is off by at most 4 * 2^-24 (p (1 - p) times its exponential's 2 |x| + 2, one rounding of
 //   the sum, two of the reciprocal), the addition by A 2^-24: with the roundings of the difference 5 steps for each of two, so 16
@@ -627,9 +628,9 @@ struct Part {
         const uint32_t u = __float_as_uint(v) >> 16;
         key[j] = ((u ^ ((u & 0x8000u) ? 0xFFFFu : 0x8000u)) << 16) | low;
       } else {
-        key[j] = (uint32_t)fmaxf(fmaf(c[j] - m, step, (float)kSteps), 0.0f) << B | low;      // (a NaN: 0)
+        key[j] = (uint32_t)fmaxf(fmaf(c[j] - m, step, (float)kSteps), 1.0f) << B | low;      // (a NaN: 1)
       }
-      // (past E: -infinity, and a higher index than any expert's)
+      // (past E: -infinity, and a higher index than any expert's.  No key is 0, which stands for an expert that is not there)
     }
     if (span.ragged) {                             // (past the end of a group: the index of one in the next)
       int n = span.end - at;
@@ -882,7 +883,7 @@ __global__ __launch_bounds__(route_threads(KIND == kBiased)) void route_kernel(R
             extra += kept && part.key[j] >= bar && !(part.x[j] == xl && (!P::biased || bias[P::biased ? j : 0] == bl)) ? 1 : 0;
           doubt |= sum_over<L>((float)extra) != 0.0f;
         }
-        doubt |= q_last == 0;                      // (as all of -infinity are)
+        doubt |= q_last <= 1;                      // (at the least step or cut off to it, as all of -infinity are)
       } else {
         doubt |= last == 0;
       }
