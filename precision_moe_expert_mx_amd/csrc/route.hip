@@ -794,7 +794,9 @@ __global__ __launch_bounds__(route_threads(KIND == kBiased)) void route_kernel(R
 #pragma unroll
     for (int j = 0; j < NE; ++j) bias[j] = span.at + j < span.end ? p.bias[span.at + j] : -__builtin_inff();
   }
-  const int64_t first = (int64_t)blockIdx.x * iters * tokens + wave * TPW + lane / L;       // token of round 0
+  // The wave's first token of round 0.  It is a scalar, and so are the end of the rounds and the mask of the tokens in doubt: a
+  // mask kept per lane makes the loop over them one of the execution mask, which a register spilled at its joins never ended.
+  const int64_t wave0 = (int64_t)blockIdx.x * iters * tokens + __builtin_amdgcn_readfirstlane(wave * TPW);
   // a token's choices, with their logits and its softmax
   auto write = [&](int64_t t, bool live, int id, float xk, float mx, float total) {
     float w;
@@ -824,8 +826,8 @@ __global__ __launch_bounds__(route_threads(KIND == kBiased)) void route_kernel(R
   for (int it0 = 0; it0 < iters; it0 += kBatch) {
     uint64_t later = 0;                            // tokens in doubt, TPW bits per round
     for (int it = it0; it < min(it0 + kBatch, iters); ++it) {
-      const int64_t t = first + (int64_t)it * tokens, tr = min(t, p.T - 1);
-      if (t - lane / L >= p.T) break;
+      const int64_t t0 = wave0 + (int64_t)it * tokens, t = t0 + lane / L, tr = min(t, p.T - 1);
+      if (t0 >= p.T) break;
       const bool live = t < p.T && (!p.valid || p.valid[tr]);
       P part;
       part.load(p, tr * E, span, bias);
@@ -904,7 +906,7 @@ __global__ __launch_bounds__(route_threads(KIND == kBiased)) void route_kernel(R
         if (later) {
           const int bit = __builtin_ctzll(later);
           if (lane / L == k) {
-            t = first - lane / L + (int64_t)(it0 + bit / TPW) * tokens + bit % TPW;
+            t = wave0 + (int64_t)(it0 + bit / TPW) * tokens + bit % TPW;
             real = true;
           }
           later &= later - 1;
