@@ -52,6 +52,12 @@ def route_scores(logits, score):
     return p
 
 
+def _chosen_scores(row, p, ids, score, renorm):
+    """Scores of a token's chosen experts; renormalised softmax scores are a softmax over the chosen, since e^x / sum over
+    all cancels to it."""
+    return route_scores(row[None, ids], score)[0] if renorm and score == "softmax" else p[ids]
+
+
 def route(logits, top, score="softmax", bias=None, groups=1, keep=None, group_top=1, renorm=True, scale=1.0, valid=None):
     """(ids int32 [T, top], weights float64 [T, top])."""
     T, E = logits.shape
@@ -68,7 +74,7 @@ def route(logits, top, score="softmax", bias=None, groups=1, keep=None, group_to
             order = sorted(range(groups), key=lambda g: (-best[g], g))[:groups if keep is None else keep]
             allowed = [e for g in order for e in range(g * size, (g + 1) * size)]
         ids[t] = sorted(allowed, key=lambda e: (-c[e], e))[:top]
-        sel = p[t, ids[t]]
+        sel = _chosen_scores(logits[t], p[t], ids[t], score, renorm)
         total = sel.sum() if renorm else 1.0
         w[t] = scale * sel / total if total > 0 else 0.0
     return ids, w
@@ -81,7 +87,7 @@ def route_bwd(dweights, ids, logits, score="softmax", renorm=True, scale=1.0):
     out = np.zeros((T, E))
     for t in range(T):
         here = [k for k in range(ids.shape[1]) if 0 <= ids[t, k] < E]
-        sel, dw = p[t, ids[t, here]], dweights[t, here]
+        sel, dw = _chosen_scores(logits[t], p[t], ids[t, here], score, renorm), dweights[t, here]
         total = sel.sum() if renorm else 1.0
         if not here or total == 0:
             continue

@@ -2,6 +2,7 @@
 import pytest
 import torch
 
+import oracle
 from gpu_util import require_gpu
 from test_gpu_route import check_route
 
@@ -35,3 +36,27 @@ def test_few_kept_experts_of_a_wide_spread(E, groups, keep, top, score):
         x[40:, E - size + 1:] -= 20.0
         for bias in (None, 0.1 * torch.randn(E, generator=g, device="cuda")):
             check_route(m, x, top, score, bias, groups, keep, 1 if bias is None else 2)
+
+
+@pytest.mark.parametrize("top", [3, 17])
+def test_softmax_weights_of_the_chosen(top):
+    """The largest logit is in a group that does not stay: the chosen ones' quotients remain, and their gradients."""
+    m = require_gpu()
+    g = torch.Generator(device="cuda").manual_seed(top)
+    x = torch.randn((5, 72), generator=g, device="cuda")
+    x[:, 0], x[:, 1:24] = torch.tensor([0.0, 60, 1000, 1e30, float("inf")]).cuda(), -1e38
+    dw = torch.randn((5, top), generator=g, device="cuda")
+    for bias in (None, torch.full((72,), -0.0, device="cuda")):
+        bias = bias if bias is None else bias.index_fill(0, torch.arange(24, device="cuda"), -10.0)
+        for dt in (torch.float32, torch.bfloat16):
+            z = x.to(dt)
+            if bias is None:
+                z[:, :24] = -1e38
+            ids, w, rid, rw = check_route(m, z, top, "softmax", bias, 3, 1)
+            assert (rid >= 24).all() and (rw > 0).all()
+            d = m.moe_route_bwd(dw, ids, z).double().cpu().numpy()
+            ref = oracle.route_bwd(dw.double().cpu().numpy(), rid, z.double().cpu().numpy())
+            # the quotients' error as in the forward pass, the dot product's of at most 17 terms, half a step of bf16
+            size = rw * (abs(dw.double().cpu().numpy()) + (rw * abs(dw.double().cpu().numpy())).sum(axis=1, keepdims=True))
+            tol = 300 * 2.0 ** -24 * size.max() + (2.0 ** -8 if dt == torch.bfloat16 else 2.0 ** -24) * abs(ref)
+            assert (abs(d - ref) <= tol).all()

@@ -126,3 +126,14 @@ def test_combine_against_torch():
     dy, dw, _ = oracle.combine_bwd(dout, pos, w, y, np.zeros_like(y))
     np.testing.assert_allclose(dy, ty.grad.numpy(), rtol=1e-12, atol=1e-15)
     np.testing.assert_allclose(dw, tw.grad.numpy(), rtol=1e-12, atol=1e-15)
+
+
+def test_softmax_weights_of_the_chosen():
+    """A logit in a group that does not stay is far larger than the chosen ones, or infinite: their quotients remain."""
+    for far in (60.0, 1000.0, np.inf):
+        x = np.array([[far, -np.inf, 1.0, 3.0]])
+        ids, w = oracle.route(x, 2, "softmax", np.array([-np.inf, -np.inf, 0, 0.5]))
+        assert ids.tolist() == [[3, 2]]
+        np.testing.assert_allclose(w, [[1 / (1 + np.exp(-2.0)), 1 / (1 + np.exp(2.0))]], rtol=1e-12)
+        d = oracle.route_bwd(np.array([[1.0, 0.0]]), ids, x)
+        np.testing.assert_allclose(d, [[0, 0, -w[0, 0] * w[0, 1], w[0, 0] * w[0, 1]]], rtol=1e-12)
