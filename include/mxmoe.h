@@ -593,7 +593,8 @@ mxmoe_status rmsnorm_bwd(const void* dy, mxmoe_dtype dydt, const void* h, mxmoe_
  *   weights f32 [T, top] = scale * p of the chosen, divided by their sum if renormalize (0 where that sum is 0)
  *   (softmax, renormalised: a softmax over the chosen logits, also where one that is not chosen is infinitely larger)
  * Both comparisons are those of fp64 values.  A logit of -infinity is an expert with p = 0.  A NaN
- * ranks last (every c of a row of softmax scores with a bias is one if a logit is) and shows in the weights that contain it.  valid (bytes [T], or NULL): tokens with 0 are padding, with ids -1 and weights 0.
+ * ranks last (every c of a row of softmax scores with a bias is one if a logit is; a group's sum of +infinity and -infinity
+ * is one) and shows in the weights that contain it.  valid (bytes [T], or NULL): tokens with 0 are padding, with ids -1 and weights 0.
  * 1 <= E <= 1024, 1 <= top <= 64, top <= E / groups * keep_groups, groups <= 64, T * top < 2^31.
  *
  * moe_sort: the chosen pairs in the order of their experts, for the `G` experts first .. first + G - 1 that are

@@ -70,7 +70,9 @@ def route(logits, top, score="softmax", bias=None, groups=1, keep=None, group_to
         c = logits[t] if bias is None else p[t] + bias
         allowed = range(E)
         if groups > 1:
-            best = [sum(sorted(c[g * size:(g + 1) * size])[-group_top:]) for g in range(groups)]
+            with np.errstate(invalid="ignore"):
+                best = [sum(sorted(c[g * size:(g + 1) * size])[-group_top:]) for g in range(groups)]
+            best = [-np.inf if v != v else v for v in best]
             order = sorted(range(groups), key=lambda g: (-best[g], g))[:groups if keep is None else keep]
             allowed = [e for g in order for e in range(g * size, (g + 1) * size)]
         ids[t] = sorted(allowed, key=lambda e: (-c[e], e))[:top]

@@ -102,7 +102,8 @@ __device__ __forceinline__ Choice route_in_fp64(const RouteArgs& p, int64_t t, d
         g2 = fmax(g2, fmin(g1, v));
         g1 = fmax(g1, v);
       }
-    const double mine = p.group_top == 2 && size > 1 ? g1 + g2 : g1;
+    double mine = p.group_top == 2 && size > 1 ? g1 + g2 : g1;
+    if (!(mine == mine)) mine = -__builtin_inf();  // (infinity - infinity)
     int rank = 0;
     for (int g = 0; g < p.groups; ++g) {
       const double other = __shfl(mine, g, 64);
@@ -198,7 +199,8 @@ __device__ __forceinline__ int route_again(const RouteArgs& p, int64_t t) {
         g2 = fmax(g2, fmin(g1, v));
         g1 = fmax(g1, v);
       }
-    const double mine = p.group_top == 2 && size > 1 ? g1 + g2 : g1;
+    double mine = p.group_top == 2 && size > 1 ? g1 + g2 : g1;
+    if (!(mine == mine)) mine = -__builtin_inf();  // (infinity - infinity)
     int rank = 0;
 #pragma unroll 1
     for (int g = 0; g < p.groups; ++g) {

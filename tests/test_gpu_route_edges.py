@@ -60,3 +60,24 @@ def test_softmax_weights_of_the_chosen(top):
             size = rw * (abs(dw.double().cpu().numpy()) + (rw * abs(dw.double().cpu().numpy())).sum(axis=1, keepdims=True))
             tol = 300 * 2.0 ** -24 * size.max() + (2.0 ** -8 if dt == torch.bfloat16 else 2.0 ** -24) * abs(ref)
             assert (abs(d - ref) <= tol).all()
+
+
+@pytest.mark.parametrize("E,groups,keep,top", [(64, 8, 3, 6), (64, 8, 3, 18), (60, 5, 2, 7), (1024, 64, 4, 12)])
+def test_groups_of_both_infinities(E, groups, keep, top):
+    """A group whose two best are +infinity and -infinity has no sum: it ranks last, and only `keep` groups stay."""
+    m = require_gpu()
+    inf = float("inf")
+    size = E // groups
+    g = torch.Generator(device="cuda").manual_seed(E)
+    x = torch.randn((6, E), generator=g, device="cuda")
+    x[:, size:2 * size] = -inf
+    x[1:, size + 1] = inf                              # +inf and -inf in group 1
+    x[2:, 0], x[2:, 1:size] = inf, -inf                # and in group 0
+    x[4, 2 * size:] = -inf                             # (nothing else but masked ones)
+    for dt in (torch.float32, torch.bfloat16):
+        for score in ("softmax", "sigmoid"):
+            check_route(m, x[[0, 1, 2, 3, 5]].to(dt), top, score, None, groups, keep, 2)
+            ids, w, rid, rw = check_route(m, x[4:5].to(dt), top, score, None, groups, keep, 2)
+    bias = 0.1 * torch.randn(E, generator=g, device="cuda")
+    bias[:size], bias[0] = -inf, inf                   # the same by the bias
+    check_route(m, torch.randn((6, E), generator=g, device="cuda"), top, "sigmoid", bias, groups, keep, 2)
