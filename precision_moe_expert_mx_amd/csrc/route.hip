@@ -1077,6 +1077,20 @@ void go_route(const RouteArgs& a, const SortArgs& q, int mode, int iters, unsign
   else a.top <= 8 ? go(route_kernel<L, NE, 8, kF32>) : go(route_kernel<L, NE, 16, kF32>);
 }
 
+// The launch of every `step` tokens (a launch has fewer than 2^32 threads).
+template <typename F>
+void in_slices(const RouteArgs& a, int64_t step, F launch) {
+  for (int64_t t = 0; t < a.T; t += step) {
+    RouteArgs p = a;
+    p.T = std::min(step, a.T - t);
+    p.logits = (const uint8_t*)a.logits + t * a.E * (a.bf16 ? 2 : 4);
+    if (a.valid) p.valid += t;
+    p.ids += t * a.top;
+    p.weights += t * a.top;
+    launch(p);
+  }
+}
+
 void launch_place(SortArgs q, hipStream_t st) {
   q.block_chunks = q.chunks ? (int)std::max<int64_t>(1, std::max<int64_t>(kPlacePairs, q.P / kCountBlocks) / q.chunk_pairs) : 0;
   const unsigned blocks = q.chunks ? (unsigned)((q.chunks + q.block_chunks - 1) / q.block_chunks) : 1;
@@ -1107,7 +1121,9 @@ hipError_t launch_route(const RouteArgs& a, const SortArgs* sort, hipStream_t st
   if (s.lanes < 0) {
     const int ne = (a.E + 63) / 64;
     auto go = [&](auto kernel) {
-      if (a.T) hipLaunchKernelGGL(kernel, dim3((unsigned)((a.T + 3) / 4)), dim3(256), 0, st, a);
+      in_slices(a, 4 * kMaxBlocks, [&](const RouteArgs& p) {
+        hipLaunchKernelGGL(kernel, dim3((unsigned)((p.T + 3) / 4)), dim3(256), 0, st, p);
+      });
     };
     if (ne <= 1) go(route_wave_kernel<1>);
     else if (ne <= 2) go(route_wave_kernel<2>);
@@ -1138,7 +1154,13 @@ hipError_t launch_route(const RouteArgs& a, const SortArgs* sort, hipStream_t st
     q.chunk_pairs = (int)(threads / s.lanes * iters * a.top);
     q.chunks = (int)blocks;
   }
-  auto go = [&](auto f) { f(a, q, mode, (int)iters, (unsigned)blocks, threads, st); };
+  // (blocks that sort or count take rounds enough to be few)
+  auto go = [&](auto f) {
+    if (mode != kNoSort) return f(a, q, mode, (int)iters, (unsigned)blocks, threads, st);
+    const int per = threads / s.lanes;
+    in_slices(a, kMaxBlocks * 256 / threads * per,
+              [&](const RouteArgs& p) { f(p, q, mode, 1, (unsigned)((p.T + per - 1) / per), threads, st); });
+  };
   if (s.experts == 4) go(go_route<16, 4>);
   else if (s.experts == 8) go(go_route<16, 8>);
   else if (s.lanes == 16) go(go_route<16, 16>);
@@ -1150,7 +1172,16 @@ hipError_t launch_route(const RouteArgs& a, const SortArgs* sort, hipStream_t st
 
 hipError_t launch_route_bwd(const RouteBwdArgs& a, hipStream_t st) {
   auto go = [&](auto kernel, int tokens) {
-    hipLaunchKernelGGL(kernel, dim3((unsigned)((a.T + 4 * tokens - 1) / (4 * tokens))), dim3(256), 0, st, a);
+    const int64_t step = 4 * tokens * kMaxBlocks, size = a.bf16 ? 2 : 4;
+    for (int64_t t = 0; t < a.T; t += step) {
+      RouteBwdArgs p = a;
+      p.T = std::min(step, a.T - t);
+      p.dweights += t * a.top;
+      p.ids += t * a.top;
+      p.logits = (const uint8_t*)a.logits + t * a.E * size;
+      p.dlogits = (uint8_t*)a.dlogits + t * a.E * size;
+      hipLaunchKernelGGL(kernel, dim3((unsigned)((p.T + 4 * tokens - 1) / (4 * tokens))), dim3(256), 0, st, p);
+    }
   };
   if (a.top > 16 || a.E > 512) go(route_bwd_kernel<64, 16>, 1);
   else if (a.E <= 64) go(route_bwd_kernel<16, 4>, 4);

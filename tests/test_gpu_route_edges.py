@@ -81,3 +81,32 @@ def test_groups_of_both_infinities(E, groups, keep, top):
     bias = 0.1 * torch.randn(E, generator=g, device="cuda")
     bias[:size], bias[0] = -inf, inf                   # the same by the bias
     check_route(m, torch.randn((6, E), generator=g, device="cuda"), top, "sigmoid", bias, groups, keep, 2)
+
+
+@pytest.mark.parametrize("E,top,T", [(2, 1, (1 << 28) + 37), (17, 17, (1 << 26) + 5)])
+def test_more_tokens_than_one_launch_holds(E, top, T):
+    """16 lanes, or a wave, for each of so many tokens are more than 2^32 threads: the last tokens are those of a second
+    launch, in both directions, some of them padding."""
+    m = require_gpu()
+    g = torch.Generator(device="cuda").manual_seed(E)
+    x = torch.empty((T, E), device="cuda", dtype=torch.bfloat16).normal_(generator=g)
+    valid = torch.ones(T, dtype=torch.uint8, device="cuda")
+    valid[T - 3] = valid[5] = 0
+    ids = torch.full((T, top), 77, device="cuda", dtype=torch.int32)
+    w = torch.full((T, top), 77.0, device="cuda")
+    m.moe_route_fwd(x, top, "sigmoid", renormalize=False, valid=valid, ids=ids, weights=w)
+    dl = m.moe_route_bwd(w, ids, x, "sigmoid", renormalize=False)
+    step = 1 << 23
+    for t in range(0, T, step):
+        xs, i, ws, d = x[t:t + step], ids[t:t + step].long(), w[t:t + step], dl[t:t + step]
+        real = valid[t:t + step].bool()
+        assert (i[~real] == -1).all() and not ws[~real].any() and not d[~real].any()
+        xs, i, ws, d = xs[real], i[real], ws[real], d[real]
+        want = xs.float().sort(dim=1, descending=True, stable=True).indices[:, :top]
+        assert torch.equal(i, want)
+        p = torch.sigmoid(xs.float())
+        # |x| < 8: three roundings and an exponential's 2 |x| + 2 units on either side
+        assert ((ws - p.gather(1, i)).abs() <= 40 * 2.0 ** -24 * ws).all()
+        slope = (p * p * (1 - p)).gather(1, i)
+        # (1 - p of torch's p has up to 2^-24 / (1 - p), that is e^8 units, off)
+        assert ((d.float().gather(1, i) - slope).abs() <= (2.0 ** -8 + 4000 * 2.0 ** -24) * slope).all()
