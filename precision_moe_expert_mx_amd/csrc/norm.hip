@@ -249,6 +249,11 @@ __global__ __launch_bounds__(WPR > 4 ? 64 * WPR : 256) void rmsnorm_kernel(NormA
     // tie of E4M3, whose 20 bits below the code are 0x80000, and a scale only where the maximum is that near to a power
     // of two.  There, and for what falls below the normal codes (2^-14 of the maximum, or scales that are not normal), y is
     // formed again in fp64 and rounded so that the code's rounding is the only one.
+    // The three units are those of normal numbers.  h w may be none where r > 1 lifts it back: a block whose maximum is at least
+    // 2^-111 r has an h w of 2^-111, and what is subnormal beside that lies below 2^-14 of the maximum.  A block of zeros is one
+    // of values below 2^-150 r, whose codes are 0 up to r = 2^13.  An r below 2^-126 leaves no block.
+    const uint32_t low = r32 < 0x1p-126f ? 0x7F800000u : __float_as_uint(0x1p-111f * fmaxf(r32, 1.0f));
+    const bool zeros = r32 > 0x1p13f;
 #pragma unroll
     for (int k = 0; k < NCH; ++k) {
       const int64_t c = 8 * (l + 64 * WPR * k);
@@ -265,7 +270,7 @@ __global__ __launch_bounds__(WPR > 4 ? 64 * WPR : 256) void rmsnorm_kernel(NormA
       }
       m = quad_max(__float_as_uint(top));           // 4 lanes hold a block of 32
       const bool again = nearest <= 8u << 12 || ((m + 4) & 0x7FFFFFu) <= 8 || m >= 0x7F800000u ||
-                         (m != 0 && (m < 0x08000000u || least >> 1 < m - 0x07000000u));
+                         ((m != 0 || zeros) && (m < low || least >> 1 < m - 0x07000000u));
       if (__ballot(again)) {
         m = 0;
         values(k, f, w);
