@@ -89,9 +89,11 @@ def route_bwd(dweights, ids, logits, score="softmax", renorm=True, scale=1.0):
     out = np.zeros((T, E))
     for t in range(T):
         here = [k for k in range(ids.shape[1]) if 0 <= ids[t, k] < E]
+        if not here:
+            continue
         sel, dw = _chosen_scores(logits[t], p[t], ids[t, here], score, renorm), dweights[t, here]
         total = sel.sum() if renorm else 1.0
-        if not here or total == 0:
+        if total == 0:
             continue
         ds = scale * dw / total
         if renorm:

@@ -137,3 +137,10 @@ def test_softmax_weights_of_the_chosen():
         np.testing.assert_allclose(w, [[1 / (1 + np.exp(-2.0)), 1 / (1 + np.exp(2.0))]], rtol=1e-12)
         d = oracle.route_bwd(np.array([[1.0, 0.0]]), ids, x)
         np.testing.assert_allclose(d, [[0, 0, -w[0, 0] * w[0, 1], w[0, 0] * w[0, 1]]], rtol=1e-12)
+
+
+def test_gradients_of_tokens_without_choices():
+    for score in ("softmax", "sigmoid"):
+        for renorm in (True, False):
+            d = oracle.route_bwd(np.ones((2, 2)), np.array([[-1, -1], [7, 1]]), np.zeros((2, 4)), score, renorm)
+            assert not d[0].any() and d[1].any() == (not renorm)
