@@ -97,7 +97,7 @@ def route_bwd(dweights, ids, logits, score="softmax", renorm=True, scale=1.0):
             continue
         ds = scale * dw / total
         if renorm:
-            ds = ds - (scale * dw * sel).sum() / total ** 2
+            ds = ds - (scale * dw * (sel / total)).sum() / total
         if score == "softmax" and renorm:              # (a softmax over the chosen: the others' gradient is 0, not a rounding)
             np.add.at(out[t], ids[t, here], ds * sel)
             continue

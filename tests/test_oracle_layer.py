@@ -144,3 +144,12 @@ def test_gradients_of_tokens_without_choices():
         for renorm in (True, False):
             d = oracle.route_bwd(np.ones((2, 2)), np.array([[-1, -1], [7, 1]]), np.zeros((2, 4)), score, renorm)
             assert not d[0].any() and d[1].any() == (not renorm)
+
+
+def test_gradients_of_vanishing_sigmoid_scores():
+    """Far below 0 a sigmoid is e^x: renormalised, weights and gradients are those of a softmax over the chosen."""
+    x = -500 - np.arange(5.0)[None]
+    ids, w = oracle.route(x, 3, "sigmoid")
+    dw = np.array([[1.0, -2.0, 0.5]])
+    np.testing.assert_allclose(w, oracle.route(x, 3)[1], rtol=1e-12)
+    np.testing.assert_allclose(oracle.route_bwd(dw, ids, x, "sigmoid"), oracle.route_bwd(dw, ids, x), rtol=1e-12)
