@@ -592,7 +592,7 @@ mxmoe_status rmsnorm_bwd(const void* dy, mxmoe_dtype dydt, const void* h, mxmoe_
  *   ids [T, top] = the experts with the largest c, in falling order; equal c go to the lower index
  *   weights f32 [T, top] = scale * p of the chosen, divided by their sum if renormalize (0 where that sum is 0)
  *   (softmax, renormalised: a softmax over the chosen logits, also where one that is not chosen is infinitely larger)
- * Both comparisons are those of fp64 values.  A logit of -infinity is an expert with p = 0.  A NaN
+ * Weights are formed in fp32, off by at most 2^-19 of themselves plus 2^-149 max(1, |scale|).  Both comparisons are those of fp64 values.  A logit of -infinity is an expert with p = 0.  A NaN
  * ranks last (every c of a row of softmax scores with a bias is one if a logit is; a group's sum of +infinity and -infinity
  * is one) and shows in the weights that contain it.  valid (bytes [T], or NULL): tokens with 0 are padding, with ids -1 and weights 0.
  * 1 <= E <= 1024, 1 <= top <= 64, top <= E / groups * keep_groups, groups <= 64, T * top < 2^31.

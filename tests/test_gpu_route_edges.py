@@ -1,10 +1,11 @@
 """Routing at the edges of its keys, masks and sizes, on the GPU against the float64 reference."""
+import numpy as np
 import pytest
 import torch
 
 import oracle
 from gpu_util import require_gpu
-from test_gpu_route import check_route
+from test_gpu_route import DT, HALF, U, check_route, f64, spread
 
 pytestmark = pytest.mark.gpu
 
@@ -110,3 +111,58 @@ def test_more_tokens_than_one_launch_holds(E, top, T):
         slope = (p * p * (1 - p)).gather(1, i)
         # (1 - p of torch's p has up to 2^-24 / (1 - p), that is e^8 units, off)
         assert ((d.float().gather(1, i) - slope).abs() <= (2.0 ** -8 + 4000 * 2.0 ** -24) * slope).all()
+
+
+def check_weights(w, rw, scale=1.0):
+    err = np.abs(f64(w) - rw)
+    tol = 2.0 ** -19 * np.abs(rw) + 2.0 ** -149 * max(1.0, abs(scale))
+    assert (err <= tol).all(), f"weights: {np.nanmax(err / tol):.3g} of the tolerance"
+
+
+def check_bwd(m, x, ids, dw, score, renorm, scale=1.0):
+    """moe_route_bwd against the reference: 64 units of each term (scores as the weights, 32; their differences, products and
+    sums over at most 16 choices), for the softmax that is not renormalised 2 |x - max| more, and half a step of bf16."""
+    got, z, d, rid = f64(m.moe_route_bwd(dw, ids, x, score, renorm, scale)), f64(x), f64(dw), ids.cpu().numpy()
+    ref = oracle.route_bwd(d, rid, z, score, renorm, scale)
+    p = oracle.route_scores(z, score)
+    q = oracle.route_scores(-z, score) if score == "sigmoid" else np.ones_like(p)
+    here = rid >= 0
+    at = np.where(here, rid, 0).astype(np.int64)
+    sel = oracle.route_scores(np.take_along_axis(z, at, axis=1), score) if renorm and score == "softmax" else np.take_along_axis(p, at, axis=1)
+    sel = np.where(here, sel, 0.0)
+    w = sel / np.maximum(sel.sum(axis=1, keepdims=True), 1e-300) if renorm else sel
+    term = abs(scale) * w * (np.abs(d) + ((w * np.abs(d)).sum(axis=1, keepdims=True) if renorm else 0))
+    size = np.zeros_like(p)
+    np.add.at(size, (np.arange(len(z))[:, None], at), np.where(here, term * np.take_along_axis(q, at, axis=1), 0.0))
+    units = np.full((len(z), 1), 64.0)
+    if score == "softmax" and not renorm:
+        size = size + p * term.sum(axis=1, keepdims=True)
+        units = units + 2 * np.minimum(spread(z), 200)
+    tol = units * U * size + HALF["bf16" if x.dtype == torch.bfloat16 else "f32"] * np.abs(ref) + 2.0 ** -133
+    if score == "softmax" and not renorm:              # (a score below 2^-126 of an expert that was not chosen counts as 0)
+        tol = tol + 2.0 ** -126 * term.sum(axis=1, keepdims=True)
+    err = np.abs(got - ref)
+    assert (err <= tol).all(), f"dlogits, {score} {renorm} {scale} {x.dtype}: {np.max(err / tol):.3g} of the tolerance"
+
+
+@pytest.mark.parametrize("E,top", [(64, 6), (256, 8), (512, 16), (1000, 16), (40, 33)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_small_weights_are_as_exact_as_large_ones(E, top, score):
+    """Chosen logits up to 100 below the largest, down to weights that are subnormal in fp32."""
+    m = require_gpu()
+    g = torch.Generator(device="cuda").manual_seed(E)
+    T = 120
+    x = torch.randn((T, E), generator=g, device="cuda") - torch.linspace(0, 90, T, device="cuda")[:, None]
+    x[:, 3] += torch.linspace(0, 90, T, device="cuda") if score == "softmax" else 0
+    bias = torch.zeros(E, device="cuda")
+    bias[3] = 1.0                                      # (always chosen)
+    for dt in DT.values():
+        for b in (None, bias):
+            for renorm in (True, False):
+                for scale in (1.0, 2.5):
+                    z = x.to(dt)
+                    ids, w = m.moe_route_fwd(z, top, score, b, renormalize=renorm, scale=scale)
+                    rid, rw = oracle.route(f64(z), top, score, None if b is None else f64(b), renorm=renorm, scale=scale)
+                    assert np.array_equal(ids.cpu().numpy(), rid)
+                    check_weights(w, rw, scale)
+                    check_bwd(m, z, ids, torch.randn((T, top), generator=g, device="cuda"), score, renorm, scale)
