@@ -166,3 +166,40 @@ def test_small_weights_are_as_exact_as_large_ones(E, top, score):
                     assert np.array_equal(ids.cpu().numpy(), rid)
                     check_weights(w, rw, scale)
                     check_bwd(m, z, ids, torch.randn((T, top), generator=g, device="cuda"), score, renorm, scale)
+
+
+@pytest.mark.parametrize("E,groups,keep,top", [(64, 1, None, 6), (256, 8, 4, 8), (1000, 1, None, 12), (60, 1, None, 20)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_biases_that_switch_experts_off(E, groups, keep, top, score):
+    """A bias of -infinity, of the type's lowest value or of 1e30 and more keeps experts out, or in, of every token."""
+    m = require_gpu()
+    g = torch.Generator(device="cuda").manual_seed(E)
+    x = torch.randn((50, E), generator=g, device="cuda")
+    for off in (float("-inf"), torch.finfo(torch.float32).min, -1e30, -1e4):
+        bias = 0.1 * torch.randn(E, generator=g, device="cuda")
+        bias[torch.rand(E, generator=g, device="cuda") < 0.3] = off
+        for dt in DT.values():
+            ids, w, _, rw = check_route(m, x.to(dt), top, score, bias, groups, keep, 2 if groups > 1 else 1)
+            assert (bias[ids.long()] > -1).all()
+            check_weights(w, rw)
+    bias[5], bias[9] = float("inf"), 1e30
+    ids = check_route(m, x, top, score, bias)[0]
+    assert (ids[:, 0] == 5).all() and (ids[:, 1] == 9).all()
+
+
+@pytest.mark.parametrize("E,groups,keep,top", [(64, 1, None, 6), (256, 8, 4, 8), (256, 8, 2, 16), (72, 9, 3, 8), (16, 2, 1, 8),
+                                               (60, 1, None, 20)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_fewer_experts_than_are_chosen(E, groups, keep, top, score):
+    """Most or all experts are kept out by -infinity, some logits are equal or masked: the index decides among those out."""
+    m = require_gpu()
+    g = torch.Generator(device="cuda").manual_seed(E)
+    for part in (0.5, 0.95, 1.0):
+        x = torch.randn((30, E), generator=g, device="cuda")
+        x[10:] = torch.randint(-2, 3, (20, E), generator=g, device="cuda").float()
+        x[20:, ::3] = -torch.inf
+        bias = 0.1 * torch.randn(E, generator=g, device="cuda")
+        bias[torch.rand(E, generator=g, device="cuda") < part] = -torch.inf
+        for dt in DT.values():
+            for group_top in (1, 2):
+                check_route(m, x.to(dt), top, score, bias, groups, keep, group_top)
