@@ -1074,10 +1074,13 @@ def moe_route_fwd(logits, top: int, score: str = "softmax", bias=None, groups: i
     """The `top` experts of each token and their weights from router logits [T, E] (f32 or bf16): (ids int32 [T, top],
     weights f32 [T, top]).
 
-    The choice goes by softmax or sigmoid scores, plus bias f32 [E] if given (which balances and does not weigh);
-    of `groups` groups of consecutive experts only the keep_groups with the largest sum of their group_top (1 or 2)
-    best stay.  Equal ones: the lower index.  Weights are the scores, divided by their sum if renormalize, times
-    scale.  valid (bool [T]): tokens that are False get ids of -1 and weights of 0."""
+    The choice goes by c: the softmax or sigmoid scores plus bias f32 [E] (which balances and does not weigh), or without
+    a bias the logits, which order the experts alike.  Of `groups` groups of consecutive experts only the keep_groups with
+    the largest sum of their group_top (1 or 2) best c stay: with group_top=2 and no bias these are sums of two logits, which
+    do not order the groups as sums of scores do (a bias of zeros gives those).  Equal ones: the lower index.  Weights are
+    the scores, divided by their sum if renormalize, times scale.  valid (bool [T]): tokens that are False get ids of -1 and
+    weights of 0.  A bias of -infinity keeps an expert out of every choice in which enough others are left; large finite
+    biases do so too and are slower, since scores are resolved relative to the largest |c|."""
     return _route("moe_route_fwd", logits, top, score, bias, groups, keep_groups, group_top, renormalize, scale, valid,
                   ids, weights, ((), ()), stream)
 

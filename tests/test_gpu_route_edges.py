@@ -203,3 +203,13 @@ def test_fewer_experts_than_are_chosen(E, groups, keep, top, score):
         for dt in DT.values():
             for group_top in (1, 2):
                 check_route(m, x.to(dt), top, score, bias, groups, keep, group_top)
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_two_best_of_a_group(dt):
+    """group_top=2 sums logits without a bias, and scores with one: here they prefer different groups."""
+    m = require_gpu()
+    x = torch.tensor([[10.0, 0.125, 4.0, 4.0]], device="cuda").to(DT[dt])
+    for score, first in (("sigmoid", [2, 3]), ("softmax", [0, 1])):
+        assert check_route(m, x, 2, score, None, 2, 1, 2)[0].tolist() == [[0, 1]]
+        assert check_route(m, x, 2, score, torch.zeros(4, device="cuda"), 2, 1, 2)[0].tolist() == [first]
