@@ -213,3 +213,29 @@ def test_two_best_of_a_group(dt):
     for score, first in (("sigmoid", [2, 3]), ("softmax", [0, 1])):
         assert check_route(m, x, 2, score, None, 2, 1, 2)[0].tolist() == [[0, 1]]
         assert check_route(m, x, 2, score, torch.zeros(4, device="cuda"), 2, 1, 2)[0].tolist() == [first]
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_gradients_of_masked_rows(score):
+    """Values of the gradients where logits are masked, infinite or far apart, and of tokens of padding."""
+    m = require_gpu()
+    g = torch.Generator(device="cuda").manual_seed(8)
+    inf = float("inf")
+    for E in (6, 64, 200):
+        for dt in (torch.float32, torch.bfloat16):
+            x = torch.randn((12, E), generator=g, device="cuda").to(dt)
+            x[1] = -inf
+            x[2, 2:] = -inf
+            x[3] = torch.finfo(dt).min
+            x[4, 1:] = torch.finfo(dt).min
+            x[5, 5] = inf
+            x[6, 2:5] = inf
+            x[7] *= 1000
+            x[8] = -500 - x[8].abs()
+            valid = torch.ones(12, dtype=torch.bool, device="cuda")
+            valid[9:11] = False
+            for bias in (None, torch.linspace(-0.1, 0.1, E, device="cuda")):
+                for renorm in (True, False):
+                    ids, w, _, rw = check_route(m, x, 4, score, bias, renorm=renorm, valid=valid)
+                    check_weights(w, rw)
+                    check_bwd(m, x, ids, torch.randn((12, 4), generator=g, device="cuda"), score, renorm)
