@@ -32,8 +32,11 @@
  *    is launched and a status != MXMOE_OK is returned, with a message from
  *    mxmoe_last_error() (thread-local, valid until the next call on the
  *    thread).  No function throws or aborts.
- *  - Offsets: int32 offs[G+1], offs[0] = 0, non-decreasing, offs[G] = M; rows of
- *    the token tensors are sorted by expert.  Invalid device offsets cannot be
+ *  - Offsets: int32 offs[G+1], offs[0] = 0, non-decreasing, offs[G] <= M; rows of
+ *    the token tensors are sorted by expert.  offs[G] < M (one GPU's share of the
+ *    rows, as moe_sort gives it): rows from offs[G] on belong to no expert here, take
+ *    part in no result, and row-wise outputs keep what they hold there (the row-wise
+ *    quantisers without offsets take every row).  Invalid device offsets cannot be
  *    detected without a synchronisation: kernels clamp them into [0, M] so no
  *    access leaves the buffers, and the results are then unspecified.
  *  - Pointers must be 16-byte aligned (4-byte for scale arrays).
@@ -164,8 +167,8 @@ mxmoe_status mx_grouped_gemm_fwd(const uint8_t* qx, const uint8_t* sx,
  *      routing offsets (32-row blocks restarting at each expert, pads and the tail 0x00); ldh % 32
  *      == 0 and ldh >= mx_colwise_ld_min(M, G).  Both copies of H leave the epilogue, so H never
  *      reaches memory in a wider format and is not read back to be quantised.
- * Precise feed; N % 256 == 0; qx/sx, qw/sw and offs as for mx_grouped_gemm_fwd.  M == 0 is a no-op
- * (nothing is written). */
+ * Precise feed; N % 256 == 0; qx/sx, qw/sw and offs as for mx_grouped_gemm_fwd.  With M == 0, or no
+ * expert that has rows, nothing is written. */
 mxmoe_status mx_grouped_gemm_fwd_swiglu(const uint8_t* qx, const uint8_t* sx,
                                         const uint8_t* qw, const uint8_t* sw,
                                         const int32_t* offs, int32_t G, int64_t M, int64_t N, int64_t K,
@@ -600,8 +603,8 @@ mxmoe_status rmsnorm_bwd(const void* dy, mxmoe_dtype dydt, const void* h, mxmoe_
  * moe_sort: the chosen pairs in the order of their experts, for the `G` experts first .. first + G - 1 that are
  * here (all, or one GPU's): offs [G + 1] with offs[0] = 0, row_idx [T * top] the token of each row, pos [T, top]
  * the row of each pair.  Rows of an expert keep the order of their tokens.  Pairs of other experts and of
- * negative ids have no row: their pos is -1, and row_idx is -1 from offs[G] on.  The forward and data-gradient products on
- * such offs (offs[G] < M = T * top) leave the rows from offs[G] on as they were, and the weight gradients do not read them.  1 <= G <= 1024.
+ * negative ids have no row: their pos is -1, and row_idx is -1 from offs[G] on.  offs[G] may so be less than T * top, the rows
+ * of the products that take it.  1 <= G <= 1024.
  * ws: moe_sort_workspace(T * top, G) bytes that the caller owns during the call (NULL where that is 0).
  *
  * moe_route_sort: both at once (the same results); ws as in moe_sort.  first + G <= E.
@@ -648,7 +651,8 @@ mxmoe_status moe_combine_bwd(const void* dout, mxmoe_dtype ddt, const int32_t* p
                              void* stream);
 
 /* Opt-in offsets validator: copies offs to the host (synchronising `stream`)
- * and checks offs[0] == 0, non-decreasing, offs[G] == M.  Returns
+ * and checks offs[0] == 0, non-decreasing, offs[G] == M (so it names the
+ * last entry of a share's offsets unless M is that).  Returns
  * MXMOE_ERR_OFFSETS with a message naming the first bad index. */
 mxmoe_status mxmoe_check_offsets(const int32_t* offs, int32_t G, int64_t M, void* stream);
 

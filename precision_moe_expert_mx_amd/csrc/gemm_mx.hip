@@ -242,7 +242,7 @@ __device__ __forceinline__ void act_epilogue(const GemmArgs& p, const Tile& t, c
   }
   // the tile holding the last routed row zeroes the tail of its 128 rows of qT and sT: the columns past
   // the last expert's blocks
-  if (t.row0 + t.rows == p.M) {
+  if (t.row0 + t.rows == t.row_end) {
     const int64_t tail = ldq - t.col_end;                           // a multiple of 32
     const int64_t chunks = tail / 16;
     for (int64_t k = tid; k < (BN / 2) * chunks; k += NT) {
@@ -730,6 +730,7 @@ __global__ __launch_bounds__(NT, 1) void mx_grouped_gemm_kernel(GemmArgs p) {
   t.row0 = uniform64(t.row0);
   t.col0 = uniform64(t.col0);
   t.col_end = uniform64(t.col_end);
+  t.row_end = uniform64(t.row_end);
   __syncthreads();                               // scheduler scratch is reused for operands
   run_tile<MODE, FEED, SDW, FP4, ACT, BWP2>(p, t, lds);
 }

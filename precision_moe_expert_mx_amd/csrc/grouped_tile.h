@@ -24,6 +24,7 @@ struct GroupTile {
   int64_t col0;   // wgrad, gated forward: first column of the expert in the column-wise layout
   int nblk;       // wgrad: blocks (of the column-wise layout) in the expert's contraction
   int64_t col_end;  // gated forward: columns of the column-wise layout holding blocks (all experts)
+  int64_t row_end;  // gated forward: rows of all experts
 };
 
 __device__ __forceinline__ int cdiv(int64_t a, int b) { return (int)((a + b - 1) / b); }
@@ -169,6 +170,7 @@ __device__ bool decode_grouped_tile(const GemmArgs& p, char* lds, GroupTile& t) 
   t.rows = (int)min((int64_t)TBM, (int64_t)s_rs[g + 1] - t.row0);
   t.col0 = CB ? CBLK * (int64_t)s_cb[g] : 0;
   t.col_end = CB ? CBLK * (int64_t)s_cb[G] : 0;
+  t.row_end = CB ? s_rs[G] : 0;
   t.nblk = cdiv(m_g, CBLK);
   if (MODE == kWgrad) {
     // offsets that are not monotone could place an expert past the leading dimension: clip
