@@ -816,9 +816,10 @@ __global__ __launch_bounds__(route_threads(KIND == kBiased)) void route_kernel(R
   }
   // The wave's first token of round 0.  It is a scalar, and so are the end of the rounds and the mask of the tokens in doubt: a
   // mask kept per lane makes the loop over them one of the execution mask, which a register spilled at its joins never ended.
-  const int64_t wave0 = (int64_t)blockIdx.x * iters * tokens + __builtin_amdgcn_readfirstlane(wave * TPW);
+  const uint32_t wave0 = blockIdx.x * (uint32_t)(iters * tokens) + __builtin_amdgcn_readfirstlane(wave * TPW);
+  const uint32_t T = (uint32_t)p.T;                // (below 2^31, and a block's tokens past them below 2^32)
   // a token's choices, with their logits and its softmax
-  auto write = [&](int64_t t, bool live, int id, float xk, float mx, float total) {
+  auto write = [&](uint32_t t, bool live, int id, float xk, float mx, float total) {
     float w;
     if (p.renorm) {
       // relative to the largest chosen logit, so that no sum vanishes
@@ -837,9 +838,9 @@ __global__ __launch_bounds__(route_threads(KIND == kBiased)) void route_kernel(R
       if (sigmoid) w = e * __builtin_amdgcn_rcpf(1.0f + __expf(-fabsf(xk)));
       else w = mx == -__builtin_inff() && xk == xk ? 0.0f : (xk == mx ? 1.0f : e) / total;
     }
-    if (chosen && t < p.T) {
+    if (chosen && t < T) {
       id = live ? id : -1;
-      p.ids[t * top + sub] = id;
+      p.ids[t * top + sub] = id;                   // (T top is below 2^31)
       p.weights[t * top + sub] = live ? w * (float)p.scale : 0.0f;
       if (mode == kCount) atomicAdd(&cnt[bucket(q, id)], 1);
       if (mode == kSortHere) cnt[t * top + sub] = id;
@@ -848,11 +849,12 @@ __global__ __launch_bounds__(route_threads(KIND == kBiased)) void route_kernel(R
   for (int it0 = 0; it0 < iters; it0 += kBatch) {
     uint64_t later = 0;                            // tokens in doubt, TPW bits per round
     for (int it = it0; it < min(it0 + kBatch, iters); ++it) {
-      const int64_t t0 = wave0 + (int64_t)it * tokens, t = t0 + lane / L, tr = min(t, p.T - 1);
-      if (t0 >= p.T) break;
-      const bool live = t < p.T && (!p.valid || p.valid[tr]);
+      const uint32_t t0 = wave0 + it * tokens, t = t0 + lane / L, tr = min(t, T - 1);
+      if (t0 >= T) break;
+      const bool live = t < T && (!p.valid || p.valid[tr]);
+      const int64_t row = (int64_t)tr * E;
       P part;
-      part.load(p, tr * E, span, bias);
+      part.load(p, row, span, bias);
       bool doubt = part.odd, kept = true;
       if (p.groups > 1) {
         const int size = E / p.groups, lanes = span.lanes, g = span.group;
@@ -883,12 +885,12 @@ __global__ __launch_bounds__(route_threads(KIND == kBiased)) void route_kernel(R
       part.template largest<LS>(best, kept);
       pick(best, sub, top, mine, last);            // lane k of the token takes choice k
       const int id = P::expert(mine), idk = chosen && id < E ? id : 0;
-      const float xk = load_logit(p.logits, tr * E + idk, bf16);
+      const float xk = load_logit(p.logits, row + idk, bf16);
       if constexpr (!P::exact) {
         constexpr int B = P::B;
         const int idl = min(P::expert(last), E - 1);
         const float bk = P::biased ? p.bias[idk] : 0.0f;
-        const float xl = load_logit(p.logits, tr * E + idl, bf16), bl = P::biased ? p.bias[idl] : 0.0f;
+        const float xl = load_logit(p.logits, row + idl, bf16), bl = P::biased ? p.bias[idl] : 0.0f;
         const uint32_t q_last = last >> B, q_mine = mine >> B, within = P::within(p);
         // neighbours in the list
         const uint32_t q_prev = (uint32_t)__shfl_up((int)q_mine, 1, 64);
@@ -917,29 +919,30 @@ __global__ __launch_bounds__(route_threads(KIND == kBiased)) void route_kernel(R
       for (int k = 0; k < TPW; ++k)
         bits |= (need >> (k * L) & (L == 64 ? ~0ull : (1ull << (L & 63)) - 1)) ? 1u << k : 0u;
       later |= (uint64_t)bits << (TPW * (it - it0));
-      write(bits >> (lane / L) & 1 ? p.T : t, live, id, xk, part.mx, part.total);
+      write(bits >> (lane / L) & 1 ? T : t, live, id, xk, part.mx, part.total);
     }
     // tokens in doubt, as many at a time as the wave holds
     while (later) {
-      int64_t t = 0;
+      uint32_t t = 0;
       bool real = false;
 #pragma unroll
       for (int k = 0; k < TPW; ++k) {
         if (later) {
           const int bit = __builtin_ctzll(later);
           if (lane / L == k) {
-            t = wave0 + (int64_t)(it0 + bit / TPW) * tokens + bit % TPW;
+            t = wave0 + (it0 + bit / TPW) * tokens + bit % TPW;
             real = true;
           }
           later &= later - 1;
         }
       }
       const int id = second_look<L, NE, KIND>(p, t, real);
-      const float xk = load_logit(p.logits, t * E + (chosen ? id : 0), bf16);
+      const int64_t row = (int64_t)t * E;
+      const float xk = load_logit(p.logits, row + (chosen ? id : 0), bf16);
       float mx = -__builtin_inff(), total = 1;
       if (!sigmoid && !p.renorm) {
         float x[NE], s = 0;
-        load_logits<NE>(p.logits, t * E, span.at, span.end, span.whole, bf16, x);
+        load_logits<NE>(p.logits, row, span.at, span.end, span.whole, bf16, x);
 #pragma unroll
         for (int j = 0; j < NE; ++j) mx = fmaxf(mx, x[j]);
         mx = max_over<L>(mx);
@@ -947,7 +950,7 @@ __global__ __launch_bounds__(route_threads(KIND == kBiased)) void route_kernel(R
         for (int j = 0; j < NE; ++j) s += relative_exp(x[j], mx);
         total = sum_over<L>(s);
       }
-      write(real ? t : p.T, true, id, xk, mx, total);
+      write(real ? t : T, true, id, xk, mx, total);
     }
   }
   if (mode == kCount) {

@@ -239,3 +239,29 @@ def test_gradients_of_masked_rows(score):
                     ids, w, _, rw = check_route(m, x, 4, score, bias, renorm=renorm, valid=valid)
                     check_weights(w, rw)
                     check_bwd(m, x, ids, torch.randn((12, 4), generator=g, device="cuda"), score, renorm)
+
+
+def test_as_many_pairs_as_there_may_be():
+    """2^31 - 1 tokens, one choice each: token, pair and row numbers up to the largest int32."""
+    m = require_gpu()
+    T, step = 2 ** 31 - 1, 1 << 26
+    x = torch.empty((T, 2), device="cuda", dtype=torch.bfloat16)
+    for t in range(0, T, step):
+        x[t:t + step].normal_(generator=torch.Generator(device="cuda").manual_seed(t))
+    ids, w, offs, row_idx, pos = m.moe_route_sort(x, 1, score="sigmoid", renormalize=False)
+    del w
+    done = [0, 0]
+    n0 = int(offs[1])
+    assert offs.tolist() == [0, n0, T]
+    for t in range(0, T, step):
+        i = (x[t:t + step, 1] > x[t:t + step, 0]).long()
+        assert torch.equal(ids[t:t + step, 0].long(), i)
+        here = torch.arange(t, min(T, t + step), device="cuda")
+        for e in (0, 1):
+            mine = here[i == e]
+            first = e * n0 + done[e]
+            want = torch.arange(first, first + len(mine), device="cuda")
+            assert torch.equal(pos[t:t + step, 0][i == e].long(), want)
+            assert torch.equal(row_idx[first:first + len(mine)].long(), mine)
+            done[e] += len(mine)
+    assert done == [n0, T - n0]
