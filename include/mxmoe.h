@@ -554,7 +554,8 @@ mxmoe_status adamw_dequantize(const uint8_t* q, const float* s, int64_t n, int32
  *   h = x + residual, added in fp32, rounded to the residual's type;  r = 1 / sqrt(mean_c h^2 + eps);  y = h r w
  * x [R, C] (xdt), residual [R, C] (rdt) or NULL (then h = x, is not written, and rdt and h are ignored), w [C]
  * (wdt), y [R, C] (ydt), h [R, C] (rdt; may be the residual's own buffer, every other output has its own).  The squares are summed
- * in fp64, everything else is fp32.  C % 8 == 0, C <= 32768, 2^-126 <= eps <= 1e30; R == 0 is a no-op.
+ * in fp64, everything else is fp32 (r too, which is subnormal and off by up to 2^-22 for rows of rms above 8.5e37).
+ * C % 8 == 0, C <= 32768, 2^-126 <= eps <= 1e30; R == 0 is a no-op.
  *
  * int8_quantize_rmsnorm_rowwise: the same y as 8-bit integers with a scale per row, q int8 [R, C], s f32 [R], as
  * int8_quantize_rowwise makes them, but in one rounding from the exact values: with v = h w (r cancels),
