@@ -439,8 +439,9 @@ __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(SortArgs p) {
 //   the sum, two of the reciprocal), the addition by A 2^-24: with the roundings of the difference 5 steps for each of two, so 16
 //   are in doubt.  A softmax score is off by at most 30 * 2^-24 of the largest (its own exponential 3, the sum's terms and 22
 //   additions): 40 steps.
-//   Experts whose bias is -infinity are left out of A and share the least step (as tokens in fp64, as for other infinities, 65536
-//   of them over 256 experts took 880 us, now 78).  A large finite bias makes the steps coarse: -5 88 us, -100 121, -1e4 335.
+//   Experts whose bias is -infinity are left out of A and share the least step (65536 tokens over 256 experts, a ninth of them kept
+//   out so: 78 us; with all tokens in fp64, as other infinities have it, 880).  A large finite bias makes the steps coarse: the
+//   same by a bias of -5 88 us, of -100 121, of -1e4 335.
 // Two experts in doubt are settled if they are alike (the same logit and bias: equal c, the index decides); a token that
 // has others, next to each other in its list or across its end, is evaluated in fp64 by its wave.
 // Threads of a block, at most: 16 waves of up to 128 registers, or with a bias 8 waves of more (with 128 they spill: 65536 tokens over
